@@ -376,6 +376,122 @@ DISCO_API int disco_fwd_host(const disco_psi* psi, const void* x_host, void* X_h
 DISCO_API int disco_bwd_host(const disco_psi* psi, const void* G_host, void* gx_host, int32_t B, int32_t C,
                              disco_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Training operators around the convolution ----------------------------
+   Activations are [B, C, P]: P the pixels of a grid (H * W), C the channels.
+   P = 1 is the layout of B rows of C features.  P and all offsets are 64-bit. */
+
+/* Channel norm: the sum of two activations, its root-mean-square norm over
+   the channels of each pixel, and an optional copy of the norm in 8 bits:
+     h = x + residual                           (h = x where residual is NULL)
+     y[b,c,p] = weight[c] * h[b,c,p] / sqrt(mean_c h[b,c,p]^2 + eps)
+     m[b,g,p] = max(1e-30, max of |y[b,c,p]| over the channels c of group g)
+     scale[b,g,p] = m / 448
+     q[b,c,p] = e4m3(y[b,c,p] * (448 / m))      (8-bit float, 448 its largest)
+   in fp32, each output rounded once (y and q come from the unrounded h).
+   Groups are runs of `group` channels, the last one shorter when group does
+   not divide C; group = 0 or >= C is one group.  A NaN in y is stored as the
+   e4m3 NaN and does not count to m; an infinite m gives an infinite scale, and
+   that group reads back as NaN.  |h| up to 1e18 / sqrt(C) keeps the sum of
+   squares within fp32; beyond it y is 0.
+   x, residual, h, y: [B, C, P] of `dtype`; weight: [C] of `dtype` (NULL: ones);
+   q: [B, C, P] bytes; scale: [B, ceil(C / group), P] fp32.
+   NULL outputs are not written: at least one of y and q is given, q and scale
+   come together, h only with residual.  eps > 0, finite.  An output may be the
+   same buffer as x or residual (h in place of the residual stream); any other
+   overlap with an input or another output is DISCO_ERR_INVALID_ARG.
+   Asynchronous on `stream`; no workspace. */
+DISCO_API int disco_rms_norm(const void* x, const void* residual, const void* weight, float eps, void* h, void* y,
+                             void* q, float* scale, int32_t group, int32_t B, int32_t C, int64_t P,
+                             disco_dtype dtype, void* stream);
+
+/* Device workspace bytes of disco_rms_norm_bwd: fp32 partial sums of dweight
+   (0 for invalid arguments). */
+DISCO_API size_t disco_rms_norm_bwd_workspace_bytes(int32_t B, int32_t C, int64_t P, disco_dtype dtype);
+
+/* Gradient of disco_rms_norm with respect to h (which is the gradient of x and
+   of residual alike) and weight, from the stored h:
+     n = h / sqrt(mean_c h^2 + eps),  g = weight * dy
+     dx = (g - n * mean_c(g n)) / sqrt(mean_c h^2 + eps) + dh
+     dweight[c] = sum_{b,p} dy * n
+   dh is the gradient that reaches h past the norm, through the residual
+   stream (NULL: none).  fp32 arithmetic, each output rounded once; the sum
+   over pixels runs in a fixed order (deterministic).
+   dy, h, dh, dx: [B, C, P] of `dtype`; weight (NULL: ones), dweight: [C] of
+   `dtype`.  dweight NULL: not computed, no workspace needed.  dx may be the
+   same buffer as dy, h or dh; any other overlap of an output with a tensor or
+   the workspace is DISCO_ERR_INVALID_ARG.  workspace: 16-byte aligned,
+   >= disco_rms_norm_bwd_workspace_bytes.  Asynchronous on `stream`. */
+DISCO_API int disco_rms_norm_bwd(const void* dy, const void* h, const void* weight, const void* dh, float eps,
+                                 void* dx, void* dweight, int32_t B, int32_t C, int64_t P, disco_dtype dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The activation that q and scale of disco_rms_norm stand for (a training
+   program keeps them in place of y and restores y for
+   disco_fused_conv_bwd_weight):  x[b,c,p] = q[b,c,p] * scale[b, c / group, p],
+   rounded once to `dtype`.  No buffers may overlap.  Asynchronous. */
+DISCO_API int disco_dequant_e4m3(const void* q, const float* scale, void* x, int32_t group, int32_t B, int32_t C,
+                                 int64_t P, disco_dtype dtype, void* stream);
+
+/* One gradient of a model: n elements at `grad` (dtype) and where the clipped
+   gradient goes: `out` (out_dtype), either `grad` itself with the same type
+   (in place) or a buffer that overlaps no gradient and no other out; NULL
+   where only the norm is wanted.  Device pointers aligned to their element
+   (views into a flat buffer need no more); n = 0 is allowed, with any
+   pointers. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t out_dtype;
+} disco_grad_tensor;
+
+/* A checked list of gradients, filled by disco_grad_plan.  It refers to the
+   caller's array, which must stay as it is while the plan is used. */
+typedef struct {
+  const disco_grad_tensor* tensors; /* host array [count] */
+  int32_t count;
+  int32_t has_out;  /* 1 if every gradient with n > 0 has an out */
+  int64_t numel;    /* elements over all gradients */
+  int32_t device;   /* device of the buffers */
+  int32_t in_place; /* 1 if some out is its gradient */
+} disco_grads;
+
+/* Init time, host only.  Checks a list of gradients (types, alignment, device
+   memory, overlaps) and fills *grads.  count = 0 is allowed.  Buffers that
+   move (gradients allocated anew each step) need a new plan. */
+DISCO_API int disco_grad_plan(const disco_grad_tensor* tensors, int32_t count, disco_grads* grads);
+
+/* Device workspace bytes of disco_grad_norm and disco_grad_norm_clip (partial
+   sums; never 0). */
+DISCO_API size_t disco_grad_workspace_bytes(const disco_grads* grads);
+
+/* Euclidean norm over all gradients of a list, times grad_scale (> 0, finite:
+   1, or the reciprocal of a loss scale), to one fp32 on the device:
+     norm = grad_scale * sqrt(sum over all tensors and elements of g^2)
+   Sums of squares are kept at three scales, so no finite gradient overflows or
+   vanishes in them; the norm itself is rounded to fp32.  An infinity gives an
+   infinite norm, a NaN gives NaN, no elements give 0.  Fixed order of
+   summation (deterministic).  workspace: 16-byte aligned,
+   >= disco_grad_workspace_bytes.  Asynchronous. */
+DISCO_API int disco_grad_norm(const disco_grads* grads, float grad_scale, float* norm, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* The gradients scaled down to a largest norm (max_norm >= 0, infinite for
+   none), given their norm on the device (from disco_grad_norm, or reduced
+   over several processes by the caller):
+     f = grad_scale                     where norm <= max_norm
+     f = grad_scale * max_norm / norm   otherwise (NaN for a NaN norm)
+     out = g * f, in fp32, rounded once to out_dtype
+   In place with f = 1 nothing is written.  Every gradient needs an out.
+   Asynchronous. */
+DISCO_API int disco_grad_clip(const disco_grads* grads, float grad_scale, float max_norm, const float* norm,
+                              void* stream);
+
+/* disco_grad_norm and disco_grad_clip in one call, with the same results. */
+DISCO_API int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, float max_norm, float* norm,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Diagnostics; BLOCKS the host (synchronises the current device).  Reads
    the device status word into *flags (0 = no fault; bit 0 = an mbarrier wait
    of the fused forward timed out, bit 1 = one of the dX GEMM timed out,

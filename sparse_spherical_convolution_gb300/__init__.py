@@ -26,6 +26,9 @@ __all__ = [
     "disco_fused_conv_bwd_input_noalloc", "disco_fused_conv_bwd_weight_workspace_bytes",
     "disco_fused_conv_bwd_weight", "disco_device_status", "disco_check_sched_takeover", "library_path",
     "load_library", "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES",
+    "DISCO_F32", "DISCO_BF16", "DISCO_F16", "dtype_code", "disco_rms_norm", "disco_rms_norm_bwd_workspace_bytes",
+    "disco_rms_norm_bwd", "disco_dequant_e4m3", "disco_grad_tensor", "disco_grads", "disco_grad_plan", "GradPlan",
+    "disco_grad_workspace_bytes", "disco_grad_norm", "disco_grad_clip", "disco_grad_norm_clip",
 ]
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -39,7 +42,9 @@ EXPORTED_SYMBOLS = [
     "disco_fused_conv_bwd_input_noalloc", "disco_fused_conv_bwd_weight_workspace_bytes",
     "disco_fused_conv_bwd_weight", "disco_device_status", "disco_psi_export_kpacked",
     "disco_check_wait_timeout", "disco_host_workspace_bytes", "disco_fwd_host", "disco_bwd_host",
-    "disco_check_sched_takeover", "disco_build_flags",
+    "disco_check_sched_takeover", "disco_build_flags", "disco_rms_norm", "disco_rms_norm_bwd_workspace_bytes",
+    "disco_rms_norm_bwd", "disco_dequant_e4m3", "disco_grad_plan", "disco_grad_workspace_bytes", "disco_grad_norm",
+    "disco_grad_clip", "disco_grad_norm_clip",
 ]
 
 
@@ -74,6 +79,17 @@ class disco_psi(ctypes.Structure):
                 ("ngrp", ctypes.c_int32), ("grp_max", ctypes.c_int32), ("ngrp_ent", ctypes.c_int64),
                 ("ngtab", ctypes.c_int64), ("bytes", ctypes.c_size_t)] + \
                [(n, ctypes.c_void_p) for n in _PSI_ARRAYS]
+
+
+class disco_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class disco_grads(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.POINTER(disco_grad_tensor)), ("count", ctypes.c_int32),
+                ("has_out", ctypes.c_int32), ("numel", ctypes.c_int64), ("device", ctypes.c_int32),
+                ("in_place", ctypes.c_int32)]
 
 
 _lib = None
@@ -140,6 +156,26 @@ def load_library():
     lib.disco_fused_conv_bwd_weight_workspace_bytes.argtypes = [PP, I32, I32, I32, ctypes.c_int]
     lib.disco_fused_conv_bwd_weight.restype = ctypes.c_int
     lib.disco_fused_conv_bwd_weight.argtypes = [PP, P, P, P, I32, I32, I32, ctypes.c_int, P, SZ, P]
+    I64, F32 = ctypes.c_int64, ctypes.c_float
+    PGR = ctypes.POINTER(disco_grads)
+    lib.disco_rms_norm.restype = ctypes.c_int
+    lib.disco_rms_norm.argtypes = [P, P, P, F32, P, P, P, P, I32, I32, I32, I64, ctypes.c_int, P]
+    lib.disco_rms_norm_bwd_workspace_bytes.restype = SZ
+    lib.disco_rms_norm_bwd_workspace_bytes.argtypes = [I32, I32, I64, ctypes.c_int]
+    lib.disco_rms_norm_bwd.restype = ctypes.c_int
+    lib.disco_rms_norm_bwd.argtypes = [P, P, P, P, F32, P, P, I32, I32, I64, ctypes.c_int, P, SZ, P]
+    lib.disco_dequant_e4m3.restype = ctypes.c_int
+    lib.disco_dequant_e4m3.argtypes = [P, P, P, I32, I32, I32, I64, ctypes.c_int, P]
+    lib.disco_grad_plan.restype = ctypes.c_int
+    lib.disco_grad_plan.argtypes = [ctypes.POINTER(disco_grad_tensor), I32, PGR]
+    lib.disco_grad_workspace_bytes.restype = SZ
+    lib.disco_grad_workspace_bytes.argtypes = [PGR]
+    lib.disco_grad_norm.restype = ctypes.c_int
+    lib.disco_grad_norm.argtypes = [PGR, F32, P, P, SZ, P]
+    lib.disco_grad_clip.restype = ctypes.c_int
+    lib.disco_grad_clip.argtypes = [PGR, F32, F32, P, P]
+    lib.disco_grad_norm_clip.restype = ctypes.c_int
+    lib.disco_grad_norm_clip.argtypes = [PGR, F32, F32, P, P, SZ, P]
     lib.disco_device_status.restype = ctypes.c_int
     lib.disco_device_status.argtypes = [ctypes.POINTER(I32), I32]
     _lib = lib
@@ -160,15 +196,20 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _dtype(t) -> int:
+def dtype_code(dtype) -> int:
+    """The library's code (DISCO_F32, DISCO_BF16, DISCO_F16) of a torch dtype."""
     import torch
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return DISCO_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return DISCO_BF16
-    if t.dtype == torch.float16:
+    if dtype == torch.float16:
         return DISCO_F16
-    raise DiscoError(-2, f"unsupported dtype {t.dtype}")
+    raise DiscoError(-2, f"unsupported dtype {dtype}")
+
+
+def _dtype(t) -> int:
+    return dtype_code(t.dtype)
 
 
 def _ptr(t):
@@ -390,6 +431,121 @@ def disco_fused_conv_bwd_input_noalloc(psi: disco_psi, dy, W, gx, B: int, Cin: i
         ctypes.byref(psi), dp, Wp, gp, B, Cin, Cout, _dtype(dy), _stream(stream)))
 
 
+def _groups(C: int, group: int) -> int:
+    return -(-C // group) if 0 < group < C else 1
+
+
+def _opt(t, name: str, numel: int, dtype):
+    return None if t is None else _dev(t, name, numel, dtype)
+
+
+def _q8(t, numel: int):
+    """Pointer of an 8-bit tensor: float8_e4m3fn, or its bytes as uint8."""
+    import torch
+    if t is not None and t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise DiscoError(-1, f"q has dtype {t.dtype}, the call needs float8_e4m3fn or uint8")
+    return _dev(t, "q", numel)
+
+
+def disco_rms_norm(x, residual, weight, eps: float, h, y, B: int, C: int, P: int, q=None, scale=None,
+                   group: int = 0, stream=None) -> None:
+    """h = x + residual, its root-mean-square norm over the C channels times
+    weight in y, and y in 8 bits with scales in q and scale; see
+    include/disco.h.  residual, weight, h, y, and q with scale may be None."""
+    import torch
+    n, dt = B * C * P, None if x is None else x.dtype
+    xp = _dev(x, "x", n)
+    rp, wp = _opt(residual, "residual", n, dt), _opt(weight, "weight", C, dt)
+    hp, yp = _opt(h, "h", n, dt), _opt(y, "y", n, dt)
+    qp = None if q is None else _q8(q, n)
+    sp = _opt(scale, "scale", B * _groups(C, group) * P, torch.float32)
+    _check(load_library().disco_rms_norm(xp, rp, wp, eps, hp, yp, qp, sp, group, B, C, P, _dtype(x),
+                                         _stream(stream)))
+
+
+def disco_rms_norm_bwd_workspace_bytes(B: int, C: int, P: int, dtype=DISCO_BF16) -> int:
+    return load_library().disco_rms_norm_bwd_workspace_bytes(B, C, P, dtype)
+
+
+def disco_rms_norm_bwd(dy, h, weight, dh, eps: float, dx, dweight, B: int, C: int, P: int, workspace=None,
+                       stream=None) -> None:
+    """dx and dweight of disco_rms_norm from the stored h; weight, dh and
+    dweight (with its workspace) may be None."""
+    n, dt = B * C * P, None if dy is None else dy.dtype
+    yp, hp = _dev(dy, "dy", n), _dev(h, "h", n, dt)
+    wp, dhp = _opt(weight, "weight", C, dt), _opt(dh, "dh", n, dt)
+    xp, dwp = _dev(dx, "dx", n, dt), _opt(dweight, "dweight", C, dt)
+    wsp, wsn = _ws(workspace)
+    _check(load_library().disco_rms_norm_bwd(yp, hp, wp, dhp, eps, xp, dwp, B, C, P, _dtype(dy), wsp, wsn,
+                                             _stream(stream)))
+
+
+def disco_dequant_e4m3(q, scale, x, B: int, C: int, P: int, group: int = 0, stream=None) -> None:
+    """x = q * scale, the activation that disco_rms_norm's q and scale stand for."""
+    import torch
+    qp = _q8(q, B * C * P)
+    sp = _dev(scale, "scale", B * _groups(C, group) * P, torch.float32)
+    xp = _dev(x, "x", B * C * P)
+    _check(load_library().disco_dequant_e4m3(qp, sp, xp, group, B, C, P, _dtype(x), _stream(stream)))
+
+
+def disco_grad_plan(grads, outs=None):
+    """(disco_grads, host array) of a list of gradients and the tensors their
+    clipped values go to (None: the norm alone; the same tensors: in place).
+    The array and the tensors have to outlive the plan; GradPlan keeps them."""
+    grads = list(grads)
+    outs = [None] * len(grads) if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise DiscoError(-1, f"{len(grads)} gradients and {len(outs)} outs")
+    arr = (disco_grad_tensor * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        e = arr[i]
+        if g is None:
+            raise DiscoError(-1, f"gradient {i} is None")
+        n = g.numel()
+        if n:  # a tensor without elements has no memory to check
+            e.grad = _dev(g, f"gradient {i}", n)
+            if o is not None:
+                e.out = _dev(o, f"out of gradient {i}", n)
+        e.n, e.dtype = n, _dtype(g)
+        if o is not None:
+            if o.numel() != n:
+                raise DiscoError(-1, f"out of gradient {i} has {o.numel()} elements, the gradient {n}")
+            e.out_dtype = _dtype(o)
+    grads_c = disco_grads()
+    _check(load_library().disco_grad_plan(arr, len(grads), ctypes.byref(grads_c)))
+    return grads_c, arr
+
+
+def disco_grad_workspace_bytes(grads: disco_grads) -> int:
+    return load_library().disco_grad_workspace_bytes(ctypes.byref(grads))
+
+
+def disco_grad_norm(grads: disco_grads, norm, workspace, grad_scale: float = 1.0, stream=None) -> None:
+    """The Euclidean norm over all gradients, times grad_scale, to ``norm`` (one fp32)."""
+    import torch
+    np_ = _dev(norm, "norm", 1, torch.float32)
+    wp, wn = _ws(workspace)
+    _check(load_library().disco_grad_norm(ctypes.byref(grads), grad_scale, np_, wp, wn, _stream(stream)))
+
+
+def disco_grad_clip(grads: disco_grads, max_norm: float, norm, grad_scale: float = 1.0, stream=None) -> None:
+    """Every gradient scaled by grad_scale and down to ``max_norm`` given ``norm``, to its out."""
+    import torch
+    np_ = _dev(norm, "norm", 1, torch.float32)
+    _check(load_library().disco_grad_clip(ctypes.byref(grads), grad_scale, max_norm, np_, _stream(stream)))
+
+
+def disco_grad_norm_clip(grads: disco_grads, max_norm: float, norm, workspace, grad_scale: float = 1.0,
+                         stream=None) -> None:
+    """disco_grad_norm and disco_grad_clip in one call."""
+    import torch
+    np_ = _dev(norm, "norm", 1, torch.float32)
+    wp, wn = _ws(workspace)
+    _check(load_library().disco_grad_norm_clip(ctypes.byref(grads), grad_scale, max_norm, np_, wp, wn,
+                                               _stream(stream)))
+
+
 def disco_device_status(clear: bool = True) -> int:
     """Device status word (0 = no bounded wait timed out); synchronises the device.
     Raises DiscoError with status DISCO_ERR_DEVICE_BOUNDS when a range check
@@ -446,3 +602,15 @@ class Psi:
         dt = getattr(torch, self._DT[name])
         esz = torch.tensor([], dtype=dt).element_size()
         return self.buffer[off:off + n * esz].view(dt).view(*[int(v) for v in shape])
+
+
+class GradPlan:
+    """A list of gradients checked once (disco_grad_plan), with the tensors it
+    refers to.  ``GradPlan(grads, outs)``; pass ``.c`` to disco_grad_norm,
+    disco_grad_clip and disco_grad_norm_clip.  Gradients allocated anew need a
+    new plan."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        self.c, self._array = disco_grad_plan(self.grads, self.outs)

@@ -1,0 +1,336 @@
+// disco_norm.cu -- channel RMS norm with the residual's addition and an
+// 8-bit copy (disco_rms_norm), its gradient (disco_rms_norm_bwd) and the
+// return from 8 bits (disco_dequant_e4m3), on activations [B, C, P].
+//
+// The general kernels below take every shape: 32 pixels per CTA, the channels
+// dealt to 8 warps, statistics joined in shared memory, the inputs read again
+// for each further pass.
+
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "disco_bounds.cuh"
+#include "disco_internal.cuh"
+
+namespace disco {
+
+DISCO_BOUNDS_READER(norm_bounds)
+
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its scale stays above 0
+constexpr int kGenWarps = 8;
+constexpr int kBwdParts = 304;  // rows of dweight partial sums: CTAs of the backward kernels
+
+__device__ __forceinline__ uint8_t to_e4m3(float v) {
+  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float from_e4m3(uint8_t v) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)v, __NV_E4M3)));
+}
+
+struct NormArgs {
+  const void *x, *res, *w;
+  void *h, *y, *q;
+  float* scale;
+  float eps;
+  int G, NG, B, C;
+  long long P, tiles;
+};
+
+// sum over the 8 warps of one value per lane (pixel)
+__device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  buf[warp][lane] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
+  return s;
+}
+__device__ __forceinline__ float warps_max(float v, float (*buf)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  buf[warp][lane] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < kGenWarps; ++i) s = fmaxf(s, buf[i][lane]);
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs a) {
+  __shared__ float buf[kGenWarps][32];
+  const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
+  T *h = (T*)a.h, *y = (T*)a.y;
+  uint8_t* q = (uint8_t*)a.q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long tpb = (a.P + 31) / 32;
+  for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
+    const bool live = p < a.P;
+    const long long base = b * a.C * a.P + p;
+    auto value = [&](int c) {
+      const long long i = base + c * a.P;
+      float v = to_f32(x[i]);
+      return res ? v + to_f32(res[i]) : v;
+    };
+    float s = 0.0f;
+    if (live)
+      for (int c = warp; c < a.C; c += kGenWarps) {
+        const float v = value(c);
+        s = fmaf(v, v, s);
+      }
+    const float r = 1.0f / sqrtf(warps_sum(s, buf) / (float)a.C + a.eps);
+    for (int g = 0; g < a.NG; ++g) {
+      const int c0 = g * a.G, c1 = min(a.C, c0 + a.G);
+      float inv = 0.0f;
+      if (q) {
+        float m = 0.0f;
+        if (live)
+          for (int c = c0 + warp; c < c1; c += kGenWarps) {
+            const float v = value(c) * r * (w ? to_f32(w[c]) : 1.0f);
+            m = fmaxf(m, fabsf(v));
+          }
+        m = fmaxf(warps_max(m, buf), kAmaxFloor);
+        inv = kE4m3Max / m;
+        if (live && warp == 0) a.scale[(b * a.NG + g) * a.P + p] = m / kE4m3Max;
+      }
+      if (live)
+        for (int c = c0 + warp; c < c1; c += kGenWarps) {
+          const long long i = base + c * a.P;
+          const float v = value(c), n = v * r * (w ? to_f32(w[c]) : 1.0f);
+          if (h) h[i] = from_f32<T>(v);
+          if (y) y[i] = from_f32<T>(n);
+          if (q) q[i] = to_e4m3(n * inv);
+        }
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const void *dy, *h, *w, *dh;
+  void* dx;
+  float* part;
+  float eps;
+  int B, C;
+  long long P, tiles;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const NormBwdArgs a) {
+  __shared__ float buf[kGenWarps][32];
+  const T *dy = (const T*)a.dy, *h = (const T*)a.h, *w = (const T*)a.w, *dh = (const T*)a.dh;
+  T* dx = (T*)a.dx;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long tpb = (a.P + 31) / 32;
+  float* part = a.part ? a.part + (long long)blockIdx.x * a.C : nullptr;
+  if (part)
+    for (int c = warp; c < a.C; c += kGenWarps)
+      if (lane == 0) part[c] = 0.0f;
+  for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
+    const bool live = p < a.P;
+    const long long base = b * a.C * a.P + p;
+    float s = 0.0f, d = 0.0f;
+    if (live)
+      for (int c = warp; c < a.C; c += kGenWarps) {
+        const long long i = base + c * a.P;
+        const float v = to_f32(h[i]);
+        s = fmaf(v, v, s);
+        d = fmaf(to_f32(dy[i]) * (w ? to_f32(w[c]) : 1.0f), v, d);
+      }
+    const float r = 1.0f / sqrtf(warps_sum(s, buf) / (float)a.C + a.eps);
+    const float k = warps_sum(d, buf) * r / (float)a.C;  // mean_c(g n)
+    for (int c = warp; c < a.C; c += kGenWarps) {
+      const long long i = base + c * a.P;
+      float u = 0.0f;
+      if (live) {
+        const float n = to_f32(h[i]) * r, g = to_f32(dy[i]);
+        float o = r * (g * (w ? to_f32(w[c]) : 1.0f) - n * k);
+        if (dh) o += to_f32(dh[i]);
+        dx[i] = from_f32<T>(o);
+        u = g * n;
+      }
+      if (part) {
+        for (int m = 16; m; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
+        if (lane == 0) part[c] += u;
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void norm_dweight_kernel(const float* part, T* dw, int parts, int C) {
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= C) return;
+  float s = 0.0f;
+  for (int i = 0; i < parts; ++i) s += part[(long long)i * C + c];
+  dw[c] = from_f32<T>(s);
+}
+
+struct DequantArgs {
+  const uint8_t* q;
+  const float* scale;
+  void* x;
+  int G, NG, C;
+  long long P, n;
+};
+
+template <typename T>
+__global__ void dequant_any_kernel(const DequantArgs a) {
+  T* x = (T*)a.x;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < a.n; i += (long long)gridDim.x * blockDim.x) {
+    const long long bc = i / a.P, p = i - bc * a.P, b = bc / a.C;
+    const int c = (int)(bc - b * a.C);
+    x[i] = from_f32<T>(from_e4m3(a.q[i]) * a.scale[(b * a.NG + c / a.G) * a.P + p]);
+  }
+}
+
+// ------------------------------------------------------------ host checks --
+
+struct Buffer {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+bool overlap(const Buffer& u, const Buffer& v) {
+  const char *a = (const char*)u.p, *b = (const char*)v.p;
+  return u.p && v.p && a < b + v.bytes && b < a + u.bytes;
+}
+
+// Device memory, alignment, and no output over another buffer but for in
+// place pairs (in_place[i] bit o: input i may be output o).
+int check_buffers(const Buffer* in, const unsigned* in_place, int nin, const Buffer* out, int nout) {
+  int rc;
+  for (int k = 0; k < nin + nout; ++k) {
+    const Buffer& u = k < nin ? in[k] : out[k - nin];
+    if (!u.p) continue;
+    if (!aligned16(u.p)) return fail(DISCO_ERR_ALIGNMENT, "%s must be 16-byte aligned", u.name);
+    if ((rc = check_dev_ptr(u.p, u.name))) return rc;
+  }
+  for (int o = 0; o < nout; ++o) {
+    for (int i = 0; i < nin; ++i)
+      if (overlap(out[o], in[i]) && !((in_place[i] >> o & 1u) && out[o].p == in[i].p))
+        return fail(DISCO_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, in[i].name);
+    for (int j = 0; j < o; ++j)
+      if (overlap(out[o], out[j])) return fail(DISCO_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, out[j].name);
+  }
+  return DISCO_OK;
+}
+
+int elem_bytes(disco_dtype dt) { return dt == DISCO_F32 ? 4 : 2; }
+
+int check_shape(int32_t B, int32_t C, int64_t P, disco_dtype dtype) {
+  if (dtype != DISCO_F32 && dtype != DISCO_BF16 && dtype != DISCO_F16) return fail(DISCO_ERR_UNSUPPORTED, "dtype");
+  if (B < 1 || C < 1 || P < 1) return fail(DISCO_ERR_INVALID_ARG, "B, C and P must be >= 1");
+  if ((double)B * C * (double)P > 1e15) return fail(DISCO_ERR_UNSUPPORTED, "more than 1e15 elements");
+  return DISCO_OK;
+}
+
+int check_eps(float eps) {
+  if (!(eps > 0.0f) || isinf(eps)) return fail(DISCO_ERR_INVALID_ARG, "eps must be positive and finite");
+  return DISCO_OK;
+}
+
+int groups(int32_t C, int32_t group, int* G) {
+  *G = group > 0 && group < C ? group : C;
+  return (C + *G - 1) / *G;
+}
+
+long long tiles_of(int B, long long P) { return (long long)B * ((P + 31) / 32); }
+int bwd_parts(int B, long long P) { return (int)min((long long)kBwdParts, tiles_of(B, P)); }
+
+}  // namespace
+}  // namespace disco
+
+using namespace disco;
+
+#define DISCO_BY_DTYPE(dtype, CALL)            \
+  switch (dtype) {                             \
+    case DISCO_F32: CALL(float); break;        \
+    case DISCO_BF16: CALL(__nv_bfloat16); break; \
+    default: CALL(__half); break;              \
+  }
+
+extern "C" int disco_rms_norm(const void* x, const void* residual, const void* weight, float eps, void* h, void* y,
+                              void* q, float* scale, int32_t group, int32_t B, int32_t C, int64_t P,
+                              disco_dtype dtype, void* stream) {
+  disco::NvtxScope nvtx_scope("disco_rms_norm");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype)) || (rc = check_eps(eps))) return rc;
+  if (!x) return fail(DISCO_ERR_INVALID_ARG, "x is null");
+  if (!y && !q) return fail(DISCO_ERR_INVALID_ARG, "neither y nor q is given");
+  if (!q != !scale) return fail(DISCO_ERR_INVALID_ARG, "q and scale come together");
+  if (h && !residual) return fail(DISCO_ERR_INVALID_ARG, "h without a residual is x itself");
+  if (group < 0) return fail(DISCO_ERR_INVALID_ARG, "group must be >= 0");
+  if ((rc = check_device())) return rc;
+  NormArgs a{x, residual, weight, h, y, q, scale, eps, 0, 0, B, C, P, tiles_of(B, P)};
+  a.NG = groups(C, group, &a.G);
+  if (!q) a.G = C, a.NG = 1;
+  const size_t n = (size_t)B * C * P, e = elem_bytes(dtype);
+  const Buffer in[] = {{x, n * e, "x"}, {residual, n * e, "residual"}, {weight, C * e, "weight"}};
+  const Buffer out[] = {{h, n * e, "h"}, {y, n * e, "y"}, {q, n, "q"}, {scale, (size_t)B * a.NG * P * 4, "scale"}};
+  const unsigned in_place[] = {3, 3, 0};
+  if ((rc = check_buffers(in, in_place, 3, out, 4))) return rc;
+  const int grid = (int)min(a.tiles, 152LL * 8);
+#define CALL(T) norm_any_kernel<T><<<grid, kGenWarps * 32, 0, (cudaStream_t)stream>>>(a)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return check_launch("norm_any_kernel");
+}
+
+extern "C" size_t disco_rms_norm_bwd_workspace_bytes(int32_t B, int32_t C, int64_t P, disco_dtype dtype) {
+  if (check_shape(B, C, P, dtype)) return 0;
+  return (size_t)bwd_parts(B, P) * C * sizeof(float);
+}
+
+extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* weight, const void* dh, float eps,
+                                  void* dx, void* dweight, int32_t B, int32_t C, int64_t P, disco_dtype dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  disco::NvtxScope nvtx_scope("disco_rms_norm_bwd");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype)) || (rc = check_eps(eps))) return rc;
+  if (!dy || !h || !dx) return fail(DISCO_ERR_INVALID_ARG, "dy, h or dx is null");
+  const size_t need = disco_rms_norm_bwd_workspace_bytes(B, C, P, dtype);
+  if (dweight && (!workspace || workspace_bytes < need))
+    return fail(DISCO_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+  if ((rc = check_device())) return rc;
+  const size_t n = (size_t)B * C * P, e = elem_bytes(dtype);
+  const Buffer in[] = {{dy, n * e, "dy"}, {h, n * e, "h"}, {weight, C * e, "weight"}, {dh, n * e, "dh"}};
+  const Buffer out[] = {{dx, n * e, "dx"}, {dweight, C * e, "dweight"}, {dweight ? workspace : nullptr, need, "workspace"}};
+  const unsigned in_place[] = {1, 1, 0, 1};
+  if ((rc = check_buffers(in, in_place, 4, out, 3))) return rc;
+  NormBwdArgs a{dy, h, weight, dh, dx, dweight ? (float*)workspace : nullptr, eps, B, C, P, tiles_of(B, P)};
+  const int grid = bwd_parts(B, P);
+  const cudaStream_t st = (cudaStream_t)stream;
+#define CALL(T)                                                                                       \
+  norm_bwd_any_kernel<T><<<grid, kGenWarps * 32, 0, st>>>(a);                                         \
+  if (dweight) norm_dweight_kernel<T><<<(C + 127) / 128, 128, 0, st>>>(a.part, (T*)dweight, grid, C)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return check_launch("norm_bwd_any_kernel");
+}
+
+extern "C" int disco_dequant_e4m3(const void* q, const float* scale, void* x, int32_t group, int32_t B, int32_t C,
+                                  int64_t P, disco_dtype dtype, void* stream) {
+  disco::NvtxScope nvtx_scope("disco_dequant_e4m3");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype))) return rc;
+  if (!q || !scale || !x) return fail(DISCO_ERR_INVALID_ARG, "q, scale or x is null");
+  if (group < 0) return fail(DISCO_ERR_INVALID_ARG, "group must be >= 0");
+  if ((rc = check_device())) return rc;
+  DequantArgs a{(const uint8_t*)q, scale, x, 0, 0, C, P, (long long)B * C * P};
+  a.NG = groups(C, group, &a.G);
+  const Buffer in[] = {{q, (size_t)a.n, "q"}, {scale, (size_t)B * a.NG * P * 4, "scale"}};
+  const Buffer out[] = {{x, (size_t)a.n * elem_bytes(dtype), "x"}};
+  const unsigned in_place[] = {0, 0};
+  if ((rc = check_buffers(in, in_place, 2, out, 1))) return rc;
+  const int grid = (int)min((a.n + 255) / 256, 152LL * 8);
+#define CALL(T) dequant_any_kernel<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return check_launch("dequant_any_kernel");
+}
