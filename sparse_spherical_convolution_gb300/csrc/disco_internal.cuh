@@ -104,6 +104,8 @@ cudaError_t btc_bounds(int32_t* v, bool clear);
 cudaError_t gemm_bounds(int32_t* v, bool clear);
 cudaError_t fused_bounds(int32_t* v, bool clear);
 cudaError_t norm_bounds(int32_t* v, bool clear);
+cudaError_t norm_tile_bounds(int32_t* v, bool clear);
+cudaError_t norm_q_bounds(int32_t* v, bool clear);
 cudaError_t norm_bwd_bounds(int32_t* v, bool clear);
 cudaError_t grad_bounds(int32_t* v, bool clear);
 // Weight gradient dW[o][j] = sum_b sum_p dy[b][o][p] X[b][j][p] (split reduction

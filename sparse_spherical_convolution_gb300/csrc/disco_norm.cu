@@ -16,9 +16,6 @@ namespace {
 
 using namespace norm;
 
-constexpr float kE4m3Max = 448.0f;
-constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its scale stays above 0
-constexpr int kGenWarps = 8;
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
@@ -27,25 +24,7 @@ __device__ __forceinline__ float from_e4m3(uint8_t v) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)v, __NV_E4M3)));
 }
 
-struct NormArgs {
-  const void *x, *res, *w;
-  void *h, *y, *q;
-  float* scale;
-  float eps, inv_C;
-  int G, NG, ng_max, B, C;  // ng_max: groups that touch one CTA's channels
-  long long P, tiles;       // tiles: of the general kernel
-};
-
-// sum over the 8 warps of one value per lane (pixel)
-__device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  buf[warp][lane] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
-  return s;
-}
+// as warps_sum, the maximum
 __device__ __forceinline__ float warps_max(float v, float (*buf)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
@@ -57,14 +36,14 @@ __device__ __forceinline__ float warps_max(float v, float (*buf)[32]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs a, const long long tiles) {
   __shared__ float buf[kGenWarps][32];
   const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
   T *h = (T*)a.h, *y = (T*)a.y;
   uint8_t* q = (uint8_t*)a.q;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long tpb = (a.P + 31) / 32;
-  for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
     const bool live = p < a.P;
     const long long base = b * a.C * a.P + p;
@@ -106,203 +85,6 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs
   }
 }
 
-
-// ---- tiles: one pass over the data ----------------------------------------
-//
-// Bound by HBM.  Every input is read once and held: a thread's V x NCH sums
-// x + residual stay in fp32 registers between the statistics and the outputs,
-// so y is computed from the unrounded h, while its shared memory already takes
-// in the next tile (thread-private cp.async).
-
-template <typename T, int V, int NCH, bool Q>
-__global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a, const Tiling g) {
-  constexpr int VB = V * (int)sizeof(T);
-  constexpr bool kAsync = VB >= 4;  // cp.async copies 4, 8 or 16 bytes
-  using W = Raw<T, V>;
-  extern __shared__ __align__(16) char smem[];
-  const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
-  const int streams = a.res ? 2 : 1;
-  W* ring = (W*)smem;
-  float* fsm = (float*)(smem + (kAsync ? (size_t)g.NT * NCH * VB * streams : 0));
-  const Joiner<V, 1> J(g, fsm, rank);
-  const int NT = g.NT, TP = J.TP;
-  const int c0 = (int)rank * g.cpc + J.j * NCH;
-  const int nc = max(0, min(min((int)(rank + 1) * g.cpc, a.C) - c0, NCH));
-  const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
-  T *h = (T*)a.h, *y = (T*)a.y;
-  W *rx = ring + threadIdx.x, *rr = rx + NT * NCH;
-  [[maybe_unused]] const long long total = (long long)a.B * a.C * a.P;  // for the range checks
-
-  float wt[NCH];
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    wt[i] = i < nc && w ? to_f32(w[c0 + i]) : 1.0f;
-    if (kAsync && i >= nc) {  // channels past the last: zeros, never copied over
-      memset(rx + i * NT, 0, VB);
-      if (res) memset(rr + i * NT, 0, VB);
-    }
-  }
-  // 8-bit copy: this CTA's groups g0 .. g0 + ng - 1, their maxima of the two
-  // last tiles in turn
-  const int first_c = (int)rank * g.cpc, last_c = min(first_c + g.cpc, a.C) - 1;
-  const int g0 = Q ? first_c / a.G : 0, ng = Q && last_c >= first_c ? last_c / a.G - g0 + 1 : 0;
-  uint32_t* gm = (uint32_t*)(fsm + Joiner<V, 1>::floats(g));
-  const int gm_half = a.ng_max * TP;
-  if (Q)
-    for (int k = threadIdx.x; k < 2 * gm_half; k += NT) gm[k] = 0u;
-
-  Cursor at(g, blockIdx.x / g.CL), ahead = at;
-  auto offset = [&](const Cursor& c) { return (c.b * a.C + c0) * a.P + c.ti * TP + J.lx * V; };
-  auto live = [&](const Cursor& c) { return c.t < g.tiles && c.ti * TP + J.lx * V < a.P; };
-  auto fetch = [&]() {
-    if (live(ahead)) {
-      const long long o = offset(ahead);
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (i < nc && DISCO_IN_BOUNDS(o + i * a.P >= 0 && o + i * a.P + V <= total)) {
-          copy_async<kAsync ? VB : 4>(rx + i * NT, x + o + i * a.P);
-          if (res) copy_async<kAsync ? VB : 4>(rr + i * NT, res + o + i * a.P);
-        }
-    }
-    copy_commit();
-    ahead.next(g);
-  };
-  if (kAsync) fetch();
-  if (g.CL > 1) cluster_barrier();  // every CTA runs before another writes its shared memory
-
-  for (int parity = 0; at.t < g.tiles; at.next(g), parity ^= 1) {
-    const long long o = offset(at);
-    const bool on = live(at);
-    F<V> v[NCH];
-    if constexpr (kAsync) {
-      copy_wait<0>();
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        v[i] = unpack<T, V>(rx[i * NT]);
-        if (res) v[i] = add(v[i], unpack<T, V>(rr[i * NT]));
-      }
-      fetch();
-    } else {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        v[i] = fill<V>(0.0f);
-        if (on && i < nc && DISCO_IN_BOUNDS(o + i * a.P >= 0 && o + i * a.P + V <= total)) {
-          v[i] = unpack<T, V>(load_stream<W>(x + o + i * a.P));
-          if (res) v[i] = add(v[i], unpack<T, V>(load_stream<W>(res + o + i * a.P)));
-        }
-      }
-    }
-    F<V> s[1] = {fill<V>(0.0f)};
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) s[0] = fma(v[i], v[i], s[0]);
-    if (h && on)
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (i < nc && DISCO_IN_BOUNDS(o + i * a.P + V <= total)) store_stream(h + o + i * a.P, packed<T, V>(v[i]));
-    J.join(s, parity);
-    F<V> r;
-#pragma unroll
-    for (int e = 0; e < V; ++e) r.v[e] = rsqrtf(fmaf(s[0].v[e], a.inv_C, a.eps));
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) v[i] = mul(mul(v[i], r), fill<V>(wt[i]));
-    if (y && on)
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (i < nc && DISCO_IN_BOUNDS(o + i * a.P + V <= total)) store_stream(y + o + i * a.P, packed<T, V>(v[i]));
-    if constexpr (Q) {
-      uint32_t* m = gm + parity * gm_half;
-      if (nc > 0) {
-        int grp = c0 / a.G, left = (grp + 1) * a.G - c0;  // channels to the group's end
-        F<V> top = fill<V>(0.0f);
-#pragma unroll
-        for (int i = 0; i < NCH; ++i)
-          if (i < nc) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));  // a NaN does not count
-            if (--left == 0 || i == nc - 1) {
-#pragma unroll
-              for (int e = 0; e < V; ++e) atomicMax(m + (grp - g0) * TP + J.lx * V + e, __float_as_uint(top.v[e]));
-              top = fill<V>(0.0f);
-              ++grp;
-              left = a.G;
-            }
-          }
-      }
-      if (g.CL > 1) cluster_barrier();
-      else __syncthreads();
-      // a group's maximum over the CTAs that hold its channels
-      auto maximum = [&](int grp, int px) {
-        uint32_t u = 0;
-        const int k0 = grp * a.G / g.cpc, k1 = (min((grp + 1) * a.G, a.C) - 1) / g.cpc;
-        if (k0 == k1) u = m[(grp - g0) * TP + px];
-        else
-          for (int k = k0; k <= k1; ++k)
-            u = max(u, peer_load(peer(m, k) + ((grp - k * g.cpc / a.G) * TP + px) * 4));
-        return fmaxf(__uint_as_float(u), kAmaxFloor);
-      };
-      if (on && nc > 0) {
-        int grp = c0 / a.G, left = 0;
-        F<V> inv;
-        uint8_t* q = (uint8_t*)a.q;
-#pragma unroll
-        for (int i = 0; i < NCH; ++i)
-          if (i < nc) {
-            if (left == 0) {
-              if (i > 0) ++grp;
-              left = i > 0 ? a.G : (grp + 1) * a.G - c0;
-#pragma unroll
-              for (int e = 0; e < V; ++e) inv.v[e] = kE4m3Max / maximum(grp, J.lx * V + e);
-            }
-            --left;
-            if (DISCO_IN_BOUNDS(o + i * a.P + V <= total))
-              store_stream(q + o + i * a.P, packed_e4m3<V>(mul(v[i], inv)));
-          }
-      }
-      // scales of the groups that begin in this CTA
-      for (int k = threadIdx.x; k < ng * TP; k += NT) {
-        const int gl = k / TP, px = k - gl * TP, grp = g0 + gl;
-        const long long p = at.ti * TP + px;
-        if (p < a.P && grp * a.G >= first_c) a.scale[(at.b * a.NG + grp) * a.P + p] = maximum(grp, px) / kE4m3Max;
-      }
-      // the other half is read no more (every CTA is past the last tile's
-      // reads at this tile's barriers): clear it for the next tile
-      uint32_t* z = gm + (parity ^ 1) * gm_half;
-      for (int k = threadIdx.x; k < gm_half; k += NT) z[k] = 0u;
-    }
-  }
-  if (Q && g.CL > 1) cluster_barrier();  // peers may still read this CTA's maxima
-}
-
-// Bytes of shared memory of a launch.
-template <int V>
-size_t norm_tile_smem(const NormArgs& a, const Tiling& g, int es, bool q) {
-  const int VB = V * es;
-  return (VB >= 4 ? (size_t)g.NT * g.NCH * VB * (a.res ? 2 : 1) : 0) + 4 * Joiner<V, 1>::floats(g) +
-         (q ? 8 * (size_t)a.ng_max * g.LX * V : 0);
-}
-
-template <typename T, int V, int NCH>
-int norm_tile(const NormArgs& a, const Tiling& g, size_t smem, cudaStream_t st) {
-  return a.q ? launch_clusters(norm_tile_kernel<T, V, NCH, true>, g, smem, st, "norm_tile_kernel", a, g)
-             : launch_clusters(norm_tile_kernel<T, V, NCH, false>, g, smem, st, "norm_tile_kernel", a, g);
-}
-
-// DISCO_ERR_UNSUPPORTED, without launching, for shapes the tiles do not take.
-template <typename T>
-int norm_by_tiles(NormArgs& a, cudaStream_t st) {
-  Tiling g;
-  if (!plan_tiles(a.B, a.C, a.P, (int)sizeof(T), 2, &g)) return DISCO_ERR_UNSUPPORTED;
-  a.ng_max = a.q ? min(a.NG, (g.cpc + a.G - 1) / a.G + 1) : 0;
-  constexpr int VM = 16 / (int)sizeof(T);
-  const size_t smem = g.V == VM ? norm_tile_smem<VM>(a, g, sizeof(T), a.q)
-                      : g.V == 2 ? norm_tile_smem<2>(a, g, sizeof(T), a.q)
-                                 : norm_tile_smem<1>(a, g, sizeof(T), a.q);
-  if (smem > kMaxSmem) return DISCO_ERR_UNSUPPORTED;
-  if (g.V == VM) return g.NCH == 4 ? norm_tile<T, VM, 4>(a, g, smem, st) : norm_tile<T, VM, 8>(a, g, smem, st);
-  if constexpr (sizeof(T) == 2)
-    if (g.V == 2) return g.NCH == 8 ? norm_tile<T, 2, 8>(a, g, smem, st) : norm_tile<T, 2, 16>(a, g, smem, st);
-  return g.NCH == 8 ? norm_tile<T, 1, 8>(a, g, smem, st) : norm_tile<T, 1, 16>(a, g, smem, st);
-}
 
 struct DequantArgs {
   const uint8_t* q;
@@ -371,36 +153,36 @@ int check_eps(float eps) {
   return DISCO_OK;
 }
 
-bool plan_tiles(int B, int C, long long P, int es, int most, Tiling* g) {
-  g->V = es == 4 ? (P % 4 == 0 ? 4 : 1) : (P % 8 == 0 ? 8 : P % 2 == 0 ? 2 : 1);
-  const bool wide = g->V * es == 16;
-  const int few = wide ? 4 : 8, many = most * few;
-  const long long vecs = P / g->V;
-  int LX = wide ? 16 : g->V * es == 4 ? 32 : 64;
-  while (LX > 1 && LX / 2 >= vecs) LX /= 2;
-  // fewer pixels to a tile while there are not two tiles for each SM
-  while (LX > 4 && (long long)B * ((vecs + LX - 1) / LX) < 2 * kSMs) LX /= 2;
-  for (;; LX /= 2) {
-    bool done = false;
-    for (int CL = 1; CL <= 8 && !done; CL *= 2)
-      for (int NCH = few; NCH <= many && !done; NCH *= 2) {
-        const int cpc = (C + CL - 1) / CL, NL = (cpc + NCH - 1) / NCH;
-        const int NT = (LX * NL + 31) / 32 * 32;
-        if (NT > kMaxThreads) continue;
-        g->CL = CL, g->NCH = NCH, g->cpc = cpc, g->NT = NT, g->LX = LX;
-        done = true;
-      }
-    if (done) break;
-    if (LX == 1) return false;
+bool plan_tiles(int B, int C, long long P, int es, bool forward, Tiling* g) {
+  g->V = 16 / es;
+  g->shifted = P % g->V != 0;
+  const int spare = g->shifted ? 1 : 0;  // lanes of a row without pixels
+  const long long words = (P + g->V - 1) / g->V + spare;
+  // lanes of a row, channels of a thread, CTAs of a cluster: long rows and one
+  // CTA first
+  struct Shape {
+    int LX, NCH, CL;
+  };
+  static const Shape fwd[] = {{16, 4, 1}, {8, 4, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}, {1, 8, 8}};
+  static const Shape bwd[] = {{16, 4, 1}, {8, 4, 1}, {4, 4, 1}, {4, 4, 2}, {4, 4, 4}, {4, 4, 8}, {2, 4, 8}, {1, 4, 8}};
+  const Shape* s = forward ? fwd : bwd;
+  const int ns = forward ? 9 : 8;
+  for (int k = 0; k < ns; ++k) {
+    int LX = s[k].LX;
+    if (LX <= spare) return false;
+    while (LX > 1 + spare && LX / 2 >= words) LX /= 2;
+    // fewer pixels to a tile while there are not two tiles for each SM
+    while (LX > 4 && B * ((words + LX - 1) / LX) < 2 * kSMs) LX /= 2;
+    const int cpc = (C + s[k].CL - 1) / s[k].CL, NL = (cpc + s[k].NCH - 1) / s[k].NCH;
+    if ((long long)LX * NL > kMaxThreads) continue;
+    while (LX * NL < 32 && LX < 32) LX *= 2;  // a warp at least
+    g->LX = LX, g->NCH = s[k].NCH, g->CL = s[k].CL, g->cpc = cpc;
+    g->NT = (LX * NL + 31) / 32 * 32;
+    g->TP = (LX - spare) * g->V;
+    g->finish(B, C, P, max(1, kSMs * max(1, kMaxThreads / g->NT) / g->CL));
+    return true;
   }
-  g->tpb = (vecs + g->LX - 1) / g->LX;
-  g->tiles = B * g->tpb;
-  const int per_sm = max(1, kMaxThreads / g->NT);
-  const long long clusters = max(1, kSMs * per_sm / g->CL);
-  g->clusters = (int)min(g->tiles, clusters);
-  g->step_b = g->clusters / g->tpb;
-  g->step_t = g->clusters % g->tpb;
-  return true;
+  return false;
 }
 
 }  // namespace norm
@@ -421,7 +203,7 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   if (h && !residual) return fail(DISCO_ERR_INVALID_ARG, "h without a residual is x itself");
   if (group < 0) return fail(DISCO_ERR_INVALID_ARG, "group must be >= 0");
   if ((rc = check_device())) return rc;
-  NormArgs a{x, residual, weight, h, y, q, scale, eps, 1.0f / (float)C, 0, 0, 0, B, C, P, (long long)B * ((P + 31) / 32)};
+  NormArgs a{x, residual, weight, h, y, q, scale, eps, 0, 0, B, C, P};
   a.NG = groups(C, group, &a.G);
   if (!q) a.G = C, a.NG = 1;
   const size_t n = (size_t)B * C * P, e = elem_bytes(dtype);
@@ -430,12 +212,11 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   const unsigned in_place[] = {3, 3, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 4))) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
-#define CALL(T) rc = norm_by_tiles<T>(a, st)
-  DISCO_BY_DTYPE(dtype, CALL)
-#undef CALL
+  rc = q ? norm_q_by_tiles(a, dtype, st) : norm_by_tiles(a, dtype, st);
   if (rc != DISCO_ERR_UNSUPPORTED) return rc;
-  const int grid = (int)min(a.tiles, 152LL * 8);
-#define CALL(T) norm_any_kernel<T><<<grid, kGenWarps * 32, 0, st>>>(a)
+  const long long tiles = (long long)B * ((P + 31) / 32);
+  const int grid = (int)min(tiles, (long long)kSMs * 8);
+#define CALL(T) norm_any_kernel<T><<<grid, kGenWarps * 32, 0, st>>>(a, tiles)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return check_launch("norm_any_kernel");

@@ -161,17 +161,72 @@ __device__ __forceinline__ W load_stream(const void* p) { return __ldcs((const W
 template <typename W>
 __device__ __forceinline__ void store_stream(void* p, W w) { __stcs((W*)p, w); }
 
-// ---- thread-private asynchronous copies ----------------------------------
-// A thread copies only what it reads itself, so its own wait orders them and
-// no barrier is needed.
+// ---- rows off alignment ------------------------------------------------------
+// Where V does not divide P a row of V-element words starts m = 0 .. V-1
+// elements past a word boundary.  The lanes of a row then move aligned words:
+// lane l's elements are the window of words l and l + 1 that starts at element
+// m, and word l of an output holds the last m elements of lane l - 1 and the
+// first V - m of lane l.
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* smem, const void* gmem) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(gmem) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(gmem), "n"(BYTES) : "memory");
+// the word that starts `bytes` (0 .. sizeof(W) - 1) into the pair (a, b)
+__device__ __forceinline__ uint32_t window(uint32_t a, uint32_t b, int bytes) { return __funnelshift_r(a, b, 8 * bytes); }
+__device__ __forceinline__ uint2 window(uint2 a, uint2 b, int bytes) {
+  uint32_t w0 = a.x, w1 = a.y, w2 = b.x;
+  if (bytes & 4) w0 = a.y, w1 = b.x, w2 = b.y;
+  const int s = 8 * (bytes & 3);
+  return make_uint2(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s));
+}
+__device__ __forceinline__ uint4 window(uint4 a, uint4 b, int bytes) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (bytes & 8)
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  if (bytes & 4)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  const int s = 8 * (bytes & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                    __funnelshift_r(w[3], w[4], s));
+}
+__device__ __forceinline__ uint32_t from_lane_below(uint32_t v) { return __shfl_up_sync(0xffffffffu, v, 1); }
+__device__ __forceinline__ uint2 from_lane_below(uint2 v) { return make_uint2(from_lane_below(v.x), from_lane_below(v.y)); }
+__device__ __forceinline__ uint4 from_lane_below(uint4 v) {
+  return make_uint4(from_lane_below(v.x), from_lane_below(v.y), from_lane_below(v.z), from_lane_below(v.w));
+}
+
+// Stores the row that starts m elements past the aligned address `p`, `n`
+// elements of it, of which this lane holds the V from lx * V on (all lanes of
+// the warp call it; the last lane of a row holds none).
+template <int V, typename W>
+__device__ __forceinline__ void store_shifted(void* p, W own, int m, int lx, int n) {
+  constexpr int ES = (int)sizeof(W) / V;
+  const W below = from_lane_below(own);
+  const W word = m ? window(below, own, (V - m) * ES) : own;
+  const int at = lx * V - m;  // the word's first element in the row
+  char* d = (char*)p + lx * (int)sizeof(W);
+  if (at >= 0 && at + V <= n) store_stream(d, word);
+  else if (at < n && at + V > 0) {
+    const uint8_t* b = (const uint8_t*)&word;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (at + e >= 0 && at + e < n) {
+        typename Word<ES>::type v;
+        memcpy(&v, b + e * ES, ES);
+        store_stream(d + e * ES, v);
+      }
+  }
+}
+
+// ---- asynchronous copies ---------------------------------------------------
+// A thread copies only what it reads itself (what its warp reads, where rows
+// are shifted), so its own wait (and the warp's) orders them.
+
+// 16 bytes, the first `bytes` of them from memory and zeros behind them
+__device__ __forceinline__ void copy_async(void* smem, const void* gmem, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
+               "l"(gmem), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -204,114 +259,253 @@ __device__ __forceinline__ uint32_t peer_load(uint32_t a) {
   return v;
 }
 
+// V neighbouring floats of shared memory
+template <int V>
+__device__ __forceinline__ F<V> load_row(const float* p) {
+  F<V> r;
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + e);
+      r.v[e] = q.x, r.v[e + 1] = q.y, r.v[e + 2] = q.z, r.v[e + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = p[e];
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void store_row(float* p, const F<V>& f) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+      *reinterpret_cast<float4*>(p + e) = make_float4(f.v[e], f.v[e + 1], f.v[e + 2], f.v[e + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) p[e] = f.v[e];
+  }
+}
+
 // ---- tiles -----------------------------------------------------------------
-// A tile is TP = LX * V neighbouring pixels of one sample with all channels.
-// A cluster of CL CTAs takes it, each CTA cpc channels: thread (lx, j) holds
-// V pixels of the NCH channels from j * NCH on.  CTAs are persistent: cluster
-// k takes tiles k, k + clusters, ...
+// A tile is TP neighbouring pixels of one sample with all channels.  A cluster
+// of CL CTAs takes it, each CTA cpc channels: thread (lx, j) holds the V pixels
+// from lx * V on (one 16-byte word of each row) of the NCH channels from
+// j * NCH on.  CTAs are persistent: cluster k takes tiles k, k + clusters, ...
+// V divides P: TP = LX * V.  Else rows are shifted (above), the last lane of a
+// row holds no pixels, and TP = (LX - 1) * V.
 
 struct Tiling {
-  int NT, LX, NCH, V, CL, cpc;
-  long long tpb, tiles;       // tiles of a sample, of the call
+  int NT, LX, NCH, V, CL, cpc, TP;
   int clusters;
-  long long step_b, step_t;   // clusters = step_b samples and step_t tiles
-};
-
-// The tile a cluster is at.
-struct Cursor {
-  long long t, b, ti;
-  __device__ __forceinline__ Cursor(const Tiling& g, long long first) : t(first), b(first / g.tpb), ti(first - b * g.tpb) {}
-  __device__ __forceinline__ void next(const Tiling& g) {
-    t += g.clusters;
-    b += g.step_b;
-    ti += g.step_t;
-    if (ti >= g.tpb) ti -= g.tpb, ++b;
+  bool shifted;
+  long long tiles;             // of the call
+  long long span;              // pixels from a sample's first tile to the end of its last
+  long long step_b, step_pos;  // what `clusters` tiles on are: samples, and pixels past them
+  long long step_off, wrap_off;  // the same in elements; from the end of one sample's tiles to the next sample
+  void finish(int B, int C, long long P, long long max_clusters) {
+    const long long tpb = (P + TP - 1) / TP;
+    tiles = B * tpb;
+    clusters = (int)(tiles < max_clusters ? tiles : max_clusters);
+    span = tpb * TP;
+    step_b = clusters / tpb;
+    step_pos = clusters % tpb * TP;
+    step_off = step_b * C * P + step_pos;
+    wrap_off = (long long)C * P - span;
   }
 };
 
-// Cuts a call on `es`-byte elements.  False where
-// the channels of a pixel do not fit the largest cluster.  `most`: largest
-// number of channels to a thread, as a multiple of the smallest (4 vectors of
-// 16 bytes, 8 narrower ones).
-bool plan_tiles(int B, int C, long long P, int es, int most, Tiling* g);
+// The tile a cluster is at: its number, sample, first pixel, and the element
+// offset of that pixel in the sample's first channel.
+struct Cursor {
+  long long t, b, pos, off;
+  __device__ __forceinline__ Cursor(const Tiling& g, int C, long long P, long long first) : t(first) {
+    const long long tpb = g.span / g.TP;
+    b = first / tpb;
+    pos = (first - b * tpb) * g.TP;
+    off = b * C * P + pos;
+  }
+  __device__ __forceinline__ void next(const Tiling& g) {
+    t += g.clusters;
+    b += g.step_b;
+    pos += g.step_pos;
+    off += g.step_off;
+    if (pos >= g.span) pos -= g.span, off += g.wrap_off, ++b;
+  }
+};
 
-// Where a thread's pixels and channels lie, and how a tile's sums are joined.
+// A thread's words of its NCH channels: `ring` in shared memory, fetched a
+// tile ahead, and the same places of a tensor.
+template <typename T, int V, int NCH, bool SHIFT>
+struct Lane {
+  using W = Raw<T, V>;
+  int lx, nc, stride;  // stride: words from one channel to the next in the ring
+  int c0, NT;
+  long long P, mine, total, left;  // mine: the thread's place in a tile; total: elements of the tensor
+  W* slot;
+
+  static __host__ __device__ size_t words(const Tiling& g) { return (size_t)NCH * g.NT + (SHIFT ? 1 : 0); }
+
+  __device__ __forceinline__ Lane(const Tiling& g, int B, int C, long long P_, int lx_, int j, int first_c, void* smem)
+      : lx(lx_), stride(g.NT), NT(g.NT), P(P_) {
+    c0 = first_c + j * NCH;
+    const int end = first_c + g.cpc < C ? first_c + g.cpc : C;
+    nc = end - c0 < 0 ? 0 : end - c0 < NCH ? end - c0 : NCH;
+    mine = c0 * P + (SHIFT ? 0 : lx * V);
+    total = (long long)B * C * P;
+    slot = (W*)smem + threadIdx.x;
+  }
+  // pixels of this thread in the tile at c: 0 .. V
+  __device__ __forceinline__ int pixels(const Tiling& g, const Cursor& c) const {
+    if (c.t >= g.tiles) return 0;
+    const long long n = P - c.pos - lx * V;
+    if constexpr (SHIFT) return lx == g.LX - 1 || n <= 0 ? 0 : n < V ? (int)n : V;
+    else return n > 0 ? V : 0;
+  }
+  // elements past a word boundary at which the row of channel i starts
+  __device__ __forceinline__ int skew(const Cursor& c, int i) const {
+    return SHIFT ? (int)((unsigned)(c.off + mine + i * P) & (V - 1)) : 0;
+  }
+  __device__ __forceinline__ void fetch(const Tiling& g, const Cursor& c, const T* p, W* to) const {
+    if (c.t >= g.tiles) return;
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const long long row = c.off + mine + i * P;
+        const int m = (int)((unsigned)row & (V - 1));
+        const long long at = row - m + lx * V;
+        if (i < nc && c.pos + lx * V - m < P && at < total && DISCO_IN_BOUNDS(at >= 0))
+          copy_async(to + i * stride, p + at, total - at >= V ? 16 : (int)(total - at) * (int)sizeof(T));
+      }
+    } else if (c.pos + lx * V < P) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (i < nc && DISCO_IN_BOUNDS(c.off + mine >= 0 && c.off + mine + i * P + V <= total))
+          copy_async(to + i * stride, p + c.off + mine + i * P);
+    }
+  }
+  // after copy_wait (and __syncwarp, if shifted)
+  __device__ __forceinline__ W read(const W* from, int i, int m) const {
+    const W w = from[i * stride];
+    if constexpr (SHIFT) return m ? window(w, from[i * stride + 1], m * (int)sizeof(T)) : w;
+    return w;
+  }
+  // channel i's V elements, packed as `w` (of any element size), to the tile at
+  // c; n: pixels of the row in the tile.  Shifted: called by whole warps.
+  template <typename WO>
+  __device__ __forceinline__ void write(void* p, const Cursor& c, int i, WO w, bool on, int n) const {
+    constexpr int ES = (int)sizeof(WO) / V;
+    const long long row = c.off + mine + i * P;
+    if constexpr (SHIFT) {
+      const int m = (int)((unsigned)row & (V - 1));
+      store_shifted<V>((char*)p + (row - m) * ES, w, m, lx, i < nc ? n : 0);
+    } else {
+      if (on && i < nc && DISCO_IN_BOUNDS(row >= 0 && row + V <= total)) store_stream((char*)p + row * ES, w);
+    }
+  }
+};
+
+// Cuts a call on `es`-byte elements.  False where the channels of a pixel do
+// not fit the largest cluster.
+bool plan_tiles(int B, int C, long long P, int es, bool forward, Tiling* g);
+
+// Where a thread's pixels and channels lie, and how a tile's sums over the
+// channels are joined: each thread's V sums go to shared memory (one row for
+// each channel lane), S threads to a pixel add the rows up, and one of them
+// turns the sums into the NOUT values that every thread then reads back.
 //
-// Sums over channels: in registers over a thread's channels, by shuffles over
-// the channel lanes of a warp (LX < 32), then through `rows` rows of shared
-// memory, S threads to a pixel; with a cluster each CTA pushes its sums to all
-// its peers, into the half of `tot` of this tile's parity, and one cluster
-// barrier a tile suffices: a CTA writes that half again two tiles later, after
-// a barrier that its peers reach only when they have read it.
-template <int V, int NSUM>
+// With a cluster that thread pushes its sums to all peers, into the half of
+// `box` of this tile's parity, and one cluster barrier a tile suffices: a CTA
+// writes that half again two tiles later, after a barrier that its peers reach
+// only when they have read it.
+template <int V, int NSUM, int NOUT>
 struct Joiner {
-  int NT, LX, TP, CL, tid, lx, j, rows, row, S, S_log, pitch;
+  int NT, LX, TP, CL, tid, lx, j, rows, S_log, pitch;
   uint32_t rank;
-  float *red, *tot;
+  float *red, *out, *box;
 
   static __host__ __device__ size_t floats(const Tiling& g) {
-    const int TP = g.LX * V, rows = g.LX < 32 ? g.NT / 32 : g.NT / g.LX;
-    return (size_t)rows * NSUM * (TP + 32) + 2 * (size_t)g.CL * NSUM * TP;
+    const int TP = g.LX * V;  // with the pixels of a last lane that holds none
+    return (size_t)(g.NT / g.LX) * NSUM * (TP + 32) + (size_t)TP * NOUT + (g.CL > 1 ? 2 * (size_t)g.CL * NSUM * TP : 0);
   }
   __device__ __forceinline__ Joiner(const Tiling& g, float* smem, uint32_t rank_)
       : NT(g.NT), LX(g.LX), TP(g.LX * V), CL(g.CL), tid(threadIdx.x), rank(rank_) {
     lx = tid & (LX - 1);
+    rows = NT / LX;
     j = tid / LX;
-    rows = LX < 32 ? NT / 32 : NT / LX;
-    row = LX < 32 ? tid / 32 : j;
     S_log = 0;
     while (S_log < 3 && (2 << S_log) <= rows && (TP << S_log) * 2 <= NT) ++S_log;
-    S = 1 << S_log;
-    pitch = TP + 32 / S;
+    pitch = TP + (32 >> S_log);
     red = smem;
-    tot = smem + rows * NSUM * (TP + 32);
+    out = smem + rows * NSUM * (TP + 32);
+    box = out + TP * NOUT;
   }
-  // s: this thread's sums of its V pixels; returns those over all channels
-  __device__ __forceinline__ void join(F<V> (&s)[NSUM], int parity) const {
-    for (int m = 16; m >= LX; m >>= 1)
+  // finish(z, r): the outputs r[NOUT] of one pixel from its sums z[NSUM]
+  template <typename Fin>
+  __device__ __forceinline__ void join(const F<V> (&s)[NSUM], F<V> (&r)[NOUT], int parity, Fin finish) const {
 #pragma unroll
-      for (int n = 0; n < NSUM; ++n) {
-        F<V> o;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o.v[e] = __shfl_xor_sync(0xffffffffu, s[n].v[e], m);
-        s[n] = add(s[n], o);
-      }
-    if (LX >= 32 || (tid & 31) < LX)
-#pragma unroll
-      for (int n = 0; n < NSUM; ++n)
-#pragma unroll
-        for (int e = 0; e < V; ++e) red[(n * rows + row) * pitch + lx * V + e] = s[n].v[e];
+    for (int n = 0; n < NSUM; ++n) store_row<V>(red + (n * rows + j) * pitch + lx * V, s[n]);
     __syncthreads();
-    float* t = tot + parity * CL * NSUM * TP;
-    for (int q0 = 0; q0 < TP * S; q0 += NT) {
-      const int q = q0 + tid, px = q >> S_log, part = q & (S - 1);
+    float* half = box + parity * CL * NSUM * TP;
+    const int S = 1 << S_log, part = tid & (S - 1);
+    for (int px = tid >> S_log, q0 = 0; q0 < (TP << S_log); q0 += NT, px += NT >> S_log) {
+      float z[NSUM], o[NOUT];
 #pragma unroll
       for (int n = 0; n < NSUM; ++n) {
-        float z = 0.0f;
-        if (px < TP)
-          for (int k = part; k < rows; k += S) z += red[(n * rows + k) * pitch + px];
-        for (int m = S / 2; m; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-        if (px < TP && part == 0) {
-          float* d = t + (rank * NSUM + n) * TP + px;
-          if (CL == 1) *d = z;
-          else
-            for (int k = 0; k < CL; ++k) peer_store(peer(d, k), z);
+        z[n] = 0.0f;
+        if (px < TP) {
+          const float* p = red + (n * rows + part) * pitch + px;
+#pragma unroll 4
+          for (int k = part; k < rows; k += S, p += S * pitch) z[n] += *p;
+        }
+        for (int m = S / 2; m; m >>= 1) z[n] += __shfl_xor_sync(0xffffffffu, z[n], m);
+      }
+      if (px < TP && part == 0) {
+        if (CL == 1) {
+          finish(z, o);
+#pragma unroll
+          for (int n = 0; n < NOUT; ++n) out[n * TP + px] = o[n];
+        } else {
+#pragma unroll
+          for (int n = 0; n < NSUM; ++n)
+            for (int k = 0; k < CL; ++k) peer_store(peer(half + (rank * NSUM + n) * TP + px, k), z[n]);
         }
       }
     }
-    if (CL == 1) __syncthreads();
-    else cluster_barrier();
+    if (CL > 1) {
+      cluster_barrier();
+      for (int px = tid; px < TP; px += NT) {
+        float z[NSUM], o[NOUT];
 #pragma unroll
-    for (int n = 0; n < NSUM; ++n) {
-      F<V> z = fill<V>(0.0f);
-      for (int k = 0; k < CL; ++k)
+        for (int n = 0; n < NSUM; ++n) {
+          z[n] = 0.0f;
+          for (int k = 0; k < CL; ++k) z[n] += half[(k * NSUM + n) * TP + px];
+        }
+        finish(z, o);
 #pragma unroll
-        for (int e = 0; e < V; ++e) z.v[e] += t[(k * NSUM + n) * TP + lx * V + e];
-      s[n] = z;
+        for (int n = 0; n < NOUT; ++n) out[n * TP + px] = o[n];
+      }
     }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NOUT; ++n) r[n] = load_row<V>(out + n * TP + lx * V);
   }
 };
 
+// ---- general kernels: 32 pixels per CTA, the channels dealt to 8 warps ------
+
+constexpr int kGenWarps = 8;
+
+// sum over the 8 warps of one value per lane (pixel)
+__device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  buf[warp][lane] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
+  return s;
+}
 // Launches a tile kernel on its clusters.
 template <typename K, typename... A>
 int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, const char* what, A... args) {
@@ -333,6 +527,24 @@ int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, con
   if (e != cudaSuccess) return fail(DISCO_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
+
+// ---- forward: arguments, and the tile kernels' translation units -------------
+
+struct NormArgs {
+  const void *x, *res, *w;
+  void *h, *y, *q;
+  float* scale;
+  float eps;
+  int G, NG, B, C;
+  long long P;
+};
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its scale stays above 0
+
+// DISCO_ERR_UNSUPPORTED, without launching, for shapes the tiles do not take.
+int norm_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);       // without q (disco_norm_tile.cu)
+int norm_q_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);     // with q (disco_norm_q.cu)
 
 // ---- host checks (disco_norm.cu) -------------------------------------------
 

@@ -1,0 +1,201 @@
+// disco_norm_tile.cuh -- the channel norm by tiles (disco_norm.cuh): one pass
+// over the data, bound by HBM.  Instantiated without the 8-bit copy in
+// disco_norm_tile.cu, with it in disco_norm_q.cu.
+//
+// Every input is read once and held: a thread's V x NCH sums x + residual
+// stay in fp32 registers between the statistics and the outputs, so y is
+// computed from the unrounded h, while its shared memory already takes in the
+// next tile (cp.async).
+#pragma once
+
+#include "disco_norm.cuh"
+
+namespace disco {
+namespace norm {
+
+// How the group maxima of the 8-bit copy are found: not at all; from one row
+// of shared memory for each channel lane (a thread's channels and a group's
+// CTAs are one); or by atomic maxima (any group size).
+enum { kNoQ = 0, kRowsQ = 1, kAtomicQ = 2 };
+
+template <typename T, int NCH, int Q, bool SHIFT>
+__global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a, const Tiling g, const int ng_max) {
+  constexpr int V = 16 / (int)sizeof(T);
+  using L = Lane<T, V, NCH, SHIFT>;
+  using W = typename L::W;
+  using Join = Joiner<V, 1, 1>;
+  extern __shared__ __align__(16) char smem[];
+  const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
+  float* fsm = (float*)(smem + L::words(g) * 16 * (a.res ? 2 : 1));
+  const Join J(g, fsm, rank);
+  const int NT = g.NT, TP = J.TP, first_c = (int)rank * g.cpc;
+  const L lane(g, a.B, a.C, a.P, J.lx, J.j, first_c, smem);
+  const int c0 = lane.c0, nc = lane.nc;
+  const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
+  W *rx = lane.slot, *rr = rx + L::words(g);
+
+  float wt[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    wt[i] = i < nc && w ? to_f32(w[c0 + i]) : 1.0f;
+    if (i >= nc) {  // channels past the last: zeros, never copied over
+      memset(rx + i * lane.stride, 0, 16);
+      if (res) memset(rr + i * lane.stride, 0, 16);
+    }
+  }
+  float* gmax = fsm + Join::floats(g);                               // kRowsQ: [channel lane][TP]
+  float* ginv = gmax + (Q == kRowsQ ? J.rows * TP : 0);              // kRowsQ: [group of this CTA][TP]
+  uint32_t* gm = (uint32_t*)gmax;                                    // kAtomicQ: [2][group that touches this CTA][TP]
+  const int gm_half = ng_max * TP;
+  if constexpr (Q == kAtomicQ)
+    for (int k = threadIdx.x; k < 2 * gm_half; k += NT) gm[k] = 0u;
+
+  Cursor at(g, a.C, a.P, blockIdx.x / g.CL), ahead = at;
+  auto fetch = [&]() {
+    lane.fetch(g, ahead, x, rx);
+    if (res) lane.fetch(g, ahead, res, rr);
+    copy_commit();
+  };
+  fetch();
+  if (g.CL > 1) cluster_barrier();  // every CTA runs before another writes its shared memory
+
+  for (int parity = 0; at.t < g.tiles; at = ahead, parity ^= 1) {
+    const bool on = lane.pixels(g, at) > 0;
+    const int n = (int)min((long long)g.TP, a.P - at.pos);  // pixels of the tile
+    ahead.next(g);
+    F<V> v[NCH], s[1] = {fill<V>(0.0f)}, r[1];
+    copy_wait<0>();
+    if (SHIFT) __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int m = lane.skew(at, i);
+      v[i] = unpack<T, V>(lane.read(rx, i, m));
+      if (res) v[i] = add(v[i], unpack<T, V>(lane.read(rr, i, m)));
+    }
+    if (SHIFT) __syncwarp();
+    fetch();
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) s[0] = fma(v[i], v[i], s[0]);
+    if (a.h)
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) lane.write(a.h, at, i, packed<T, V>(v[i]), on, n);
+    J.join(s, r, parity, [&](const float(&z)[1], float(&out)[1]) { out[0] = 1.0f / sqrtf(z[0] / (float)a.C + a.eps); });
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) v[i] = mul(mul(v[i], r[0]), fill<V>(wt[i]));
+    if (a.y)
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) lane.write(a.y, at, i, packed<T, V>(v[i]), on, n);
+
+    if constexpr (Q == kRowsQ) {
+      F<V> top = fill<V>(0.0f);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (i < nc)
+#pragma unroll
+          for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));  // a NaN does not count
+      store_row<V>(gmax + J.j * TP + J.lx * V, top);
+      __syncthreads();
+      const int g0 = first_c / a.G, lanes = a.NG == 1 ? J.rows : a.G / NCH;
+      for (int k = threadIdx.x; k < ng_max * TP; k += NT) {
+        const int gl = k / TP, px = k - gl * TP;
+        const int r0 = gl * lanes, r1 = min(r0 + lanes, J.rows);
+        float m = kAmaxFloor;
+        for (int z = r0; z < r1; ++z) m = fmaxf(m, gmax[z * TP + px]);
+        ginv[k] = kE4m3Max / m;
+        if (px < n && g0 + gl < a.NG)
+          a.scale[(at.b * a.NG + g0 + gl) * a.P + at.pos + px] = m / kE4m3Max;
+      }
+      __syncthreads();
+      const F<V> inv = load_row<V>(ginv + min(J.j / lanes, ng_max - 1) * TP + J.lx * V);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) lane.write(a.q, at, i, packed_e4m3<V>(mul(v[i], inv)), on, n);
+    }
+
+    if constexpr (Q == kAtomicQ) {
+      const int last_c = min(first_c + g.cpc, a.C) - 1;
+      const int g0 = first_c / a.G, ng = last_c >= first_c ? last_c / a.G - g0 + 1 : 0;
+      uint32_t* m = gm + parity * gm_half;
+      if (nc > 0) {
+        int grp = c0 / a.G, left = (grp + 1) * a.G - c0;  // channels to the group's end
+        F<V> top = fill<V>(0.0f);
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+          if (i < nc) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));
+            if (--left == 0 || i == nc - 1) {
+#pragma unroll
+              for (int e = 0; e < V; ++e) atomicMax(m + (grp - g0) * TP + J.lx * V + e, __float_as_uint(top.v[e]));
+              top = fill<V>(0.0f);
+              ++grp;
+              left = a.G;
+            }
+          }
+      }
+      if (g.CL > 1) cluster_barrier();
+      else __syncthreads();
+      // a group's maximum over the CTAs that hold its channels
+      auto maximum = [&](int grp, int px) {
+        uint32_t u = 0;
+        const int k0 = grp * a.G / g.cpc, k1 = (min((grp + 1) * a.G, a.C) - 1) / g.cpc;
+        if (k0 == k1) u = m[(grp - g0) * TP + px];
+        else
+          for (int k = k0; k <= k1; ++k)
+            u = max(u, peer_load(peer(m, k) + ((grp - k * g.cpc / a.G) * TP + px) * 4));
+        return fmaxf(__uint_as_float(u), kAmaxFloor);
+      };
+      int grp = c0 / a.G - 1, left = 0;
+      F<V> inv = fill<V>(0.0f);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        if (i < nc) {
+          if (left == 0) {
+            ++grp;
+            left = i > 0 ? a.G : (grp + 1) * a.G - c0;
+#pragma unroll 1
+            for (int e = 0; e < V; ++e) {
+              const float u = kE4m3Max / maximum(grp, J.lx * V + e);
+#pragma unroll
+              for (int k = 0; k < V; ++k) inv.v[k] = k == e ? u : inv.v[k];
+            }
+          }
+          --left;
+        }
+        if (SHIFT) __syncwarp();
+        lane.write(a.q, at, i, packed_e4m3<V>(mul(v[i], inv)), on, n);
+      }
+      // scales of the groups that begin in this CTA
+      for (int k = threadIdx.x; k < ng * TP; k += NT) {
+        const int gl = k / TP, px = k - gl * TP, grp = g0 + gl;
+        if (px < n && grp * a.G >= first_c)
+          a.scale[(at.b * a.NG + grp) * a.P + at.pos + px] = maximum(grp, px) / kE4m3Max;
+      }
+      // the other half is read no more (every CTA is past the last tile's
+      // reads at this tile's barriers): clear it for the next tile
+      uint32_t* z = gm + (parity ^ 1) * gm_half;
+      for (int k = threadIdx.x; k < gm_half; k += NT) z[k] = 0u;
+    }
+  }
+  if (Q == kAtomicQ && g.CL > 1) cluster_barrier();  // peers may still read this CTA's maxima
+}
+
+template <int Q, typename T, int NCH, bool SHIFT>
+int launch_norm_tile(const NormArgs& a, const Tiling& g, int ng_max, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int TP = g.LX * V;
+  const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * (a.res ? 2 : 1);
+  const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * TP : Q == kAtomicQ ? 8 * (size_t)ng_max * TP : 0;
+  const size_t smem = ring + 4 * Joiner<V, 1, 1>::floats(g) + qb;
+  if (smem > kMaxSmem) return DISCO_ERR_UNSUPPORTED;
+  return launch_clusters(norm_tile_kernel<T, NCH, Q, SHIFT>, g, smem, st, "norm_tile_kernel", a, g, ng_max);
+}
+
+template <int Q, typename T>
+int norm_tile(const NormArgs& a, const Tiling& g, int ng_max, cudaStream_t st) {
+  if (g.shifted)
+    return g.NCH == 4 ? launch_norm_tile<Q, T, 4, true>(a, g, ng_max, st) : launch_norm_tile<Q, T, 8, true>(a, g, ng_max, st);
+  return g.NCH == 4 ? launch_norm_tile<Q, T, 4, false>(a, g, ng_max, st) : launch_norm_tile<Q, T, 8, false>(a, g, ng_max, st);
+}
+
+}  // namespace norm
+}  // namespace disco
