@@ -212,7 +212,7 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   const unsigned in_place[] = {3, 3, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 4))) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
-  rc = q ? norm_q_by_tiles(a, dtype, st) : norm_by_tiles(a, dtype, st);
+  rc = P == 1 ? norm_by_rows(a, dtype, st) : q ? norm_q_by_tiles(a, dtype, st) : norm_by_tiles(a, dtype, st);
   if (rc != DISCO_ERR_UNSUPPORTED) return rc;
   const long long tiles = (long long)B * ((P + 31) / 32);
   const int grid = (int)min(tiles, (long long)kSMs * 8);

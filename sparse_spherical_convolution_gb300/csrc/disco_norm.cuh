@@ -506,29 +506,43 @@ __device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
   for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
   return s;
 }
-// Launches a tile kernel on its clusters.
+// ---- launches ----------------------------------------------------------------
+
 template <typename K, typename... A>
-int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, const char* what, A... args) {
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+int launch(K kernel, int grid, int threads, int cluster, size_t smem, cudaStream_t st, const char* what, A... args) {
+  if (smem + 1024 > 48 * 1024 &&  // with a kernel's static arrays
+      cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    (void)cudaGetLastError();
     return fail(DISCO_ERR_CUDA, "%s: shared memory of %zu bytes refused", what, smem);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(g.clusters * g.CL));
-  cfg.blockDim = dim3((unsigned)g.NT);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)g.CL;
+  at[0].val.clusterDim.x = (unsigned)cluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = g.CL > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) return fail(DISCO_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
-  return check_launch(what);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(DISCO_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+  }
+  return DISCO_OK;
+}
+template <typename K, typename... A>
+int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, const char* what, A... args) {
+  return launch(kernel, g.clusters * g.CL, g.NT, g.CL, smem, st, what, args...);
+}
+template <typename K, typename... A>
+int launch_grid(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const char* what, A... args) {
+  return launch(kernel, grid, threads, 1, smem, st, what, args...);
 }
 
-// ---- forward: arguments, and the tile kernels' translation units -------------
+// ---- arguments, and the kernels by translation unit ---------------------------
 
 struct NormArgs {
   const void *x, *res, *w;
@@ -539,12 +553,25 @@ struct NormArgs {
   long long P;
 };
 
+struct NormBwdArgs {
+  const void *dy, *h, *w, *dh;
+  void* dx;
+  float* part;  // rows of fp32 partial sums of dweight, or null
+  float eps;
+  int B, C;
+  long long P;
+};
+
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its scale stays above 0
 
 // DISCO_ERR_UNSUPPORTED, without launching, for shapes the tiles do not take.
 int norm_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);       // without q (disco_norm_tile.cu)
 int norm_q_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);     // with q (disco_norm_q.cu)
+
+int norm_by_rows(const NormArgs& a, disco_dtype dtype, cudaStream_t st);        // P = 1 (disco_norm_rows.cu)
+int norm_bwd_by_rows(const NormBwdArgs& a, disco_dtype dtype, cudaStream_t st);
+int norm_bwd_rows_parts(int B, int C, int es);  // rows of partial sums of that call, 0: not taken
 
 // ---- host checks (disco_norm.cu) -------------------------------------------
 

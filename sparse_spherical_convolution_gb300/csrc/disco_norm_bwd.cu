@@ -18,19 +18,10 @@ using namespace norm;
 
 constexpr int kGenParts = 304;  // rows of partial sums of the general kernel: its CTAs
 
-struct NormBwdArgs {
-  const void *dy, *h, *w, *dh;
-  void* dx;
-  float* part;
-  float eps;
-  int B, C;
-  long long P, tiles;  // tiles: of the general kernel
-};
-
 // Any shape: 32 pixels per CTA, the channels dealt to 8 warps, the inputs read
 // again for the second pass.
 template <typename T>
-__global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const NormBwdArgs a, const long long tiles) {
   __shared__ float buf[kGenWarps][32];
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *w = (const T*)a.w, *dh = (const T*)a.dh;
   T* dx = (T*)a.dx;
@@ -40,7 +31,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const Norm
   if (part)
     for (int c = warp; c < a.C; c += kGenWarps)
       if (lane == 0) part[c] = 0.0f;
-  for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
     const bool live = p < a.P;
     const long long base = b * a.C * a.P + p;
@@ -196,7 +187,10 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, T*
 // Rows of partial sums of a call.
 int bwd_parts(int B, int C, long long P, int es) {
   Tiling g;
-  if (plan_tiles(B, C, P, es, false, &g)) return g.clusters;
+  if (P == 1) {
+    const int rows = norm_bwd_rows_parts(B, C, es);
+    if (rows) return rows;
+  } else if (plan_tiles(B, C, P, es, false, &g)) return g.clusters;
   return (int)min((long long)kGenParts, (long long)B * ((P + 31) / 32));
 }
 
@@ -211,9 +205,9 @@ template <typename T>
 int bwd_main(const NormBwdArgs& a, cudaStream_t st) {
   Tiling g;
   const int es = (int)sizeof(T);
-  if (plan_tiles(a.B, a.C, a.P, es, false, &g))
+  if (a.P > 1 && plan_tiles(a.B, a.C, a.P, es, false, &g))
     return g.shifted ? launch_bwd_tile<T, true>(a, g, st) : launch_bwd_tile<T, false>(a, g, st);
-  norm_bwd_any_kernel<T><<<bwd_parts(a.B, a.C, a.P, es), kGenWarps * 32, 0, st>>>(a);
+  norm_bwd_any_kernel<T><<<bwd_parts(a.B, a.C, a.P, es), kGenWarps * 32, 0, st>>>(a, (long long)a.B * ((a.P + 31) / 32));
   return check_launch("norm_bwd_any_kernel");
 }
 
@@ -244,12 +238,14 @@ extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* wei
   const Buffer out[] = {{dx, n * e, "dx"}, {dweight, C * e, "dweight"}, {dweight ? workspace : nullptr, need, "workspace"}};
   const unsigned in_place[] = {1, 1, 0, 1};
   if ((rc = check_buffers(in, in_place, 4, out, 3))) return rc;
-  const NormBwdArgs a{dy, h, weight, dh, dx, dweight ? (float*)workspace : nullptr, eps, B, C, P,
-                      (long long)B * ((P + 31) / 32)};
+  const NormBwdArgs a{dy, h, weight, dh, dx, dweight ? (float*)workspace : nullptr, eps, B, C, P};
   const cudaStream_t st = (cudaStream_t)stream;
+  rc = P == 1 ? norm_bwd_by_rows(a, dtype, st) : DISCO_ERR_UNSUPPORTED;
+  if (rc == DISCO_ERR_UNSUPPORTED) {
 #define CALL(T) rc = bwd_main<T>(a, st)
-  DISCO_BY_DTYPE(dtype, CALL)
+    DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
+  }
   if (rc || !dweight) return rc;
   const int parts = (int)(need / ((size_t)C * sizeof(float)));
 #define CALL(T) norm_dweight_kernel<T><<<(C + 31) / 32, 256, 0, st>>>(a.part, (T*)dweight, parts, C)
