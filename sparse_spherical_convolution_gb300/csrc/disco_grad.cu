@@ -2,17 +2,20 @@
 // scaling to a largest norm (disco_grad_norm, disco_grad_clip).
 //
 // The list of gradients travels in the kernels' parameters, so a call depends
-// on no device table and no earlier copy.  Work is cut into chunks of
-// kChunk elements that do not cross tensors; a CTA takes chunks blockIdx.x,
-// blockIdx.x + gridDim.x, ...
+// on no device table and no earlier copy.  Work is cut into chunks that do not
+// cross tensors, dealt to persistent CTAs in turn.
 //
 // Sums of squares are kept at three scales, sum g^2, sum (g 2^-80)^2 and
 // sum (g 2^90)^2: where the first is infinite the second holds the answer,
-// where it is below 2^-60 (its terms near the smallest fp32) the third.
+// where it is below 2^-60 (its terms near the smallest fp32) the third.  A
+// thread adds in fp32, a CTA joins its threads in 64 bits and leaves one row of
+// partial sums, and every CTA of the scaling kernel adds those rows up for
+// itself: two launches, no atomics, one order of summation.
 
 #include <math.h>
 #include <stdio.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include "disco_bounds.cuh"
 #include "disco_internal.cuh"
@@ -23,108 +26,313 @@ DISCO_BOUNDS_READER(grad_bounds)
 
 namespace {
 
-constexpr int kChunk = 4096;
 constexpr int kThreads = 256;
-constexpr int kGrid = 304;       // CTAs of a norm launch = rows of its partial sums
-constexpr int kMaxTensors = 256; // gradients of one launch
+constexpr int kSMs = 152;
+constexpr int kNormGrid = kSMs * 4;  // CTAs of a norm launch at most = rows of its partial sums
+constexpr int kClipGrid = kSMs * 6;
+constexpr int kUnroll = 4;           // 16-byte loads a thread has in flight
 
 struct Entry {
   const void* g;
   void* o;
   long long n;
-  long long chunk0;  // first chunk of the tensor
-  int dt, odt;
+  int chunk0;        // first chunk of the tensor
+  short dt, odt;
 };
+// The gradients of one launch; kernel parameters end at 32,764 bytes, and a
+// short list takes a short table.
+template <int N>
 struct Table {
-  Entry e[kMaxTensors];
-  long long chunks;
-  int count;
+  Entry e[N];
+  long long chunk;   // elements of a chunk
+  int chunks, count;
 };
-
-__device__ __forceinline__ float load_as_f32(const void* p, long long i, int dt) {
-  if (dt == DISCO_F32) return ((const float*)p)[i];
-  if (dt == DISCO_BF16) return to_f32(((const __nv_bfloat16*)p)[i]);
-  return to_f32(((const __half*)p)[i]);
-}
-__device__ __forceinline__ void store_f32(void* p, long long i, int dt, float v) {
-  if (dt == DISCO_F32) ((float*)p)[i] = v;
-  else if (dt == DISCO_BF16) ((__nv_bfloat16*)p)[i] = from_f32<__nv_bfloat16>(v);
-  else ((__half*)p)[i] = from_f32<__half>(v);
-}
+constexpr int kShort = 64, kLong = 1000;
+static_assert(sizeof(Table<kLong>) + 64 <= 32764, "kernel parameters");
 
 // the tensor that chunk c belongs to
-__device__ __forceinline__ int find(const Table& t, long long c) {
+template <int N>
+__device__ __forceinline__ const Entry& find(const Table<N>& t, int c) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (t.e[mid].chunk0 <= c) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  return t.e[lo];
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table t, double* part) {
-  float a = 0.0f, b = 0.0f, c = 0.0f;
-  for (long long k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const Entry& e = t.e[find(t, k)];
-    const long long i0 = (k - e.chunk0) * kChunk, i1 = min(e.n, i0 + kChunk);
-    for (long long i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const float v = load_as_f32(e.g, i, e.dt);
-      const float u = v * 0x1p-80f, w = v * 0x1p90f;
-      a = fmaf(v, v, a);
-      b = fmaf(u, u, b);
-      c = fmaf(w, w, c);
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z, w;\n"
+      "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z;\n"
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float s) {
+  float2 r;
+  asm("{.reg .b64 x, y, w;\n"
+      "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4};\n"
+      "mul.rn.f32x2 w, x, y;\n"
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(s));
+  return r;
+}
+
+// The three sums of a thread, two terms at a time.
+struct Sums {
+  float2 a = {0.0f, 0.0f}, b = {0.0f, 0.0f}, c = {0.0f, 0.0f};
+  template <typename T>
+  __device__ __forceinline__ void add(float2 v) {
+    a = fma2(v, v, a);
+    if constexpr (!__is_same(T, __half)) {
+      const float2 u = mul2(v, 0x1p-80f), w = mul2(v, 0x1p90f);
+      b = fma2(u, u, b);
+      c = fma2(w, w, c);
     }
   }
-  __shared__ double s[3][kThreads];
-  s[0][threadIdx.x] = a;
-  s[1][threadIdx.x] = b;
-  s[2][threadIdx.x] = c;
-  for (int m = kThreads / 2; m; m >>= 1) {
-    __syncthreads();
-    if (threadIdx.x < m)
-      for (int j = 0; j < 3; ++j) s[j][threadIdx.x] += s[j][threadIdx.x + m];
+  // fp16 squares lie within fp32's range: their sum stands in the first alone,
+  // and an infinity or NaN in all
+  __device__ __forceinline__ void add_f16(const Sums& s) {
+    const float z = s.a.x + s.a.y;
+    a.x += z;
+    if (!isfinite(z)) b.x = c.x = z;
   }
-  if (threadIdx.x < 3) part[(long long)blockIdx.x * 3 + threadIdx.x] = s[threadIdx.x][0];
+};
+
+template <typename T>
+__device__ __forceinline__ void sum_word(Sums& s, const uint4& w) {
+  T t[16 / sizeof(T)];
+  memcpy(t, &w, 16);
+#pragma unroll
+  for (int e = 0; e < (int)(16 / sizeof(T)); e += 2) s.add<T>(make_float2(to_f32(t[e]), to_f32(t[e + 1])));
 }
 
-__global__ void grad_norm_finish_kernel(const double* part, int parts, float grad_scale, float* norm) {
-  double s[3] = {0.0, 0.0, 0.0};
-  for (int i = 0; i < parts; ++i)
-    for (int j = 0; j < 3; ++j) s[j] += part[(long long)i * 3 + j];
-  double v = sqrt(s[0]);
-  if (isinf(s[0])) v = sqrt(s[1]) * 0x1p80;
-  else if (s[0] < 0x1p-60) v = sqrt(s[2]) * 0x1p-90;
-  *norm = (float)(v * grad_scale);
+// elements [i0, i1) of a tensor; i0 is a multiple of 16
+template <typename T>
+__device__ __forceinline__ void sum_chunk(Sums& s, const T* g, long long i0, long long i1) {
+  constexpr int V = 16 / sizeof(T);
+  long long i = i0;
+  if (((uintptr_t)g & 15) == 0) {
+    const uint4* p = (const uint4*)(g + i0);
+    const long long words = (i1 - i0) / V;
+    long long k = threadIdx.x;
+    for (; k + (kUnroll - 1) * kThreads < words; k += kUnroll * kThreads) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) w[u] = p[k + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) sum_word<T>(s, w[u]);
+    }
+    for (; k < words; k += kThreads) sum_word<T>(s, p[k]);
+    i = i0 + words * V;
+  }
+  // the rest, and tensors off a 16-byte boundary, by elements
+  for (i += threadIdx.x; i < i1; i += 8 * kThreads) {
+    T t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t[u] = i + u * kThreads < i1 ? g[i + u * kThreads] : from_f32<T>(0.0f);
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) s.add<T>(make_float2(to_f32(t[u]), to_f32(t[u + 1])));
+  }
 }
 
+// Sum of `v` over the CTA's threads, in 64 bits and one order, to all of them.
+__device__ __forceinline__ double cta_sum(double v, double* buf) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) v += buf[k];
+  return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<N> t, double* part) {
+  __shared__ double buf[kThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  Sums s;
+  for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const Entry& e = find(t, k);
+    const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
+    if (e.dt == DISCO_F32) sum_chunk(s, (const float*)e.g, i0, i1);
+    else if (e.dt == DISCO_BF16) sum_chunk(s, (const __nv_bfloat16*)e.g, i0, i1);
+    else {
+      Sums h;
+      sum_chunk(h, (const __half*)e.g, i0, i1);
+      s.add_f16(h);
+    }
+  }
+  const double a = cta_sum((double)s.a.x + s.a.y, buf), b = cta_sum((double)s.b.x + s.b.y, buf),
+               c = cta_sum((double)s.c.x + s.c.y, buf);
+  if (threadIdx.x == 0) {
+    part[3 * blockIdx.x] = a;
+    part[3 * blockIdx.x + 1] = b;
+    part[3 * blockIdx.x + 2] = c;
+  }
+}
+
+// The norm from all rows of partial sums (every thread of the CTA gets it).
+__device__ __forceinline__ float norm_of(const double* part, int parts, float grad_scale, double* buf) {
+  double a = 0.0, b = 0.0, c = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) {
+    a += part[3 * i];
+    b += part[3 * i + 1];
+    c += part[3 * i + 2];
+  }
+  a = cta_sum(a, buf);
+  b = cta_sum(b, buf);
+  c = cta_sum(c, buf);
+  double v = sqrt(a);
+  if (isinf(a)) v = sqrt(b) * 0x1p80;
+  else if (a < 0x1p-60) v = sqrt(c) * 0x1p-90;
+  return (float)(v * grad_scale);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* part, int parts, float grad_scale, float* norm) {
+  __shared__ double buf[kThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float v = norm_of(part, parts, grad_scale, buf);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T, typename O>
+__device__ __forceinline__ void clip_chunk(const T* g, O* o, long long i0, long long i1, float f) {
+  constexpr int V = 16 / sizeof(T);
+  long long i = i0;
+  if ((((uintptr_t)g | (uintptr_t)o) & 15) == 0) {
+    const uint4* p = (const uint4*)(g + i0);
+    O* q = o + i0;
+    const long long words = (i1 - i0) / V;
+    auto put = [&](const uint4& w, long long k) {
+      T t[V];
+      O r[V];
+      memcpy(t, &w, 16);
+#pragma unroll
+      for (int e = 0; e < V; ++e) r[e] = from_f32<O>(to_f32(t[e]) * f);
+      constexpr int B = V * (int)sizeof(O);  // 8, 16 or 32 bytes
+      if constexpr (B == 8) {
+        uint2 z;
+        memcpy(&z, r, 8);
+        __stcs((uint2*)(q + k * V), z);
+      } else {
+        uint4 z[B / 16];
+        memcpy(z, r, B);
+#pragma unroll
+        for (int u = 0; u < B / 16; ++u) __stcs((uint4*)(q + k * V) + u, z[u]);
+      }
+    };
+    long long k = threadIdx.x;
+    for (; k + (kUnroll - 1) * kThreads < words; k += kUnroll * kThreads) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) w[u] = __ldcs(p + k + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) put(w[u], k + u * kThreads);
+    }
+    for (; k < words; k += kThreads) put(__ldcs(p + k), k);
+    i = i0 + words * V;
+  }
+  for (i += threadIdx.x; i < i1; i += 8 * kThreads) {
+    T t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u * kThreads < i1) t[u] = g[i + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u * kThreads < i1) o[i + u * kThreads] = from_f32<O>(to_f32(t[u]) * f);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_entry(const Entry& e, long long i0, long long i1, float f) {
+  if (e.odt == DISCO_F32) clip_chunk((const T*)e.g, (float*)e.o, i0, i1, f);
+  else if (e.odt == DISCO_BF16) clip_chunk((const T*)e.g, (__nv_bfloat16*)e.o, i0, i1, f);
+  else clip_chunk((const T*)e.g, (__half*)e.o, i0, i1, f);
+}
+
+// part: the rows of partial sums of this call's norm (the norm is written to
+// *norm by CTA 0), or null: the norm is read from *norm.
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-    grad_clip_kernel(const __grid_constant__ Table t, float grad_scale, float max_norm, const float* norm) {
-  const float n = *norm;
-  const float f = n <= max_norm ? grad_scale : grad_scale * (max_norm / n);
-  for (long long k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const Entry& e = t.e[find(t, k)];
-    if (e.o == e.g && f == 1.0f) continue;
-    const long long i0 = (k - e.chunk0) * kChunk, i1 = min(e.n, i0 + kChunk);
-    for (long long i = i0 + threadIdx.x; i < i1; i += kThreads)
-      store_f32(e.o, i, e.odt, load_as_f32(e.g, i, e.dt) * f);
+    grad_clip_kernel(const __grid_constant__ Table<N> t, const double* part, int parts, float grad_scale, float max_norm, float* norm) {
+  __shared__ double buf[kThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float n;
+  if (part) {
+    n = norm_of(part, parts, grad_scale, buf);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  } else {
+    n = *norm;
   }
+  const float f = n <= max_norm ? grad_scale : grad_scale * (max_norm / n);
+  // last chunks first: the norm's pass read them last, they may still be in L2
+  for (int k = t.chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
+    const Entry& e = find(t, k);
+    if (e.o == e.g && f == 1.0f) continue;
+    const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
+    if (e.dt == DISCO_F32) clip_entry<float>(e, i0, i1, f);
+    else if (e.dt == DISCO_BF16) clip_entry<__nv_bfloat16>(e, i0, i1, f);
+    else clip_entry<__half>(e, i0, i1, f);
+  }
+}
+
+// Elements of a chunk: four chunks for each CTA of the norm where there is
+// enough work, 1024 (one load for each thread) to 16384 (all of a thread's
+// loads twice), and more where there would be more than 2^28 chunks.
+long long chunk_of(const disco_grads* g) {
+  long long c = 1024;
+  while (c < 16384 && g->numel / c > 4 * kNormGrid) c *= 2;
+  while (g->numel / c > (1 << 28)) c *= 2;
+  return c;
 }
 
 // Fills `t` from tensors[*next ...]; false when none with elements is left.
-bool fill(const disco_grads* g, int* next, Table* t) {
+template <int N>
+bool fill(const disco_grads* g, int* next, Table<N>* t) {
   t->count = 0;
   t->chunks = 0;
-  for (; *next < g->count && t->count < kMaxTensors; ++*next) {
+  t->chunk = chunk_of(g);
+  for (; *next < g->count && t->count < N; ++*next) {
     const disco_grad_tensor& s = g->tensors[*next];
     if (s.n < 1) continue;
-    t->e[t->count++] = Entry{s.grad, s.out, s.n, t->chunks, s.dtype, s.out_dtype};
-    t->chunks += (s.n + kChunk - 1) / kChunk;
+    t->e[t->count++] = Entry{s.grad, s.out, s.n, t->chunks, (short)s.dtype, (short)s.out_dtype};
+    t->chunks += (int)((s.n + t->chunk - 1) / t->chunk);
   }
   return t->count > 0;
 }
 
-int launches(const disco_grads* g) { return g->count / kMaxTensors + 1; }
+// A launch that may begin while the kernel before it on the stream ends; the
+// kernel waits (griddepcontrol.wait) before it reads what that one wrote.
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, int grid, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int launch_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return DISCO_OK;
+  (void)cudaGetLastError();
+  return fail(DISCO_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// at most: norm launches of a list
+int launches(const disco_grads* g) { return g->count / kLong + 1; }
 
 int elem_bytes(int dt) { return dt == DISCO_F32 ? 4 : 2; }
 
@@ -190,27 +398,45 @@ int check_max_norm(const disco_grads* g, float max_norm) {
   return DISCO_OK;
 }
 
-int run_norm(const disco_grads* g, float grad_scale, float* norm, void* ws, cudaStream_t st) {
-  Table t;
-  int next = 0, parts = 0;
-  double* part = (double*)ws;
+// Partial sums of all gradients; *parts: rows.
+template <int N>
+int norm_parts(const disco_grads* g, double* part, int* parts, cudaStream_t st) {
+  Table<N> t;
+  int next = 0;
+  *parts = 0;
   while (fill(g, &next, &t)) {
-    const int grid = (int)(t.chunks < kGrid ? t.chunks : kGrid);
-    grad_norm_kernel<<<grid, kThreads, 0, st>>>(t, part + 3LL * parts);
-    parts += grid;
+    const int grid = t.chunks < kNormGrid ? t.chunks : kNormGrid;
+    grad_norm_kernel<N><<<grid, kThreads, 0, st>>>(t, part + 3LL * *parts);
+    const int rc = launch_status(cudaGetLastError(), "grad_norm_kernel");
+    if (rc) return rc;
+    *parts += grid;
   }
-  grad_norm_finish_kernel<<<1, 1, 0, st>>>(part, parts, grad_scale, norm);
-  return check_launch("grad_norm_kernel");
+  return DISCO_OK;
 }
 
-int run_clip(const disco_grads* g, float grad_scale, float max_norm, const float* norm, cudaStream_t st) {
-  Table t;
+template <int N>
+int clip_all(const disco_grads* g, const double* part, int parts, float grad_scale, float max_norm, float* norm, cudaStream_t st) {
+  Table<N> t;
   int next = 0;
   while (fill(g, &next, &t)) {
-    const int grid = (int)(t.chunks < kGrid * 4 ? t.chunks : kGrid * 4);
-    grad_clip_kernel<<<grid, kThreads, 0, st>>>(t, grad_scale, max_norm, norm);
+    const int grid = t.chunks < kClipGrid ? t.chunks : kClipGrid;
+    const int rc = launch_status(launch_after(grad_clip_kernel<N>, grid, st, t, part, parts, grad_scale, max_norm, norm),
+                                 "grad_clip_kernel");
+    if (rc) return rc;
+    part = nullptr;  // a further launch reads the norm
   }
-  return check_launch("grad_clip_kernel");
+  return DISCO_OK;
+}
+
+int norm_parts(const disco_grads* g, double* part, int* parts, cudaStream_t st) {
+  return g->count <= kShort ? norm_parts<kShort>(g, part, parts, st) : norm_parts<kLong>(g, part, parts, st);
+}
+int clip_all(const disco_grads* g, const double* part, int parts, float grad_scale, float max_norm, float* norm, cudaStream_t st) {
+  return g->count <= kShort ? clip_all<kShort>(g, part, parts, grad_scale, max_norm, norm, st)
+                            : clip_all<kLong>(g, part, parts, grad_scale, max_norm, norm, st);
+}
+int finish_norm(const double* part, int parts, float grad_scale, float* norm, cudaStream_t st) {
+  return launch_status(launch_after(grad_norm_finish_kernel, 1, st, part, parts, grad_scale, norm), "grad_norm_finish_kernel");
 }
 
 int check_workspace(const disco_grads* g, void* ws, size_t bytes) {
@@ -268,7 +494,7 @@ extern "C" int disco_grad_plan(const disco_grad_tensor* tensors, int32_t count, 
 
 extern "C" size_t disco_grad_workspace_bytes(const disco_grads* grads) {
   if (!grads || grads->count < 0) return 0;
-  return (size_t)launches(grads) * kGrid * 3 * sizeof(double);
+  return (size_t)launches(grads) * kNormGrid * 3 * sizeof(double);
 }
 
 extern "C" int disco_grad_norm(const disco_grads* grads, float grad_scale, float* norm, void* workspace,
@@ -278,7 +504,9 @@ extern "C" int disco_grad_norm(const disco_grads* grads, float grad_scale, float
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_workspace(grads, workspace, workspace_bytes)) ||
       (rc = check_scalar(norm, "norm")))
     return rc;
-  return run_norm(grads, grad_scale, norm, workspace, (cudaStream_t)stream);
+  int parts;
+  if ((rc = norm_parts(grads, (double*)workspace, &parts, (cudaStream_t)stream))) return rc;
+  return finish_norm((const double*)workspace, parts, grad_scale, norm, (cudaStream_t)stream);
 }
 
 extern "C" int disco_grad_clip(const disco_grads* grads, float grad_scale, float max_norm, const float* norm,
@@ -287,7 +515,8 @@ extern "C" int disco_grad_clip(const disco_grads* grads, float grad_scale, float
   int rc;
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) || (rc = check_scalar(norm, "norm")))
     return rc;
-  return run_clip(grads, grad_scale, max_norm, norm, (cudaStream_t)stream);
+  // the kernel writes the norm only where it computes it
+  return clip_all(grads, nullptr, 0, grad_scale, max_norm, const_cast<float*>(norm), (cudaStream_t)stream);
 }
 
 extern "C" int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, float max_norm, float* norm,
@@ -297,6 +526,8 @@ extern "C" int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, 
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) ||
       (rc = check_workspace(grads, workspace, workspace_bytes)) || (rc = check_scalar(norm, "norm")))
     return rc;
-  if ((rc = run_norm(grads, grad_scale, norm, workspace, (cudaStream_t)stream))) return rc;
-  return run_clip(grads, grad_scale, max_norm, norm, (cudaStream_t)stream);
+  int parts;
+  if ((rc = norm_parts(grads, (double*)workspace, &parts, (cudaStream_t)stream))) return rc;
+  if (parts == 0) return finish_norm((const double*)workspace, 0, grad_scale, norm, (cudaStream_t)stream);
+  return clip_all(grads, (const double*)workspace, parts, grad_scale, max_norm, norm, (cudaStream_t)stream);
 }

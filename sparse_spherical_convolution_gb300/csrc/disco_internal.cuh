@@ -108,6 +108,7 @@ cudaError_t norm_tile_bounds(int32_t* v, bool clear);
 cudaError_t norm_q_bounds(int32_t* v, bool clear);
 cudaError_t norm_rows_bounds(int32_t* v, bool clear);
 cudaError_t norm_bwd_bounds(int32_t* v, bool clear);
+cudaError_t dequant_bounds(int32_t* v, bool clear);
 cudaError_t grad_bounds(int32_t* v, bool clear);
 // Weight gradient dW[o][j] = sum_b sum_p dy[b][o][p] X[b][j][p] (split reduction
 // through fp32 partials of dw_partial_bytes bytes, then rounded to bf16).

@@ -1,6 +1,5 @@
 // disco_norm.cu -- channel RMS norm with the residual's addition and an
-// 8-bit copy (disco_rms_norm), its gradient (disco_rms_norm_bwd) and the
-// return from 8 bits (disco_dequant_e4m3), on activations [B, C, P].
+// 8-bit copy (disco_rms_norm), on activations [B, C, P].
 //
 // The general kernels below take every shape: 32 pixels per CTA, the channels
 // dealt to 8 warps, statistics joined in shared memory, the inputs read again
@@ -20,10 +19,6 @@ using namespace norm;
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)v, __NV_E4M3)));
-}
-
 // as warps_sum, the maximum
 __device__ __forceinline__ float warps_max(float v, float (*buf)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -85,29 +80,6 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs
   }
 }
 
-
-struct DequantArgs {
-  const uint8_t* q;
-  const float* scale;
-  void* x;
-  int G, NG, C;
-  long long P, n;
-};
-
-template <typename T>
-__global__ void dequant_any_kernel(const DequantArgs a) {
-  T* x = (T*)a.x;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < a.n; i += (long long)gridDim.x * blockDim.x) {
-    const long long bc = i / a.P, p = i - bc * a.P, b = bc / a.C;
-    const int c = (int)(bc - b * a.C);
-    x[i] = from_f32<T>(from_e4m3(a.q[i]) * a.scale[(b * a.NG + c / a.G) * a.P + p]);
-  }
-}
-
-int groups(int32_t C, int32_t group, int* G) {
-  *G = group > 0 && group < C ? group : C;
-  return (C + *G - 1) / *G;
-}
 
 }  // namespace
 
@@ -220,25 +192,4 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return check_launch("norm_any_kernel");
-}
-
-extern "C" int disco_dequant_e4m3(const void* q, const float* scale, void* x, int32_t group, int32_t B, int32_t C,
-                                  int64_t P, disco_dtype dtype, void* stream) {
-  disco::NvtxScope nvtx_scope("disco_dequant_e4m3");
-  int rc;
-  if ((rc = check_shape(B, C, P, dtype))) return rc;
-  if (!q || !scale || !x) return fail(DISCO_ERR_INVALID_ARG, "q, scale or x is null");
-  if (group < 0) return fail(DISCO_ERR_INVALID_ARG, "group must be >= 0");
-  if ((rc = check_device())) return rc;
-  DequantArgs a{(const uint8_t*)q, scale, x, 0, 0, C, P, (long long)B * C * P};
-  a.NG = groups(C, group, &a.G);
-  const Buffer in[] = {{q, (size_t)a.n, "q"}, {scale, (size_t)B * a.NG * P * 4, "scale"}};
-  const Buffer out[] = {{x, (size_t)a.n * elem_bytes(dtype), "x"}};
-  const unsigned in_place[] = {0, 0};
-  if ((rc = check_buffers(in, in_place, 2, out, 1))) return rc;
-  const int grid = (int)min((a.n + 255) / 256, 152LL * 8);
-#define CALL(T) dequant_any_kernel<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a)
-  DISCO_BY_DTYPE(dtype, CALL)
-#undef CALL
-  return check_launch("dequant_any_kernel");
 }

@@ -155,6 +155,21 @@ __device__ __forceinline__ typename Word<V>::type packed_e4m3(const F<V>& f) {
   return raw;
 }
 
+// V e4m3 values
+template <int V>
+__device__ __forceinline__ F<V> unpack_e4m3(const typename Word<V>::type& raw) {
+  __nv_fp8x2_storage_t t[V / 2];
+  memcpy(t, &raw, V);
+  F<V> r;
+#pragma unroll
+  for (int e = 0; e < V; e += 2) {
+    const __half2_raw p = __nv_cvt_fp8x2_to_halfraw2(t[e / 2], __NV_E4M3);  // exact: fp16 holds every e4m3 value
+    const float2 f = __half22float2(__half2(p));
+    r.v[e] = f.x, r.v[e + 1] = f.y;
+  }
+  return r;
+}
+
 // Each tensor is read once and written once: streaming (evict-first) access.
 template <typename W>
 __device__ __forceinline__ W load_stream(const void* p) { return __ldcs((const W*)p); }
@@ -188,6 +203,8 @@ __device__ __forceinline__ uint4 window(uint4 a, uint4 b, int bytes) {
   return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
                     __funnelshift_r(w[3], w[4], s));
 }
+__device__ __forceinline__ uint32_t from_lane_above(uint32_t v) { return __shfl_down_sync(0xffffffffu, v, 1); }
+__device__ __forceinline__ uint2 from_lane_above(uint2 v) { return make_uint2(from_lane_above(v.x), from_lane_above(v.y)); }
 __device__ __forceinline__ uint32_t from_lane_below(uint32_t v) { return __shfl_up_sync(0xffffffffu, v, 1); }
 __device__ __forceinline__ uint2 from_lane_below(uint2 v) { return make_uint2(from_lane_below(v.x), from_lane_below(v.y)); }
 __device__ __forceinline__ uint4 from_lane_below(uint4 v) {
@@ -583,6 +600,11 @@ struct Buffer {
 int check_buffers(const Buffer* in, const unsigned* in_place, int nin, const Buffer* out, int nout);
 int check_shape(int32_t B, int32_t C, int64_t P, disco_dtype dtype);
 int check_eps(float eps);
+// groups of a pixel's channels; *G: channels of one
+inline int groups(int32_t C, int32_t group, int* G) {
+  *G = group > 0 && group < C ? group : C;
+  return (C + *G - 1) / *G;
+}
 inline int elem_bytes(disco_dtype dt) { return dt == DISCO_F32 ? 4 : 2; }
 
 // CALL(T) for the element type of dtype.
