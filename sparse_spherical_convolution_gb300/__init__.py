@@ -190,7 +190,7 @@ def _check(status: int):
 def _stream(stream):
     import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -252,9 +252,9 @@ def _ws(t, name: str = "workspace"):
     import torch
     if t is None:
         return None, 0
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise DiscoError(-1, f"{name} must be a tensor on the current CUDA device")
-    return _ptr(t), t.numel() * t.element_size()
+    return _ptr(t), t.nbytes
 
 
 def _sizes(psi):
@@ -435,16 +435,31 @@ def _groups(C: int, group: int) -> int:
     return -(-C // group) if 0 < group < C else 1
 
 
-def _opt(t, name: str, numel: int, dtype):
-    return None if t is None else _dev(t, name, numel, dtype)
-
-
-def _q8(t, numel: int):
-    """Pointer of an 8-bit tensor: float8_e4m3fn, or its bytes as uint8."""
+def _on(t, name: str) -> int:
+    """The current CUDA device, which ``t`` has to be on."""
     import torch
-    if t is not None and t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t is None or not t.is_cuda:
+        _dev(t, name, 0)
+    return torch.cuda.current_device()
+
+
+def _in(t, name: str, numel: int, dtype, device: int):
+    """Address of a device tensor after _dev's checks, None for None."""
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        return _dev(t, name, numel, dtype)
+    return t.data_ptr()
+
+
+def _q8(t, numel: int, device: int):
+    """Address of an 8-bit tensor: float8_e4m3fn, or its bytes as uint8."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise DiscoError(-1, f"q has dtype {t.dtype}, the call needs float8_e4m3fn or uint8")
-    return _dev(t, "q", numel)
+    return _in(t, "q", numel, t.dtype, device)
 
 
 def disco_rms_norm(x, residual, weight, eps: float, h, y, B: int, C: int, P: int, q=None, scale=None,
@@ -453,14 +468,13 @@ def disco_rms_norm(x, residual, weight, eps: float, h, y, B: int, C: int, P: int
     weight in y, and y in 8 bits with scales in q and scale; see
     include/disco.h.  residual, weight, h, y, and q with scale may be None."""
     import torch
-    n, dt = B * C * P, None if x is None else x.dtype
-    xp = _dev(x, "x", n)
-    rp, wp = _opt(residual, "residual", n, dt), _opt(weight, "weight", C, dt)
-    hp, yp = _opt(h, "h", n, dt), _opt(y, "y", n, dt)
-    qp = None if q is None else _q8(q, n)
-    sp = _opt(scale, "scale", B * _groups(C, group) * P, torch.float32)
-    _check(load_library().disco_rms_norm(xp, rp, wp, eps, hp, yp, qp, sp, group, B, C, P, _dtype(x),
-                                         _stream(stream)))
+    n, dev = B * C * P, _on(x, "x")
+    dt = x.dtype
+    code = dtype_code(dt)
+    _check((_lib or load_library()).disco_rms_norm(
+        _in(x, "x", n, dt, dev), _in(residual, "residual", n, dt, dev), _in(weight, "weight", C, dt, dev), eps,
+        _in(h, "h", n, dt, dev), _in(y, "y", n, dt, dev), _q8(q, n, dev),
+        _in(scale, "scale", B * _groups(C, group) * P, torch.float32, dev), group, B, C, P, code, _stream(stream)))
 
 
 def disco_rms_norm_bwd_workspace_bytes(B: int, C: int, P: int, dtype=DISCO_BF16) -> int:
@@ -471,22 +485,22 @@ def disco_rms_norm_bwd(dy, h, weight, dh, eps: float, dx, dweight, B: int, C: in
                        stream=None) -> None:
     """dx and dweight of disco_rms_norm from the stored h; weight, dh and
     dweight (with its workspace) may be None."""
-    n, dt = B * C * P, None if dy is None else dy.dtype
-    yp, hp = _dev(dy, "dy", n), _dev(h, "h", n, dt)
-    wp, dhp = _opt(weight, "weight", C, dt), _opt(dh, "dh", n, dt)
-    xp, dwp = _dev(dx, "dx", n, dt), _opt(dweight, "dweight", C, dt)
+    n, dev = B * C * P, _on(dy, "dy")
+    dt = dy.dtype
+    code = dtype_code(dt)
     wsp, wsn = _ws(workspace)
-    _check(load_library().disco_rms_norm_bwd(yp, hp, wp, dhp, eps, xp, dwp, B, C, P, _dtype(dy), wsp, wsn,
-                                             _stream(stream)))
+    _check((_lib or load_library()).disco_rms_norm_bwd(
+        _in(dy, "dy", n, dt, dev), _in(h, "h", n, dt, dev), _in(weight, "weight", C, dt, dev), _in(dh, "dh", n, dt, dev),
+        eps, _in(dx, "dx", n, dt, dev), _in(dweight, "dweight", C, dt, dev), B, C, P, code, wsp, wsn, _stream(stream)))
 
 
 def disco_dequant_e4m3(q, scale, x, B: int, C: int, P: int, group: int = 0, stream=None) -> None:
     """x = q * scale, the activation that disco_rms_norm's q and scale stand for."""
     import torch
-    qp = _q8(q, B * C * P)
-    sp = _dev(scale, "scale", B * _groups(C, group) * P, torch.float32)
-    xp = _dev(x, "x", B * C * P)
-    _check(load_library().disco_dequant_e4m3(qp, sp, xp, group, B, C, P, _dtype(x), _stream(stream)))
+    n, dev = B * C * P, _on(q, "q")
+    _check((_lib or load_library()).disco_dequant_e4m3(
+        _q8(q, n, dev), _in(scale, "scale", B * _groups(C, group) * P, torch.float32, dev),
+        None if x is None else _in(x, "x", n, x.dtype, dev), group, B, C, P, -1 if x is None else _dtype(x), _stream(stream)))
 
 
 def disco_grad_plan(grads, outs=None):
@@ -524,25 +538,25 @@ def disco_grad_workspace_bytes(grads: disco_grads) -> int:
 def disco_grad_norm(grads: disco_grads, norm, workspace, grad_scale: float = 1.0, stream=None) -> None:
     """The Euclidean norm over all gradients, times grad_scale, to ``norm`` (one fp32)."""
     import torch
-    np_ = _dev(norm, "norm", 1, torch.float32)
+    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
     wp, wn = _ws(workspace)
-    _check(load_library().disco_grad_norm(ctypes.byref(grads), grad_scale, np_, wp, wn, _stream(stream)))
+    _check((_lib or load_library()).disco_grad_norm(ctypes.byref(grads), grad_scale, np_, wp, wn, _stream(stream)))
 
 
 def disco_grad_clip(grads: disco_grads, max_norm: float, norm, grad_scale: float = 1.0, stream=None) -> None:
     """Every gradient scaled by grad_scale and down to ``max_norm`` given ``norm``, to its out."""
     import torch
-    np_ = _dev(norm, "norm", 1, torch.float32)
-    _check(load_library().disco_grad_clip(ctypes.byref(grads), grad_scale, max_norm, np_, _stream(stream)))
+    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
+    _check((_lib or load_library()).disco_grad_clip(ctypes.byref(grads), grad_scale, max_norm, np_, _stream(stream)))
 
 
 def disco_grad_norm_clip(grads: disco_grads, max_norm: float, norm, workspace, grad_scale: float = 1.0,
                          stream=None) -> None:
     """disco_grad_norm and disco_grad_clip in one call."""
     import torch
-    np_ = _dev(norm, "norm", 1, torch.float32)
+    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
     wp, wn = _ws(workspace)
-    _check(load_library().disco_grad_norm_clip(ctypes.byref(grads), grad_scale, max_norm, np_, wp, wn,
+    _check((_lib or load_library()).disco_grad_norm_clip(ctypes.byref(grads), grad_scale, max_norm, np_, wp, wn,
                                                _stream(stream)))
 
 

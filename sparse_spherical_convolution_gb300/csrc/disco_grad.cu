@@ -3,14 +3,18 @@
 //
 // The list of gradients travels in the kernels' parameters, so a call depends
 // on no device table and no earlier copy.  Work is cut into chunks that do not
-// cross tensors, dealt to persistent CTAs in turn.
+// cross tensors, dealt to the warps of persistent CTAs in turn: a warp's chunk
+// may be a bias of a few elements without idling a CTA.
 //
 // Sums of squares are kept at three scales, sum g^2, sum (g 2^-80)^2 and
 // sum (g 2^90)^2: where the first is infinite the second holds the answer,
-// where it is below 2^-60 (its terms near the smallest fp32) the third.  A
-// thread adds in fp32, a CTA joins its threads in 64 bits and leaves one row of
+// where it is below 2^-60 (its terms near the smallest fp32) the third.  All
+// in fp32 (all terms are positive, threads and CTAs join pairwise; the few
+// fp64 units of this GPU took longer than the loads): a CTA leaves one row of
 // partial sums, and every CTA of the scaling kernel adds those rows up for
-// itself: two launches, no atomics, one order of summation.
+// itself: two launches, no atomics, one order of summation.  A short list runs
+// in one launch of one cluster, whose CTAs exchange their rows through
+// distributed shared memory.
 
 #include <math.h>
 #include <stdio.h>
@@ -28,9 +32,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSMs = 152;
-constexpr int kNormGrid = kSMs * 4;  // CTAs of a norm launch at most = rows of its partial sums
-constexpr int kClipGrid = kSMs * 6;
-constexpr int kUnroll = 4;           // 16-byte loads a thread has in flight
+constexpr int kNormPerSM = 4, kClipPerSM = 2;  // resident CTAs of the large kernels
+constexpr int kNormGrid = kSMs * kNormPerSM;   // CTAs of a norm launch at most = rows of its partial sums
+constexpr int kClipGrid = kSMs * kClipPerSM;
+constexpr int kNormUnroll = 8, kClipUnroll = 4;  // 16-byte loads a lane has in flight
+// Longest chunks, in elements.  Scaling writes as it reads: with one round of a
+// warp's 16-bit loads to a chunk the warps of a CTA stay side by side in memory
+// (1024: 115 us for 113 million bf16 elements into fp32; 2048: 128; 4096: 155,
+// 4 CTAs to an SM: 141 to 152).  The norm only reads (8192: 45 us, 1024: 54).
+constexpr int kNormChunk = 8192, kClipChunk = 1024;
+constexpr int kCluster = 16;                     // CTAs of the small kernel
 
 struct Entry {
   const void* g;
@@ -40,26 +51,29 @@ struct Entry {
   short dt, odt;
 };
 // The gradients of one launch; kernel parameters end at 32,764 bytes, and a
-// short list takes a short table.
+// launch costs more the longer they are.
 template <int N>
 struct Table {
   Entry e[N];
   long long chunk;   // elements of a chunk
   int chunks, count;
 };
-constexpr int kShort = 64, kLong = 1000;
+constexpr int kShort = 64, kMiddle = 256, kLong = 1000;
 static_assert(sizeof(Table<kLong>) + 64 <= 32764, "kernel parameters");
 
-// the tensor that chunk c belongs to
+// the tensor that chunk c belongs to; `at`: the last answer, often this one too
 template <int N>
-__device__ __forceinline__ const Entry& find(const Table<N>& t, int c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (t.e[mid].chunk0 <= c) lo = mid;
-    else hi = mid - 1;
+__device__ __forceinline__ const Entry& find(const Table<N>& t, int c, int& at) {
+  if (c < t.e[at].chunk0 || (at + 1 < t.count && c >= t.e[at + 1].chunk0)) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (t.e[mid].chunk0 <= c) lo = mid;
+      else hi = mid - 1;
+    }
+    at = lo;
   }
-  return t.e[lo];
+  return t.e[at];
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -112,194 +126,251 @@ __device__ __forceinline__ void sum_word(Sums& s, const uint4& w) {
   for (int e = 0; e < (int)(16 / sizeof(T)); e += 2) s.add<T>(make_float2(to_f32(t[e]), to_f32(t[e + 1])));
 }
 
-// elements [i0, i1) of a tensor; i0 is a multiple of 16
+// elements [i0, i1) of a tensor, by one warp; i0 is a multiple of 16
 template <typename T>
-__device__ __forceinline__ void sum_chunk(Sums& s, const T* g, long long i0, long long i1) {
+__device__ __forceinline__ void sum_elements(Sums& s, const T* g, long long i0, long long i1) {
   constexpr int V = 16 / sizeof(T);
-  long long i = i0;
+  const int lane = threadIdx.x & 31;
+  g += i0;
+  const int n = (int)(i1 - i0);
+  int i = 0;
   if (((uintptr_t)g & 15) == 0) {
-    const uint4* p = (const uint4*)(g + i0);
-    const long long words = (i1 - i0) / V;
-    long long k = threadIdx.x;
-    for (; k + (kUnroll - 1) * kThreads < words; k += kUnroll * kThreads) {
-      uint4 w[kUnroll];
+    const uint4* p = (const uint4*)g;
+    const int words = n / V;
+    int k = lane;
+    for (; k + (kNormUnroll - 1) * 32 < words; k += kNormUnroll * 32) {
+      uint4 w[kNormUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) w[u] = p[k + u * kThreads];
+      for (int u = 0; u < kNormUnroll; ++u) w[u] = p[k + u * 32];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) sum_word<T>(s, w[u]);
+      for (int u = 0; u < kNormUnroll; ++u) sum_word<T>(s, w[u]);
     }
-    for (; k < words; k += kThreads) sum_word<T>(s, p[k]);
-    i = i0 + words * V;
+    for (; k < words; k += 32) sum_word<T>(s, p[k]);
+    i = words * V;
   }
   // the rest, and tensors off a 16-byte boundary, by elements
-  for (i += threadIdx.x; i < i1; i += 8 * kThreads) {
+  for (i += lane; i < n; i += 8 * 32) {
     T t[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) t[u] = i + u * kThreads < i1 ? g[i + u * kThreads] : from_f32<T>(0.0f);
+    for (int u = 0; u < 8; ++u) t[u] = i + u * 32 < n ? g[i + u * 32] : from_f32<T>(0.0f);
 #pragma unroll
     for (int u = 0; u < 8; u += 2) s.add<T>(make_float2(to_f32(t[u]), to_f32(t[u + 1])));
   }
 }
 
-// Sum of `v` over the CTA's threads, in 64 bits and one order, to all of them.
-__device__ __forceinline__ double cta_sum(double v, double* buf) {
+struct Row {
+  float v[3];
+};
+// The sums over the CTA's threads, in one order, to all of them.
+__device__ __forceinline__ Row cta_sum(Row r, Row* buf) {
 #pragma unroll
-  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = 0.0;
+  for (int m = 16; m; m >>= 1)
 #pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) v += buf[k];
-  return v;
+    for (int n = 0; n < 3; ++n) r.v[n] += __shfl_xor_sync(0xffffffffu, r.v[n], m);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x / 32] = r;
+  __syncthreads();
+  r = buf[0];
+#pragma unroll
+  for (int k = 1; k < kThreads / 32; ++k)
+#pragma unroll
+    for (int n = 0; n < 3; ++n) r.v[n] += buf[k].v[n];
+  return r;
+}
+__device__ __forceinline__ Row row_of(const Sums& s) { return Row{{s.a.x + s.a.y, s.b.x + s.b.y, s.c.x + s.c.y}}; }
+__device__ __forceinline__ float norm_of(const Row& r, float grad_scale) {
+  float v = sqrtf(r.v[0]);
+  if (isinf(r.v[0])) v = sqrtf(r.v[1]) * 0x1p80f;
+  else if (r.v[0] < 0x1p-60f) v = sqrtf(r.v[2]) * 0x1p-90f;
+  return v * grad_scale;
+}
+
+// A CTA's warps take neighbouring chunks.
+constexpr int kWarps = kThreads / 32;
+__device__ __forceinline__ int first_chunk() { return blockIdx.x * kWarps + threadIdx.x / 32; }
+
+// chunk k's squares
+template <int N>
+__device__ __forceinline__ void sum_chunk(Sums& s, const Table<N>& t, int k, int& at) {
+  const Entry& e = find(t, k, at);
+  const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
+  if (e.dt == DISCO_F32) sum_elements(s, (const float*)e.g, i0, i1);
+  else if (e.dt == DISCO_BF16) sum_elements(s, (const __nv_bfloat16*)e.g, i0, i1);
+  else {
+    Sums h;
+    sum_elements(h, (const __half*)e.g, i0, i1);
+    s.add_f16(h);
+  }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<N> t, double* part) {
-  __shared__ double buf[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kNormPerSM) grad_norm_kernel(const __grid_constant__ Table<N> t, Row* part) {
+  __shared__ Row buf[kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;");
   Sums s;
-  for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const Entry& e = find(t, k);
-    const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
-    if (e.dt == DISCO_F32) sum_chunk(s, (const float*)e.g, i0, i1);
-    else if (e.dt == DISCO_BF16) sum_chunk(s, (const __nv_bfloat16*)e.g, i0, i1);
-    else {
-      Sums h;
-      sum_chunk(h, (const __half*)e.g, i0, i1);
-      s.add_f16(h);
-    }
-  }
-  const double a = cta_sum((double)s.a.x + s.a.y, buf), b = cta_sum((double)s.b.x + s.b.y, buf),
-               c = cta_sum((double)s.c.x + s.c.y, buf);
-  if (threadIdx.x == 0) {
-    part[3 * blockIdx.x] = a;
-    part[3 * blockIdx.x + 1] = b;
-    part[3 * blockIdx.x + 2] = c;
-  }
+  int at = 0;
+  for (int k = first_chunk(); k < t.chunks; k += gridDim.x * kWarps) sum_chunk(s, t, k, at);
+  const Row r = cta_sum(row_of(s), buf);
+  if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
 
-// The norm from all rows of partial sums (every thread of the CTA gets it).
-__device__ __forceinline__ float norm_of(const double* part, int parts, float grad_scale, double* buf) {
-  double a = 0.0, b = 0.0, c = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) {
-    a += part[3 * i];
-    b += part[3 * i + 1];
-    c += part[3 * i + 2];
-  }
-  a = cta_sum(a, buf);
-  b = cta_sum(b, buf);
-  c = cta_sum(c, buf);
-  double v = sqrt(a);
-  if (isinf(a)) v = sqrt(b) * 0x1p80;
-  else if (a < 0x1p-60) v = sqrt(c) * 0x1p-90;
-  return (float)(v * grad_scale);
+// All rows of partial sums, to every thread of the CTA.
+__device__ __forceinline__ Row sum_rows(const Row* part, int parts, Row* buf) {
+  Row r{{0.0f, 0.0f, 0.0f}};
+  for (int i = threadIdx.x; i < parts; i += kThreads)
+#pragma unroll
+    for (int n = 0; n < 3; ++n) r.v[n] += part[i].v[n];
+  return cta_sum(r, buf);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* part, int parts, float grad_scale, float* norm) {
-  __shared__ double buf[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const Row* part, int parts, float grad_scale, float* norm) {
+  __shared__ Row buf[kThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float v = norm_of(part, parts, grad_scale, buf);
+  const float v = norm_of(sum_rows(part, parts, buf), grad_scale);
   if (threadIdx.x == 0) *norm = v;
 }
 
+// out = g f of elements [i0, i1), by one warp
 template <typename T, typename O>
-__device__ __forceinline__ void clip_chunk(const T* g, O* o, long long i0, long long i1, float f) {
-  constexpr int V = 16 / sizeof(T);
-  long long i = i0;
+__device__ __forceinline__ void clip_elements(const T* g, O* o, long long i0, long long i1, float f) {
+  constexpr int V = 16 / sizeof(T), B = V * (int)sizeof(O);  // B: 8, 16 or 32 bytes
+  const int lane = threadIdx.x & 31;
+  g += i0;
+  o += i0;
+  const int n = (int)(i1 - i0);
+  int i = 0;
   if ((((uintptr_t)g | (uintptr_t)o) & 15) == 0) {
-    const uint4* p = (const uint4*)(g + i0);
-    O* q = o + i0;
-    const long long words = (i1 - i0) / V;
-    auto put = [&](const uint4& w, long long k) {
+    const uint4* p = (const uint4*)g;
+    const int words = n / V;
+    auto put = [&](const uint4& w, int k) {
       T t[V];
       O r[V];
       memcpy(t, &w, 16);
 #pragma unroll
       for (int e = 0; e < V; ++e) r[e] = from_f32<O>(to_f32(t[e]) * f);
-      constexpr int B = V * (int)sizeof(O);  // 8, 16 or 32 bytes
       if constexpr (B == 8) {
         uint2 z;
         memcpy(&z, r, 8);
-        __stcs((uint2*)(q + k * V), z);
+        __stcs((uint2*)o + k, z);
       } else {
         uint4 z[B / 16];
         memcpy(z, r, B);
 #pragma unroll
-        for (int u = 0; u < B / 16; ++u) __stcs((uint4*)(q + k * V) + u, z[u]);
+        for (int u = 0; u < B / 16; ++u) __stcs((uint4*)o + k * (B / 16) + u, z[u]);
       }
     };
-    long long k = threadIdx.x;
-    for (; k + (kUnroll - 1) * kThreads < words; k += kUnroll * kThreads) {
-      uint4 w[kUnroll];
+    int k = lane;
+    for (; k + (kClipUnroll - 1) * 32 < words; k += kClipUnroll * 32) {
+      uint4 w[kClipUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) w[u] = __ldcs(p + k + u * kThreads);
+      for (int u = 0; u < kClipUnroll; ++u) w[u] = __ldcs(p + k + u * 32);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) put(w[u], k + u * kThreads);
+      for (int u = 0; u < kClipUnroll; ++u) put(w[u], k + u * 32);
     }
-    for (; k < words; k += kThreads) put(__ldcs(p + k), k);
-    i = i0 + words * V;
+    for (; k < words; k += 32) put(__ldcs(p + k), k);
+    i = words * V;
   }
-  for (i += threadIdx.x; i < i1; i += 8 * kThreads) {
+  for (i += lane; i < n; i += 8 * 32) {
     T t[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (i + u * kThreads < i1) t[u] = g[i + u * kThreads];
+      if (i + u * 32 < n) t[u] = g[i + u * 32];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (i + u * kThreads < i1) o[i + u * kThreads] = from_f32<O>(to_f32(t[u]) * f);
+      if (i + u * 32 < n) o[i + u * 32] = from_f32<O>(to_f32(t[u]) * f);
   }
 }
 
 template <typename T>
 __device__ __forceinline__ void clip_entry(const Entry& e, long long i0, long long i1, float f) {
-  if (e.odt == DISCO_F32) clip_chunk((const T*)e.g, (float*)e.o, i0, i1, f);
-  else if (e.odt == DISCO_BF16) clip_chunk((const T*)e.g, (__nv_bfloat16*)e.o, i0, i1, f);
-  else clip_chunk((const T*)e.g, (__half*)e.o, i0, i1, f);
+  if (e.odt == DISCO_F32) clip_elements((const T*)e.g, (float*)e.o, i0, i1, f);
+  else if (e.odt == DISCO_BF16) clip_elements((const T*)e.g, (__nv_bfloat16*)e.o, i0, i1, f);
+  else clip_elements((const T*)e.g, (__half*)e.o, i0, i1, f);
+}
+
+// factor of the clipped gradients
+__device__ __forceinline__ float factor(float norm, float grad_scale, float max_norm) {
+  return norm <= max_norm ? grad_scale : grad_scale * (max_norm / norm);
+}
+
+template <int N>
+__device__ __forceinline__ void clip_chunk(const Table<N>& t, int k, int& at, float f) {
+  const Entry& e = find(t, k, at);
+  if (e.o == e.g && f == 1.0f) return;
+  const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
+  if (e.dt == DISCO_F32) clip_entry<float>(e, i0, i1, f);
+  else if (e.dt == DISCO_BF16) clip_entry<__nv_bfloat16>(e, i0, i1, f);
+  else clip_entry<__half>(e, i0, i1, f);
 }
 
 // part: the rows of partial sums of this call's norm (the norm is written to
 // *norm by CTA 0), or null: the norm is read from *norm.
 template <int N>
-__global__ void __launch_bounds__(kThreads)
-    grad_clip_kernel(const __grid_constant__ Table<N> t, const double* part, int parts, float grad_scale, float max_norm, float* norm) {
-  __shared__ double buf[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kClipPerSM)
+    grad_clip_kernel(const __grid_constant__ Table<N> t, const Row* part, int parts, float grad_scale, float max_norm, float* norm) {
+  __shared__ Row buf[kThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float n;
   if (part) {
-    n = norm_of(part, parts, grad_scale, buf);
+    n = norm_of(sum_rows(part, parts, buf), grad_scale);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   } else {
     n = *norm;
   }
-  const float f = n <= max_norm ? grad_scale : grad_scale * (max_norm / n);
+  const float f = factor(n, grad_scale, max_norm);
+  int at = 0;
   // last chunks first: the norm's pass read them last, they may still be in L2
-  for (int k = t.chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
-    const Entry& e = find(t, k);
-    if (e.o == e.g && f == 1.0f) continue;
-    const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
-    if (e.dt == DISCO_F32) clip_entry<float>(e, i0, i1, f);
-    else if (e.dt == DISCO_BF16) clip_entry<__nv_bfloat16>(e, i0, i1, f);
-    else clip_entry<__half>(e, i0, i1, f);
-  }
+  for (int k = t.chunks - 1 - first_chunk(); k >= 0; k -= gridDim.x * kWarps) clip_chunk(t, k, at, f);
 }
 
-// Elements of a chunk: four chunks for each CTA of the norm where there is
-// enough work, 1024 (one load for each thread) to 16384 (all of a thread's
-// loads twice), and more where there would be more than 2^28 chunks.
-long long chunk_of(const disco_grads* g) {
-  long long c = 1024;
-  while (c < 16384 && g->numel / c > 4 * kNormGrid) c *= 2;
-  while (g->numel / c > (1 << 28)) c *= 2;
+// A short list in one launch: the CTAs of one cluster take its chunks in turn,
+// push their rows of sums to one another, and scale the chunks they summed.
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    grad_small_kernel(const __grid_constant__ Table<N> t, float grad_scale, float max_norm, bool clip, float* norm) {
+  __shared__ Row buf[kThreads / 32], box[kCluster];
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  Sums s;
+  int at = 0;
+  for (int k = first_chunk(); k < t.chunks; k += kCluster * kWarps) sum_chunk(s, t, k, at);
+  Row r = cta_sum(row_of(s), buf);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs: its memory may be written
+  if (threadIdx.x < kCluster) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(to)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&box[blockIdx.x]))), "r"(threadIdx.x));
+#pragma unroll
+    for (int n = 0; n < 3; ++n) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * n), "f"(r.v[n]) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  r = box[0];
+#pragma unroll
+  for (int k = 1; k < kCluster; ++k)
+#pragma unroll
+    for (int n = 0; n < 3; ++n) r.v[n] += box[k].v[n];
+  const float n = norm_of(r, grad_scale);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  if (!clip) return;
+  const float f = factor(n, grad_scale, max_norm);
+  for (int k = first_chunk(); k < t.chunks; k += kCluster * kWarps) clip_chunk(t, k, at, f);
+}
+
+// Elements of a chunk (a warp's): two for each warp of the norm's grid where
+// there is enough work, from 256 (one 16-byte load of 16-bit elements for each
+// lane) to `most`, and more where there would be more than 2^27 chunks.
+long long chunk_of(const disco_grads* g, int most) {
+  long long c = 256;
+  while (c < most && g->numel / c > 2 * kNormGrid * kWarps) c *= 2;
+  while (g->numel / c > (1 << 27)) c *= 2;
   return c;
 }
 
 // Fills `t` from tensors[*next ...]; false when none with elements is left.
 template <int N>
-bool fill(const disco_grads* g, int* next, Table<N>* t) {
+bool fill(const disco_grads* g, int* next, int most, Table<N>* t) {
   t->count = 0;
   t->chunks = 0;
-  t->chunk = chunk_of(g);
+  t->chunk = chunk_of(g, most);
   for (; *next < g->count && t->count < N; ++*next) {
     const disco_grad_tensor& s = g->tensors[*next];
     if (s.n < 1) continue;
@@ -398,15 +469,40 @@ int check_max_norm(const disco_grads* g, float max_norm) {
   return DISCO_OK;
 }
 
+// Elements of a list that one cluster takes.
+constexpr long long kSmall = 1 << 16;
+
+template <int N>
+int run_small(const disco_grads* g, float grad_scale, float max_norm, bool clip, float* norm, cudaStream_t st) {
+  Table<N> t;
+  int next = 0;
+  fill(g, &next, kClipChunk, &t);
+  cudaError_t e = cudaFuncSetAttribute((const void*)grad_small_kernel<N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, grad_small_kernel<N>, t, grad_scale, max_norm, clip, norm);
+  }
+  return launch_status(e, "grad_small_kernel");
+}
+
 // Partial sums of all gradients; *parts: rows.
 template <int N>
-int norm_parts(const disco_grads* g, double* part, int* parts, cudaStream_t st) {
+int norm_parts(const disco_grads* g, Row* part, int* parts, cudaStream_t st) {
   Table<N> t;
   int next = 0;
   *parts = 0;
-  while (fill(g, &next, &t)) {
-    const int grid = t.chunks < kNormGrid ? t.chunks : kNormGrid;
-    grad_norm_kernel<N><<<grid, kThreads, 0, st>>>(t, part + 3LL * *parts);
+  while (fill(g, &next, kNormChunk, &t)) {
+    const int ctas = (t.chunks + kWarps - 1) / kWarps, grid = ctas < kNormGrid ? ctas : kNormGrid;
+    grad_norm_kernel<N><<<grid, kThreads, 0, st>>>(t, part + *parts);
     const int rc = launch_status(cudaGetLastError(), "grad_norm_kernel");
     if (rc) return rc;
     *parts += grid;
@@ -415,11 +511,11 @@ int norm_parts(const disco_grads* g, double* part, int* parts, cudaStream_t st) 
 }
 
 template <int N>
-int clip_all(const disco_grads* g, const double* part, int parts, float grad_scale, float max_norm, float* norm, cudaStream_t st) {
+int clip_all(const disco_grads* g, const Row* part, int parts, float grad_scale, float max_norm, float* norm, cudaStream_t st) {
   Table<N> t;
   int next = 0;
-  while (fill(g, &next, &t)) {
-    const int grid = t.chunks < kClipGrid ? t.chunks : kClipGrid;
+  while (fill(g, &next, kClipChunk, &t)) {
+    const int ctas = (t.chunks + kWarps - 1) / kWarps, grid = ctas < kClipGrid ? ctas : kClipGrid;
     const int rc = launch_status(launch_after(grad_clip_kernel<N>, grid, st, t, part, parts, grad_scale, max_norm, norm),
                                  "grad_clip_kernel");
     if (rc) return rc;
@@ -428,15 +524,29 @@ int clip_all(const disco_grads* g, const double* part, int parts, float grad_sca
   return DISCO_OK;
 }
 
-int norm_parts(const disco_grads* g, double* part, int* parts, cudaStream_t st) {
-  return g->count <= kShort ? norm_parts<kShort>(g, part, parts, st) : norm_parts<kLong>(g, part, parts, st);
-}
-int clip_all(const disco_grads* g, const double* part, int parts, float grad_scale, float max_norm, float* norm, cudaStream_t st) {
-  return g->count <= kShort ? clip_all<kShort>(g, part, parts, grad_scale, max_norm, norm, st)
-                            : clip_all<kLong>(g, part, parts, grad_scale, max_norm, norm, st);
-}
-int finish_norm(const double* part, int parts, float grad_scale, float* norm, cudaStream_t st) {
+int finish_norm(const Row* part, int parts, float grad_scale, float* norm, cudaStream_t st) {
   return launch_status(launch_after(grad_norm_finish_kernel, 1, st, part, parts, grad_scale, norm), "grad_norm_finish_kernel");
+}
+
+// The norm, and with `clip` the scaled gradients, by tables of N.
+template <int N>
+int run(const disco_grads* g, float grad_scale, float max_norm, bool clip, float* norm, void* ws, cudaStream_t st) {
+  if (g->count <= N && g->numel <= kSmall) return run_small<N>(g, grad_scale, max_norm, clip, norm, st);
+  Row* part = (Row*)ws;
+  int parts, rc = norm_parts<N>(g, part, &parts, st);
+  if (rc) return rc;
+  return clip ? clip_all<N>(g, part, parts, grad_scale, max_norm, norm, st) : finish_norm(part, parts, grad_scale, norm, st);
+}
+
+#define DISCO_BY_COUNT(count, CALL)            \
+  ((count) <= kShort    ? CALL(kShort)         \
+   : (count) <= kMiddle ? CALL(kMiddle)        \
+                        : CALL(kLong))
+
+int run(const disco_grads* g, float grad_scale, float max_norm, bool clip, float* norm, void* ws, cudaStream_t st) {
+#define CALL(N) run<N>(g, grad_scale, max_norm, clip, norm, ws, st)
+  return DISCO_BY_COUNT(g->count, CALL);
+#undef CALL
 }
 
 int check_workspace(const disco_grads* g, void* ws, size_t bytes) {
@@ -494,7 +604,7 @@ extern "C" int disco_grad_plan(const disco_grad_tensor* tensors, int32_t count, 
 
 extern "C" size_t disco_grad_workspace_bytes(const disco_grads* grads) {
   if (!grads || grads->count < 0) return 0;
-  return (size_t)launches(grads) * kNormGrid * 3 * sizeof(double);
+  return (size_t)launches(grads) * kNormGrid * sizeof(Row);
 }
 
 extern "C" int disco_grad_norm(const disco_grads* grads, float grad_scale, float* norm, void* workspace,
@@ -504,9 +614,7 @@ extern "C" int disco_grad_norm(const disco_grads* grads, float grad_scale, float
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_workspace(grads, workspace, workspace_bytes)) ||
       (rc = check_scalar(norm, "norm")))
     return rc;
-  int parts;
-  if ((rc = norm_parts(grads, (double*)workspace, &parts, (cudaStream_t)stream))) return rc;
-  return finish_norm((const double*)workspace, parts, grad_scale, norm, (cudaStream_t)stream);
+  return run(grads, grad_scale, 0.0f, false, norm, workspace, (cudaStream_t)stream);
 }
 
 extern "C" int disco_grad_clip(const disco_grads* grads, float grad_scale, float max_norm, const float* norm,
@@ -516,7 +624,9 @@ extern "C" int disco_grad_clip(const disco_grads* grads, float grad_scale, float
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) || (rc = check_scalar(norm, "norm")))
     return rc;
   // the kernel writes the norm only where it computes it
-  return clip_all(grads, nullptr, 0, grad_scale, max_norm, const_cast<float*>(norm), (cudaStream_t)stream);
+#define CALL(N) clip_all<N>(grads, nullptr, 0, grad_scale, max_norm, const_cast<float*>(norm), (cudaStream_t)stream)
+  return DISCO_BY_COUNT(grads->count, CALL);
+#undef CALL
 }
 
 extern "C" int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, float max_norm, float* norm,
@@ -526,8 +636,5 @@ extern "C" int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, 
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) ||
       (rc = check_workspace(grads, workspace, workspace_bytes)) || (rc = check_scalar(norm, "norm")))
     return rc;
-  int parts;
-  if ((rc = norm_parts(grads, (double*)workspace, &parts, (cudaStream_t)stream))) return rc;
-  if (parts == 0) return finish_norm((const double*)workspace, 0, grad_scale, norm, (cudaStream_t)stream);
-  return clip_all(grads, (const double*)workspace, parts, grad_scale, max_norm, norm, (cudaStream_t)stream);
+  return run(grads, grad_scale, max_norm, true, norm, workspace, (cudaStream_t)stream);
 }
