@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantArgs a, 
         const long long row = row0 + i * a.P;
         const int m = (int)((unsigned)row & (V - 1));
         const WQ above = from_lane_above(w[i]);
-        const F<V> v = mul(unpack_e4m3<V>(m ? window(w[i], above, m) : w[i]), s);
-        store_shifted<V>((T*)a.x + row - m, packed<T, V>(v), m, lx, i < nc ? n : 0);
+        const F<V> v = mul(unpack_e4m3<V>(window(w[i], above, m)), s);
+        store_shifted<V>((T*)a.x + row - m, packed<T, V>(v), m, lx, g.LX, n, i < nc);
       }
     } else if (nc > 0 && px < n) {
       if (DISCO_IN_BOUNDS(s0 + V <= (long long)a.B * a.NG * a.P)) {

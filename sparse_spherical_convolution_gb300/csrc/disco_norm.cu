@@ -130,31 +130,36 @@ bool plan_tiles(int B, int C, long long P, int es, bool forward, Tiling* g) {
   g->shifted = P % g->V != 0;
   const int spare = g->shifted ? 1 : 0;  // lanes of a row without pixels
   const long long words = (P + g->V - 1) / g->V + spare;
-  // lanes of a row, channels of a thread, CTAs of a cluster: long rows and one
-  // CTA first
+  // Lanes of a row, channels of a thread, CTAs of a cluster, in the order of
+  // preference; the first that gives the SM three quarters of kMaxThreads.
   struct Shape {
     int LX, NCH, CL;
   };
-  static const Shape fwd[] = {{16, 4, 1}, {8, 4, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}, {1, 8, 8}};
+  static const Shape fwd[] = {{16, 4, 1}, {8, 4, 1}, {16, 8, 1}, {8, 8, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}, {1, 8, 8}};
+  static const Shape fwd_shifted[] = {{32, 4, 1}, {16, 4, 1}, {32, 8, 1}, {16, 8, 1}, {8, 8, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}};
   static const Shape bwd[] = {{16, 4, 1}, {8, 4, 1}, {4, 4, 1}, {4, 4, 2}, {4, 4, 4}, {4, 4, 8}, {2, 4, 8}, {1, 4, 8}};
-  const Shape* s = forward ? fwd : bwd;
-  const int ns = forward ? 9 : 8;
+  const Shape* s = !forward ? bwd : g->shifted ? fwd_shifted : fwd;
+  const int ns = forward ? 11 : 8;
+  int best = 0;
   for (int k = 0; k < ns; ++k) {
     int LX = s[k].LX;
-    if (LX <= spare) return false;
+    if (LX <= spare) break;
     while (LX > 1 + spare && LX / 2 >= words) LX /= 2;
     // fewer pixels to a tile while there are not two tiles for each SM
     while (LX > 4 && B * ((words + LX - 1) / LX) < 2 * kSMs) LX /= 2;
     const int cpc = (C + s[k].CL - 1) / s[k].CL, NL = (cpc + s[k].NCH - 1) / s[k].NCH;
     if ((long long)LX * NL > kMaxThreads) continue;
     while (LX * NL < 32 && LX < 32) LX *= 2;  // a warp at least
-    g->LX = LX, g->NCH = s[k].NCH, g->CL = s[k].CL, g->cpc = cpc;
-    g->NT = (LX * NL + 31) / 32 * 32;
-    g->TP = (LX - spare) * g->V;
-    g->finish(B, C, P, max(1, kSMs * max(1, kMaxThreads / g->NT) / g->CL));
-    return true;
+    const int NT = (LX * NL + 31) / 32 * 32, threads = NT * (kMaxThreads / NT);
+    if (threads <= best) continue;
+    best = threads;
+    g->LX = LX, g->NCH = s[k].NCH, g->CL = s[k].CL, g->cpc = cpc, g->NT = NT;
+    if (best >= kMaxThreads * 3 / 4 || s[k].CL > 1) break;
   }
-  return false;
+  if (!best) return false;
+  g->TP = (g->LX - spare) * g->V;
+  g->finish(B, C, P, max(1, kSMs * (kMaxThreads / g->NT) / g->CL));
+  return true;
 }
 
 }  // namespace norm

@@ -212,17 +212,35 @@ __device__ __forceinline__ uint4 from_lane_below(uint4 v) {
 }
 
 // Stores the row that starts m elements past the aligned address `p`, `n`
-// elements of it, of which this lane holds the V from lx * V on (all lanes of
-// the warp call it; the last lane of a row holds none).
+// elements of it (the same for the whole warp), of which this lane holds the V
+// from lx * V on.  All lanes of the warp call it; the last of a row's LX lanes
+// holds no elements, rows with `valid` false are not stored.  In a full tile,
+// n = (LX - 1) V, the V elements that share a word with another tile (the row's
+// first V - m and last m) go out one to a lane.
 template <int V, typename W>
-__device__ __forceinline__ void store_shifted(void* p, W own, int m, int lx, int n) {
-  constexpr int ES = (int)sizeof(W) / V;
+__device__ __forceinline__ void store_shifted(void* p, W own, int m, int lx, int LX, int n, bool valid) {
+  constexpr int ES = (int)sizeof(W) / V, NW = (int)sizeof(W) / 4;
   const W below = from_lane_below(own);
   const W word = m ? window(below, own, (V - m) * ES) : own;
   const int at = lx * V - m;  // the word's first element in the row
   char* d = (char*)p + lx * (int)sizeof(W);
-  if (at >= 0 && at + V <= n) store_stream(d, word);
-  else if (at < n && at + V > 0) {
+  if (valid && at >= 0 && at + V <= n) store_stream(d, word);
+  if (n == (LX - 1) * V && LX >= V) {
+    uint32_t own32[NW];
+    memcpy(own32, &own, sizeof(W));
+    const int e = lx & (V - 1), from = e < V - m ? 0 : LX - 2;
+    uint32_t v = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const uint32_t o = __shfl_sync(0xffffffffu, own32[k], from, LX);
+      v = e * ES / 4 == k ? o : v;
+    }
+    v >>= 8 * (e * ES & 3);
+    if (valid && m > 0 && lx < V) {
+      const typename Word<ES>::type one = (typename Word<ES>::type)v;
+      store_stream((char*)p + (m + from * V + e) * ES, one);
+    }
+  } else if (valid && at < n && at + V > 0 && !(at >= 0 && at + V <= n)) {
     const uint8_t* b = (const uint8_t*)&word;
 #pragma unroll
     for (int e = 0; e < V; ++e)
@@ -356,15 +374,15 @@ struct Cursor {
 template <typename T, int V, int NCH, bool SHIFT>
 struct Lane {
   using W = Raw<T, V>;
-  int lx, nc, stride;  // stride: words from one channel to the next in the ring
-  int c0, NT;
-  long long P, mine, total, left;  // mine: the thread's place in a tile; total: elements of the tensor
+  int lx, LX, nc, stride;  // stride: words from one channel to the next in the ring
+  int c0;
+  long long P, mine, total;  // mine: the thread's place in a tile; total: elements of the tensor
   W* slot;
 
   static __host__ __device__ size_t words(const Tiling& g) { return (size_t)NCH * g.NT + (SHIFT ? 1 : 0); }
 
   __device__ __forceinline__ Lane(const Tiling& g, int B, int C, long long P_, int lx_, int j, int first_c, void* smem)
-      : lx(lx_), stride(g.NT), NT(g.NT), P(P_) {
+      : lx(lx_), LX(g.LX), stride(g.NT), P(P_) {
     c0 = first_c + j * NCH;
     const int end = first_c + g.cpc < C ? first_c + g.cpc : C;
     nc = end - c0 < 0 ? 0 : end - c0 < NCH ? end - c0 : NCH;
@@ -386,6 +404,16 @@ struct Lane {
   __device__ __forceinline__ void fetch(const Tiling& g, const Cursor& c, const T* p, W* to) const {
     if (c.t >= g.tiles) return;
     if constexpr (SHIFT) {
+      const T* q = p + lx * V;
+      // every word of the tile within its row, and none near the tensor's end
+      if (c.pos + LX * V <= P && c.off + mine + NCH * P + (LX + 1) * V <= total) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const long long row = (c.off + mine + i * P) & ~(long long)(V - 1);
+          if (i < nc && DISCO_IN_BOUNDS(row >= 0)) copy_async(to + i * stride, q + row);
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         const long long row = c.off + mine + i * P;
@@ -404,7 +432,7 @@ struct Lane {
   // after copy_wait (and __syncwarp, if shifted)
   __device__ __forceinline__ W read(const W* from, int i, int m) const {
     const W w = from[i * stride];
-    if constexpr (SHIFT) return m ? window(w, from[i * stride + 1], m * (int)sizeof(T)) : w;
+    if constexpr (SHIFT) return window(w, from[i * stride + 1], m * (int)sizeof(T));
     return w;
   }
   // channel i's V elements, packed as `w` (of any element size), to the tile at
@@ -415,7 +443,7 @@ struct Lane {
     const long long row = c.off + mine + i * P;
     if constexpr (SHIFT) {
       const int m = (int)((unsigned)row & (V - 1));
-      store_shifted<V>((char*)p + (row - m) * ES, w, m, lx, i < nc ? n : 0);
+      store_shifted<V>((char*)p + (row & ~(long long)(V - 1)) * ES, w, m, lx, LX, n, i < nc);
     } else {
       if (on && i < nc && DISCO_IN_BOUNDS(row >= 0 && row + V <= total)) store_stream((char*)p + row * ES, w);
     }

@@ -134,16 +134,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
     if (SHIFT) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      F<V> vh = unpack<T, V>(k_h[i]), rg = mul(unpack<T, V>(k_dy[i]), rk[0]);
-      if (SHIFT)  // elements past the row's end are another row's, or nothing
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (e >= px) vh.v[e] = rg.v[e] = 0.0f;
+      const F<V> vh = unpack<T, V>(k_h[i]);
+      F<V> rg = mul(unpack<T, V>(k_dy[i]), rk[0]);
       F<V> d = mul(vh, rk[1]);
       if (dh) d = add(d, unpack<T, V>(lane.read(r_dh, i, lane.skew(at, i))));
       d = fma(rg, fill<V>(wt[i]), d);
       lane.write(a.dx, at, i, packed<T, V>(d), px > 0, n);
-      if (px > 0 && i < nc) {
+      if (SHIFT && px < V) {  // what lies past the row's end is another row's, or nothing
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (e < px) dw[i][0] = fmaf(rg.v[e], vh.v[e], dw[i][0]);
+      } else if (px > 0) {
         F<2> t{dw[i][0], dw[i][1]};
 #pragma unroll
         for (int e = 0; e < V; e += 2) t = fma(F<2>{rg.v[e], rg.v[e + 1]}, F<2>{vh.v[e], vh.v[e + 1]}, t);
