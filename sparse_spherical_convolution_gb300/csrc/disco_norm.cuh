@@ -551,10 +551,16 @@ __device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
   for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
   return s;
 }
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- launches ----------------------------------------------------------------
 
+// after: the kernel may begin while the one before it on the stream ends, once
+// all its CTAs have called let_next_begin(); it calls wait_for_previous() before
+// it reads what that one wrote.
 template <typename K, typename... A>
-int launch(K kernel, int grid, int threads, int cluster, size_t smem, cudaStream_t st, const char* what, A... args) {
+int launch(K kernel, int grid, int threads, int cluster, bool after, size_t smem, cudaStream_t st, const char* what, A... args) {
   if (smem + 1024 > 48 * 1024 &&  // with a kernel's static arrays
       cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -565,12 +571,21 @@ int launch(K kernel, int grid, int threads, int cluster, size_t smem, cudaStream
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = n;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -580,11 +595,11 @@ int launch(K kernel, int grid, int threads, int cluster, size_t smem, cudaStream
 }
 template <typename K, typename... A>
 int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, const char* what, A... args) {
-  return launch(kernel, g.clusters * g.CL, g.NT, g.CL, smem, st, what, args...);
+  return launch(kernel, g.clusters * g.CL, g.NT, g.CL, false, smem, st, what, args...);
 }
 template <typename K, typename... A>
 int launch_grid(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const char* what, A... args) {
-  return launch(kernel, grid, threads, 1, smem, st, what, args...);
+  return launch(kernel, grid, threads, 1, false, smem, st, what, args...);
 }
 
 // ---- arguments, and the kernels by translation unit ---------------------------

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   using W = typename L::W;
   using Join = Joiner<V, 2, 2>;
   extern __shared__ __align__(16) char smem[];
+  let_next_begin();
   const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
   float* fsm = (float*)(smem + L::words(g) * 16 * (a.dh ? 3 : 2));
   const Join J(g, fsm, rank);
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, T*
   __shared__ float buf[8][32];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.0f;
+  wait_for_previous();
   if (c < C)
 #pragma unroll 8
     for (int i = k; i < parts; i += 8) s += part[(long long)i * C + c];
@@ -249,8 +251,9 @@ extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* wei
   }
   if (rc || !dweight) return rc;
   const int parts = (int)(need / ((size_t)C * sizeof(float)));
-#define CALL(T) norm_dweight_kernel<T><<<(C + 31) / 32, 256, 0, st>>>(a.part, (T*)dweight, parts, C)
+#define CALL(T) \
+  rc = launch(norm_dweight_kernel<T>, (C + 31) / 32, 256, 1, true, 0, st, "norm_dweight_kernel", (const float*)a.part, (T*)dweight, parts, C)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
-  return check_launch("norm_dweight_kernel");
+  return rc;
 }

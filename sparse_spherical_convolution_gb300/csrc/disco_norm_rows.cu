@@ -61,14 +61,17 @@ struct Place {
   __device__ __forceinline__ bool any(int i) const { return at(i) < C; }
   __device__ __forceinline__ bool whole(int i) const { return WHOLE ? any(i) : at(i) >= 0 && at(i) + V <= C; }
   __device__ __forceinline__ bool in(int i, int e) const { return WHOLE ? any(i) : at(i) + e >= 0 && at(i) + e < C; }
-  __device__ __forceinline__ void fetch(const T* p, uint4* to, int NT, long long r, long long B) const {
-    const long long total = B * C;
+  // element offset of word 0 of row r in the tensor
+  __device__ __forceinline__ long long origin(long long r) const { return r * C + at(0); }
+  // row r, whose origin is o
+  __device__ __forceinline__ void fetch(const T* p, uint4* to, int NT, long long o, bool last) const {
 #pragma unroll
-    for (int i = 0; i < NWD; ++i) {
-      const long long o = r * C + at(i);
-      if (any(i) && DISCO_IN_BOUNDS(o >= 0 && o < total))
-        copy_async(to + i * NT, p + o, total - o >= V ? 16 : (int)(total - o) * (int)sizeof(T));
-    }
+    for (int i = 0; i < NWD; ++i)
+      if (any(i) && DISCO_IN_BOUNDS(o + i * LANES * V >= 0)) {
+        // a last partial word ends with the row's elements where the tensor ends
+        const int bytes = !WHOLE && last && !whole(i) && at(i) >= 0 ? (C - at(i)) * (int)sizeof(T) : 16;
+        copy_async(to + i * NT, p + o + i * LANES * V, min(bytes, 16));
+      }
   }
   // the elements of word i that are the row's; zeros in place of the others
   __device__ __forceinline__ F<V> own(F<V> v, int i) const {
@@ -78,9 +81,9 @@ struct Place {
     return v;
   }
   template <typename W>
-  __device__ __forceinline__ void write(void* p, long long r, int i, W w) const {
+  __device__ __forceinline__ void write(void* p, long long o, int i, W w) const {
     constexpr int ES = (int)sizeof(W) / V;
-    char* d = (char*)p + (r * C + at(i)) * ES;
+    char* d = (char*)p + o * ES + i * LANES * (int)sizeof(W);
     if (whole(i)) {
       store_stream(d, w);
     } else if (!WHOLE && any(i)) {
@@ -109,9 +112,11 @@ struct Place {
   // N values over the team's threads; buf: this row's parity of two
   template <int N, typename Op>
   __device__ __forceinline__ void reduce(float (&v)[N], float (&buf)[N][kThreads / 32], Op op) const {
-    for (int k = min(LANES, 32) / 2; k; k >>= 1)
 #pragma unroll
-      for (int n = 0; n < N; ++n) v[n] = op(v[n], __shfl_xor_sync(0xffffffffu, v[n], k));
+    for (int k = 16; k; k >>= 1)
+      if (k < LANES)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = op(v[n], __shfl_xor_sync(0xffffffffu, v[n], k));
     if (LANES <= 32) return;
     const int w0 = team * (LANES / 32), nw = LANES / 32;
     if ((threadIdx.x & 31) == 0)
@@ -130,7 +135,7 @@ struct Place {
 // it holds one in registers; the gradient reads its row twice from the ring, so
 // one of its kDepth is the current row (kDepth = 1: nothing ahead, the row is too long).
 constexpr int ahead_of(int NWD) { return NWD >= 4 ? 1 : 4 / NWD; }
-constexpr int depth_of(int NWD) { return NWD == 8 ? 1 : NWD == 4 ? 2 : NWD == 2 ? 3 : 4; }
+constexpr int depth_of(int NWD) { return NWD == 8 ? 1 : NWD == 4 ? 2 : 4; }
 
 template <int V>
 __device__ __forceinline__ float across(const F<V>& f) {
@@ -138,6 +143,14 @@ __device__ __forceinline__ float across(const F<V>& f) {
 #pragma unroll
   for (int e = 0; e < V; ++e) s += f.v[e];
   return s;
+}
+
+// 1 / x for x >= kAmaxFloor to an ulp (the e4m3 values it scales have 4 bits); 0
+// for an infinite x
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // How a group's maximum is found: its words are the row; are gw = G / V
@@ -167,17 +180,19 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
       }
   }
   uint32_t* gm = (uint32_t*)(smem + (size_t)kAhead * words * 16 * (res ? 2 : 1)) + (size_t)P.team * a.NG;  // kAtomic
-  auto fetch = [&](long long r, int slot) {
+  const long long step_o = P.step * a.C;
+  auto fetch = [&](long long r, long long o, int slot) {
     if (r < a.B) {
-      P.fetch(x, rx + slot * words, g.NT, r, a.B);
-      if (res) P.fetch(res, rr + slot * words, g.NT, r, a.B);
+      P.fetch(x, rx + slot * words, g.NT, o, r == a.B - 1);
+      if (res) P.fetch(res, rr + slot * words, g.NT, o, r == a.B - 1);
     }
     copy_commit();
   };
-  for (int k = 0; k < kAhead; ++k) fetch(P.row + k * P.step, k);
+  long long o = P.origin(P.row);
+  for (int k = 0; k < kAhead; ++k) fetch(P.row + k * P.step, o + k * step_o, k);
   int parity = 0, slot = 0;
   for (long long lead = P.lead, row = P.row; lead < a.B;
-       lead += P.step, row += P.step, parity ^= 1, slot = slot + 1 == kAhead ? 0 : slot + 1) {
+       lead += P.step, row += P.step, o += step_o, parity ^= 1, slot = slot + 1 == kAhead ? 0 : slot + 1) {
     P.recompute();
     const bool on = row < a.B;
     F<V> v[NWD], s = fill<V>(0.0f);
@@ -187,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
       v[i] = unpack<T, V>(rx[slot * words + i * g.NT]);
       if (res) v[i] = add(v[i], unpack<T, V>(rr[slot * words + i * g.NT]));
     }
-    fetch(row + kAhead * P.step, slot);
+    fetch(row + kAhead * P.step, o + kAhead * step_o, slot);
 #pragma unroll
     for (int i = 0; i < NWD; ++i) {
       v[i] = P.own(v[i], i);
@@ -195,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
     }
     if (a.h && on)
 #pragma unroll
-      for (int i = 0; i < NWD; ++i) P.write(a.h, row, i, packed<T, V>(v[i]));
+      for (int i = 0; i < NWD; ++i) P.write(a.h, o, i, packed<T, V>(v[i]));
     float sum[1] = {across(s)};
     P.reduce(sum, buf[0][parity], [](float p, float q) { return p + q; });
     const F<V> r = fill<V>(1.0f / sqrtf(sum[0] / (float)a.C + a.eps));
@@ -203,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
     for (int i = 0; i < NWD; ++i) v[i] = mul(mul(v[i], r), unpack<T, V>(wt[i]));
     if (a.y && on)
 #pragma unroll
-      for (int i = 0; i < NWD; ++i) P.write(a.y, row, i, packed<T, V>(v[i]));
+      for (int i = 0; i < NWD; ++i) P.write(a.y, o, i, packed<T, V>(v[i]));
 
     if constexpr (Q) {
       if (!WHOLE && qmode == kAtomic) {
@@ -241,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
                 }
                 v[i].v[e] *= inv;
               }
-            if (on) P.write(a.q, row, i, packed_e4m3<V>(v[i]));
+            if (on) P.write(a.q, o, i, packed_e4m3<V>(v[i]));
           }
         if (on)
           for (int k = P.lane; k < a.NG; k += P.LANES)
@@ -260,17 +275,25 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
           P.reduce(all, buf[1][parity], [](float p, float q) { return fmaxf(p, q); });
           if (on && P.lane == 0) a.scale[row] = all[0] / kE4m3Max;
         }
-        const int gw = a.G / V;
+        if (qmode == kLanes) {
+          const int gw = a.G / V;
+#pragma unroll
+          for (int k = 16; k; k >>= 1)
+            if (k < gw)
+#pragma unroll
+              for (int i = 0; i < NWD; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], k));
+          if (on && (P.lane & (gw - 1)) == 0) {
+            float* to = a.scale + row * a.NG + P.lane / gw;
+            const int next = P.LANES / gw;
+#pragma unroll
+            for (int i = 0; i < NWD; ++i)
+              if (P.any(i)) to[i * next] = top[i] / kE4m3Max;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < NWD; ++i) {
-          if (qmode == kLanes) {
-            for (int k = gw / 2; k; k >>= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], k));
-            if (on && P.any(i) && (P.lane & (gw - 1)) == 0)
-              a.scale[row * a.NG + (P.lane + i * P.LANES) / gw] = top[i] / kE4m3Max;
-          } else {
-            top[i] = all[0];
-          }
-          if (on) P.write(a.q, row, i, packed_e4m3<V>(mul(v[i], fill<V>(kE4m3Max / top[i]))));
+          const float inv = kE4m3Max * reciprocal(qmode == kLanes ? top[i] : all[0]);
+          if (on) P.write(a.q, o, i, packed_e4m3<V>(mul(v[i], fill<V>(inv))));
         }
       }
     }
@@ -282,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
   constexpr int V = 16 / (int)sizeof(T);
   using W = Raw<T, V>;
   extern __shared__ __align__(16) char smem[];
+  let_next_begin();
   __shared__ float buf[2][2][kThreads / 32];
   Place<T, NWD, WHOLE> P(g, a.C);
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *dh = (const T*)a.dh;
@@ -299,22 +323,25 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
       for (int k = 0; k < kDepth; ++k)
         for (int n = 0; n < streams; ++n) ring[(k * streams + n) * words + i * g.NT] = make_uint4(0, 0, 0, 0);
   }
-  auto fetch = [&](long long r, int slot) {
+  const long long step_o = P.step * a.C;
+  auto fetch = [&](long long r, long long o, int slot) {
     if (r < a.B) {
       uint4* to = ring + slot * streams * words;
-      P.fetch(dy, to, g.NT, r, a.B);
-      P.fetch(h, to + words, g.NT, r, a.B);
-      if (dh) P.fetch(dh, to + 2 * words, g.NT, r, a.B);
+      const bool last = r == a.B - 1;
+      P.fetch(dy, to, g.NT, o, last);
+      P.fetch(h, to + words, g.NT, o, last);
+      if (dh) P.fetch(dh, to + 2 * words, g.NT, o, last);
     }
     copy_commit();
   };
-  for (int k = 0; k < kDepth - 1; ++k) fetch(P.row + k * P.step, k);
+  long long o = P.origin(P.row);
+  for (int k = 0; k < kDepth - 1; ++k) fetch(P.row + k * P.step, o + k * step_o, k);
   int parity = 0, slot = 0;
   for (long long lead = P.lead, row = P.row; lead < a.B;
-       lead += P.step, row += P.step, parity ^= 1, slot = slot + 1 == kDepth ? 0 : slot + 1) {
+       lead += P.step, row += P.step, o += step_o, parity ^= 1, slot = slot + 1 == kDepth ? 0 : slot + 1) {
     P.recompute();
     const bool on = row < a.B;
-    fetch(row + (kDepth - 1) * P.step, slot == 0 ? kDepth - 1 : slot - 1);  // the slot of the row before
+    fetch(row + (kDepth - 1) * P.step, o + (kDepth - 1) * step_o, slot == 0 ? kDepth - 1 : slot - 1);  // the row before's slot
     copy_wait<kDepth - 1>();
     const uint4 *r_dy = ring + slot * streams * words, *r_h = r_dy + words, *r_dh = r_h + words;
     F<V> s = fill<V>(0.0f), d = s;
@@ -333,10 +360,10 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
 #pragma unroll
       for (int i = 0; i < NWD; ++i) {
         const F<V> vh = P.own(unpack<T, V>(r_h[i * g.NT]), i), rg = mul(P.own(unpack<T, V>(r_dy[i * g.NT]), i), r);
-        F<V> o = mul(vh, k);
-        if (dh) o = add(o, unpack<T, V>(r_dh[i * g.NT]));
-        o = fma(rg, unpack<T, V>(wt[i]), o);
-        P.write(a.dx, row, i, packed<T, V>(o));
+        F<V> d = mul(vh, k);
+        if (dh) d = add(d, unpack<T, V>(r_dh[i * g.NT]));
+        d = fma(rg, unpack<T, V>(wt[i]), d);
+        P.write(a.dx, o, i, packed<T, V>(d));
         dw[i] = fma(rg, vh, dw[i]);
       }
     }
@@ -372,12 +399,10 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 bool plan_rows(int B, int C, int es, bool forward, Rows* g) {
   const int V = 16 / es, words = (C + V - 1) / V + (C % V ? 1 : 0);  // of a row, with a partial one at each end
   g->period = V / gcd(C, V);
-  // words to a thread: 4, where the gradient holds its sums of dweight too 2; one
-  // for short rows, and for few rows, so that a call spreads over the SMs; more
-  // where the largest team needs it
+  // words to a thread: 4; one for short rows, and for few rows, so that a call
+  // spreads over the SMs; 8 where the largest team needs it
   const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= kThreads;
-  const int usual = forward ? 4 : 2;
-  g->NWD = few || words <= 32 ? 1 : words <= usual * kThreads ? usual : words <= 4 * kThreads ? 4 : 8;
+  g->NWD = few || words <= 8 ? 1 : words <= 4 * kThreads ? 4 : 8;
   if (words > g->NWD * kThreads || (!forward && es == 2 && g->NWD == 8)) return false;
   g->LANES = 1;
   while (g->LANES * g->NWD < words) g->LANES *= 2;
@@ -438,8 +463,7 @@ int norm_bwd_rows(const NormBwdArgs& a, cudaStream_t st) {
     if (g.NWD == 8) return launch_bwd_rows<T, 8, false>(a, g, st);
   const bool whole = g.period == 1;
   if (g.NWD == 1) return whole ? launch_bwd_rows<T, 1, true>(a, g, st) : launch_bwd_rows<T, 1, false>(a, g, st);
-  if (g.NWD == 2) return whole ? launch_bwd_rows<T, 2, true>(a, g, st) : launch_bwd_rows<T, 2, false>(a, g, st);
-  return launch_bwd_rows<T, 4, false>(a, g, st);
+  return whole ? launch_bwd_rows<T, 4, true>(a, g, st) : launch_bwd_rows<T, 4, false>(a, g, st);
 }
 
 }  // namespace
