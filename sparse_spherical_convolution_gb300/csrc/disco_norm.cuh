@@ -274,8 +274,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // address of `p` (this CTA's shared memory) in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
@@ -485,9 +488,11 @@ struct Joiner {
     out = smem + rows * NSUM * (TP + 32);
     box = out + TP * NOUT;
   }
-  // finish(z, r): the outputs r[NOUT] of one pixel from its sums z[NSUM]
+  // Hands in this thread's sums.  finish(z, r): the outputs r[NOUT] of one pixel
+  // from its sums z[NSUM].  The outputs are there after collect(); what a thread
+  // does in between hides the exchange.
   template <typename Fin>
-  __device__ __forceinline__ void join(const F<V> (&s)[NSUM], F<V> (&r)[NOUT], int parity, Fin finish) const {
+  __device__ __forceinline__ void submit(const F<V> (&s)[NSUM], int parity, Fin finish) const {
 #pragma unroll
     for (int n = 0; n < NSUM; ++n) store_row<V>(red + (n * rows + j) * pitch + lx * V, s[n]);
     __syncthreads();
@@ -517,8 +522,13 @@ struct Joiner {
         }
       }
     }
+    if (CL > 1) cluster_arrive();
+  }
+  template <typename Fin>
+  __device__ __forceinline__ void collect(F<V> (&r)[NOUT], int parity, Fin finish) const {
     if (CL > 1) {
-      cluster_barrier();
+      cluster_wait();
+      const float* half = box + parity * CL * NSUM * TP;
       for (int px = tid; px < TP; px += NT) {
         float z[NSUM], o[NOUT];
 #pragma unroll

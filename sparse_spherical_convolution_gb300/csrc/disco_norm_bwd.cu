@@ -126,11 +126,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
       s[0] = fma(vh, vh, s[0]);
       s[1] = fma(mul(unpack<T, V>(k_dy[i]), fill<V>(wt[i])), vh, s[1]);
     }
-    J.join(s, rk, parity, [&](const float(&z)[2], float(&out)[2]) {
+    auto finish = [&](const float(&z)[2], float(&out)[2]) {
       const float r = 1.0f / sqrtf(z[0] / (float)a.C + a.eps);
       out[0] = r;
       out[1] = -(z[1] / (float)a.C * r) * r * r;
-    });
+    };
+    J.submit(s, parity, finish);
+    J.collect(rk, parity, finish);
     copy_wait<1>();  // this tile's dh; the next dy and h may be on their way
     if (SHIFT) __syncwarp();
 #pragma unroll
@@ -168,23 +170,23 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   }
 }
 
-// dweight[c]: the rows of partial sums, 8 threads to a channel.
+// dweight[c]: the rows of partial sums, 32 threads to a channel, all of a
+// thread's loads in flight (up to 10 rows: 304 CTAs).
 template <typename T>
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, T* dw, int parts, int C) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* part, T* dw, int parts, int C) {
+  __shared__ float buf[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.0f;
   wait_for_previous();
   if (c < C)
-#pragma unroll 8
-    for (int i = k; i < parts; i += 8) s += part[(long long)i * C + c];
+#pragma unroll 10
+    for (int i = k; i < parts; i += 32) s += part[(long long)i * C + c];
   buf[k][lane] = s;
   __syncthreads();
-  if (k == 0 && c < C) {
-    s = 0.0f;
-    for (int i = 0; i < 8; ++i) s += buf[i][lane];
-    dw[c] = from_f32<T>(s);
-  }
+  s = buf[lane][k];  // channel k of this CTA
+#pragma unroll
+  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (lane == 0 && blockIdx.x * 32 + k < C) dw[blockIdx.x * 32 + k] = from_f32<T>(s);
 }
 
 // Rows of partial sums of a call.
@@ -252,7 +254,7 @@ extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* wei
   if (rc || !dweight) return rc;
   const int parts = (int)(need / ((size_t)C * sizeof(float)));
 #define CALL(T) \
-  rc = launch(norm_dweight_kernel<T>, (C + 31) / 32, 256, 1, true, 0, st, "norm_dweight_kernel", (const float*)a.part, (T*)dweight, parts, C)
+  rc = launch(norm_dweight_kernel<T>, (C + 31) / 32, 1024, 1, true, 0, st, "norm_dweight_kernel", (const float*)a.part, (T*)dweight, parts, C)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return rc;

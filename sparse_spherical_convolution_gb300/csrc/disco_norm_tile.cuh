@@ -76,10 +76,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
     fetch();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) s[0] = fma(v[i], v[i], s[0]);
+    auto finish = [&](const float(&z)[1], float(&out)[1]) { out[0] = 1.0f / sqrtf(z[0] / (float)a.C + a.eps); };
+    J.submit(s, parity, finish);
     if (a.h)
 #pragma unroll
       for (int i = 0; i < NCH; ++i) lane.write(a.h, at, i, packed<T, V>(v[i]), on, n);
-    J.join(s, r, parity, [&](const float(&z)[1], float(&out)[1]) { out[0] = 1.0f / sqrtf(z[0] / (float)a.C + a.eps); });
+    J.collect(r, parity, finish);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) v[i] = mul(mul(v[i], r[0]), fill<V>(wt[i]));
     if (a.y)
