@@ -4,6 +4,8 @@
 // Bound by HBM: 1 byte read and 2 or 4 written to an element, and the scales.
 // A thread takes V neighbouring pixels of kRun channels of one group, so the
 // scales are read once for the run; its kRun loads of q are in flight together.
+// Where V does not divide P the words are not pixels (rows off alignment,
+// disco_norm.cuh) and a run's channels lie `apart` apart: one skew, one V scales.
 
 #include "disco_norm.cuh"
 
@@ -28,7 +30,7 @@ struct DequantArgs {
 
 // Blocks of LX lanes x J runs.  Runs of a sample: per_group of each group.
 struct Cut {
-  int LX, J, TP, per_group;
+  int LX, J, TP, per_group, apart;
   long long runs, run_blocks, px_tiles, blocks;  // of a sample; of the call
 };
 
@@ -41,27 +43,25 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantArgs a, 
   for (long long blk = blockIdx.x; blk < g.blocks; blk += gridDim.x) {
     const long long t = blk % g.px_tiles, rb = blk / g.px_tiles, b = rb / g.run_blocks;
     const long long run = (rb - b * g.run_blocks) * g.J + j;
-    const int grp = (int)(run / g.per_group);
-    const int c0 = grp * a.G + (int)(run - (long long)grp * g.per_group) * kRun;
-    const int nc = run < g.runs ? max(0, min(kRun, min((grp + 1) * a.G, a.C) - c0)) : 0;
-    const long long pos = t * g.TP, row0 = (b * a.C + c0) * a.P + pos;
+    const int grp = (int)(run / g.per_group), in_group = (int)(run - (long long)grp * g.per_group), apart = SHIFT ? g.apart : 1;
+    const int c0 = grp * a.G + in_group / apart * (apart * kRun) + in_group % apart;
+    const int nc = run < g.runs ? max(0, min(kRun, (min((grp + 1) * a.G, a.C) - c0 + apart - 1) / apart)) : 0;
+    const long long pos = t * g.TP, row0 = (b * a.C + c0) * a.P + pos, step = apart * a.P;
     const int n = (int)min((long long)g.TP, a.P - pos);  // pixels of the tile
-    const int px = lx * V;
+    const int m = SHIFT ? (int)((unsigned)row0 & (V - 1)) : 0, px = lx * V - m;
     const long long s0 = (b * a.NG + grp) * a.P + pos + px;
     F<V> s = fill<V>(0.0f);
     WQ w[kRun];
     if constexpr (SHIFT) {
-      if (nc > 0 && lx < g.LX - 1)
+      if (nc > 0)
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (px + e < n) s.v[e] = a.scale[s0 + e];
+          if (px + e >= 0 && px + e < n) s.v[e] = a.scale[s0 + e];
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         memset(&w[i], 0, sizeof(WQ));
-        const long long row = row0 + i * a.P;
-        const int m = (int)((unsigned)row & (V - 1));
-        const long long at = row - m + px;
-        if (i < nc && px - m < n && DISCO_IN_BOUNDS(at >= 0 && at < a.n)) {
+        const long long at = row0 + i * step + px;
+        if (i < nc && px < n && DISCO_IN_BOUNDS(at >= 0 && at < a.n)) {
           if (at + V <= a.n) {
             w[i] = load_stream<WQ>(a.q + at);
           } else {
@@ -74,13 +74,8 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantArgs a, 
         }
       }
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const long long row = row0 + i * a.P;
-        const int m = (int)((unsigned)row & (V - 1));
-        const WQ above = from_lane_above(w[i]);
-        const F<V> v = mul(unpack_e4m3<V>(window(w[i], above, m)), s);
-        store_shifted<V>((T*)a.x + row - m, packed<T, V>(v), m, lx, g.LX, n, i < nc);
-      }
+      for (int i = 0; i < kRun; ++i)
+        store_words<V>((T*)a.x + row0 + i * step - m, packed<T, V>(mul(unpack_e4m3<V>(w[i]), s)), m, lx, g.LX, n, i < nc);
     } else if (nc > 0 && px < n) {
       if (DISCO_IN_BOUNDS(s0 + V <= (long long)a.B * a.NG * a.P)) {
 #pragma unroll
@@ -161,14 +156,16 @@ int dequant(const DequantArgs& a, cudaStream_t st) {
     return check_launch("dequant_rows_kernel");
   }
   Cut g;
-  const bool shifted = a.P % V != 0;
+  g.apart = 1;
+  while (a.P * g.apart % V) g.apart *= 2;
+  const bool shifted = g.apart > 1;
   const int spare = shifted ? 1 : 0;
   const long long words = (a.P + V - 1) / V + spare;
   g.LX = 32;
   while (g.LX > 1 + spare && g.LX / 2 >= words) g.LX /= 2;
   g.J = kThreads / g.LX;
   g.TP = (g.LX - spare) * V;
-  g.per_group = (a.G + kRun - 1) / kRun;
+  g.per_group = (a.G + kRun * g.apart - 1) / (kRun * g.apart) * g.apart;
   g.runs = (long long)a.NG * g.per_group;
   g.run_blocks = (g.runs + g.J - 1) / g.J;
   g.px_tiles = (a.P + g.TP - 1) / g.TP;

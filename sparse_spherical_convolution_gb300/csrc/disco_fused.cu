@@ -838,7 +838,7 @@ extern "C" int disco_device_status(int32_t* flags, int32_t clear) {
   if (e == cudaSuccess) e = gemm_status(flags, clear != 0);
   int32_t bounds = 0;
   for (auto fn : {contract_bounds, psi_bounds, tc_bounds, btc_bounds, gemm_bounds, fused_bounds, norm_bounds,
-                  norm_tile_bounds, norm_q_bounds, norm_bwd_bounds, norm_rows_bounds,
+                  norm_tile_bounds, norm_q_bounds, norm_q_any_bounds, norm_bwd_bounds, norm_rows_bounds,
                   dequant_bounds, grad_bounds})
     if (e == cudaSuccess) e = fn(&bounds, clear != 0);
   *flags |= bounds;

@@ -106,6 +106,7 @@ cudaError_t fused_bounds(int32_t* v, bool clear);
 cudaError_t norm_bounds(int32_t* v, bool clear);
 cudaError_t norm_tile_bounds(int32_t* v, bool clear);
 cudaError_t norm_q_bounds(int32_t* v, bool clear);
+cudaError_t norm_q_any_bounds(int32_t* v, bool clear);
 cudaError_t norm_rows_bounds(int32_t* v, bool clear);
 cudaError_t norm_bwd_bounds(int32_t* v, bool clear);
 cudaError_t dequant_bounds(int32_t* v, bool clear);

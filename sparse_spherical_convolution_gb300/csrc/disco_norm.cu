@@ -127,31 +127,46 @@ int check_eps(float eps) {
 
 bool plan_tiles(int B, int C, long long P, int es, bool forward, Tiling* g) {
   g->V = 16 / es;
-  g->shifted = P % g->V != 0;
-  const int spare = g->shifted ? 1 : 0;  // lanes of a row without pixels
+  g->apart = 1;
+  while (P * g->apart % g->V) g->apart *= 2;
+  g->shifted = g->apart > 1;
+  const int spare = g->shifted ? 1 : 0;  // a row's words cover one less than their pixels
   const long long words = (P + g->V - 1) / g->V + spare;
-  // Lanes of a row, channels of a thread, CTAs of a cluster, in the order of
-  // preference; the first that gives the SM three quarters of kMaxThreads.
+  // Lanes of a row, channels of a thread, CTAs of a cluster, for up to so many
+  // channels, in the order of preference; the first that gives the SM three
+  // quarters of kMaxThreads.
   struct Shape {
-    int LX, NCH, CL;
+    int LX, NCH, CL, most;
   };
-  static const Shape fwd[] = {{16, 4, 1}, {8, 4, 1}, {16, 8, 1}, {8, 8, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}, {1, 8, 8}};
-  static const Shape fwd_shifted[] = {{32, 4, 1}, {16, 4, 1}, {32, 8, 1}, {16, 8, 1}, {8, 8, 1}, {16, 8, 2}, {8, 8, 2}, {4, 8, 2}, {4, 8, 4}, {4, 8, 8}, {2, 8, 8}};
-  static const Shape bwd[] = {{16, 4, 1}, {8, 4, 1}, {4, 4, 1}, {4, 4, 2}, {4, 4, 4}, {4, 4, 8}, {2, 4, 8}, {1, 4, 8}};
-  const Shape* s = !forward ? bwd : g->shifted ? fwd_shifted : fwd;
+  constexpr int kAny = 1 << 30;
+  static const Shape fwd[] = {{16, 4, 1, kAny}, {8, 4, 1, kAny},  {16, 8, 1, kAny}, {8, 8, 1, 256},   {16, 8, 2, kAny}, {8, 8, 2, kAny},
+                              {4, 8, 2, kAny},  {4, 8, 4, kAny},  {4, 8, 8, kAny},  {2, 8, 8, kAny},  {1, 8, 8, kAny}};
+  static const Shape fwd_odd[] = {{32, 4, 1, kAny}, {16, 4, 1, kAny}, {32, 8, 1, kAny}, {16, 8, 1, kAny}, {8, 8, 1, 256}, {16, 8, 2, kAny},
+                                  {8, 8, 2, kAny},  {4, 8, 2, kAny},  {4, 8, 4, kAny},  {4, 8, 8, kAny},  {2, 8, 8, kAny}};
+  static const Shape bwd[] = {{16, 4, 1, kAny}, {8, 4, 1, kAny}, {4, 4, 1, kAny}, {4, 4, 2, kAny},
+                              {4, 4, 4, kAny},  {4, 4, 8, kAny}, {2, 4, 8, kAny}, {1, 4, 8, kAny}};
+  static const Shape bwd_odd[] = {{32, 4, 1, kAny}, {16, 4, 1, kAny}, {8, 4, 1, kAny}, {8, 4, 2, kAny},
+                                  {8, 4, 4, kAny},  {8, 4, 8, kAny},  {4, 4, 8, kAny}, {2, 4, 8, kAny}};
+  const Shape* s = !forward ? (g->shifted ? bwd_odd : bwd) : !g->shifted ? fwd : fwd_odd;
   const int ns = forward ? 11 : 8;
   int best = 0;
   for (int k = 0; k < ns; ++k) {
     int LX = s[k].LX;
     if (LX <= spare) break;
+    if (C > s[k].most) continue;
     while (LX > 1 + spare && LX / 2 >= words) LX /= 2;
     // fewer pixels to a tile while there are not two tiles for each SM
     while (LX > 4 && B * ((words + LX - 1) / LX) < 2 * kSMs) LX /= 2;
-    const int cpc = (C + s[k].CL - 1) / s[k].CL, NL = (cpc + s[k].NCH - 1) / s[k].NCH;
+    const int cpc = (C + s[k].CL - 1) / s[k].CL, block = g->apart * s[k].NCH;  // channels of `apart` threads
+    const int NL = (cpc + block - 1) / block * g->apart;
     if ((long long)LX * NL > kMaxThreads) continue;
     while (LX * NL < 32 && LX < 32) LX *= 2;  // a warp at least
     const int NT = (LX * NL + 31) / 32 * 32, threads = NT * (kMaxThreads / NT);
     if (threads <= best) continue;
+    // the ring, and a Joiner's sums (of two kinds in the gradient)
+    const size_t sums = forward ? 1 : 2, slots = (size_t)g->V * (LX + spare);
+    const size_t ring = (size_t)NT * s[k].NCH * 16 * (forward ? 2 : 3);
+    if (ring + 4 * sums * ((NT / LX) * (slots + 36) + slots * (1 + 2 * s[k].CL)) + 64 > kMaxSmem) continue;
     best = threads;
     g->LX = LX, g->NCH = s[k].NCH, g->CL = s[k].CL, g->cpc = cpc, g->NT = NT;
     if (best >= kMaxThreads * 3 / 4 || s[k].CL > 1) break;
@@ -180,7 +195,7 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   if (h && !residual) return fail(DISCO_ERR_INVALID_ARG, "h without a residual is x itself");
   if (group < 0) return fail(DISCO_ERR_INVALID_ARG, "group must be >= 0");
   if ((rc = check_device())) return rc;
-  NormArgs a{x, residual, weight, h, y, q, scale, eps, 0, 0, B, C, P};
+  NormArgs a{x, residual, weight, h, y, q, scale, eps, 1.0f / (float)C, 0, 0, B, C, P};
   a.NG = groups(C, group, &a.G);
   if (!q) a.G = C, a.NG = 1;
   const size_t n = (size_t)B * C * P, e = elem_bytes(dtype);

@@ -93,6 +93,8 @@ __device__ __forceinline__ F<V> add(const F<V>& a, const F<V>& b) {
   return r;
 }
 
+__device__ __forceinline__ uint4 operator&(uint4 a, uint4 b) { return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w); }
+
 // ---- V elements of type T as one word ------------------------------------
 
 template <int BYTES> struct Word;
@@ -179,66 +181,35 @@ __device__ __forceinline__ void store_stream(void* p, W w) { __stcs((W*)p, w); }
 // ---- rows off alignment ------------------------------------------------------
 // Where V does not divide P a row of V-element words starts m = 0 .. V-1
 // elements past a word boundary.  The lanes of a row then move aligned words:
-// lane l's elements are the window of words l and l + 1 that starts at element
-// m, and word l of an output holds the last m elements of lane l - 1 and the
-// first V - m of lane l.
+// word l holds the elements from l V - m on, and a row's first and last words
+// are shared with its neighbours in memory.
 
-// the word that starts `bytes` (0 .. sizeof(W) - 1) into the pair (a, b)
-__device__ __forceinline__ uint32_t window(uint32_t a, uint32_t b, int bytes) { return __funnelshift_r(a, b, 8 * bytes); }
-__device__ __forceinline__ uint2 window(uint2 a, uint2 b, int bytes) {
-  uint32_t w0 = a.x, w1 = a.y, w2 = b.x;
-  if (bytes & 4) w0 = a.y, w1 = b.x, w2 = b.y;
-  const int s = 8 * (bytes & 3);
-  return make_uint2(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s));
-}
-__device__ __forceinline__ uint4 window(uint4 a, uint4 b, int bytes) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (bytes & 8)
-#pragma unroll
-    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-  if (bytes & 4)
-#pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-  const int s = 8 * (bytes & 3);
-  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                    __funnelshift_r(w[3], w[4], s));
-}
-__device__ __forceinline__ uint32_t from_lane_above(uint32_t v) { return __shfl_down_sync(0xffffffffu, v, 1); }
-__device__ __forceinline__ uint2 from_lane_above(uint2 v) { return make_uint2(from_lane_above(v.x), from_lane_above(v.y)); }
-__device__ __forceinline__ uint32_t from_lane_below(uint32_t v) { return __shfl_up_sync(0xffffffffu, v, 1); }
-__device__ __forceinline__ uint2 from_lane_below(uint2 v) { return make_uint2(from_lane_below(v.x), from_lane_below(v.y)); }
-__device__ __forceinline__ uint4 from_lane_below(uint4 v) {
-  return make_uint4(from_lane_below(v.x), from_lane_below(v.y), from_lane_below(v.z), from_lane_below(v.w));
-}
-
-// Stores the row that starts m elements past the aligned address `p`, `n`
-// elements of it (the same for the whole warp), of which this lane holds the V
-// from lx * V on.  All lanes of the warp call it; the last of a row's LX lanes
-// holds no elements, rows with `valid` false are not stored.  In a full tile,
-// n = (LX - 1) V, the V elements that share a word with another tile (the row's
-// first V - m and last m) go out one to a lane.
+// Stores words of a row that starts m elements past the aligned address `p`: n
+// elements of it (the same for the whole warp), of which this lane holds word lx.
+// All lanes of the warp call it; rows with `valid` false are not stored.  In a
+// full tile, n = (LX - 1) V, the V elements in words that another tile shares
+// (the row's first V - m and last m, words 0 and LX - 1) go out one to a lane.
 template <int V, typename W>
-__device__ __forceinline__ void store_shifted(void* p, W own, int m, int lx, int LX, int n, bool valid) {
+__device__ __forceinline__ void store_words(void* p, W word, int m, int lx, int LX, int n, bool valid) {
   constexpr int ES = (int)sizeof(W) / V, NW = (int)sizeof(W) / 4;
-  const W below = from_lane_below(own);
-  const W word = m ? window(below, own, (V - m) * ES) : own;
   const int at = lx * V - m;  // the word's first element in the row
   char* d = (char*)p + lx * (int)sizeof(W);
   if (valid && at >= 0 && at + V <= n) store_stream(d, word);
   if (n == (LX - 1) * V && LX >= V) {
-    uint32_t own32[NW];
-    memcpy(own32, &own, sizeof(W));
-    const int e = lx & (V - 1), from = e < V - m ? 0 : LX - 2;
+    uint32_t w[NW];
+    memcpy(w, &word, sizeof(W));
+    const int e = lx & (V - 1), from = e < m ? LX - 1 : 0;
     uint32_t v = 0;
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      const uint32_t o = __shfl_sync(0xffffffffu, own32[k], from, LX);
+      const uint32_t o = __shfl_sync(0xffffffffu, w[k], from, LX);
       v = e * ES / 4 == k ? o : v;
     }
     v >>= 8 * (e * ES & 3);
     if (valid && m > 0 && lx < V) {
-      const typename Word<ES>::type one = (typename Word<ES>::type)v;
-      store_stream((char*)p + (m + from * V + e) * ES, one);
+      typename Word<ES>::type one;
+      memcpy(&one, &v, ES);
+      store_stream((char*)p + (from * V + e) * ES, one);
     }
   } else if (valid && at < n && at + V > 0 && !(at >= 0 && at + V <= n)) {
     const uint8_t* b = (const uint8_t*)&word;
@@ -253,8 +224,7 @@ __device__ __forceinline__ void store_shifted(void* p, W own, int m, int lx, int
 }
 
 // ---- asynchronous copies ---------------------------------------------------
-// A thread copies only what it reads itself (what its warp reads, where rows
-// are shifted), so its own wait (and the warp's) orders them.
+// A thread copies only what it reads itself, so its own wait orders them.
 
 // 16 bytes, the first `bytes` of them from memory and zeros behind them
 __device__ __forceinline__ void copy_async(void* smem, const void* gmem, int bytes = 16) {
@@ -327,14 +297,20 @@ __device__ __forceinline__ void store_row(float* p, const F<V>& f) {
 
 // ---- tiles -----------------------------------------------------------------
 // A tile is TP neighbouring pixels of one sample with all channels.  A cluster
-// of CL CTAs takes it, each CTA cpc channels: thread (lx, j) holds the V pixels
-// from lx * V on (one 16-byte word of each row) of the NCH channels from
-// j * NCH on.  CTAs are persistent: cluster k takes tiles k, k + clusters, ...
-// V divides P: TP = LX * V.  Else rows are shifted (above), the last lane of a
-// row holds no pixels, and TP = (LX - 1) * V.
+// of CL CTAs takes it, each CTA cpc channels: thread (lx, j) holds word lx (16
+// bytes, V pixels) of the rows of NCH channels.  CTAs are persistent: cluster k
+// takes tiles k, k + clusters, ...
+// V divides P: TP = LX * V, thread j's channels are j * NCH and the next ones.
+// Else (shifted) words are not pixels: the LX words of a row cover TP = (LX - 1) V
+// pixels and parts of two neighbouring tiles'.  A thread's channels lie `apart`
+// = V / gcd(P, V) channels apart, so that its rows have one skew m, and its V sums
+// stand for the pixels from lx V - m on: only the sums and factors are realigned,
+// in shared memory, once a tile.  (Shifting the words themselves into place took
+// 15 instructions for each: gradient of 64 channels, 84 million elements, 195 us;
+// 4-byte accesses to whole pixels 170.)
 
 struct Tiling {
-  int NT, LX, NCH, V, CL, cpc, TP;
+  int NT, LX, NCH, V, CL, cpc, TP, apart;
   int clusters;
   bool shifted;
   long long tiles;             // of the call
@@ -372,84 +348,83 @@ struct Cursor {
   }
 };
 
-// A thread's words of its NCH channels: `ring` in shared memory, fetched a
-// tile ahead, and the same places of a tensor.
+// A thread's words of its NCH channels: `slot` in shared memory, fetched a tile
+// ahead, and their places in a tensor.
 template <typename T, int V, int NCH, bool SHIFT>
 struct Lane {
   using W = Raw<T, V>;
   int lx, LX, nc, stride;  // stride: words from one channel to the next in the ring
-  int c0;
-  long long P, mine, total;  // mine: the thread's place in a tile; total: elements of the tensor
+  int c0, apart;
+  long long P, mine, step, total;  // mine: the thread's place in a tile; step: elements from one of its rows to the next
   W* slot;
 
-  static __host__ __device__ size_t words(const Tiling& g) { return (size_t)NCH * g.NT + (SHIFT ? 1 : 0); }
+  static __host__ __device__ size_t words(const Tiling& g) { return (size_t)NCH * g.NT; }
 
   __device__ __forceinline__ Lane(const Tiling& g, int B, int C, long long P_, int lx_, int j, int first_c, void* smem)
-      : lx(lx_), LX(g.LX), stride(g.NT), P(P_) {
-    c0 = first_c + j * NCH;
-    const int end = first_c + g.cpc < C ? first_c + g.cpc : C;
-    nc = end - c0 < 0 ? 0 : end - c0 < NCH ? end - c0 : NCH;
+      : lx(lx_), LX(g.LX), stride(g.NT), apart(SHIFT ? g.apart : 1), P(P_) {
+    c0 = first_c + (SHIFT ? j / apart * (apart * NCH) + j % apart : j * NCH);
+    const int end = first_c + g.cpc < C ? first_c + g.cpc : C, room = (end - c0 + apart - 1) / apart;
+    nc = end <= c0 ? 0 : room < NCH ? room : NCH;
     mine = c0 * P + (SHIFT ? 0 : lx * V);
+    step = apart * P;
     total = (long long)B * C * P;
     slot = (W*)smem + threadIdx.x;
   }
-  // pixels of this thread in the tile at c: 0 .. V
-  __device__ __forceinline__ int pixels(const Tiling& g, const Cursor& c) const {
-    if (c.t >= g.tiles) return 0;
-    const long long n = P - c.pos - lx * V;
-    if constexpr (SHIFT) return lx == g.LX - 1 || n <= 0 ? 0 : n < V ? (int)n : V;
-    else return n > 0 ? V : 0;
+  __device__ __forceinline__ int channel(int i) const { return c0 + i * apart; }
+  // elements past a word boundary at which the thread's rows start
+  __device__ __forceinline__ int skew(const Cursor& c) const { return SHIFT ? (int)((unsigned)(c.off + mine) & (V - 1)) : 0; }
+  // whether element e is one of the tile's n pixels
+  __device__ __forceinline__ bool in(int e, int m, int n) const {
+    const int px = lx * V - m + e;
+    return px < n && (!SHIFT || px >= 0);
   }
-  // elements past a word boundary at which the row of channel i starts
-  __device__ __forceinline__ int skew(const Cursor& c, int i) const {
-    return SHIFT ? (int)((unsigned)(c.off + mine + i * P) & (V - 1)) : 0;
+  // Ones in the bits of a word's elements that are the tile's: the others are
+  // another tile's, another row's, or nothing, and may be NaN.
+  __device__ __forceinline__ uint4 mask(int m, int n) const {
+    T t[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if constexpr (sizeof(T) == 2) {
+        const uint16_t u = in(e, m, n) ? 0xffffu : 0u;
+        memcpy(&t[e], &u, 2);
+      } else {
+        const uint32_t u = in(e, m, n) ? 0xffffffffu : 0u;
+        memcpy(&t[e], &u, 4);
+      }
+    }
+    uint4 r;
+    memcpy(&r, t, 16);
+    return r;
   }
   __device__ __forceinline__ void fetch(const Tiling& g, const Cursor& c, const T* p, W* to) const {
     if (c.t >= g.tiles) return;
-    if constexpr (SHIFT) {
-      const T* q = p + lx * V;
-      // every word of the tile within its row, and none near the tensor's end
-      if (c.pos + LX * V <= P && c.off + mine + NCH * P + (LX + 1) * V <= total) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const long long row = (c.off + mine + i * P) & ~(long long)(V - 1);
-          if (i < nc && DISCO_IN_BOUNDS(row >= 0)) copy_async(to + i * stride, q + row);
-        }
-        return;
-      }
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const long long row = c.off + mine + i * P;
-        const int m = (int)((unsigned)row & (V - 1));
-        const long long at = row - m + lx * V;
-        if (i < nc && c.pos + lx * V - m < P && at < total && DISCO_IN_BOUNDS(at >= 0))
-          copy_async(to + i * stride, p + at, total - at >= V ? 16 : (int)(total - at) * (int)sizeof(T));
-      }
-    } else if (c.pos + lx * V < P) {
+    const int m = skew(c);
+    const long long row = c.off + mine - m + (SHIFT ? lx * V : 0);
+    if (c.pos + lx * V - m >= P) return;
+    // a word that the tensor's end cuts short is near only the last sample's end
+    if (!SHIFT || row + (NCH - 1) * step + V <= total) {
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
-        if (i < nc && DISCO_IN_BOUNDS(c.off + mine >= 0 && c.off + mine + i * P + V <= total))
-          copy_async(to + i * stride, p + c.off + mine + i * P);
-    }
-  }
-  // after copy_wait (and __syncwarp, if shifted)
-  __device__ __forceinline__ W read(const W* from, int i, int m) const {
-    const W w = from[i * stride];
-    if constexpr (SHIFT) return window(w, from[i * stride + 1], m * (int)sizeof(T));
-    return w;
-  }
-  // channel i's V elements, packed as `w` (of any element size), to the tile at
-  // c; n: pixels of the row in the tile.  Shifted: called by whole warps.
-  template <typename WO>
-  __device__ __forceinline__ void write(void* p, const Cursor& c, int i, WO w, bool on, int n) const {
-    constexpr int ES = (int)sizeof(WO) / V;
-    const long long row = c.off + mine + i * P;
-    if constexpr (SHIFT) {
-      const int m = (int)((unsigned)row & (V - 1));
-      store_shifted<V>((char*)p + (row & ~(long long)(V - 1)) * ES, w, m, lx, LX, n, i < nc);
+        if (i < nc && DISCO_IN_BOUNDS(row >= 0 && row + i * step + V <= total)) copy_async(to + i * stride, p + row + i * step);
     } else {
-      if (on && i < nc && DISCO_IN_BOUNDS(row >= 0 && row + V <= total)) store_stream((char*)p + row * ES, w);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const long long left = total - (row + i * step);
+        if (i < nc && left > 0 && DISCO_IN_BOUNDS(row >= 0))
+          copy_async(to + i * stride, p + row + i * step, left >= V ? 16 : (int)left * (int)sizeof(T));
+      }
     }
+  }
+  // after copy_wait
+  __device__ __forceinline__ W read(const W* from, int i) const { return from[i * stride]; }
+  // channel i's word, packed as `w` (of any element size), to the tile at c, which
+  // has n pixels.  Shifted: called by whole warps.
+  template <typename WO>
+  __device__ __forceinline__ void write(void* p, const Cursor& c, int m, int i, WO w, int n) const {
+    constexpr int ES = (int)sizeof(WO) / V;
+    char* d = (char*)p + (c.off + mine + i * step - m) * ES;
+    if constexpr (SHIFT) store_words<V>(d, w, m, lx, LX, n, i < nc);
+    else if (i < nc && lx * V < n && DISCO_IN_BOUNDS(c.off + mine + i * step + V <= total)) store_stream(d, w);
   }
 };
 
@@ -458,92 +433,121 @@ struct Lane {
 bool plan_tiles(int B, int C, long long P, int es, bool forward, Tiling* g);
 
 // Where a thread's pixels and channels lie, and how a tile's sums over the
-// channels are joined: each thread's V sums go to shared memory (one row for
-// each channel lane), S threads to a pixel add the rows up, and one of them
-// turns the sums into the NOUT values that every thread then reads back.
+// channels are joined: each thread's V sums go to shared memory (one row of
+// `slots` for each channel lane), S threads to a pixel add the rows up, and one
+// of them turns the sums into the NOUT values that every thread then reads back.
+// Pixel px has slot px; shifted, the slots stand in V rows of LX + 1 (pixel px at
+// row (px + V) mod V), so that the lanes' accesses lie side by side for any skew.
 //
 // With a cluster that thread pushes its sums to all peers, into the half of
 // `box` of this tile's parity, and one cluster barrier a tile suffices: a CTA
 // writes that half again two tiles later, after a barrier that its peers reach
 // only when they have read it.
-template <int V, int NSUM, int NOUT>
+template <int V, int NSUM, int NOUT, bool SHIFT>
 struct Joiner {
-  int NT, LX, TP, CL, tid, lx, j, rows, S_log, pitch;
+  int NT, LX, slots, CL, tid, lx, j, rows, S_log, pitch;
   uint32_t rank;
   float *red, *out, *box;
 
+  static __host__ __device__ int slots_of(const Tiling& g) { return SHIFT ? V * (g.LX + 1) : V * g.LX; }
+  static __host__ __device__ int pitch_of(const Tiling& g) { return (slots_of(g) + 3) / 4 * 4 + 32; }  // at most
   static __host__ __device__ size_t floats(const Tiling& g) {
-    const int TP = g.LX * V;  // with the pixels of a last lane that holds none
-    return (size_t)(g.NT / g.LX) * NSUM * (TP + 32) + (size_t)TP * NOUT + (g.CL > 1 ? 2 * (size_t)g.CL * NSUM * TP : 0);
+    return ((size_t)(g.NT / g.LX) * NSUM * pitch_of(g) + (size_t)slots_of(g) * (NOUT + (g.CL > 1 ? 2 * g.CL * NSUM : 0)) + 3) / 4 * 4;
   }
   __device__ __forceinline__ Joiner(const Tiling& g, float* smem, uint32_t rank_)
-      : NT(g.NT), LX(g.LX), TP(g.LX * V), CL(g.CL), tid(threadIdx.x), rank(rank_) {
+      : NT(g.NT), LX(g.LX), slots(slots_of(g)), CL(g.CL), tid(threadIdx.x), rank(rank_) {
     lx = tid & (LX - 1);
     rows = NT / LX;
     j = tid / LX;
     S_log = 0;
-    while (S_log < 3 && (2 << S_log) <= rows && (TP << S_log) * 2 <= NT) ++S_log;
-    pitch = TP + (32 >> S_log);
+    while (S_log < 3 && (2 << S_log) <= rows && (slots << S_log) * 2 <= NT) ++S_log;
+    pitch = pitch_of(g) - 32 + (32 >> S_log);
     red = smem;
-    out = smem + rows * NSUM * (TP + 32);
-    box = out + TP * NOUT;
+    out = smem + rows * NSUM * pitch_of(g);
+    box = out + slots * NOUT;
+  }
+  __device__ __forceinline__ int slot(int px) const { return SHIFT ? ((px + V) % V) * (LX + 1) + (px + V) / V : px; }
+  // this thread's V values, of skew m, in a row of slots
+  __device__ __forceinline__ void put(float* p, const F<V>& f, int m) const {
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int t = e + V - m;
+        p[(t & (V - 1)) * (LX + 1) + lx + (t / V)] = f.v[e];
+      }
+    } else {
+      store_row<V>(p + lx * V, f);
+    }
+  }
+  __device__ __forceinline__ F<V> get(const float* p, int m) const {
+    if constexpr (SHIFT) {
+      F<V> f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int t = e + V - m;
+        f.v[e] = p[(t & (V - 1)) * (LX + 1) + lx + (t / V)];
+      }
+      return f;
+    } else {
+      return load_row<V>(p + lx * V);
+    }
   }
   // Hands in this thread's sums.  finish(z, r): the outputs r[NOUT] of one pixel
   // from its sums z[NSUM].  The outputs are there after collect(); what a thread
   // does in between hides the exchange.
   template <typename Fin>
-  __device__ __forceinline__ void submit(const F<V> (&s)[NSUM], int parity, Fin finish) const {
+  __device__ __forceinline__ void submit(const F<V> (&s)[NSUM], int m, int parity, Fin finish) const {
 #pragma unroll
-    for (int n = 0; n < NSUM; ++n) store_row<V>(red + (n * rows + j) * pitch + lx * V, s[n]);
+    for (int n = 0; n < NSUM; ++n) put(red + (n * rows + j) * pitch, s[n], m);
     __syncthreads();
-    float* half = box + parity * CL * NSUM * TP;
+    float* half = box + parity * CL * NSUM * slots;
     const int S = 1 << S_log, part = tid & (S - 1);
-    for (int px = tid >> S_log, q0 = 0; q0 < (TP << S_log); q0 += NT, px += NT >> S_log) {
+    for (int px = tid >> S_log, q0 = 0; q0 < (slots << S_log); q0 += NT, px += NT >> S_log) {
       float z[NSUM], o[NOUT];
 #pragma unroll
       for (int n = 0; n < NSUM; ++n) {
         z[n] = 0.0f;
-        if (px < TP) {
+        if (px < slots) {
           const float* p = red + (n * rows + part) * pitch + px;
 #pragma unroll 4
           for (int k = part; k < rows; k += S, p += S * pitch) z[n] += *p;
         }
-        for (int m = S / 2; m; m >>= 1) z[n] += __shfl_xor_sync(0xffffffffu, z[n], m);
+        for (int k = S / 2; k; k >>= 1) z[n] += __shfl_xor_sync(0xffffffffu, z[n], k);
       }
-      if (px < TP && part == 0) {
+      if (px < slots && part == 0) {
         if (CL == 1) {
           finish(z, o);
 #pragma unroll
-          for (int n = 0; n < NOUT; ++n) out[n * TP + px] = o[n];
+          for (int n = 0; n < NOUT; ++n) out[n * slots + px] = o[n];
         } else {
 #pragma unroll
           for (int n = 0; n < NSUM; ++n)
-            for (int k = 0; k < CL; ++k) peer_store(peer(half + (rank * NSUM + n) * TP + px, k), z[n]);
+            for (int k = 0; k < CL; ++k) peer_store(peer(half + (rank * NSUM + n) * slots + px, k), z[n]);
         }
       }
     }
     if (CL > 1) cluster_arrive();
   }
   template <typename Fin>
-  __device__ __forceinline__ void collect(F<V> (&r)[NOUT], int parity, Fin finish) const {
+  __device__ __forceinline__ void collect(F<V> (&r)[NOUT], int m, int parity, Fin finish) const {
     if (CL > 1) {
       cluster_wait();
-      const float* half = box + parity * CL * NSUM * TP;
-      for (int px = tid; px < TP; px += NT) {
+      const float* half = box + parity * CL * NSUM * slots;
+      for (int px = tid; px < slots; px += NT) {
         float z[NSUM], o[NOUT];
 #pragma unroll
         for (int n = 0; n < NSUM; ++n) {
           z[n] = 0.0f;
-          for (int k = 0; k < CL; ++k) z[n] += half[(k * NSUM + n) * TP + px];
+          for (int k = 0; k < CL; ++k) z[n] += half[(k * NSUM + n) * slots + px];
         }
         finish(z, o);
 #pragma unroll
-        for (int n = 0; n < NOUT; ++n) out[n * TP + px] = o[n];
+        for (int n = 0; n < NOUT; ++n) out[n * slots + px] = o[n];
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NOUT; ++n) r[n] = load_row<V>(out + n * TP + lx * V);
+    for (int n = 0; n < NOUT; ++n) r[n] = get(out + n * slots, m);
   }
 };
 
@@ -618,7 +622,7 @@ struct NormArgs {
   const void *x, *res, *w;
   void *h, *y, *q;
   float* scale;
-  float eps;
+  float eps, inv_C;
   int G, NG, B, C;
   long long P;
 };
@@ -627,10 +631,13 @@ struct NormBwdArgs {
   const void *dy, *h, *w, *dh;
   void* dx;
   float* part;  // rows of fp32 partial sums of dweight, or null
-  float eps;
+  float eps, inv_C;
   int B, C;
   long long P;
 };
+
+// 1 / sqrt(mean + eps) from the sum of squares, within 3 ulp; 0 for an infinite sum
+__device__ __forceinline__ float inverse_rms(float sum, float inv_C, float eps) { return rsqrtf(fmaf(sum, inv_C, eps)); }
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its scale stays above 0
@@ -639,6 +646,7 @@ constexpr float kAmaxFloor = 1e-30f;  // group maximum of an all-zero group: its
 int norm_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);       // without q (disco_norm_tile.cu)
 int norm_q_by_tiles(const NormArgs& a, disco_dtype dtype, cudaStream_t st);     // with q (disco_norm_q.cu)
 
+int norm_q_any_by_tiles(const NormArgs& a, const Tiling& g, disco_dtype dtype, cudaStream_t st);  // groups of any size
 int norm_by_rows(const NormArgs& a, disco_dtype dtype, cudaStream_t st);        // P = 1 (disco_norm_rows.cu)
 int norm_bwd_by_rows(const NormBwdArgs& a, disco_dtype dtype, cudaStream_t st);
 int norm_bwd_rows_parts(int B, int C, int es);  // rows of partial sums of that call, 0: not taken

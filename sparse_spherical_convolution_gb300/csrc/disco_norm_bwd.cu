@@ -72,21 +72,21 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   constexpr int V = 16 / (int)sizeof(T), NCH = 4;
   using L = Lane<T, V, NCH, SHIFT>;
   using W = typename L::W;
-  using Join = Joiner<V, 2, 2>;
+  using Join = Joiner<V, 2, 2, SHIFT>;
   extern __shared__ __align__(16) char smem[];
   let_next_begin();
   const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
   float* fsm = (float*)(smem + L::words(g) * 16 * (a.dh ? 3 : 2));
   const Join J(g, fsm, rank);
   const L lane(g, a.B, a.C, a.P, J.lx, J.j, (int)rank * g.cpc, smem);
-  const int c0 = lane.c0, nc = lane.nc;
+  const int nc = lane.nc;
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *w = (const T*)a.w, *dh = (const T*)a.dh;
   W *r_dy = lane.slot, *r_h = r_dy + L::words(g), *r_dh = r_h + L::words(g);
 
   float wt[NCH], dw[NCH][2];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    wt[i] = i < nc && w ? to_f32(w[c0 + i]) : 1.0f;
+    wt[i] = i < nc && w ? to_f32(w[lane.channel(i)]) : 1.0f;
     dw[i][0] = dw[i][1] = 0.0f;
     if (i >= nc) {  // channels past the last: zeros, never copied over
       memset(r_dy + i * lane.stride, 0, 16);
@@ -103,19 +103,18 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   if (g.CL > 1) cluster_barrier();  // every CTA runs before another writes its shared memory
 
   for (int parity = 0; at.t < g.tiles; at = ahead, parity ^= 1) {
-    const int px = lane.pixels(g, at);
-    const int n = (int)min((long long)g.TP, a.P - at.pos);  // pixels of the tile
+    const int n = (int)min((long long)g.TP, a.P - at.pos), m = lane.skew(at);  // n: pixels of the tile
     ahead.next(g);
     W k_dy[NCH], k_h[NCH];
     copy_wait<1>();  // all but dh
-    if (SHIFT) __syncwarp();
+    uint4 mask;
+    if (SHIFT) mask = lane.mask(m, n);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int m = lane.skew(at, i);
-      k_dy[i] = lane.read(r_dy, i, m);
-      k_h[i] = lane.read(r_h, i, m);
+      k_dy[i] = lane.read(r_dy, i);
+      k_h[i] = lane.read(r_h, i);
+      if (SHIFT) k_dy[i] = k_dy[i] & mask, k_h[i] = k_h[i] & mask;
     }
-    if (SHIFT) __syncwarp();
     lane.fetch(g, ahead, dy, r_dy);
     lane.fetch(g, ahead, h, r_h);
     copy_commit();
@@ -127,34 +126,31 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
       s[1] = fma(mul(unpack<T, V>(k_dy[i]), fill<V>(wt[i])), vh, s[1]);
     }
     auto finish = [&](const float(&z)[2], float(&out)[2]) {
-      const float r = 1.0f / sqrtf(z[0] / (float)a.C + a.eps);
+      const float r = inverse_rms(z[0], a.inv_C, a.eps);
       out[0] = r;
-      out[1] = -(z[1] / (float)a.C * r) * r * r;
+      out[1] = -(z[1] * a.inv_C * r) * r * r;
     };
-    J.submit(s, parity, finish);
-    J.collect(rk, parity, finish);
+    J.submit(s, m, parity, finish);
+    J.collect(rk, m, parity, finish);
+    if (SHIFT)  // no statistics where there are no pixels
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (!lane.in(e, m, n)) rk[0].v[e] = rk[1].v[e] = 0.0f;
     copy_wait<1>();  // this tile's dh; the next dy and h may be on their way
-    if (SHIFT) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const F<V> vh = unpack<T, V>(k_h[i]);
-      F<V> rg = mul(unpack<T, V>(k_dy[i]), rk[0]);
+      const F<V> vh = unpack<T, V>(k_h[i]), rg = mul(unpack<T, V>(k_dy[i]), rk[0]);
       F<V> d = mul(vh, rk[1]);
-      if (dh) d = add(d, unpack<T, V>(lane.read(r_dh, i, lane.skew(at, i))));
+      if (dh) d = add(d, unpack<T, V>(lane.read(r_dh, i)));
       d = fma(rg, fill<V>(wt[i]), d);
-      lane.write(a.dx, at, i, packed<T, V>(d), px > 0, n);
-      if (SHIFT && px < V) {  // what lies past the row's end is another row's, or nothing
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (e < px) dw[i][0] = fmaf(rg.v[e], vh.v[e], dw[i][0]);
-      } else if (px > 0) {
+      lane.write(a.dx, at, m, i, packed<T, V>(d), n);
+      if (SHIFT || J.lx * V < n) {
         F<2> t{dw[i][0], dw[i][1]};
 #pragma unroll
         for (int e = 0; e < V; e += 2) t = fma(F<2>{rg.v[e], rg.v[e + 1]}, F<2>{vh.v[e], vh.v[e + 1]}, t);
         dw[i][0] = t.v[0], dw[i][1] = t.v[1];
       }
     }
-    if (SHIFT) __syncwarp();
     if (dh) lane.fetch(g, ahead, dh, r_dh);
     copy_commit();
   }
@@ -166,7 +162,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   for (int i = 0; i < NCH; ++i) {
     float z = dw[i][0] + dw[i][1];
     for (int m = g.LX / 2; m; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-    if (J.lx == 0 && i < nc) row[c0 + i] = z;
+    if (J.lx == 0 && i < nc) row[lane.channel(i)] = z;
   }
 }
 
@@ -202,7 +198,7 @@ int bwd_parts(int B, int C, long long P, int es) {
 template <typename T, bool SHIFT>
 int launch_bwd_tile(const NormBwdArgs& a, const Tiling& g, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  const size_t smem = Lane<T, V, 4, SHIFT>::words(g) * 16 * (a.dh ? 3 : 2) + 4 * Joiner<V, 2, 2>::floats(g);
+  const size_t smem = Lane<T, V, 4, SHIFT>::words(g) * 16 * (a.dh ? 3 : 2) + 4 * Joiner<V, 2, 2, SHIFT>::floats(g);
   return launch_clusters(norm_bwd_tile_kernel<T, SHIFT>, g, smem, st, "norm_bwd_tile_kernel", a, g);
 }
 
@@ -243,7 +239,7 @@ extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* wei
   const Buffer out[] = {{dx, n * e, "dx"}, {dweight, C * e, "dweight"}, {dweight ? workspace : nullptr, need, "workspace"}};
   const unsigned in_place[] = {1, 1, 0, 1};
   if ((rc = check_buffers(in, in_place, 4, out, 3))) return rc;
-  const NormBwdArgs a{dy, h, weight, dh, dx, dweight ? (float*)workspace : nullptr, eps, B, C, P};
+  const NormBwdArgs a{dy, h, weight, dh, dx, dweight ? (float*)workspace : nullptr, eps, 1.0f / (float)C, B, C, P};
   const cudaStream_t st = (cudaStream_t)stream;
   rc = P == 1 ? norm_bwd_by_rows(a, dtype, st) : DISCO_ERR_UNSUPPORTED;
   if (rc == DISCO_ERR_UNSUPPORTED) {

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
       for (int i = 0; i < NWD; ++i) P.write(a.h, o, i, packed<T, V>(v[i]));
     float sum[1] = {across(s)};
     P.reduce(sum, buf[0][parity], [](float p, float q) { return p + q; });
-    const F<V> r = fill<V>(1.0f / sqrtf(sum[0] / (float)a.C + a.eps));
+    const F<V> r = fill<V>(inverse_rms(sum[0], a.inv_C, a.eps));
 #pragma unroll
     for (int i = 0; i < NWD; ++i) v[i] = mul(mul(v[i], r), unpack<T, V>(wt[i]));
     if (a.y && on)
@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
     }
     float z[2] = {across(s), across(d)};
     P.reduce(z, buf[parity], [](float p, float q) { return p + q; });
-    const float r1 = 1.0f / sqrtf(z[0] / (float)a.C + a.eps);
-    const F<V> r = fill<V>(r1), k = fill<V>(-(z[1] / (float)a.C * r1) * r1 * r1);
+    const float r1 = inverse_rms(z[0], a.inv_C, a.eps);
+    const F<V> r = fill<V>(r1), k = fill<V>(-(z[1] * a.inv_C * r1) * r1 * r1);
     asm volatile("" ::: "memory");  // the second pass reads the ring again: the registers are dweight's
     if (on) {
 #pragma unroll

@@ -23,30 +23,30 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
   constexpr int V = 16 / (int)sizeof(T);
   using L = Lane<T, V, NCH, SHIFT>;
   using W = typename L::W;
-  using Join = Joiner<V, 1, 1>;
+  using Join = Joiner<V, 1, 1, SHIFT>;
   extern __shared__ __align__(16) char smem[];
   const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
   float* fsm = (float*)(smem + L::words(g) * 16 * (a.res ? 2 : 1));
   const Join J(g, fsm, rank);
-  const int NT = g.NT, TP = J.TP, first_c = (int)rank * g.cpc;
+  const int NT = g.NT, slots = J.slots, first_c = (int)rank * g.cpc;
   const L lane(g, a.B, a.C, a.P, J.lx, J.j, first_c, smem);
-  const int c0 = lane.c0, nc = lane.nc;
+  const int nc = lane.nc;
   const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
   W *rx = lane.slot, *rr = rx + L::words(g);
 
   float wt[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    wt[i] = i < nc && w ? to_f32(w[c0 + i]) : 1.0f;
+    wt[i] = i < nc && w ? to_f32(w[lane.channel(i)]) : 1.0f;
     if (i >= nc) {  // channels past the last: zeros, never copied over
       memset(rx + i * lane.stride, 0, 16);
       if (res) memset(rr + i * lane.stride, 0, 16);
     }
   }
-  float* gmax = fsm + Join::floats(g);                               // kRowsQ: [channel lane][TP]
-  float* ginv = gmax + (Q == kRowsQ ? J.rows * TP : 0);              // kRowsQ: [group of this CTA][TP]
-  uint32_t* gm = (uint32_t*)gmax;                                    // kAtomicQ: [2][group that touches this CTA][TP]
-  const int gm_half = ng_max * TP;
+  float* gmax = fsm + Join::floats(g);                      // kRowsQ: [channel lane][slots]
+  float* ginv = gmax + (Q == kRowsQ ? J.rows * slots : 0);  // kRowsQ: [group of this CTA][slots]
+  uint32_t* gm = (uint32_t*)gmax;                           // kAtomicQ: [2][group that touches this CTA][slots]
+  const int gm_half = ng_max * slots;
   if constexpr (Q == kAtomicQ)
     for (int k = threadIdx.x; k < 2 * gm_half; k += NT) gm[k] = 0u;
 
@@ -60,33 +60,29 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
   if (g.CL > 1) cluster_barrier();  // every CTA runs before another writes its shared memory
 
   for (int parity = 0; at.t < g.tiles; at = ahead, parity ^= 1) {
-    const bool on = lane.pixels(g, at) > 0;
-    const int n = (int)min((long long)g.TP, a.P - at.pos);  // pixels of the tile
+    const int n = (int)min((long long)g.TP, a.P - at.pos), m = lane.skew(at);  // n: pixels of the tile
     ahead.next(g);
     F<V> v[NCH], s[1] = {fill<V>(0.0f)}, r[1];
     copy_wait<0>();
-    if (SHIFT) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int m = lane.skew(at, i);
-      v[i] = unpack<T, V>(lane.read(rx, i, m));
-      if (res) v[i] = add(v[i], unpack<T, V>(lane.read(rr, i, m)));
+      v[i] = unpack<T, V>(lane.read(rx, i));
+      if (res) v[i] = add(v[i], unpack<T, V>(lane.read(rr, i)));
     }
-    if (SHIFT) __syncwarp();
     fetch();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) s[0] = fma(v[i], v[i], s[0]);
-    auto finish = [&](const float(&z)[1], float(&out)[1]) { out[0] = 1.0f / sqrtf(z[0] / (float)a.C + a.eps); };
-    J.submit(s, parity, finish);
+    auto finish = [&](const float(&z)[1], float(&out)[1]) { out[0] = inverse_rms(z[0], a.inv_C, a.eps); };
+    J.submit(s, m, parity, finish);
     if (a.h)
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) lane.write(a.h, at, i, packed<T, V>(v[i]), on, n);
-    J.collect(r, parity, finish);
+      for (int i = 0; i < NCH; ++i) lane.write(a.h, at, m, i, packed<T, V>(v[i]), n);
+    J.collect(r, m, parity, finish);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) v[i] = mul(mul(v[i], r[0]), fill<V>(wt[i]));
     if (a.y)
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) lane.write(a.y, at, i, packed<T, V>(v[i]), on, n);
+      for (int i = 0; i < NCH; ++i) lane.write(a.y, at, m, i, packed<T, V>(v[i]), n);
 
     if constexpr (Q == kRowsQ) {
       F<V> top = fill<V>(0.0f);
@@ -95,82 +91,66 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
         if (i < nc)
 #pragma unroll
           for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));  // a NaN does not count
-      store_row<V>(gmax + J.j * TP + J.lx * V, top);
+      J.put(gmax + J.j * slots, top, m);
       __syncthreads();
       const int g0 = first_c / a.G, lanes = a.NG == 1 ? J.rows : a.G / NCH;
-      for (int k = threadIdx.x; k < ng_max * TP; k += NT) {
-        const int gl = k / TP, px = k - gl * TP;
+      for (int k = threadIdx.x; k < ng_max * n; k += NT) {
+        const int gl = k / n, px = k - gl * n, to = J.slot(px);
         const int r0 = gl * lanes, r1 = min(r0 + lanes, J.rows);
-        float m = kAmaxFloor;
-        for (int z = r0; z < r1; ++z) m = fmaxf(m, gmax[z * TP + px]);
-        ginv[k] = kE4m3Max / m;
-        if (px < n && g0 + gl < a.NG)
-          a.scale[(at.b * a.NG + g0 + gl) * a.P + at.pos + px] = m / kE4m3Max;
+        float t = kAmaxFloor;
+        for (int z = r0; z < r1; ++z) t = fmaxf(t, gmax[z * slots + to]);
+        ginv[gl * slots + to] = kE4m3Max / t;
+        if (g0 + gl < a.NG) a.scale[(at.b * a.NG + g0 + gl) * a.P + at.pos + px] = t / kE4m3Max;
       }
       __syncthreads();
-      const F<V> inv = load_row<V>(ginv + min(J.j / lanes, ng_max - 1) * TP + J.lx * V);
+      const F<V> inv = J.get(ginv + min(J.j / lanes, ng_max - 1) * slots, m);
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) lane.write(a.q, at, i, packed_e4m3<V>(mul(v[i], inv)), on, n);
+      for (int i = 0; i < NCH; ++i) lane.write(a.q, at, m, i, packed_e4m3<V>(mul(v[i], inv)), n);
     }
 
     if constexpr (Q == kAtomicQ) {
       const int last_c = min(first_c + g.cpc, a.C) - 1;
       const int g0 = first_c / a.G, ng = last_c >= first_c ? last_c / a.G - g0 + 1 : 0;
-      uint32_t* m = gm + parity * gm_half;
-      if (nc > 0) {
-        int grp = c0 / a.G, left = (grp + 1) * a.G - c0;  // channels to the group's end
-        F<V> top = fill<V>(0.0f);
+      uint32_t* mx = gm + parity * gm_half;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
-          if (i < nc) {
+      for (int i = 0; i < NCH; ++i)
+        if (i < nc) {
+          uint32_t* to = mx + (lane.channel(i) / a.G - g0) * slots;
 #pragma unroll
-            for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));
-            if (--left == 0 || i == nc - 1) {
-#pragma unroll
-              for (int e = 0; e < V; ++e) atomicMax(m + (grp - g0) * TP + J.lx * V + e, __float_as_uint(top.v[e]));
-              top = fill<V>(0.0f);
-              ++grp;
-              left = a.G;
-            }
+          for (int e = 0; e < V; ++e) {
+            const int px = J.lx * V - m + e;  // a NaN does not count
+            if (lane.in(e, m, n)) atomicMax(to + J.slot(px), __float_as_uint(fmaxf(0.0f, fabsf(v[i].v[e]))));
           }
-      }
+        }
       if (g.CL > 1) cluster_barrier();
       else __syncthreads();
       // a group's maximum over the CTAs that hold its channels
-      auto maximum = [&](int grp, int px) {
+      auto maximum = [&](int grp, int slot) {
         uint32_t u = 0;
         const int k0 = grp * a.G / g.cpc, k1 = (min((grp + 1) * a.G, a.C) - 1) / g.cpc;
-        if (k0 == k1) u = m[(grp - g0) * TP + px];
+        if (k0 == k1) u = mx[(grp - g0) * slots + slot];
         else
           for (int k = k0; k <= k1; ++k)
-            u = max(u, peer_load(peer(m, k) + ((grp - k * g.cpc / a.G) * TP + px) * 4));
+            u = max(u, peer_load(peer(mx, k) + ((grp - k * g.cpc / a.G) * slots + slot) * 4));
         return fmaxf(__uint_as_float(u), kAmaxFloor);
       };
-      int grp = c0 / a.G - 1, left = 0;
-      F<V> inv = fill<V>(0.0f);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        if (i < nc) {
-          if (left == 0) {
-            ++grp;
-            left = i > 0 ? a.G : (grp + 1) * a.G - c0;
+        if (i < nc)
 #pragma unroll 1
-            for (int e = 0; e < V; ++e) {
-              const float u = kE4m3Max / maximum(grp, J.lx * V + e);
+          for (int e = 0; e < V; ++e) {
+            const float u = lane.in(e, m, n) ? kE4m3Max / maximum(lane.channel(i) / a.G, J.slot(J.lx * V - m + e)) : 0.0f;
 #pragma unroll
-              for (int k = 0; k < V; ++k) inv.v[k] = k == e ? u : inv.v[k];
-            }
+            for (int k = 0; k < V; ++k) v[i].v[k] *= k == e ? u : 1.0f;
           }
-          --left;
-        }
         if (SHIFT) __syncwarp();
-        lane.write(a.q, at, i, packed_e4m3<V>(mul(v[i], inv)), on, n);
+        lane.write(a.q, at, m, i, packed_e4m3<V>(v[i]), n);
       }
       // scales of the groups that begin in this CTA
-      for (int k = threadIdx.x; k < ng * TP; k += NT) {
-        const int gl = k / TP, px = k - gl * TP, grp = g0 + gl;
-        if (px < n && grp * a.G >= first_c)
-          a.scale[(at.b * a.NG + grp) * a.P + at.pos + px] = maximum(grp, px) / kE4m3Max;
+      for (int k = threadIdx.x; k < ng * n; k += NT) {
+        const int gl = k / n, px = k - gl * n, grp = g0 + gl;
+        if (grp * a.G >= first_c)
+          a.scale[(at.b * a.NG + grp) * a.P + at.pos + px] = maximum(grp, J.slot(px)) / kE4m3Max;
       }
       // the other half is read no more (every CTA is past the last tile's
       // reads at this tile's barriers): clear it for the next tile
@@ -184,10 +164,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
 template <int Q, typename T, int NCH, bool SHIFT>
 int launch_norm_tile(const NormArgs& a, const Tiling& g, int ng_max, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  const int TP = g.LX * V;
-  const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * (a.res ? 2 : 1);
-  const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * TP : Q == kAtomicQ ? 8 * (size_t)ng_max * TP : 0;
-  const size_t smem = ring + 4 * Joiner<V, 1, 1>::floats(g) + qb;
+  using Join = Joiner<V, 1, 1, SHIFT>;
+  const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * (a.res ? 2 : 1), slots = Join::slots_of(g);
+  const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * slots : Q == kAtomicQ ? 8 * ng_max * slots : 0;
+  const size_t smem = ring + 4 * Join::floats(g) + qb;
   if (smem > kMaxSmem) return DISCO_ERR_UNSUPPORTED;
   return launch_clusters(norm_tile_kernel<T, NCH, Q, SHIFT>, g, smem, st, "norm_tile_kernel", a, g, ng_max);
 }
