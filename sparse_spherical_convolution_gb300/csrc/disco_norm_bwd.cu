@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_tile_kernel(const NormBw
   using W = typename L::W;
   using Join = Joiner<V, 2, 2, SHIFT>;
   extern __shared__ __align__(16) char smem[];
-  let_next_begin();
+  if (a.part) let_next_begin();
   const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
   float* fsm = (float*)(smem + L::words(g) * 16 * (a.dh ? 3 : 2));
   const Join J(g, fsm, rank);

@@ -68,9 +68,9 @@ struct Place {
 #pragma unroll
     for (int i = 0; i < NWD; ++i)
       if (any(i) && DISCO_IN_BOUNDS(o + i * LANES * V >= 0)) {
-        // a last partial word ends with the row's elements where the tensor ends
-        const int bytes = !WHOLE && last && !whole(i) && at(i) >= 0 ? (C - at(i)) * (int)sizeof(T) : 16;
-        copy_async(to + i * NT, p + o + i * LANES * V, min(bytes, 16));
+        // the tensor's last word ends with its last row
+        const int bytes = !WHOLE && last ? min((C - at(i)) * (int)sizeof(T), 16) : 16;
+        copy_async(to + i * NT, p + o + i * LANES * V, bytes);
       }
   }
   // the elements of word i that are the row's; zeros in place of the others
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
   constexpr int V = 16 / (int)sizeof(T);
   using W = Raw<T, V>;
   extern __shared__ __align__(16) char smem[];
-  let_next_begin();
+  if (a.part) let_next_begin();
   __shared__ float buf[2][2][kThreads / 32];
   Place<T, NWD, WHOLE> P(g, a.C);
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *dh = (const T*)a.dh;
@@ -418,7 +418,10 @@ bool plan_rows(int B, int C, int es, bool forward, Rows* g) {
   const int lcm = per_cta / gcd(per_cta, g->period) * g->period;
   units = (units + lcm - 1) / lcm * lcm;
   g->units = (int)units;
-  g->grid = (int)(units / per_cta);
+  // CTAs up to the last unit that has a row
+  const long long span = (long long)g->period * g->U, turn = (B - 1) / span, rho = B - 1 - turn * span;
+  const long long used = turn * g->period + min((long long)g->period - 1, rho) + 1;
+  g->grid = (int)((min(units, used) + per_cta - 1) / per_cta);
   return true;
 }
 

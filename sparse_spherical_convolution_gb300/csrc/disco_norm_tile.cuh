@@ -43,12 +43,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
       if (res) memset(rr + i * lane.stride, 0, 16);
     }
   }
-  float* gmax = fsm + Join::floats(g);                      // kRowsQ: [channel lane][slots]
-  float* ginv = gmax + (Q == kRowsQ ? J.rows * slots : 0);  // kRowsQ: [group of this CTA][slots]
-  uint32_t* gm = (uint32_t*)gmax;                           // kAtomicQ: [2][group that touches this CTA][slots]
+  float* gmax = fsm + Join::floats(g);  // kRowsQ: [channel lane][slots]
+  float* ginv = gmax + (Q == kRowsQ ? J.rows : 2 * ng_max) * slots;  // [group of this CTA][slots]
+  uint32_t* gm = (uint32_t*)gmax;       // kAtomicQ: [2][group that touches this CTA][slots], the last tiles' in turn
   const int gm_half = ng_max * slots;
-  if constexpr (Q == kAtomicQ)
+  int grp[NCH];  // kAtomicQ: the groups of this thread's channels
+  if constexpr (Q == kAtomicQ) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) grp[i] = lane.channel(i) / a.G;
     for (int k = threadIdx.x; k < 2 * gm_half; k += NT) gm[k] = 0u;
+  }
 
   Cursor at(g, a.C, a.P, blockIdx.x / g.CL), ahead = at;
   auto fetch = [&]() {
@@ -109,48 +113,42 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
     }
 
     if constexpr (Q == kAtomicQ) {
-      const int last_c = min(first_c + g.cpc, a.C) - 1;
-      const int g0 = first_c / a.G, ng = last_c >= first_c ? last_c / a.G - g0 + 1 : 0;
+      const int last_c = min(first_c + g.cpc, a.C) - 1, g0 = first_c / a.G;
+      const int ng = last_c >= first_c ? last_c / a.G - g0 + 1 : 0;
       uint32_t* mx = gm + parity * gm_half;
+      F<V> top = fill<V>(0.0f);
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
         if (i < nc) {
-          uint32_t* to = mx + (lane.channel(i) / a.G - g0) * slots;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const int px = J.lx * V - m + e;  // a NaN does not count
-            if (lane.in(e, m, n)) atomicMax(to + J.slot(px), __float_as_uint(fmaxf(0.0f, fabsf(v[i].v[e]))));
+          for (int e = 0; e < V; ++e) top.v[e] = fmaxf(top.v[e], fabsf(v[i].v[e]));  // a NaN does not count
+          if (i == nc - 1 || grp[i] != grp[i + 1 < NCH ? i + 1 : i]) {
+            uint32_t* to = mx + (grp[i] - g0) * slots;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              if (lane.in(e, m, n)) atomicMax(to + J.slot(J.lx * V - m + e), __float_as_uint(top.v[e]));
+            top = fill<V>(0.0f);
           }
         }
       if (g.CL > 1) cluster_barrier();
       else __syncthreads();
-      // a group's maximum over the CTAs that hold its channels
-      auto maximum = [&](int grp, int slot) {
-        uint32_t u = 0;
-        const int k0 = grp * a.G / g.cpc, k1 = (min((grp + 1) * a.G, a.C) - 1) / g.cpc;
-        if (k0 == k1) u = mx[(grp - g0) * slots + slot];
+      for (int k = threadIdx.x; k < ng * n; k += NT) {
+        const int gl = k / n, px = k - gl * n, of = g0 + gl, to = J.slot(px);
+        uint32_t u = 0;  // the group's maximum over the CTAs that hold its channels
+        const int k0 = of * a.G / g.cpc, k1 = (min((of + 1) * a.G, a.C) - 1) / g.cpc;
+        if (k0 == k1) u = mx[gl * slots + to];
         else
-          for (int k = k0; k <= k1; ++k)
-            u = max(u, peer_load(peer(mx, k) + ((grp - k * g.cpc / a.G) * slots + slot) * 4));
-        return fmaxf(__uint_as_float(u), kAmaxFloor);
-      };
+          for (int z = k0; z <= k1; ++z) u = max(u, peer_load(peer(mx, z) + ((of - z * g.cpc / a.G) * slots + to) * 4));
+        const float t = fmaxf(__uint_as_float(u), kAmaxFloor);
+        ginv[gl * slots + to] = kE4m3Max / t;
+        if (of * a.G >= first_c) a.scale[(at.b * a.NG + of) * a.P + at.pos + px] = t / kE4m3Max;  // its first CTA
+      }
+      __syncthreads();
+      F<V> inv = fill<V>(0.0f);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        if (i < nc)
-#pragma unroll 1
-          for (int e = 0; e < V; ++e) {
-            const float u = lane.in(e, m, n) ? kE4m3Max / maximum(lane.channel(i) / a.G, J.slot(J.lx * V - m + e)) : 0.0f;
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[i].v[k] *= k == e ? u : 1.0f;
-          }
-        if (SHIFT) __syncwarp();
-        lane.write(a.q, at, m, i, packed_e4m3<V>(v[i]), n);
-      }
-      // scales of the groups that begin in this CTA
-      for (int k = threadIdx.x; k < ng * n; k += NT) {
-        const int gl = k / n, px = k - gl * n, grp = g0 + gl;
-        if (grp * a.G >= first_c)
-          a.scale[(at.b * a.NG + grp) * a.P + at.pos + px] = maximum(grp, J.slot(px)) / kE4m3Max;
+        if (i < nc && (i == 0 || grp[i] != grp[i - (i > 0)])) inv = J.get(ginv + (grp[i] - g0) * slots, m);
+        lane.write(a.q, at, m, i, packed_e4m3<V>(mul(v[i], inv)), n);
       }
       // the other half is read no more (every CTA is past the last tile's
       // reads at this tile's barriers): clear it for the next tile
@@ -166,7 +164,7 @@ int launch_norm_tile(const NormArgs& a, const Tiling& g, int ng_max, cudaStream_
   constexpr int V = 16 / (int)sizeof(T);
   using Join = Joiner<V, 1, 1, SHIFT>;
   const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * (a.res ? 2 : 1), slots = Join::slots_of(g);
-  const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * slots : Q == kAtomicQ ? 8 * ng_max * slots : 0;
+  const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * slots : Q == kAtomicQ ? 12 * ng_max * slots : 0;
   const size_t smem = ring + 4 * Join::floats(g) + qb;
   if (smem > kMaxSmem) return DISCO_ERR_UNSUPPORTED;
   return launch_clusters(norm_tile_kernel<T, NCH, Q, SHIFT>, g, smem, st, "norm_tile_kernel", a, g, ng_max);

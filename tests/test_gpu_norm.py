@@ -95,6 +95,14 @@ SHAPES = [
     (1, 513, 72), (1, 1024, 40), (1, 1025, 33), (1, 2100, 16), (1, 5000, 9),
 ]
 
+# more than one tile or row to a thread: tiles past the resident clusters, rows
+# past the resident teams; pixel counts 2, 4 and odd modulo 8 with the channels
+# of a pixel in one CTA and over a cluster; rows shorter than a vector
+LONG = [
+    (4, 8, 60000), (4, 8, 60001), (3, 24, 30002), (2, 40, 250), (3, 24, 12), (1, 520, 333), (1, 1100, 58), (2, 300, 1201),
+    (5000, 3, 1), (20011, 7, 1), (3000, 257, 1), (2000, 1000, 1), (1300, 2048, 1), (300, 9000, 1),
+]
+
 
 @pytest.mark.parametrize("dtype", [F32, BF, F16], ids=["f32", "bf16", "f16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -107,6 +115,15 @@ def test_norm_matches_64_bits(lib, shape, dtype):
     for group in {0, min(C, 32), max(1, C // 3), 1}:
         _check(_run(lib, x, r, w, y=group == 0, q=True, group=group), x, r, w, group)
     _check(_run(lib, x, None, w, y=True, q=True, group=C + 5), x, None, w, C + 5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_norm_of_many_tiles(lib, shape, dtype):
+    B, C, P = shape
+    x, r, w = _randn(shape, dtype, 31), _randn(shape, dtype, 32, 3.0), _randn((C,), dtype, 33)
+    for group in (0, min(C, 32), max(1, C // 3)):
+        _check(_run(lib, x, r, w, y=group == 0, q=True, group=group), x, r, w, group)
 
 
 def _run_bwd(lib, dy, h, weight, dh, dweight=True):
@@ -142,6 +159,27 @@ def test_gradient_matches_64_bits(lib, shape, dtype):
             assert_close(dw, rw, (B * P + C / 2 + 8) * U32 * Sw + UNIT[dtype] * rw.abs() * 1.01 + TINY[dtype], "dweight")
             dx2, dw2 = _run_bwd(lib, dy, h, weight, skip, True)
             assert torch.equal(dx, dx2) and torch.equal(dw, dw2)   # fixed order of summation
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_gradient_of_many_tiles(lib, shape, dtype):
+    """The sum over pixels: a thread adds the pixels of its tiles, 16 or 32 lanes
+    and then the CTAs join pairwise, so B P terms are off by far less than B P u;
+    the bound stays B P u."""
+    B, C, P = shape
+    dy, h, dh, w = _randn(shape, dtype, 34), _randn(shape, dtype, 35, 2.0), _randn(shape, dtype, 36), _randn((C,), dtype, 37)
+    dx, dw = _run_bwd(lib, dy, h, w, dh)
+    rx, S, rw, Sw = norm_bwd64(dy, h, w, dh, EPS)
+    assert_close(dx, rx, (2 * C + 16) * U32 * S + UNIT[dtype] * rx.abs() * 1.01 + TINY[dtype], "dx")
+    assert_close(dw, rw, (B * P + C / 2 + 8) * U32 * Sw + UNIT[dtype] * rw.abs() * 1.01 + TINY[dtype], "dweight")
+    # nothing but the tile's own pixels enters: a NaN stays in its pixel and out of other channels' sums of later calls
+    h2 = h.clone()
+    h2[0, 0, 0] = float("nan")
+    dx2, _ = _run_bwd(lib, dy, h2, w, dh)
+    clean = torch.ones((B, C, P), dtype=torch.bool)
+    clean[0, :, 0] = False
+    assert torch.equal(dx2.cpu()[clean], dx.cpu()[clean]) and bool(torch.isnan(dx2[0, :, 0]).all())
 
 
 @pytest.mark.parametrize("shape", [(2, 6, 1), (1, 40, 12), (3, 9, 35)], ids=lambda s: "x".join(map(str, s)))
@@ -232,7 +270,8 @@ def test_in_place(lib, shape):
 
 @pytest.mark.parametrize("dtype", [F32, BF, F16], ids=["f32", "bf16", "f16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1), (5, 100, 1), (3, 2051, 1), (2, 33, 7), (1, 64, 4096), (3, 20, 1001),
-                                   (2, 48, 130)], ids=lambda s: "x".join(map(str, s)))
+                                   (2, 48, 130), (1, 70, 30004), (2, 129, 5001), (4000, 33, 1)],
+                         ids=lambda s: "x".join(map(str, s)))
 def test_dequant(lib, shape, dtype):
     B, C, P = shape
     q = _randn(shape, F32, 22, 100.0).clamp(-448, 448).to(torch.float8_e4m3fn)
