@@ -187,25 +187,41 @@ def _check(status: int):
         raise DiscoError(status, load_library().disco_last_error().decode())
 
 
-def _stream(stream):
+_torch = None          # torch, its current-device and raw-stream calls and the type codes, from the first use on
+_device = _raw_stream = None
+_CODES = {}
+
+
+def _runtime():
+    """Imports torch (the module itself loads without it)."""
+    global _torch, _device, _raw_stream
     import torch
+    _CODES.update({torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16})
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                   (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    _torch = torch
+    return torch
+
+
+def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        if _torch is None:
+            _runtime()
+        return _raw_stream(_torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def dtype_code(dtype) -> int:
     """The library's code (DISCO_F32, DISCO_BF16, DISCO_F16) of a torch dtype."""
-    import torch
-    if dtype == torch.float32:
-        return DISCO_F32
-    if dtype == torch.bfloat16:
-        return DISCO_BF16
-    if dtype == torch.float16:
-        return DISCO_F16
-    raise DiscoError(-2, f"unsupported dtype {dtype}")
+    if _torch is None:
+        _runtime()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise DiscoError(-2, f"unsupported dtype {dtype}")
+    return code
 
 
 def _dtype(t) -> int:
@@ -437,29 +453,38 @@ def _groups(C: int, group: int) -> int:
 
 def _on(t, name: str) -> int:
     """The current CUDA device, which ``t`` has to be on."""
-    import torch
     if t is None or not t.is_cuda:
         _dev(t, name, 0)
-    return torch.cuda.current_device()
+    if _torch is None:
+        _runtime()
+    return _device()
 
 
 def _in(t, name: str, numel: int, dtype, device: int):
     """Address of a device tensor after _dev's checks, None for None."""
     if t is None:
         return None
-    if t.get_device() != device or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+    if t.get_device() != device or t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         return _dev(t, name, numel, dtype)
     return t.data_ptr()
 
 
 def _q8(t, numel: int, device: int):
     """Address of an 8-bit tensor: float8_e4m3fn, or its bytes as uint8."""
-    import torch
     if t is None:
         return None
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t.dtype not in (_torch.float8_e4m3fn, _torch.uint8):
         raise DiscoError(-1, f"q has dtype {t.dtype}, the call needs float8_e4m3fn or uint8")
     return _in(t, "q", numel, t.dtype, device)
+
+
+def _bytes(t, name: str, device: int):
+    """(address, bytes) of an optional device workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        return _ws(t, name)
+    return t.data_ptr(), t.nbytes
 
 
 def disco_rms_norm(x, residual, weight, eps: float, h, y, B: int, C: int, P: int, q=None, scale=None,
@@ -467,14 +492,13 @@ def disco_rms_norm(x, residual, weight, eps: float, h, y, B: int, C: int, P: int
     """h = x + residual, its root-mean-square norm over the C channels times
     weight in y, and y in 8 bits with scales in q and scale; see
     include/disco.h.  residual, weight, h, y, and q with scale may be None."""
-    import torch
     n, dev = B * C * P, _on(x, "x")
     dt = x.dtype
-    code = dtype_code(dt)
     _check((_lib or load_library()).disco_rms_norm(
         _in(x, "x", n, dt, dev), _in(residual, "residual", n, dt, dev), _in(weight, "weight", C, dt, dev), eps,
         _in(h, "h", n, dt, dev), _in(y, "y", n, dt, dev), _q8(q, n, dev),
-        _in(scale, "scale", B * _groups(C, group) * P, torch.float32, dev), group, B, C, P, code, _stream(stream)))
+        None if scale is None else _in(scale, "scale", B * _groups(C, group) * P, _torch.float32, dev), group, B, C, P,
+        dtype_code(dt), _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_rms_norm_bwd_workspace_bytes(B: int, C: int, P: int, dtype=DISCO_BF16) -> int:
@@ -488,19 +512,20 @@ def disco_rms_norm_bwd(dy, h, weight, dh, eps: float, dx, dweight, B: int, C: in
     n, dev = B * C * P, _on(dy, "dy")
     dt = dy.dtype
     code = dtype_code(dt)
-    wsp, wsn = _ws(workspace)
+    wp, wn = _bytes(workspace, "workspace", dev)
     _check((_lib or load_library()).disco_rms_norm_bwd(
         _in(dy, "dy", n, dt, dev), _in(h, "h", n, dt, dev), _in(weight, "weight", C, dt, dev), _in(dh, "dh", n, dt, dev),
-        eps, _in(dx, "dx", n, dt, dev), _in(dweight, "dweight", C, dt, dev), B, C, P, code, wsp, wsn, _stream(stream)))
+        eps, _in(dx, "dx", n, dt, dev), _in(dweight, "dweight", C, dt, dev), B, C, P, code, wp, wn,
+        _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_dequant_e4m3(q, scale, x, B: int, C: int, P: int, group: int = 0, stream=None) -> None:
     """x = q * scale, the activation that disco_rms_norm's q and scale stand for."""
-    import torch
     n, dev = B * C * P, _on(q, "q")
     _check((_lib or load_library()).disco_dequant_e4m3(
-        _q8(q, n, dev), _in(scale, "scale", B * _groups(C, group) * P, torch.float32, dev),
-        None if x is None else _in(x, "x", n, x.dtype, dev), group, B, C, P, -1 if x is None else _dtype(x), _stream(stream)))
+        _q8(q, n, dev), _in(scale, "scale", B * _groups(C, group) * P, _torch.float32, dev),
+        None if x is None else _in(x, "x", n, x.dtype, dev), group, B, C, P, -1 if x is None else dtype_code(x.dtype),
+        _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_grad_plan(grads, outs=None):
@@ -537,27 +562,29 @@ def disco_grad_workspace_bytes(grads: disco_grads) -> int:
 
 def disco_grad_norm(grads: disco_grads, norm, workspace, grad_scale: float = 1.0, stream=None) -> None:
     """The Euclidean norm over all gradients, times grad_scale, to ``norm`` (one fp32)."""
-    import torch
-    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
-    wp, wn = _ws(workspace)
-    _check((_lib or load_library()).disco_grad_norm(ctypes.byref(grads), grad_scale, np_, wp, wn, _stream(stream)))
+    dev = _on(norm, "norm")
+    np_ = _in(norm, "norm", 1, _torch.float32, dev)
+    wp, wn = _bytes(workspace, "workspace", dev)
+    _check((_lib or load_library()).disco_grad_norm(grads, grad_scale, np_, wp, wn,
+                                                    _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_grad_clip(grads: disco_grads, max_norm: float, norm, grad_scale: float = 1.0, stream=None) -> None:
     """Every gradient scaled by grad_scale and down to ``max_norm`` given ``norm``, to its out."""
-    import torch
-    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
-    _check((_lib or load_library()).disco_grad_clip(ctypes.byref(grads), grad_scale, max_norm, np_, _stream(stream)))
+    dev = _on(norm, "norm")
+    np_ = _in(norm, "norm", 1, _torch.float32, dev)
+    _check((_lib or load_library()).disco_grad_clip(grads, grad_scale, max_norm, np_,
+                                                    _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_grad_norm_clip(grads: disco_grads, max_norm: float, norm, workspace, grad_scale: float = 1.0,
                          stream=None) -> None:
     """disco_grad_norm and disco_grad_clip in one call."""
-    import torch
-    np_ = _in(norm, "norm", 1, torch.float32, _on(norm, "norm"))
-    wp, wn = _ws(workspace)
-    _check((_lib or load_library()).disco_grad_norm_clip(ctypes.byref(grads), grad_scale, max_norm, np_, wp, wn,
-                                               _stream(stream)))
+    dev = _on(norm, "norm")
+    np_ = _in(norm, "norm", 1, _torch.float32, dev)
+    wp, wn = _bytes(workspace, "workspace", dev)
+    _check((_lib or load_library()).disco_grad_norm_clip(grads, grad_scale, max_norm, np_, wp, wn,
+                                                         _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_device_status(clear: bool = True) -> int:
