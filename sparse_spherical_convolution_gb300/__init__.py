@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build_mod
 
@@ -536,21 +537,21 @@ def disco_grad_plan(grads, outs=None):
     outs = [None] * len(grads) if outs is None else list(outs)
     if len(outs) != len(grads):
         raise DiscoError(-1, f"{len(grads)} gradients and {len(outs)} outs")
-    arr = (disco_grad_tensor * len(grads))()
+    fields, dev = [], None
     for i, (g, o) in enumerate(zip(grads, outs)):
-        e = arr[i]
         if g is None:
             raise DiscoError(-1, f"gradient {i} is None")
-        n = g.numel()
+        n, gp, op = g.numel(), None, None
         if n:  # a tensor without elements has no memory to check
-            e.grad = _dev(g, f"gradient {i}", n)
+            if dev is None:
+                dev = _on(g, f"gradient {i}")
+            gp = _in(g, "a gradient", n, g.dtype, dev)
             if o is not None:
-                e.out = _dev(o, f"out of gradient {i}", n)
-        e.n, e.dtype = n, _dtype(g)
-        if o is not None:
-            if o.numel() != n:
-                raise DiscoError(-1, f"out of gradient {i} has {o.numel()} elements, the gradient {n}")
-            e.out_dtype = _dtype(o)
+                op = _in(o, "an out", n, o.dtype, dev)
+        elif o is not None and o.numel():
+            raise DiscoError(-1, f"out of gradient {i} has {o.numel()} elements, the gradient 0")
+        fields += (gp or 0, op or 0, n, dtype_code(g.dtype), 0 if o is None else dtype_code(o.dtype))
+    arr = (disco_grad_tensor * len(grads)).from_buffer_copy(struct.pack("QQqii" * len(grads), *fields))
     grads_c = disco_grads()
     _check(load_library().disco_grad_plan(arr, len(grads), ctypes.byref(grads_c)))
     return grads_c, arr

@@ -1,9 +1,15 @@
 // disco_norm.cu -- channel RMS norm with the residual's addition and an
-// 8-bit copy (disco_rms_norm), on activations [B, C, P].
+// 8-bit copy (disco_rms_norm), on activations [B, C, P]: checks, the choice of a
+// kernel, and the general one.
 //
-// The general kernels below take every shape: 32 pixels per CTA, the channels
-// dealt to 8 warps, statistics joined in shared memory, the inputs read again
-// for each further pass.
+//   h = x + residual,  y = weight h / sqrt(mean_c h^2 + eps),
+//   q = e4m3(y 448 / m), scale = m / 448, m the largest |y| of a group of channels
+//
+// P = 1: rows of features (disco_norm_rows.cu).  Else tiles of pixels
+// (disco_norm_tile.cuh).  What neither takes (rows past 32,768 16-bit or 16,384
+// fp32 features, pixels whose channels fit no cluster, group maxima that fit no
+// shared memory) runs the general kernel below, which takes every shape and
+// reads the inputs again for each further pass.  It is bound by those reads: [1,512,360x720] bf16 with a residual takes it 468 us, the tiles 174.
 
 #include "disco_norm.cuh"
 
@@ -19,27 +25,16 @@ using namespace norm;
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
-// as warps_sum, the maximum
-__device__ __forceinline__ float warps_max(float v, float (*buf)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  buf[warp][lane] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kGenWarps; ++i) s = fmaxf(s, buf[i][lane]);
-  return s;
-}
-
-template <typename T>
+template <typename T, bool ROW>
 __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs a, const long long tiles) {
+  using D = Dealt<ROW>;
   __shared__ float buf[kGenWarps][32];
   const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
   T *h = (T*)a.h, *y = (T*)a.y;
   uint8_t* q = (uint8_t*)a.q;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long tpb = (a.P + 31) / 32;
+  const long long tpb = (a.P + D::PX - 1) / D::PX;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
+    const long long b = t / tpb, p = (t - b * tpb) * D::PX + D::pixel();
     const bool live = p < a.P;
     const long long base = b * a.C * a.P + p;
     auto value = [&](int c) {
@@ -49,27 +44,28 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs
     };
     float s = 0.0f;
     if (live)
-      for (int c = warp; c < a.C; c += kGenWarps) {
+      for (int c = D::first(); c < a.C; c += D::STEP) {
         const float v = value(c);
         s = fmaf(v, v, s);
       }
-    const float r = 1.0f / sqrtf(warps_sum(s, buf) / (float)a.C + a.eps);
+    s = D::join(s, buf, [](float u, float v) { return u + v; });
+    const float r = 1.0f / sqrtf(s / (float)a.C + a.eps);
     for (int g = 0; g < a.NG; ++g) {
       const int c0 = g * a.G, c1 = min(a.C, c0 + a.G);
       float inv = 0.0f;
       if (q) {
         float m = 0.0f;
         if (live)
-          for (int c = c0 + warp; c < c1; c += kGenWarps) {
+          for (int c = c0 + D::first(); c < c1; c += D::STEP) {
             const float v = value(c) * r * (w ? to_f32(w[c]) : 1.0f);
-            m = fmaxf(m, fabsf(v));
+            m = fmaxf(m, fabsf(v));  // a NaN does not count
           }
-        m = fmaxf(warps_max(m, buf), kAmaxFloor);
+        m = fmaxf(D::join(m, buf, [](float u, float v) { return fmaxf(u, v); }), kAmaxFloor);
         inv = kE4m3Max / m;
-        if (live && warp == 0) a.scale[(b * a.NG + g) * a.P + p] = m / kE4m3Max;
+        if (live && D::first() == 0) a.scale[(b * a.NG + g) * a.P + p] = m / kE4m3Max;
       }
       if (live)
-        for (int c = c0 + warp; c < c1; c += kGenWarps) {
+        for (int c = c0 + D::first(); c < c1; c += D::STEP) {
           const long long i = base + c * a.P;
           const float v = value(c), n = v * r * (w ? to_f32(w[c]) : 1.0f);
           if (h) h[i] = from_f32<T>(v);
@@ -79,7 +75,6 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs
     }
   }
 }
-
 
 }  // namespace
 
@@ -208,7 +203,9 @@ extern "C" int disco_rms_norm(const void* x, const void* residual, const void* w
   if (rc != DISCO_ERR_UNSUPPORTED) return rc;
   const long long tiles = (long long)B * ((P + 31) / 32);
   const int grid = (int)min(tiles, (long long)kSMs * 8);
-#define CALL(T) norm_any_kernel<T><<<grid, kGenWarps * 32, 0, st>>>(a, tiles)
+#define CALL(T)                                                                     \
+  if (P == 1) norm_any_kernel<T, true><<<grid, kGenWarps * 32, 0, st>>>(a, tiles);  \
+  else norm_any_kernel<T, false><<<grid, kGenWarps * 32, 0, st>>>(a, tiles)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return check_launch("norm_any_kernel");

@@ -551,20 +551,32 @@ struct Joiner {
   }
 };
 
-// ---- general kernels: 32 pixels per CTA, the channels dealt to 8 warps ------
+// ---- general kernels: any shape ----------------------------------------------
+// A CTA of 8 warps takes 32 pixels, one to a lane, and deals the channels to its
+// warps; ROW (P = 1): one row, the channels dealt to its 256 threads.
 
 constexpr int kGenWarps = 8;
 
-// sum over the 8 warps of one value per lane (pixel)
-__device__ __forceinline__ float warps_sum(float v, float (*buf)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  buf[warp][lane] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kGenWarps; ++i) s += buf[i][lane];
-  return s;
-}
+template <bool ROW>
+struct Dealt {
+  static constexpr int PX = ROW ? 1 : 32, STEP = ROW ? kGenWarps * 32 : kGenWarps;  // pixels of a tile; channel step
+  static __device__ __forceinline__ int pixel() { return ROW ? 0 : threadIdx.x & 31; }
+  static __device__ __forceinline__ int first() { return ROW ? threadIdx.x : threadIdx.x / 32; }
+  // over the threads of a pixel
+  template <typename Op>
+  static __device__ __forceinline__ float join(float v, float (*buf)[32], Op op) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (ROW)
+      for (int m = 16; m; m >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, m));
+    __syncthreads();
+    buf[warp][lane] = v;
+    __syncthreads();
+    v = buf[0][lane];
+    for (int i = 1; i < kGenWarps; ++i) v = op(v, buf[i][lane]);
+    return v;
+  }
+};
+
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

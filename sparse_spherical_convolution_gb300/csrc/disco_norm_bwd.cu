@@ -4,7 +4,15 @@
 //   dx = r (g - n mean_c(g n)) + dh = (r g) - h k + dh,  k = r^3 mean_c(g h)
 //   dweight[c] = sum over pixels of dy h r
 // One pass over dy, h and dh; dweight leaves as one row of fp32 partial sums
-// for each cluster of CTAs, summed in a fixed order by a second kernel.
+// for each cluster of CTAs, summed in a fixed order by a second kernel that may
+// start while the first ends.
+//
+// Measured (both kernels, GB300): [1,512,360x720] bf16 with dh 196 us, 5.4 TB/s
+// (80 % of the copy rate); [2,128,361x720] 87 us, 6.1 TB/s; [20,64,65344] 102 us,
+// the same with odd rows 149 us.  HBM bounds up to 256 channels.  At 512 one CTA
+// holds rows of 64 bytes, or a pair rows of 128 bytes and a cluster barrier a tile:
+// 198 and 228 us.  Odd rows are bound by instructions (two sums and two factors a
+// pixel to realign, 16 shared-memory accesses each way).
 
 #include "disco_norm.cuh"
 
@@ -18,34 +26,35 @@ using namespace norm;
 
 constexpr int kGenParts = 304;  // rows of partial sums of the general kernel: its CTAs
 
-// Any shape: 32 pixels per CTA, the channels dealt to 8 warps, the inputs read
-// again for the second pass.
-template <typename T>
+// Any shape; the inputs are read again for the second pass.  A channel's sum over
+// pixels stands in this CTA's row of partial sums.
+template <typename T, bool ROW>
 __global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const NormBwdArgs a, const long long tiles) {
+  using D = Dealt<ROW>;
   __shared__ float buf[kGenWarps][32];
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *w = (const T*)a.w, *dh = (const T*)a.dh;
   T* dx = (T*)a.dx;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long tpb = (a.P + 31) / 32;
+  const long long tpb = (a.P + D::PX - 1) / D::PX;
   float* part = a.part ? a.part + (long long)blockIdx.x * a.C : nullptr;
-  if (part)
-    for (int c = warp; c < a.C; c += kGenWarps)
-      if (lane == 0) part[c] = 0.0f;
+  const bool owner = D::pixel() == 0;  // of its channels' sums
+  if (part && owner)
+    for (int c = D::first(); c < a.C; c += D::STEP) part[c] = 0.0f;
+  auto plus = [](float u, float v) { return u + v; };
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const long long b = t / tpb, p = (t - b * tpb) * 32 + lane;
+    const long long b = t / tpb, p = (t - b * tpb) * D::PX + D::pixel();
     const bool live = p < a.P;
     const long long base = b * a.C * a.P + p;
     float s = 0.0f, d = 0.0f;
     if (live)
-      for (int c = warp; c < a.C; c += kGenWarps) {
+      for (int c = D::first(); c < a.C; c += D::STEP) {
         const long long i = base + c * a.P;
         const float v = to_f32(h[i]);
         s = fmaf(v, v, s);
         d = fmaf(to_f32(dy[i]) * (w ? to_f32(w[c]) : 1.0f), v, d);
       }
-    const float r = 1.0f / sqrtf(warps_sum(s, buf) / (float)a.C + a.eps);
-    const float k = warps_sum(d, buf) * r / (float)a.C;  // mean_c(g n)
-    for (int c = warp; c < a.C; c += kGenWarps) {
+    const float r = 1.0f / sqrtf(D::join(s, buf, plus) / (float)a.C + a.eps);
+    const float k = D::join(d, buf, plus) * r / (float)a.C;  // mean_c(g n)
+    for (int c = D::first(); c < a.C; c += D::STEP) {
       const long long i = base + c * a.P;
       float u = 0.0f;
       if (live) {
@@ -56,8 +65,9 @@ __global__ void __launch_bounds__(kGenWarps * 32) norm_bwd_any_kernel(const Norm
         u = g * n;
       }
       if (part) {
-        for (int m = 16; m; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
-        if (lane == 0) part[c] += u;
+        if (!ROW)
+          for (int m = 16; m; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
+        if (owner) part[c] += u;
       }
     }
   }
@@ -208,7 +218,10 @@ int bwd_main(const NormBwdArgs& a, cudaStream_t st) {
   const int es = (int)sizeof(T);
   if (a.P > 1 && plan_tiles(a.B, a.C, a.P, es, false, &g))
     return g.shifted ? launch_bwd_tile<T, true>(a, g, st) : launch_bwd_tile<T, false>(a, g, st);
-  norm_bwd_any_kernel<T><<<bwd_parts(a.B, a.C, a.P, es), kGenWarps * 32, 0, st>>>(a, (long long)a.B * ((a.P + 31) / 32));
+  const int grid = bwd_parts(a.B, a.C, a.P, es);
+  const long long tiles = (long long)a.B * ((a.P + 31) / 32);
+  if (a.P == 1) norm_bwd_any_kernel<T, true><<<grid, kGenWarps * 32, 0, st>>>(a, tiles);
+  else norm_bwd_any_kernel<T, false><<<grid, kGenWarps * 32, 0, st>>>(a, tiles);
   return check_launch("norm_bwd_any_kernel");
 }
 

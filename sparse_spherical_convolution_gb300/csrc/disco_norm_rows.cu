@@ -12,6 +12,14 @@
 // warp, or a team of several warps) only takes rows of one residue: a thread's
 // words hold the same features in all its rows, so the gain and the sums of
 // dweight stay in registers.  The first and last word of a row are partial.
+//
+// Measured (kernels, GB300): [16384,2048] bf16, residual, h, q and scales in groups
+// of 128: 41 us, 5.7 TB/s (83 % of the copy rate, DRAM 56 % busy, issue 53 %: the
+// 8-bit form is bound by instructions, without it 8 bytes an element run at 5.7
+// TB/s too); gradient 42 us and the sum of dweight 5, 4.3 TB/s (issue 50 %, 16
+// warps to an SM, since dweight takes 32 registers of a thread); 2560 rows of
+// 15507 features 55 us, 5.7 TB/s.  16 rows of 512: 5 us, the latency of a launch
+// and one load.
 
 #include "disco_norm.cuh"
 

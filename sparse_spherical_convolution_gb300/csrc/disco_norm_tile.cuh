@@ -1,11 +1,23 @@
 // disco_norm_tile.cuh -- the channel norm by tiles (disco_norm.cuh): one pass
-// over the data, bound by HBM.  Instantiated without the 8-bit copy in
-// disco_norm_tile.cu, with it in disco_norm_q.cu.
+// over the data.  Instantiated without the 8-bit copy in disco_norm_tile.cu, with
+// it in disco_norm_q.cu and disco_norm_q_any.cu.
 //
-// Every input is read once and held: a thread's V x NCH sums x + residual
-// stay in fp32 registers between the statistics and the outputs, so y is
-// computed from the unrounded h, while its shared memory already takes in the
-// next tile (cp.async).
+// Bound by HBM: x and residual read once, h, y, q and scales written once.  A
+// thread's V x NCH sums x + residual stay in fp32 registers between the
+// statistics and the outputs, so y and q are computed from the unrounded h, while
+// its shared memory already takes in the next tile (cp.async).  Without that
+// prefetch, at the same occupancy, [2,128,361x720] took 114 us, with it 88.
+//
+// Measured (kernel, GB300; the copy rate of this card is 6.78 TB/s):
+//   [1,512,360x720] bf16, residual, h and y         170 us  6.2 TB/s, DRAM 75 % busy
+//   [2,128,361x720] bf16, the same and q, groups 32  99 us  6.2 TB/s, DRAM 71 %
+//   [20,64,65343] bf16 (odd rows), residual         113 us  5.9 TB/s (as for 65344)
+//   [3,80,181x361] fp16, no residual                 23 us  2.7 TB/s: it lies in L2,
+//     and with 11 tiles to a CTA the latency of a tile's joins shows; 80 channels
+//     fill 5 of 6 blocks of 16 where rows are odd
+// 512 channels of 518 KB rows take a pair of CTAs with 256-byte row pieces: 128-byte
+// pieces in one CTA took 186 to 204 us (each piece lies in another 2 MB page).
+
 #pragma once
 
 #include "disco_norm.cuh"

@@ -100,7 +100,7 @@ SHAPES = [
 # of a pixel in one CTA and over a cluster; rows shorter than a vector
 LONG = [
     (4, 8, 60000), (4, 8, 60001), (3, 24, 30002), (2, 40, 250), (3, 24, 12), (1, 520, 333), (1, 1100, 58), (2, 300, 1201),
-    (5000, 3, 1), (20011, 7, 1), (3000, 257, 1), (2000, 1000, 1), (1300, 2048, 1), (300, 9000, 1),
+    (5000, 3, 1), (20011, 7, 1), (3000, 257, 1), (2000, 1000, 1), (1300, 2048, 1), (300, 9000, 1), (40, 33000, 1),
 ]
 
 
