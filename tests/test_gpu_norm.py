@@ -100,7 +100,7 @@ SHAPES = [
 # of a pixel in one CTA and over a cluster; rows shorter than a vector
 LONG = [
     (4, 8, 60000), (4, 8, 60001), (3, 24, 30002), (2, 40, 250), (3, 24, 12), (1, 520, 333), (1, 1100, 58), (2, 300, 1201),
-    (5000, 3, 1), (20011, 7, 1), (3000, 257, 1), (2000, 1000, 1), (1300, 2048, 1), (300, 9000, 1), (40, 33000, 1),
+    (5000, 3, 1), (20011, 7, 1), (3000, 257, 1), (2000, 1000, 1), (1300, 2048, 1), (300, 9000, 1), (40, 33000, 1), (1, 40000, 3),
 ]
 
 
@@ -321,6 +321,33 @@ def test_streams(lib):
     torch.cuda.synchronize()
     for y, dx, dw, *_ in res:
         assert torch.equal(y, want) and torch.equal(dx, dxw) and torch.equal(dw, dww)
+
+
+@pytest.mark.parametrize("shape", [(2, 48, 4096), (40, 1000, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_graph_capture(lib, shape):
+    """The calls can be captured; a replay sees the inputs of its own time."""
+    B, C, P = shape
+    x, r, w = _randn(shape, BF, 41).cuda(), _randn(shape, BF, 42).cuda(), _randn((C,), BF, 43).cuda()
+    h, y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(lib.disco_rms_norm_bwd_workspace_bytes(*shape), dtype=torch.uint8, device="cuda")
+
+    def calls():
+        lib.disco_rms_norm(x, r, w, EPS, h, y, *shape)
+        lib.disco_rms_norm_bwd(y, h, w, r, EPS, dx, dw, *shape, ws)
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    x.mul_(2)
+    g.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (h, y, dx, dw)]
+    calls()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (h, y, dx, dw)))
+    _check({"h": h, "y": y}, x.cpu(), r.cpu(), w.cpu(), 0)
 
 
 def test_offsets_past_32_bits(lib):
