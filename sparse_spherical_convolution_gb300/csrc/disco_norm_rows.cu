@@ -16,9 +16,9 @@
 // Measured (kernels, GB300): [16384,2048] bf16, residual, h, q and scales in groups
 // of 128: 41 us, 5.7 TB/s (83 % of the copy rate, DRAM 56 % busy, issue 53 %: the
 // 8-bit form is bound by instructions, without it 8 bytes an element run at 5.7
-// TB/s too); gradient 42 us and the sum of dweight 5, 4.3 TB/s (issue 50 %, 16
-// warps to an SM, since dweight takes 32 registers of a thread); 2560 rows of
-// 15507 features 55 us, 5.7 TB/s.  16 rows of 512: 5 us, the latency of a launch
+// TB/s too); gradient and the sum of dweight 45 us, 4.4 TB/s (issue 50 %, 16 warps
+// to an SM: dweight's sums, and dy and h between their two uses, take the
+// registers); 2560 rows of 15507 features 55 us, 5.7 TB/s.  16 rows of 512: 5 us, the latency of a launch
 // and one load.
 
 #include "disco_norm.cuh"
@@ -143,7 +143,9 @@ struct Place {
 // it holds one in registers; the gradient reads its row twice from the ring, so
 // one of its kDepth is the current row (kDepth = 1: nothing ahead, the row is too long).
 constexpr int ahead_of(int NWD) { return NWD >= 4 ? 1 : 4 / NWD; }
-constexpr int depth_of(int NWD) { return NWD == 8 ? 1 : NWD == 4 ? 2 : 4; }
+constexpr int depth_of(int NWD) { return NWD == 8 ? 1 : NWD >= 2 ? 2 : 4; }
+// Threads of a CTA of the gradient at most: pairs of small CTAs where rows allow.
+constexpr int bwd_threads(int NWD) { return NWD <= 2 ? 256 : kThreads; }
 
 template <int V>
 __device__ __forceinline__ float across(const F<V>& f) {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
 }
 
 template <typename T, int NWD, bool WHOLE>
-__global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdArgs a, const Rows g) {
+__global__ void __launch_bounds__(bwd_threads(NWD), NWD <= 2 ? 2 : 1) norm_bwd_rows_kernel(const NormBwdArgs a, const Rows g) {
   constexpr int V = 16 / (int)sizeof(T);
   using W = Raw<T, V>;
   extern __shared__ __align__(16) char smem[];
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
     P.reduce(z, buf[parity], [](float p, float q) { return p + q; });
     const float r1 = inverse_rms(z[0], a.inv_C, a.eps);
     const F<V> r = fill<V>(r1), k = fill<V>(-(z[1] * a.inv_C * r1) * r1 * r1);
-    asm volatile("" ::: "memory");  // the second pass reads the ring again: the registers are dweight's
+    if (NWD > 2) asm volatile("" ::: "memory");  // the second pass reads the ring again: the registers are dweight's
     if (on) {
 #pragma unroll
       for (int i = 0; i < NWD; ++i) {
@@ -407,21 +409,24 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 bool plan_rows(int B, int C, int es, bool forward, Rows* g) {
   const int V = 16 / es, words = (C + V - 1) / V + (C % V ? 1 : 0);  // of a row, with a partial one at each end
   g->period = V / gcd(C, V);
-  // words to a thread: 4; one for short rows, and for few rows, so that a call
-  // spreads over the SMs; 8 where the largest team needs it
-  const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= kThreads;
-  g->NWD = few || words <= 8 ? 1 : words <= 4 * kThreads ? 4 : 8;
-  if (words > g->NWD * kThreads || (!forward && es == 2 && g->NWD == 8)) return false;
+  // Words to a thread: 4, in the gradient 2 (42.9 us for 16384 rows of 2048 bf16, 4
+  // words 52); one for short rows, and for few rows, so that a call spreads over
+  // the SMs; more where the largest team needs it.
+  const int most = forward ? kThreads : bwd_threads(1);  // threads of a team
+  const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= most;
+  g->NWD = few || words <= 8 ? 1 : !forward && words <= 2 * most ? 2 : words <= 4 * kThreads ? 4 : 8;
+  const int threads = forward ? kThreads : bwd_threads(g->NWD);
+  if (words > g->NWD * threads || (!forward && es == 2 && g->NWD == 8)) return false;
   g->LANES = 1;
   while (g->LANES * g->NWD < words) g->LANES *= 2;
   g->U = g->LANES < 32 ? 32 / g->LANES : 1;
   const int unit_threads = g->LANES < 32 ? 32 : g->LANES;
   const long long wanted = ((long long)B + g->U - 1) / g->U;  // units, one row each
-  const int per_sm = g->NWD == 1 ? 2 : 1;                     // CTAs of kThreads threads, by their registers
-  g->NT = kThreads;
+  const int per_sm = threads < kThreads || g->NWD == 1 ? 2 : 1;  // CTAs of `threads` threads, by their registers
+  g->NT = threads;
   while (g->NT > unit_threads && g->NT > 128 && wanted * unit_threads < (long long)kSMs * g->NT) g->NT /= 2;
   const int per_cta = g->NT / unit_threads;
-  long long units = min((wanted + g->period - 1) / g->period * g->period, (long long)kSMs * per_sm * (kThreads / g->NT) * per_cta);
+  long long units = min((wanted + g->period - 1) / g->period * g->period, (long long)kSMs * per_sm * (threads / g->NT) * per_cta);
   // whole CTAs, and a multiple of period
   const int lcm = per_cta / gcd(per_cta, g->period) * g->period;
   units = (units + lcm - 1) / lcm * lcm;
@@ -474,6 +479,7 @@ int norm_bwd_rows(const NormBwdArgs& a, cudaStream_t st) {
     if (g.NWD == 8) return launch_bwd_rows<T, 8, false>(a, g, st);
   const bool whole = g.period == 1;
   if (g.NWD == 1) return whole ? launch_bwd_rows<T, 1, true>(a, g, st) : launch_bwd_rows<T, 1, false>(a, g, st);
+  if (g.NWD == 2) return whole ? launch_bwd_rows<T, 2, true>(a, g, st) : launch_bwd_rows<T, 2, false>(a, g, st);
   return whole ? launch_bwd_rows<T, 4, true>(a, g, st) : launch_bwd_rows<T, 4, false>(a, g, st);
 }
 
