@@ -38,12 +38,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
   using Join = Joiner<V, 1, 1, SHIFT>;
   extern __shared__ __align__(16) char smem[];
   const uint32_t rank = g.CL > 1 ? cluster_rank() : 0;
-  float* fsm = (float*)(smem + L::words(g) * 16 * (a.res ? 2 : 1));
+  float* fsm = (float*)(smem + L::words(g) * 16 * 2);
   const Join J(g, fsm, rank);
   const int NT = g.NT, slots = J.slots, first_c = (int)rank * g.cpc;
   const L lane(g, a.B, a.C, a.P, J.lx, J.j, first_c, smem);
   const int nc = lane.nc;
   const T *x = (const T*)a.x, *res = (const T*)a.res, *w = (const T*)a.w;
+  // Tiles fetched ahead: one of two tensors or two of one, about 64 KB in flight to
+  // an SM either way ([4,128,361x720] without residual 86 us, one ahead 100).  Odd
+  // rows are bound by instructions: one (22.6 us for [3,80,181x361], two 24.5).
+  const int depth = res || SHIFT ? 1 : 2;
   W *rx = lane.slot, *rr = rx + L::words(g);
 
   float wt[NCH];
@@ -52,7 +56,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
     wt[i] = i < nc && w ? to_f32(w[lane.channel(i)]) : 1.0f;
     if (i >= nc) {  // channels past the last: zeros, never copied over
       memset(rx + i * lane.stride, 0, 16);
-      if (res) memset(rr + i * lane.stride, 0, 16);
+      memset(rr + i * lane.stride, 0, 16);
     }
   }
   float* gmax = fsm + Join::floats(g);  // kRowsQ: [channel lane][slots]
@@ -67,25 +71,28 @@ __global__ void __launch_bounds__(kMaxThreads) norm_tile_kernel(const NormArgs a
   }
 
   Cursor at(g, a.C, a.P, blockIdx.x / g.CL), ahead = at;
-  auto fetch = [&]() {
-    lane.fetch(g, ahead, x, rx);
+  auto fetch = [&](W* to) {
+    lane.fetch(g, ahead, x, to);
     if (res) lane.fetch(g, ahead, res, rr);
     copy_commit();
+    ahead.next(g);
   };
-  fetch();
+  fetch(rx);
+  if (depth == 2) fetch(rr);
   if (g.CL > 1) cluster_barrier();  // every CTA runs before another writes its shared memory
 
-  for (int parity = 0; at.t < g.tiles; at = ahead, parity ^= 1) {
+  for (int parity = 0; at.t < g.tiles; at.next(g), parity ^= 1) {
     const int n = (int)min((long long)g.TP, a.P - at.pos), m = lane.skew(at);  // n: pixels of the tile
-    ahead.next(g);
+    W* from = depth == 2 && parity ? rr : rx;
     F<V> v[NCH], s[1] = {fill<V>(0.0f)}, r[1];
-    copy_wait<0>();
+    if (depth == 2) copy_wait<1>();
+    else copy_wait<0>();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      v[i] = unpack<T, V>(lane.read(rx, i));
+      v[i] = unpack<T, V>(lane.read(from, i));
       if (res) v[i] = add(v[i], unpack<T, V>(lane.read(rr, i)));
     }
-    fetch();
+    fetch(from);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) s[0] = fma(v[i], v[i], s[0]);
     auto finish = [&](const float(&z)[1], float(&out)[1]) { out[0] = inverse_rms(z[0], a.inv_C, a.eps); };
@@ -175,7 +182,7 @@ template <int Q, typename T, int NCH, bool SHIFT>
 int launch_norm_tile(const NormArgs& a, const Tiling& g, int ng_max, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
   using Join = Joiner<V, 1, 1, SHIFT>;
-  const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * (a.res ? 2 : 1), slots = Join::slots_of(g);
+  const size_t ring = Lane<T, V, NCH, SHIFT>::words(g) * 16 * 2, slots = Join::slots_of(g);
   const size_t qb = Q == kRowsQ ? 4 * ((size_t)(g.NT / g.LX) + ng_max) * slots : Q == kAtomicQ ? 12 * ng_max * slots : 0;
   const size_t smem = ring + 4 * Join::floats(g) + qb;
   if (smem > kMaxSmem) return DISCO_ERR_UNSUPPORTED;
