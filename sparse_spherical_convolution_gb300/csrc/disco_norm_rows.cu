@@ -144,8 +144,6 @@ struct Place {
 // one of its kDepth is the current row (kDepth = 1: nothing ahead, the row is too long).
 constexpr int ahead_of(int NWD) { return NWD >= 4 ? 1 : 4 / NWD; }
 constexpr int depth_of(int NWD) { return NWD == 8 ? 1 : NWD >= 2 ? 2 : 4; }
-// Threads of a CTA of the gradient at most: pairs of small CTAs where rows allow.
-constexpr int bwd_threads(int NWD) { return NWD <= 2 ? 256 : kThreads; }
 
 template <int V>
 __device__ __forceinline__ float across(const F<V>& f) {
@@ -311,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
 }
 
 template <typename T, int NWD, bool WHOLE>
-__global__ void __launch_bounds__(bwd_threads(NWD), NWD <= 2 ? 2 : 1) norm_bwd_rows_kernel(const NormBwdArgs a, const Rows g) {
+__global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdArgs a, const Rows g) {
   constexpr int V = 16 / (int)sizeof(T);
   using W = Raw<T, V>;
   extern __shared__ __align__(16) char smem[];
@@ -411,18 +409,18 @@ bool plan_rows(int B, int C, int es, bool forward, Rows* g) {
   g->period = V / gcd(C, V);
   // Words to a thread: 4, in the gradient 2 (42.9 us for 16384 rows of 2048 bf16, 4
   // words 52); one for short rows, and for few rows, so that a call spreads over
-  // the SMs; more where the largest team needs it.
-  const int most = forward ? kThreads : bwd_threads(1);  // threads of a team
-  const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= most;
-  g->NWD = few || words <= 8 ? 1 : !forward && words <= 2 * most ? 2 : words <= 4 * kThreads ? 4 : 8;
-  const int threads = forward ? kThreads : bwd_threads(g->NWD);
-  if (words > g->NWD * threads || (!forward && es == 2 && g->NWD == 8)) return false;
+  // the SMs; more where the largest team needs it.  The gradient takes pairs of
+  // smaller CTAs where a team fits one.
+  const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= kThreads;
+  g->NWD = few || words <= 8 ? 1 : !forward && words <= 2 * kThreads ? 2 : words <= 4 * kThreads ? 4 : 8;
+  const int threads = !forward && words <= g->NWD * kThreads / 2 ? kThreads / 2 : kThreads;
+  if (words > g->NWD * kThreads || (!forward && es == 2 && g->NWD == 8)) return false;
   g->LANES = 1;
   while (g->LANES * g->NWD < words) g->LANES *= 2;
   g->U = g->LANES < 32 ? 32 / g->LANES : 1;
   const int unit_threads = g->LANES < 32 ? 32 : g->LANES;
   const long long wanted = ((long long)B + g->U - 1) / g->U;  // units, one row each
-  const int per_sm = threads < kThreads || g->NWD == 1 ? 2 : 1;  // CTAs of `threads` threads, by their registers
+  const int per_sm = threads < kThreads || (forward && g->NWD == 1) ? 2 : 1;  // CTAs of `threads` threads, by their registers
   g->NT = threads;
   while (g->NT > unit_threads && g->NT > 128 && wanted * unit_threads < (long long)kSMs * g->NT) g->NT /= 2;
   const int per_cta = g->NT / unit_threads;
