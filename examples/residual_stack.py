@@ -118,7 +118,8 @@ def main(argv=None):
     ap.add_argument("--nlat", type=int, default=33)
     ap.add_argument("--nlon", type=int, default=64)
     ap.add_argument("--lr", type=float, default=1.0)
-    ap.add_argument("--max-norm", type=float, default=0.5)
+    ap.add_argument("--max-norm", type=float, default=0.2,
+                    help="limit of the gradients' norm; at the default sizes it starts at 0.25")
     a = ap.parse_args(argv)
     s = Stack(a.layers, a.channels, a.nlat, a.nlon, a.batch)
     g = torch.Generator(device="cuda").manual_seed(1)
