@@ -540,7 +540,8 @@ int finish_norm(const Row* part, int parts, float grad_scale, float* norm, cudaS
 // The norm, and with `clip` the scaled gradients, by tables of N.
 template <int N>
 int run(const disco_grads* g, float grad_scale, float max_norm, bool clip, float* norm, void* ws, cudaStream_t st) {
-  if (g->count <= N && g->numel <= kSmall) return run_small<N>(g, grad_scale, max_norm, clip, norm, st);
+  // a list without elements, of any length, is a short one: its norm is written too
+  if (g->numel == 0 || (g->count <= N && g->numel <= kSmall)) return run_small<N>(g, grad_scale, max_norm, clip, norm, st);
   Row* part = (Row*)ws;
   int parts, rc = norm_parts<N>(g, part, &parts, st);
   if (rc) return rc;

@@ -1,0 +1,102 @@
+"""Gradient lists longer than one launch takes (1000 tensors), with empty
+tensors among them or nothing else, and norms whose unscaled value lies outside
+fp32's range.
+
+Bound of the norm.  All sums are fp32 and all terms positive, so the sum of
+squares is off by at most one rounding (2^-24) for each addition on a term's way
+to the result.  These lists run in two launches or more: a chunk has 256 elements,
+8 to a lane in two chains of 4, and a warp takes at most 3 of a launch's (fewer than
+9728 and one for each tensor, over up to 4864 warps): 12 additions, 1 of the two
+chains, 5 over the lanes, 7 over the warps, fewer than 8 over a thread's rows of
+partial sums, again 5 and 7.  Below 48, which is 24 roundings of the root; the
+root, the scale and its power of two add 3.
+"""
+import math
+
+import pytest
+import torch
+
+from tests._train_ops import TINY, U32, UNIT
+
+pytestmark = pytest.mark.gpu
+F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
+NORM_TOL = 27 * U32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_spherical_convolution_gb300 import build
+    build.build()
+    import sparse_spherical_convolution_gb300 as d
+    d.disco_device_status(clear=True)
+    return d
+
+
+def _norm64(grads):
+    flat = torch.cat([g.double().flatten() for g in grads]) if grads else torch.zeros(1, dtype=torch.float64)
+    return float(flat.square().sum().sqrt())
+
+
+def _lists(count, seed):
+    """count gradients of three types, every fifth empty, of 1 to 300 elements."""
+    g = torch.Generator().manual_seed(seed)
+    sizes = [0 if i % 5 == 2 else 1 + (37 * i) % 300 for i in range(count)]
+    return [(1e-2 * torch.randn(n, generator=g)).to((F32, BF, F16)[i % 3]).cuda() for i, n in enumerate(sizes)]
+
+
+def _buffers(lib, plan):
+    return (torch.full((1,), -1.0, device="cuda"),
+            torch.full((lib.disco_grad_workspace_bytes(plan.c),), 0xFF, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("in_place", [False, True], ids=["f32 out", "in place"])
+@pytest.mark.parametrize("count", [999, 1000, 1001, 2000, 2103])
+def test_lists_of_several_launches(lib, count, in_place):
+    keep = _lists(count, count)
+    want = _norm64(keep)
+    for max_norm, scale in ((0.37 * want, 1.0), (0.2 * want, 0.25), (2 * want, 0.5)):
+        factor = scale if scale * want <= max_norm else max_norm / want
+        results = []
+        for joint in (True, False):
+            grads = [g.clone() for g in keep]
+            outs = grads if in_place else [torch.full_like(g, 9.0, dtype=F32) for g in grads]
+            plan = lib.GradPlan(grads, outs)
+            norm, ws = _buffers(lib, plan)
+            if joint:
+                lib.disco_grad_norm_clip(plan.c, max_norm, norm, ws, grad_scale=scale)
+            else:
+                lib.disco_grad_norm(plan.c, norm, ws, grad_scale=scale)
+                lib.disco_grad_clip(plan.c, max_norm, norm, grad_scale=scale)
+            torch.cuda.synchronize()
+            assert abs(float(norm) - scale * want) <= NORM_TOL * scale * want
+            for o, g in zip(outs, keep):
+                w = g.double() * factor
+                tol = (NORM_TOL + 5 * U32 + UNIT[o.dtype] * 1.01) * w.abs() + TINY[o.dtype] * 1.01
+                assert bool(((o.double() - w).abs() <= tol).all())
+            results.append((norm, outs))
+        assert float(results[0][0]) == float(results[1][0])
+        assert all(torch.equal(a, b) for a, b in zip(results[0][1], results[1][1]))
+
+
+@pytest.mark.parametrize("count", [1, 1000, 1001, 2103])
+def test_lists_of_empty_tensors(lib, count):
+    """No elements: the norm is 0, whichever call computes it."""
+    empty = [torch.empty(0, dtype=(F32, BF, F16)[i % 3], device="cuda") for i in range(count)]
+    plan = lib.GradPlan(empty, empty)
+    norm, ws = _buffers(lib, plan)
+    lib.disco_grad_norm_clip(plan.c, 1.0, norm, ws)
+    assert float(norm) == 0.0
+    norm.fill_(-1.0)
+    lib.disco_grad_norm(plan.c, norm, ws)
+    assert float(norm) == 0.0
+    lib.disco_grad_clip(plan.c, 1.0, norm)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("count", [1001, 2103])
+def test_one_tensor_with_elements_at_the_end(lib, count):
+    grads = [torch.empty(0, device="cuda") for _ in range(count - 1)] + [torch.tensor([3.0, 4.0], device="cuda")]
+    plan = lib.GradPlan(grads, grads)
+    norm, ws = _buffers(lib, plan)
+    lib.disco_grad_norm_clip(plan.c, 2.5, norm, ws)
+    assert float(norm) == 5.0 and grads[-1].tolist() == [1.5, 2.0]
