@@ -17,6 +17,7 @@ namespace norm {
 constexpr int kSMs = 152;
 constexpr int kMaxThreads = 512;
 constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kStaticSmem = 1024;  // at most, of the kernels of rows; those of tiles have none
 
 // ---- V fp32 values, two to an instruction (f32x2) where V is even ---------
 
@@ -585,12 +586,17 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // after: the kernel may begin while the one before it on the stream ends, once
 // all its CTAs have called let_next_begin(); it calls wait_for_previous() before
 // it reads what that one wrote.
+// most: the dynamic shared memory that any launch of this kernel may ask for.  The
+// limit set on a kernel is shared by all host threads: set to what one call needs,
+// it would refuse another thread's larger launch.
 template <typename K, typename... A>
-int launch(K kernel, int grid, int threads, int cluster, bool after, size_t smem, cudaStream_t st, const char* what, A... args) {
-  if (smem + 1024 > 48 * 1024 &&  // with a kernel's static arrays
-      cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+int launch(K kernel, int grid, int threads, int cluster, bool after, size_t smem, size_t most, cudaStream_t st,
+           const char* what, A... args) {
+  if (smem > most) return fail(DISCO_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory", what, smem);
+  if (smem + kStaticSmem > 48 * 1024 &&
+      cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
     (void)cudaGetLastError();
-    return fail(DISCO_ERR_CUDA, "%s: shared memory of %zu bytes refused", what, smem);
+    return fail(DISCO_ERR_CUDA, "%s: shared memory of %zu bytes refused", what, most);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -621,11 +627,11 @@ int launch(K kernel, int grid, int threads, int cluster, bool after, size_t smem
 }
 template <typename K, typename... A>
 int launch_clusters(K kernel, const Tiling& g, size_t smem, cudaStream_t st, const char* what, A... args) {
-  return launch(kernel, g.clusters * g.CL, g.NT, g.CL, false, smem, st, what, args...);
+  return launch(kernel, g.clusters * g.CL, g.NT, g.CL, false, smem, kMaxSmem, st, what, args...);
 }
 template <typename K, typename... A>
 int launch_grid(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const char* what, A... args) {
-  return launch(kernel, grid, threads, 1, false, smem, st, what, args...);
+  return launch(kernel, grid, threads, 1, false, smem, kMaxSmem - kStaticSmem, st, what, args...);
 }
 
 // ---- arguments, and the kernels by translation unit ---------------------------

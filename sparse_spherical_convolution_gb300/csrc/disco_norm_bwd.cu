@@ -263,7 +263,7 @@ extern "C" int disco_rms_norm_bwd(const void* dy, const void* h, const void* wei
   if (rc || !dweight) return rc;
   const int parts = (int)(need / ((size_t)C * sizeof(float)));
 #define CALL(T) \
-  rc = launch(norm_dweight_kernel<T>, (C + 31) / 32, 1024, 1, true, 0, st, "norm_dweight_kernel", (const float*)a.part, (T*)dweight, parts, C)
+  rc = launch(norm_dweight_kernel<T>, (C + 31) / 32, 1024, 1, true, 0, 0, st, "norm_dweight_kernel", (const float*)a.part, (T*)dweight, parts, C)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return rc;

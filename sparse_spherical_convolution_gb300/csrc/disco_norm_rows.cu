@@ -440,7 +440,7 @@ template <typename T, int NWD, bool Q, bool WHOLE>
 int launch_rows(const NormArgs& a, const Rows& g, int qmode, cudaStream_t st) {
   const size_t smem = (size_t)ahead_of(NWD) * g.NT * NWD * 16 * (a.res ? 2 : 1) +
                       (Q && qmode == kAtomic ? (size_t)(g.NT / g.LANES) * a.NG * 4 : 0);
-  if (smem > kMaxSmem - 1024) return DISCO_ERR_UNSUPPORTED;
+  if (smem > kMaxSmem - kStaticSmem) return DISCO_ERR_UNSUPPORTED;
   return launch_grid(norm_rows_kernel<T, NWD, Q, WHOLE>, g.grid, g.NT, smem, st, "norm_rows_kernel", a, g, qmode);
 }
 
