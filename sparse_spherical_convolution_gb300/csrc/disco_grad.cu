@@ -185,11 +185,15 @@ __device__ __forceinline__ Row cta_sum(Row r, Row* buf) {
   return r;
 }
 __device__ __forceinline__ Row row_of(const Sums& s) { return Row{{s.a.x + s.a.y, s.b.x + s.b.y, s.c.x + s.c.y}}; }
+// The scaled norm.  Powers of two are joined last: a root outside fp32's range may
+// have a product with grad_scale inside it.
 __device__ __forceinline__ float norm_of(const Row& r, float grad_scale) {
-  float v = sqrtf(r.v[0]);
-  if (isinf(r.v[0])) v = sqrtf(r.v[1]) * 0x1p80f;
-  else if (r.v[0] < 0x1p-60f) v = sqrtf(r.v[2]) * 0x1p-90f;
-  return v * grad_scale;
+  int e;
+  const float m = frexpf(grad_scale, &e);
+  float v = r.v[0];
+  if (isinf(v)) v = r.v[1], e += 80;
+  else if (v < 0x1p-60f) v = r.v[2], e -= 90;
+  return scalbnf(sqrtf(v) * m, e);
 }
 
 // A CTA's warps take neighbouring chunks.

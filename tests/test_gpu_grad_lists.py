@@ -100,3 +100,32 @@ def test_one_tensor_with_elements_at_the_end(lib, count):
     norm, ws = _buffers(lib, plan)
     lib.disco_grad_norm_clip(plan.c, 2.5, norm, ws)
     assert float(norm) == 5.0 and grads[-1].tolist() == [1.5, 2.0]
+
+
+# gradients (value, elements, type), grad_scale: the norm itself lies in fp32's
+# range, before the scale it is above it or among its subnormals
+SCALED = [
+    (3e38, 4, BF, 2.0 ** -16), (3e38, 4, F32, 2.0 ** -16), (3e38, 70_000, F32, 2.0 ** -100), (1e38, 9_000, BF, 2.0 ** -149),
+    (2.0 ** -148, 3, F32, 2.0 ** 16), (2.0 ** -148, 3, F32, 2.0 ** 100), (1e-40, 70_000, F32, 2.0 ** 127), (65504.0, 1000, F16, 2.0 ** 100),
+    (1.0, 5000, F32, 2.0 ** -149), (1.0, 70_000, BF, 2.0 ** 119),
+]
+
+
+@pytest.mark.parametrize("value,n,dtype,scale", SCALED, ids=lambda v: f"{v:.3g}" if isinstance(v, (int, float)) else str(v)[6:])
+def test_norm_outside_the_range_before_its_scale(lib, value, n, dtype, scale):
+    """Lists of one launch and of two (70,000 elements; there each thread adds
+    at most 3 chunks too)."""
+    g = [torch.full((n,), value).to(dtype).cuda()]
+    want = scale * math.sqrt(n) * float(g[0][0].double())
+    tiny = TINY[F32] * 1.01                            # a norm among the subnormals is rounded to their spacing
+    for joint in (True, False):
+        outs = [torch.empty((n,), dtype=F32, device="cuda")]
+        plan = lib.GradPlan(g, outs)
+        norm, ws = _buffers(lib, plan)
+        if joint:
+            lib.disco_grad_norm_clip(plan.c, math.inf, norm, ws, grad_scale=scale)
+            w = g[0].double() * scale
+            assert bool(((outs[0].double() - w).abs() <= U32 * w + tiny).all())
+        else:
+            lib.disco_grad_norm(plan.c, norm, ws, grad_scale=scale)
+        assert abs(float(norm) - want) <= NORM_TOL * want + tiny, (float(norm), want)
