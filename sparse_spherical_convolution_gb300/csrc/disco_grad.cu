@@ -245,10 +245,25 @@ template <int BYTES> struct Word;
 template <> struct Word<8> { using type = uint2; };
 template <> struct Word<16> { using type = uint4; };
 
+// Factor a b of the clipped gradients, out = (g a) b.  a = 1 but for a product that
+// nears fp32's subnormals (gradients 2^100 times past max_norm): it is split evenly
+// there, so that neither factor is rounded among them.
+struct Factor {
+  float a, b;
+};
+__device__ __forceinline__ Factor factor(float norm, float grad_scale, float max_norm) {
+  if (norm <= max_norm) return {1.0f, grad_scale};
+  if (!(norm < INFINITY)) return {1.0f, grad_scale * (max_norm / norm)};  // 0 or NaN
+  int es, em, en;
+  const float m = frexpf(grad_scale, &es) * (frexpf(max_norm, &em) / frexpf(norm, &en));
+  const int e = es + em - en, half = e < -100 ? e / 2 : 0;
+  return {scalbnf(1.0f, half), scalbnf(m, e - half)};
+}
+
 // out = g f of elements [i0, i1), by one warp.  A lane takes V elements, 16 bytes of
 // the wider side, so that both the loads and the stores of a warp lie side by side.
 template <typename T, typename O>
-__device__ __forceinline__ void clip_elements(const T* g, O* o, long long i0, long long i1, float f) {
+__device__ __forceinline__ void clip_elements(const T* g, O* o, long long i0, long long i1, Factor f) {
   constexpr int V = 16 / (sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
   constexpr int U = sizeof(T) < sizeof(O) ? 2 * kClipUnroll : kClipUnroll;  // loads in flight, of 8 or 16 bytes
   using WT = typename Word<V * (int)sizeof(T)>::type;
@@ -267,7 +282,7 @@ __device__ __forceinline__ void clip_elements(const T* g, O* o, long long i0, lo
       WO z;
       memcpy(t, &w, sizeof(w));
 #pragma unroll
-      for (int e = 0; e < V; ++e) r[e] = from_f32<O>(to_f32(t[e]) * f);
+      for (int e = 0; e < V; ++e) r[e] = from_f32<O>(to_f32(t[e]) * f.a * f.b);
       memcpy(&z, r, sizeof(z));
       __stcs((WO*)o + k, z);
     };
@@ -289,26 +304,21 @@ __device__ __forceinline__ void clip_elements(const T* g, O* o, long long i0, lo
       if (i + u * 32 < n) t[u] = g[i + u * 32];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (i + u * 32 < n) o[i + u * 32] = from_f32<O>(to_f32(t[u]) * f);
+      if (i + u * 32 < n) o[i + u * 32] = from_f32<O>(to_f32(t[u]) * f.a * f.b);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void clip_entry(const Entry& e, long long i0, long long i1, float f) {
+__device__ __forceinline__ void clip_entry(const Entry& e, long long i0, long long i1, Factor f) {
   if (e.odt == DISCO_F32) clip_elements((const T*)e.g, (float*)e.o, i0, i1, f);
   else if (e.odt == DISCO_BF16) clip_elements((const T*)e.g, (__nv_bfloat16*)e.o, i0, i1, f);
   else clip_elements((const T*)e.g, (__half*)e.o, i0, i1, f);
 }
 
-// factor of the clipped gradients
-__device__ __forceinline__ float factor(float norm, float grad_scale, float max_norm) {
-  return norm <= max_norm ? grad_scale : grad_scale * (max_norm / norm);
-}
-
 template <int N>
-__device__ __forceinline__ void clip_chunk(const Table<N>& t, int k, int& at, float f) {
+__device__ __forceinline__ void clip_chunk(const Table<N>& t, int k, int& at, Factor f) {
   const Entry& e = find(t, k, at);
-  if (e.o == e.g && f == 1.0f) return;
+  if (e.o == e.g && f.b == 1.0f) return;  // then a is 1 too
   const long long i0 = (k - e.chunk0) * t.chunk, i1 = min(e.n, i0 + t.chunk);
   if (e.dt == DISCO_F32) clip_entry<float>(e, i0, i1, f);
   else if (e.dt == DISCO_BF16) clip_entry<__nv_bfloat16>(e, i0, i1, f);
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kClipPerSM)
   } else {
     n = *norm;
   }
-  const float f = factor(n, grad_scale, max_norm);
+  const Factor f = factor(n, grad_scale, max_norm);
   int at = 0;
   // last chunks first: the norm's pass read them last, they may still be in L2
   for (int k = t.chunks - 1 - first_chunk(); k >= 0; k -= gridDim.x * kWarps) clip_chunk(t, k, at, f);
@@ -364,7 +374,7 @@ __global__ void __launch_bounds__(kThreads)
   const float n = norm_of(r, grad_scale);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   if (!clip) return;
-  const float f = factor(n, grad_scale, max_norm);
+  const Factor f = factor(n, grad_scale, max_norm);
   for (int k = first_chunk(); k < t.chunks; k += kCluster * kWarps) clip_chunk(t, k, at, f);
 }
 

@@ -129,3 +129,38 @@ def test_norm_outside_the_range_before_its_scale(lib, value, n, dtype, scale):
         else:
             lib.disco_grad_norm(plan.c, norm, ws, grad_scale=scale)
         assert abs(float(norm) - want) <= NORM_TOL * want + tiny, (float(norm), want)
+
+
+# gradients (value, elements, type), grad_scale and max_norm: the factor, or a
+# quotient on its way, lies near or below the smallest normal fp32 value 2^-126
+SMALL_FACTORS = [
+    (1e30, 4, F32, 1.0, 1e-10), (1e33, 4, F32, 2.0 ** 14, 1e-6), (3e38, 1, BF, 1.0, 1e-6), (3e38, 2, F32, 2.0 ** -16, 1.0),
+    (1e38, 70_000, F32, 2.0 ** -30, 1e-20), (2.0 ** 127, 1, F32, 1.0, 2.0 ** -120), (6e4, 9, F16, 2.0 ** 100, 1e-30),
+    (1e20, 5, F32, 1.0, 0.0), (1e-30, 5, F32, 2.0 ** 20, 1e-36),
+]
+
+
+@pytest.mark.parametrize("value,n,dtype,scale,max_norm", SMALL_FACTORS,
+                         ids=lambda v: f"{v:.3g}" if isinstance(v, (int, float)) else str(v)[6:])
+def test_small_factors(lib, value, n, dtype, scale, max_norm):
+    """Clipped gradients keep fp32's relative accuracy down to its subnormals,
+    however far their norm is above max_norm: the factor's 3 operations, a
+    second product, and the norm's own error."""
+    g = [torch.cat([torch.full((n,), value), torch.tensor([value / 1024, -value / 7, 0.0])]).to(dtype).cuda()]
+    N = scale * float(g[0].double().norm())
+    assert N > max_norm
+    want = g[0].double() * (scale * max_norm / N)
+    for joint in (True, False):
+        for odt in (F32, dtype):
+            outs = [torch.empty_like(g[0], dtype=odt)]
+            plan = lib.GradPlan(g, outs)
+            norm, ws = _buffers(lib, plan)
+            if joint:
+                lib.disco_grad_norm_clip(plan.c, max_norm, norm, ws, grad_scale=scale)
+            else:
+                lib.disco_grad_norm(plan.c, norm, ws, grad_scale=scale)
+                lib.disco_grad_clip(plan.c, max_norm, norm, grad_scale=scale)
+            assert abs(float(norm) - N) <= NORM_TOL * N
+            # TINY[odt]: half a subnormal step of the type; fp32's own for the product before it
+            tol = (NORM_TOL + 6 * U32 + UNIT[odt] * 1.01) * want.abs() + 1.01 * (TINY[odt] + 2 * TINY[F32])
+            assert bool(((outs[0].double() - want).abs() <= tol).all()), (outs[0][:1], want[:1])
