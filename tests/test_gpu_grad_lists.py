@@ -164,3 +164,19 @@ def test_small_factors(lib, value, n, dtype, scale, max_norm):
             # TINY[odt]: half a subnormal step of the type; fp32's own for the product before it
             tol = (NORM_TOL + 6 * U32 + UNIT[odt] * 1.01) * want.abs() + 1.01 * (TINY[odt] + 2 * TINY[F32])
             assert bool(((outs[0].double() - want).abs() <= tol).all()), (outs[0][:1], want[:1])
+
+
+def test_norm_of_a_hundred_million_elements(lib):
+    """Chunks of 8192 elements, 128 to each of a lane's two chains, and at most
+    ceil(chunks / 4864) chunks to a warp: so many additions and 36 of the joins
+    on a term's way, half of that in the root.  A lost chunk would show."""
+    n = 100_000_007
+    g = torch.randn(n, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    chunks = -(-n // 8192)
+    tol = ((-(-chunks // 4864) * 128 + 36) / 2 + 3) * U32
+    want = _norm64([g])
+    assert math.sqrt(1 - 8192 / n) < 1 - tol
+    plan = lib.GradPlan([g])
+    norm, ws = _buffers(lib, plan)
+    lib.disco_grad_norm(plan.c, norm, ws)
+    assert abs(float(norm) - want) <= tol * want, float(norm) / want - 1
