@@ -185,14 +185,15 @@ __device__ __forceinline__ Row cta_sum(Row r, Row* buf) {
   return r;
 }
 __device__ __forceinline__ Row row_of(const Sums& s) { return Row{{s.a.x + s.a.y, s.b.x + s.b.y, s.c.x + s.c.y}}; }
-// The scaled norm.  Powers of two are joined last: a root outside fp32's range may
-// have a product with grad_scale inside it.
+// The scaled norm.  Where the root lies outside fp32's range, or might be rounded among
+// its subnormals, powers of two are joined last: the product may lie inside it.
 __device__ __forceinline__ float norm_of(const Row& r, float grad_scale) {
+  float v = r.v[0];
+  if (!(isinf(v) || v < 0x1p-60f)) return sqrtf(v) * grad_scale;
   int e;
   const float m = frexpf(grad_scale, &e);
-  float v = r.v[0];
   if (isinf(v)) v = r.v[1], e += 80;
-  else if (v < 0x1p-60f) v = r.v[2], e -= 90;
+  else v = r.v[2], e -= 90;
   return scalbnf(sqrtf(v) * m, e);
 }
 
@@ -253,7 +254,8 @@ struct Factor {
 };
 __device__ __forceinline__ Factor factor(float norm, float grad_scale, float max_norm) {
   if (norm <= max_norm) return {1.0f, grad_scale};
-  if (!(norm < INFINITY)) return {1.0f, grad_scale * (max_norm / norm)};  // 0 or NaN
+  const float q = max_norm / norm, f = grad_scale * q;
+  if ((q >= 0x1p-100f && f >= 0x1p-100f) || !(norm < INFINITY)) return {1.0f, f};  // or 0, or NaN
   int es, em, en;
   const float m = frexpf(grad_scale, &es) * (frexpf(max_norm, &em) / frexpf(norm, &en));
   const int e = es + em - en, half = e < -100 ? e / 2 : 0;
