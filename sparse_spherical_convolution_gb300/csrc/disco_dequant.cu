@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantArgs a, 
       }
 #pragma unroll
       for (int i = 0; i < kRun; ++i)
-        store_words<V>((T*)a.x + row0 + i * step - m, packed<T, V>(mul(unpack_e4m3<V>(w[i]), s)), m, lx, g.LX, n, i < nc);
+        store_words<V>((T*)a.x + row0 + i * step - m, row0 + i * step - m, a.n, packed<T, V>(mul(unpack_e4m3<V>(w[i]), s)), m, lx, g.LX, n, i < nc);
     } else if (nc > 0 && px < n) {
       if (DISCO_IN_BOUNDS(s0 + V <= (long long)a.B * a.NG * a.P)) {
 #pragma unroll

@@ -185,17 +185,18 @@ __device__ __forceinline__ void store_stream(void* p, W w) { __stcs((W*)p, w); }
 // word l holds the elements from l V - m on, and a row's first and last words
 // are shared with its neighbours in memory.
 
-// Stores words of a row that starts m elements past the aligned address `p`: n
-// elements of it (the same for the whole warp), of which this lane holds word lx.
+// Stores words of a row that starts m elements past the aligned address `p` (element
+// `first` of a tensor of `total`): n elements of it (the same for the whole warp), of which this lane holds word lx.
 // All lanes of the warp call it; rows with `valid` false are not stored.  In a
 // full tile, n = (LX - 1) V, the V elements in words that another tile shares
 // (the row's first V - m and last m, words 0 and LX - 1) go out one to a lane.
 template <int V, typename W>
-__device__ __forceinline__ void store_words(void* p, W word, int m, int lx, int LX, int n, bool valid) {
+__device__ __forceinline__ void store_words(void* p, long long first, long long total, W word, int m, int lx, int LX, int n,
+                                            bool valid) {
   constexpr int ES = (int)sizeof(W) / V, NW = (int)sizeof(W) / 4;
   const int at = lx * V - m;  // the word's first element in the row
   char* d = (char*)p + lx * (int)sizeof(W);
-  if (valid && at >= 0 && at + V <= n) store_stream(d, word);
+  if (valid && at >= 0 && at + V <= n && DISCO_IN_BOUNDS(first + m >= 0 && first + lx * V + V <= total)) store_stream(d, word);
   if (n == (LX - 1) * V && LX >= V) {
     uint32_t w[NW];
     memcpy(w, &word, sizeof(W));
@@ -207,7 +208,7 @@ __device__ __forceinline__ void store_words(void* p, W word, int m, int lx, int 
       v = e * ES / 4 == k ? o : v;
     }
     v >>= 8 * (e * ES & 3);
-    if (valid && m > 0 && lx < V) {
+    if (valid && m > 0 && lx < V && DISCO_IN_BOUNDS(first + from * V + e >= 0 && first + from * V + e < total)) {
       typename Word<ES>::type one;
       memcpy(&one, &v, ES);
       store_stream((char*)p + (from * V + e) * ES, one);
@@ -216,7 +217,7 @@ __device__ __forceinline__ void store_words(void* p, W word, int m, int lx, int 
     const uint8_t* b = (const uint8_t*)&word;
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (at + e >= 0 && at + e < n) {
+      if (at + e >= 0 && at + e < n && DISCO_IN_BOUNDS(first + m + at + e >= 0 && first + m + at + e < total)) {
         typename Word<ES>::type v;
         memcpy(&v, b + e * ES, ES);
         store_stream(d + e * ES, v);
@@ -424,7 +425,7 @@ struct Lane {
   __device__ __forceinline__ void write(void* p, const Cursor& c, int m, int i, WO w, int n) const {
     constexpr int ES = (int)sizeof(WO) / V;
     char* d = (char*)p + (c.off + mine + i * step - m) * ES;
-    if constexpr (SHIFT) store_words<V>(d, w, m, lx, LX, n, i < nc);
+    if constexpr (SHIFT) store_words<V>(d, c.off + mine + i * step - m, total, w, m, lx, LX, n, i < nc);
     else if (i < nc && lx * V < n && DISCO_IN_BOUNDS(c.off + mine + i * step + V <= total)) store_stream(d, w);
   }
 };

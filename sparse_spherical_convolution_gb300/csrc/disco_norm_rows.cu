@@ -45,9 +45,10 @@ struct Rows {
 template <typename T, int NWD, bool WHOLE>
 struct Place {
   static constexpr int V = 16 / (int)sizeof(T);
-  int lane, team, LANES, C, m;  // team: of the CTA
-  long long row, step, lead;    // first row; rows to the next one; first row of the unit (loops run by units)
-  __device__ __forceinline__ Place(const Rows& g, int C_) : LANES(g.LANES), C(C_) {
+  int lane, team, LANES, B, C, m;  // team: of the CTA
+  long long row, step, lead;       // first row; rows to the next one; first row of the unit (loops run by units)
+  long long total;                 // elements of a tensor
+  __device__ __forceinline__ Place(const Rows& g, int B_, int C_) : LANES(g.LANES), B(B_), C(C_), total((long long)B_ * C_) {
     lane = threadIdx.x & (LANES - 1);
     team = threadIdx.x / LANES;
     const int per_cta = LANES < 32 ? g.NT / 32 : g.NT / LANES;
@@ -71,14 +72,20 @@ struct Place {
   __device__ __forceinline__ bool in(int i, int e) const { return WHOLE ? any(i) : at(i) + e >= 0 && at(i) + e < C; }
   // element offset of word 0 of row r in the tensor
   __device__ __forceinline__ long long origin(long long r) const { return r * C + at(0); }
-  // row r, whose origin is o
-  __device__ __forceinline__ void fetch(const T* p, uint4* to, int NT, long long o, bool last) const {
+  // Elements from row r's first to the tensor's end, or more than the row's words
+  // hold.  The words of the last row, and with rows shorter than a word those of
+  // the rows before it, would end past the tensor.
+  __device__ __forceinline__ int rest(long long r) const {
+    return !WHOLE && r >= B - 1 - (V - 2) / C ? (int)(B - r) * C : C + V;
+  }
+  // a row whose origin is o, left = rest() of it
+  __device__ __forceinline__ void fetch(const T* p, uint4* to, int NT, long long o, int left) const {
 #pragma unroll
     for (int i = 0; i < NWD; ++i)
-      if (any(i) && DISCO_IN_BOUNDS(o + i * LANES * V >= 0)) {
-        // the tensor's last word ends with its last row
-        const int bytes = !WHOLE && last ? min((C - at(i)) * (int)sizeof(T), 16) : 16;
-        copy_async(to + i * NT, p + o + i * LANES * V, bytes);
+      if (any(i)) {
+        const int bytes = WHOLE ? 16 : min((left - at(i)) * (int)sizeof(T), 16);
+        const long long word = o + i * LANES * V;
+        if (DISCO_IN_BOUNDS(word >= 0 && word + bytes / (int)sizeof(T) <= total)) copy_async(to + i * NT, p + word, bytes);
       }
   }
   // the elements of word i that are the row's; zeros in place of the others
@@ -91,14 +98,15 @@ struct Place {
   template <typename W>
   __device__ __forceinline__ void write(void* p, long long o, int i, W w) const {
     constexpr int ES = (int)sizeof(W) / V;
-    char* d = (char*)p + o * ES + i * LANES * (int)sizeof(W);
+    const long long word = o + i * LANES * V;
+    char* d = (char*)p + word * ES;
     if (whole(i)) {
-      store_stream(d, w);
+      if (DISCO_IN_BOUNDS(word >= 0 && word + V <= total)) store_stream(d, w);
     } else if (!WHOLE && any(i)) {
       const uint8_t* b = (const uint8_t*)&w;
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (in(i, e)) {
+        if (in(i, e) && DISCO_IN_BOUNDS(word + e >= 0 && word + e < total)) {
           typename Word<ES>::type v;
           memcpy(&v, b + e * ES, ES);
           store_stream(d + e * ES, v);
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
   using W = Raw<T, V>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float buf[2][2][1][kThreads / 32];
-  Place<T, NWD, WHOLE> P(g, a.C);
+  Place<T, NWD, WHOLE> P(g, a.B, a.C);
   const T *x = (const T*)a.x, *res = (const T*)a.res;
   constexpr int kAhead = ahead_of(NWD);
   const int words = g.NT * NWD;  // of one row of all teams
@@ -191,8 +199,9 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const NormArgs a, c
   const long long step_o = P.step * a.C;
   auto fetch = [&](long long r, long long o, int slot) {
     if (r < a.B) {
-      P.fetch(x, rx + slot * words, g.NT, o, r == a.B - 1);
-      if (res) P.fetch(res, rr + slot * words, g.NT, o, r == a.B - 1);
+      const int left = P.rest(r);
+      P.fetch(x, rx + slot * words, g.NT, o, left);
+      if (res) P.fetch(res, rr + slot * words, g.NT, o, left);
     }
     copy_commit();
   };
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
   extern __shared__ __align__(16) char smem[];
   if (a.part) let_next_begin();
   __shared__ float buf[2][2][kThreads / 32];
-  Place<T, NWD, WHOLE> P(g, a.C);
+  Place<T, NWD, WHOLE> P(g, a.B, a.C);
   const T *dy = (const T*)a.dy, *h = (const T*)a.h, *dh = (const T*)a.dh;
   constexpr int kDepth = depth_of(NWD);
   const int words = g.NT * NWD, streams = dh ? 3 : 2;  // words: of one row of all teams and one tensor
@@ -335,10 +344,10 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const NormBwdAr
   auto fetch = [&](long long r, long long o, int slot) {
     if (r < a.B) {
       uint4* to = ring + slot * streams * words;
-      const bool last = r == a.B - 1;
-      P.fetch(dy, to, g.NT, o, last);
-      P.fetch(h, to + words, g.NT, o, last);
-      if (dh) P.fetch(dh, to + 2 * words, g.NT, o, last);
+      const int left = P.rest(r);
+      P.fetch(dy, to, g.NT, o, left);
+      P.fetch(h, to + words, g.NT, o, left);
+      if (dh) P.fetch(dh, to + 2 * words, g.NT, o, left);
     }
     copy_commit();
   };
