@@ -532,7 +532,7 @@ def disco_dequant_e4m3(q, scale, x, B: int, C: int, P: int, group: int = 0, stre
 def disco_grad_plan(grads, outs=None):
     """(disco_grads, host array) of a list of gradients and the tensors their
     clipped values go to (None: the norm alone; the same tensors: in place).
-    The array and the tensors have to outlive the plan; GradPlan keeps them."""
+    The struct keeps the array it points to, and the tensors, alive."""
     grads = list(grads)
     outs = [None] * len(grads) if outs is None else list(outs)
     if len(outs) != len(grads):
@@ -554,6 +554,7 @@ def disco_grad_plan(grads, outs=None):
     arr = (disco_grad_tensor * len(grads)).from_buffer_copy(struct.pack("QQqii" * len(grads), *fields))
     grads_c = disco_grads()
     _check(load_library().disco_grad_plan(arr, len(grads), ctypes.byref(grads_c)))
+    grads_c.keep = (arr, grads, outs)
     return grads_c, arr
 
 
@@ -648,9 +649,9 @@ class Psi:
 
 class GradPlan:
     """A list of gradients checked once (disco_grad_plan), with the tensors it
-    refers to.  ``GradPlan(grads, outs)``; pass ``.c`` to disco_grad_norm,
-    disco_grad_clip and disco_grad_norm_clip.  Gradients allocated anew need a
-    new plan."""
+    refers to.  ``GradPlan(grads, outs)``; pass ``.c`` (which keeps the tensors
+    too) to disco_grad_norm, disco_grad_clip and disco_grad_norm_clip.
+    Gradients allocated anew need a new plan."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
