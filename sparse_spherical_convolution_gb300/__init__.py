@@ -601,7 +601,8 @@ def disco_device_status(clear: bool = True) -> int:
 # ------------------------------------------------------------ convenience
 
 class Psi:
-    """psi built on the device, with the torch buffers that own its memory.
+    """psi built on the device, with the torch buffers that own its memory
+    (``.c``, the struct that the calls take, keeps its buffer alive).
 
     ``Psi(grid_in, grid_out, kind, n_radial, cutoff)`` runs disco_psi_plan and
     disco_build_psi_kpacked on the current CUDA device and stream."""
@@ -620,6 +621,7 @@ class Psi:
         self.workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device="cuda")
         self.c = disco_psi_plan(gi, go, self.basis, self.workspace, stream)
         self.buffer = torch.empty(max(self.c.bytes, 256), dtype=torch.uint8, device="cuda")
+        self.c.keep = self.buffer  # the struct points into it
         disco_build_psi_kpacked(self.c, self.buffer, self.workspace, stream)
 
     def _sizes(self):

@@ -31,3 +31,16 @@ def test_grad_plan_struct_keeps_its_list(lib, in_place):
     del c, c2
     gc.collect()
     assert array() is None and all(r() is None for r in alive)
+
+
+@pytest.mark.gpu
+def test_psi_struct_keeps_its_buffer(lib):
+    grid = (9, 16, 1)
+    psi = lib.Psi(grid, grid, 1, 3, 0.5)
+    buffer, c = weakref.ref(psi.buffer), psi.c
+    del psi
+    gc.collect()
+    assert buffer() is not None and buffer().data_ptr() <= c.row_ptr < buffer().data_ptr() + buffer().nbytes
+    del c
+    gc.collect()
+    assert buffer() is None
