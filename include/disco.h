@@ -473,7 +473,8 @@ DISCO_API size_t disco_grad_workspace_bytes(const disco_grads* grads);
    vanishes in them; the norm itself is rounded to fp32.  An infinity gives an
    infinite norm, a NaN gives NaN, no elements give 0.  Fixed order of
    summation (deterministic).  workspace: 16-byte aligned,
-   >= disco_grad_workspace_bytes.  Asynchronous. */
+   >= disco_grad_workspace_bytes.  norm, workspace and the gradients may not
+   overlap (DISCO_ERR_INVALID_ARG).  Asynchronous. */
 DISCO_API int disco_grad_norm(const disco_grads* grads, float grad_scale, float* norm, void* workspace,
                               size_t workspace_bytes, void* stream);
 
@@ -483,12 +484,13 @@ DISCO_API int disco_grad_norm(const disco_grads* grads, float grad_scale, float*
      f = grad_scale                     where norm <= max_norm
      f = grad_scale * max_norm / norm   otherwise (NaN for a NaN norm)
      out = g * f, in fp32, rounded once to out_dtype
-   In place with f = 1 nothing is written.  Every gradient needs an out.
-   Asynchronous. */
+   In place with f = 1 nothing is written.  Every gradient needs an out, none
+   of which may overlap norm (DISCO_ERR_INVALID_ARG).  Asynchronous. */
 DISCO_API int disco_grad_clip(const disco_grads* grads, float grad_scale, float max_norm, const float* norm,
                               void* stream);
 
-/* disco_grad_norm and disco_grad_clip in one call, with the same results. */
+/* disco_grad_norm and disco_grad_clip in one call, with the same results; norm
+   and workspace may overlap neither gradients nor outs. */
 DISCO_API int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, float max_norm, float* norm,
                                    void* workspace, size_t workspace_bytes, void* stream);
 

@@ -494,6 +494,26 @@ int check_max_norm(const disco_grads* g, float max_norm) {
   return DISCO_OK;
 }
 
+bool overlap(const void* p, size_t n, const void* q, size_t m) { return (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n; }
+
+// No kernel may read or write the gradients (`grads`) and outs (`outs`) where another
+// of the call writes the norm or partial sums (ws, null: none), nor these each other.
+int check_apart(const disco_grads* g, bool grads, bool outs, const float* norm, const void* ws, size_t ws_bytes) {
+  if (ws && overlap(norm, 4, ws, ws_bytes)) return fail(DISCO_ERR_INVALID_ARG, "norm overlaps the workspace");
+  for (int32_t i = 0; i < g->count; ++i) {
+    const disco_grad_tensor& t = g->tensors[i];
+    if (t.n < 1) continue;
+    for (int o = 0; o < 2; ++o) {
+      if (!(o ? outs && t.out : grads)) continue;
+      const void* p = o ? t.out : t.grad;
+      const size_t bytes = (size_t)t.n * elem_bytes(o ? t.out_dtype : t.dtype);
+      const char* what = overlap(norm, 4, p, bytes) ? "norm" : ws && overlap(ws, ws_bytes, p, bytes) ? "the workspace" : nullptr;
+      if (what) return fail(DISCO_ERR_INVALID_ARG, "%s overlaps %sgradient %d", what, o ? "the out of " : "", i);
+    }
+  }
+  return DISCO_OK;
+}
+
 // Elements of a list that one cluster takes.
 constexpr long long kSmall = 1 << 16;
 
@@ -638,7 +658,8 @@ extern "C" int disco_grad_norm(const disco_grads* grads, float grad_scale, float
   disco::NvtxScope nvtx_scope("disco_grad_norm");
   int rc;
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_workspace(grads, workspace, workspace_bytes)) ||
-      (rc = check_scalar(norm, "norm")))
+      (rc = check_scalar(norm, "norm")) ||
+      (rc = check_apart(grads, true, false, norm, workspace, disco_grad_workspace_bytes(grads))))
     return rc;
   return run(grads, grad_scale, 0.0f, false, norm, workspace, (cudaStream_t)stream);
 }
@@ -647,7 +668,8 @@ extern "C" int disco_grad_clip(const disco_grads* grads, float grad_scale, float
                                void* stream) {
   disco::NvtxScope nvtx_scope("disco_grad_clip");
   int rc;
-  if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) || (rc = check_scalar(norm, "norm")))
+  if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) || (rc = check_scalar(norm, "norm")) ||
+      (rc = check_apart(grads, false, true, norm, nullptr, 0)))
     return rc;
   // the kernel writes the norm only where it computes it
 #define CALL(N) clip_all<N>(grads, nullptr, 0, grad_scale, max_norm, const_cast<float*>(norm), (cudaStream_t)stream)
@@ -660,7 +682,8 @@ extern "C" int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, 
   disco::NvtxScope nvtx_scope("disco_grad_norm_clip");
   int rc;
   if ((rc = check_grads(grads, grad_scale)) || (rc = check_max_norm(grads, max_norm)) ||
-      (rc = check_workspace(grads, workspace, workspace_bytes)) || (rc = check_scalar(norm, "norm")))
+      (rc = check_workspace(grads, workspace, workspace_bytes)) || (rc = check_scalar(norm, "norm")) ||
+      (rc = check_apart(grads, true, true, norm, workspace, disco_grad_workspace_bytes(grads))))
     return rc;
   return run(grads, grad_scale, max_norm, true, norm, workspace, (cudaStream_t)stream);
 }

@@ -180,3 +180,42 @@ def test_norm_of_a_hundred_million_elements(lib):
     norm, ws = _buffers(lib, plan)
     lib.disco_grad_norm(plan.c, norm, ws)
     assert abs(float(norm) - want) <= tol * want, float(norm) / want - 1
+
+
+def test_norm_and_workspace_apart_from_the_gradients(lib):
+    """A norm or workspace inside a gradient, an out or one another is refused;
+    beside them it is taken, and so is a workspace in the outs of a call that
+    does not write them."""
+    flat, dst = torch.ones(20_000, device="cuda"), torch.zeros(20_000, device="cuda")
+    need = lib.disco_grad_workspace_bytes(lib.GradPlan([flat]).c)
+    assert need % 16 == 0 and need < 8_000 * 4
+    grads, outs = [flat[:100], flat[100:9_000]], [dst[:100], dst[100:9_000]]
+    plan, same = lib.GradPlan(grads, outs), lib.GradPlan(grads, grads)
+    norm, ws = _buffers(lib, plan)
+
+    def refused(text, fn, *args):
+        with pytest.raises(lib.DiscoError) as e:
+            fn(*args)
+        assert e.value.status == -1 and text in str(e.value), str(e.value)
+
+    def words(t, first):                                 # a workspace from element `first` of t
+        return t[first:first + need // 4].view(torch.uint8)
+
+    joint, alone, clip = lib.disco_grad_norm_clip, lib.disco_grad_norm, lib.disco_grad_clip
+    refused("norm overlaps gradient 0", joint, plan.c, 1.0, flat[99:100], ws)
+    refused("norm overlaps gradient 1", alone, plan.c, flat[100:101], ws)
+    refused("norm overlaps the out of gradient 1", joint, plan.c, 1.0, dst[8_999:9_000], ws)
+    refused("norm overlaps the out of gradient 0", clip, plan.c, 1.0, dst[:1])
+    refused("norm overlaps the out of gradient 0", clip, same.c, 1.0, flat[:1])
+    refused("the workspace overlaps gradient 1", joint, plan.c, 1.0, norm, words(flat, 8_996))
+    refused("the workspace overlaps gradient 0", alone, plan.c, norm, words(flat, 0))
+    refused("the workspace overlaps the out of gradient 1", joint, plan.c, 1.0, norm, words(dst, 8_000))
+    for fn, args in ((joint, (plan.c, 1.0)), (alone, (plan.c,))):
+        refused("norm overlaps the workspace", fn, *args, ws.view(torch.float32)[need // 4 - 1:], ws)
+    want = math.sqrt(9_000)
+    joint(plan.c, 1.0, flat[9_000:9_001], words(flat, 9_004))
+    assert abs(float(flat[9_000]) - want) <= NORM_TOL * want
+    alone(plan.c, dst[9_000:9_001], words(dst, 0))
+    assert abs(float(dst[9_000]) - want) <= NORM_TOL * want
+    clip(plan.c, 1.0, flat[9_000:9_001])
+    assert bool(((dst[:9_000] - 1 / want).abs() <= (NORM_TOL + 6 * U32) / want).all())
