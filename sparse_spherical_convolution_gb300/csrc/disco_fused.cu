@@ -266,8 +266,9 @@ template <int K, int S, bool ANISO>
 int launch_fused(const FusedArgs& a, cudaStream_t st) {
   auto kern = fused_fwd_kernel<K, S, ANISO>;
   const size_t smem = FusedCfg<K, S, ANISO>::smem_bytes(a.MT);
-  if (smem > 227 * 1024) return fail(DISCO_ERR_UNSUPPORTED, "fused tile needs %zu bytes of shared memory", smem);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  constexpr size_t kMaxSmem = 227 * 1024;  // the limit of every launch: shared by all host threads
+  if (smem > kMaxSmem) return fail(DISCO_ERR_UNSUPPORTED, "fused tile needs %zu bytes of shared memory", smem);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
     return check_launch("disco_fused_conv attribute");
   dim3 grid((a.Wout + kFNW - 1) / kFNW, a.Hout, a.B);
   kern<<<grid, kFThreads, smem, st>>>(a);

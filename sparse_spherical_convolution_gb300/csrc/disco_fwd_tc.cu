@@ -923,13 +923,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// The limit of every launch: it belongs to the kernel and is shared by all host
+// threads, so it is not set to what one grid needs.
+constexpr size_t kMaxSmem = 227 * 1024;
+
 template <int K, int S, int STAGES>
 int launch_tc_stages(const disco_psi* psi, const CUtensorMap& map, const CUtensorMap& nmap,
                      const CUtensorMap& omap, TcArgs a, cudaStream_t st) {
   using Cfg = TcCfg<K, S, STAGES>;
   const size_t smem = Cfg::smem(a.TLB);
   auto kern = fwd_tc_kernel<K, S, STAGES>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) !=
       cudaSuccess)
     return check_launch("disco_fwd (tensor cores) attribute");
   dim3 grid((a.Wout + kTW * Cfg::NT - 1) / (kTW * Cfg::NT), (a.BC + 127) / 128, a.Hout);
@@ -939,7 +943,6 @@ int launch_tc_stages(const disco_psi* psi, const CUtensorMap& map, const CUtenso
 
 template <int K, int S>
 int launch_tc(const disco_psi* psi, const void* x, void* X, int BC, cudaStream_t st, bool f16) {
-  constexpr size_t kMaxSmem = 227 * 1024;
   const CUtensorMapDataType dt16 = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int Hin = psi->grid_in.nlat, Win = psi->grid_in.nlon;
   TcArgs a;
@@ -993,7 +996,7 @@ int launch_tc(const disco_psi* psi, const void* x, void* X, int BC, cudaStream_t
     // persistent form: one CTA per SM over all tiles
     const size_t smem = PCfg<K, S>::smem(a.TLB);
     auto kern = fwd_tcp_kernel<K, S>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
       return check_launch("disco_fwd (tensor cores) attribute");
     const long long ntiles = (long long)((a.Wout + kTW * NT3 - 1) / (kTW * NT3)) * ((BC + 127) / 128) * a.Hout;
     const int grid = (int)(ntiles < sm_count_f() ? ntiles : sm_count_f());

@@ -89,3 +89,37 @@ def test_norm_of_tiles_with_two_group_sizes(lib):
         q, s = outputs(groups[k])
         lib.disco_rms_norm(x, None, None, 1e-5, None, None, B, C, P, q=q, scale=s, group=groups[k])
         assert all(torch.equal(results[j][0], q) and torch.equal(results[j][1], s) for j in range(k, THREADS, 2))
+
+
+def test_contractions_of_two_grids(lib):
+    """Two threads, each waiting for its own call before the next."""
+    C, grids = 128, [(9, 64, 1), (9, 128, 1)]           # table rows of the forward: 80 and 144 entries
+    psis = [lib.Psi(g, g, 1, 3, 0.8) for g in grids]
+    failed, start, results, ins = [], threading.Barrier(2), [None, None], []
+    for k, (nlat, nlon, _) in enumerate(grids):
+        ins.append(torch.randn((1, C, nlat, nlon), generator=torch.Generator().manual_seed(k)).bfloat16().cuda())
+
+    def work(k):
+        s, c = torch.cuda.Stream(), psis[k].c
+        nlat, nlon, _ = grids[k]
+        X = results[k] = torch.empty((1, C, c.K, nlat, nlon), dtype=torch.bfloat16, device="cuda")
+        args = (ctypes.byref(c), _ptr(ins[k]), _ptr(X), 1, C, lib.DISCO_BF16, ctypes.c_void_p(s.cuda_stream))
+        fn = lib.load_library().disco_fwd
+        torch.cuda.synchronize()
+        start.wait()
+        for _ in range(CALLS):
+            if fn(*args) != 0:
+                failed.append(lib.disco_last_error())
+            s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, (len(failed), failed[0])
+    for k in range(2):
+        want = torch.empty_like(results[k])
+        lib.disco_fwd(psis[k].c, ins[k], want, 1, C)
+        assert torch.equal(results[k], want)
+    assert lib.disco_device_status() == 0
