@@ -387,7 +387,11 @@ DISCO_API int disco_bwd_host(const disco_psi* psi, const void* G_host, void* gx_
      m[b,g,p] = max(1e-30, max of |y[b,c,p]| over the channels c of group g)
      scale[b,g,p] = m / 448
      q[b,c,p] = e4m3(y[b,c,p] * (448 / m))      (8-bit float, 448 its largest)
-   in fp32, each output rounded once (y and q come from the unrounded h).
+   in fp32, each output rounded once (y and q come from the unrounded h).  The
+   fp32 value that q rounds is within a few units of its last place, so where
+   y * (448 / m) is that near to the middle of two e4m3 values either may be
+   stored (one code in 50,000 of normally distributed values differs from the
+   formula's in exact arithmetic).
    Groups are runs of `group` channels, the last one shorter when group does
    not divide C; group = 0 or >= C is one group.  A NaN in y is stored as the
    e4m3 NaN and does not count to m; an infinite m gives an infinite scale, and
@@ -484,6 +488,8 @@ DISCO_API int disco_grad_norm(const disco_grads* grads, float grad_scale, float*
      f = grad_scale                     where norm <= max_norm
      f = grad_scale * max_norm / norm   otherwise (NaN for a NaN norm)
      out = g * f, in fp32, rounded once to out_dtype
+   f keeps fp32's accuracy where it lies below fp32's range (gradients far
+   above max_norm).
    In place with f = 1 nothing is written.  Every gradient needs an out, none
    of which may overlap norm (DISCO_ERR_INVALID_ARG).  Asynchronous. */
 DISCO_API int disco_grad_clip(const disco_grads* grads, float grad_scale, float max_norm, const float* norm,

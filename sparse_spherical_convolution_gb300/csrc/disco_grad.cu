@@ -19,9 +19,9 @@
 // Bound by HBM for long lists (every gradient is read twice where they do not fit
 // on the chip, and written once), by launches for short ones.  Measured (GB300):
 // 48 gradients of [512,512,9] bf16 into fp32, 679 MB and 226 MB read again: norm 37
-// us (6.1 TB/s), both 150 us a call; 8 of [64,64,3] 7.5 us;
-// 240 ragged ones of two types (2.5 million elements, outs packed back to back)
-// 12.3 us; 32 thousand elements in the one cluster 7.2 us, in two launches 8.9,
+// us (6.1 TB/s), both 144.5 us a call, into bf16 119, in place 101; 8 of [64,64,3]
+// 7.2 to 8.4 us (by host); 240 ragged ones of two types (2.5 million elements, outs
+// packed back to back) 12.4 us; 32 thousand elements in the one cluster 7.2 us, in two launches 8.9,
 // 262 thousand 16.4 and 9.0, hence kSmall.
 
 #include <math.h>

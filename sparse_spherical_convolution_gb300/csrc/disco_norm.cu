@@ -9,7 +9,8 @@
 // (disco_norm_tile.cuh).  What neither takes (rows past 32,768 16-bit or 16,384
 // fp32 features, pixels whose channels fit no cluster, group maxima that fit no
 // shared memory) runs the general kernel below, which takes every shape and
-// reads the inputs again for each further pass.  It is bound by those reads: [1,512,360x720] bf16 with a residual takes it 468 us, the tiles 174.
+// reads the inputs again for each further pass.  It is bound by those reads:
+// [1,512,360x720] bf16 with a residual takes it 468 us, the tiles 174.
 
 #include "disco_norm.cuh"
 
@@ -21,10 +22,10 @@ namespace {
 
 using namespace norm;
 
-
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
+
 template <typename T, bool ROW>
 __global__ void __launch_bounds__(kGenWarps * 32) norm_any_kernel(const NormArgs a, const long long tiles) {
   using D = Dealt<ROW>;

@@ -8,8 +8,9 @@
 // start while the first ends.
 //
 // Measured (both kernels, GB300): [1,512,360x720] bf16 with dh 196 us, 5.4 TB/s
-// (80 % of the copy rate); [2,128,361x720] 87 us, 6.1 TB/s; [20,64,65344] 102 us,
-// the same with odd rows 149 us.  HBM bounds up to 256 channels.  At 512 one CTA
+// (80 % of the copy rate); [2,128,361x720] 88 us, 6.0 TB/s; [20,64,65344] 105 us,
+// the same with odd rows 149 us; [3,91,151250] (odd rows) 94 us, 3.5 TB/s.  HBM
+// bounds up to 256 channels.  At 512 one CTA
 // holds rows of 64 bytes, or a pair rows of 128 bytes and a cluster barrier a tile:
 // 198 and 228 us.  Odd rows are bound by instructions (two sums and two factors a
 // pixel to realign, 16 shared-memory accesses each way).

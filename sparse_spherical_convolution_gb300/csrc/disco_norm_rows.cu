@@ -13,13 +13,15 @@
 // words hold the same features in all its rows, so the gain and the sums of
 // dweight stay in registers.  The first and last word of a row are partial.
 //
-// Measured (kernels, GB300): [16384,2048] bf16, residual, h, q and scales in groups
-// of 128: 41 us, 5.7 TB/s (83 % of the copy rate, DRAM 56 % busy, issue 53 %: the
-// 8-bit form is bound by instructions, without it 8 bytes an element run at 5.7
-// TB/s too); gradient and the sum of dweight 45 us, 4.4 TB/s (issue 50 %, 16 warps
-// to an SM: dweight's sums, and dy and h between their two uses, take the
-// registers); 2560 rows of 15507 features 55 us, 5.7 TB/s.  16 rows of 512: 5 us, the latency of a launch
-// and one load.
+// Measured (calls, GB300): [16384,2048] bf16, residual, h, q and scales in groups
+// of 128: 42.6 us, 5.5 TB/s (82 % of the copy rate, DRAM 57 % busy, issue 53 %: the
+// 8-bit form is bound by instructions); 2560 rows of 15507 features 55 us, 5.7 TB/s;
+// 1600 rows of 24576 90 us, 3.5 TB/s (8 words to a thread: 128 registers, with
+// spills); [12518,1693] with q, one group, 45 us, 4.2 TB/s (partial words).
+// Gradient and the sum of dweight: [16384,2048] 45.1 us, 4.5 TB/s;
+// [8599,6164] 133 us, 2.4 TB/s (issue 56 %, 16 warps to an SM: one row's join is
+// waited for before the next row's sums begin).  16 rows of 512: a kernel of 5 us,
+// the latency of a launch and one load.
 
 #include "disco_norm.cuh"
 
@@ -416,10 +418,10 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 bool plan_rows(int B, int C, int es, bool forward, Rows* g) {
   const int V = 16 / es, words = (C + V - 1) / V + (C % V ? 1 : 0);  // of a row, with a partial one at each end
   g->period = V / gcd(C, V);
-  // Words to a thread: 4, in the gradient 2 (42.9 us for 16384 rows of 2048 bf16, 4
-  // words 52); one for short rows, and for few rows, so that a call spreads over
-  // the SMs; more where the largest team needs it.  The gradient takes pairs of
-  // smaller CTAs where a team fits one.
+  // Words to a thread: 4, in the gradient 2 (16384 rows of 2048 bf16 45.1 us, with 4
+  // words 47.6; 8599 rows of 6164 133 and 164); one for short rows, and for few rows,
+  // so that a call spreads over the SMs; more where the largest team needs it.  The
+  // gradient takes pairs of smaller CTAs where a team fits one.
   const bool few = (long long)B * words <= 2LL * kSMs * kThreads && words <= kThreads;
   g->NWD = few || words <= 8 ? 1 : !forward && words <= 2 * kThreads ? 2 : words <= 4 * kThreads ? 4 : 8;
   const int threads = !forward && words <= g->NWD * kThreads / 2 ? kThreads / 2 : kThreads;

@@ -8,13 +8,20 @@
 // its shared memory already takes in the next tile (cp.async).  Without that
 // prefetch, at the same occupancy, [2,128,361x720] took 114 us, with it 88.
 //
-// Measured (kernel, GB300; the copy rate of this card is 6.78 TB/s):
-//   [1,512,360x720] bf16, residual, h and y         170 us  6.2 TB/s, DRAM 75 % busy
-//   [2,128,361x720] bf16, the same and q, groups 32  99 us  6.2 TB/s, DRAM 71 %
-//   [20,64,65343] bf16 (odd rows), residual         113 us  5.9 TB/s (as for 65344)
-//   [3,80,181x361] fp16, no residual                 23 us  2.7 TB/s: it lies in L2,
-//     and with 11 tiles to a CTA the latency of a tile's joins shows; 80 channels
-//     fill 5 of 6 blocks of 16 where rows are odd
+// Measured (calls, GB300; the copy rate of this card is 6.78 TB/s):
+//   [1,512,360x720] bf16, residual, h and y         174 us  6.1 TB/s, DRAM 75 % busy
+//   [2,128,361x720] bf16, the same and q, groups 32 101 us  6.0 TB/s, DRAM 70 %
+//   [14,54,20000] fp32, residual                     41 us  5.9 TB/s
+//   [20,64,65343] bf16 (odd rows), residual         112 us  6.0 TB/s (111 for 65344)
+//   [12,6,379015] fp32 (odd rows), residual         118 us  3.7 TB/s: channels come in
+//     blocks of 16 (32 for 16 bits), 10 of a block's 16 places hold none of the 6
+//   [3,80,181x361] fp16, no residual                 23 us  2.8 TB/s: it lies in L2,
+//     and with 11 tiles to a CTA the latency of a tile's joins shows; one CTA of 384
+//     threads to an SM (the planner's 512 threads, whatever a kernel's registers)
+//   [2,128,361x719] bf16 (odd rows), residual and q 147 us  4.1 TB/s
+// With q where a lane's channels or a CTA straddle groups, maxima are shared-memory
+// atomics: [1,256,361x719] bf16, groups of 32, 244 us (2.5 TB/s); [3,433,11250],
+// groups of 128, 49 us; fp32 [1,171,238050], groups of 55, 171 us.
 // 512 channels of 518 KB rows take a pair of CTAs with 256-byte row pieces: 128-byte
 // pieces in one CTA took 186 to 204 us (each piece lies in another 2 MB page).
 
