@@ -500,6 +500,89 @@ DISCO_API int disco_grad_clip(const disco_grads* grads, float grad_scale, float 
 DISCO_API int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, float max_norm, float* norm,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Pointwise feed-forward in 8-bit integers ------------------------------
+   Layers over the channels of each pixel, between the convolutions and in
+   heads.  A token is one pixel of one sample (one row of features for P = 1).
+   Activations are kept in 8-bit integers with an fp32 scale for each token,
+   weights W [Cout, Cin] with one for each output channel.  The 8-bit
+   activation serves the product and, kept in place of the 16-bit one, the
+   gradients. */
+
+/* The tokens of an activation in 8-bit integers:
+     a[b,p] = max(1e-30, max_c |x[b,c,p]|),  scale[b,p] = a / 127
+     q[b,c,p] = 127 x[b,c,p] / a rounded to the nearest integer, ties to even
+   q is exactly that of the formula for every type (fp32 included), -127 .. 127.
+   A token that holds an infinity or a NaN has that scale and q = 0, and reads
+   back as NaN.  With P = 1 and B = Cout this is the 8-bit form of a weight.
+   x: [B, C, P] of `dtype`; q: [B, C, P] int8; scale: [B, P] fp32.  No buffers
+   may overlap.  Asynchronous on `stream`; no workspace. */
+DISCO_API int disco_quant_i8(const void* x, void* q, float* scale, int32_t B, int32_t C, int64_t P, disco_dtype dtype,
+                             void* stream);
+
+/* Product of activations and weights in 8-bit integers:
+     y[b,o,p] = scale[b,p] * wscale[o] * sum_c W[o,c] q[b,c,p]
+   The products are exact and summed in fp32, so the sum is exact while it and
+   its parts stay within 2^24 (always for Cin <= 1024); y is rounded once.  A
+   scale that is infinite or NaN reaches the outputs of its token, or of its
+   output channel, alone.
+   q: [B, Cin, P] int8, scale: [B, P]; W: [Cout, Cin] int8, wscale: [Cout];
+   y: [B, Cout, P] of `dtype`.  workspace: 16-byte aligned, >=
+   disco_matmul_i8_workspace_bytes (0 for invalid arguments).  No buffers may
+   overlap.  Asynchronous. */
+DISCO_API size_t disco_matmul_i8_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype);
+DISCO_API int disco_matmul_i8(const void* q, const float* scale, const void* W, const float* wscale, void* y, int32_t B,
+                              int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Gradient of the product with respect to the activation that q and scale stand
+   for (the rounding to 8 bits counts as the identity):
+     dx[b,c,p] = sum_o (wscale[o] W[o,c]) dy[b,o,p]
+   wscale[o] W[o,c] is rounded to `dtype`, sums are fp32, dx is rounded once.
+   dy: [B, Cout, P], dx: [B, Cin, P], bf16 or fp16 (DISCO_ERR_UNSUPPORTED
+   else).  Workspace, overlaps and order as above. */
+DISCO_API size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P,
+                                                           disco_dtype dtype);
+DISCO_API int disco_matmul_i8_bwd_input(const void* dy, const void* W, const float* wscale, void* dx, int32_t B,
+                                        int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Gradient of the product with respect to the weight that W and wscale stand
+   for, from the kept 8-bit activation:
+     dW[o,c] = sum_{b,p} dy[b,o,p] (scale[b,p] q[b,c,p])
+   scale[b,p] q[b,c,p] is rounded to `dtype`; sums are fp32 in a fixed order
+   (deterministic), dW is rounded once.  dy: [B, Cout, P], dW: [Cout, Cin], bf16
+   or fp16.  Workspace, overlaps and order as above. */
+DISCO_API size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P,
+                                                            disco_dtype dtype);
+DISCO_API int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const float* scale, void* dW, int32_t B,
+                                         int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* SiLU: g / (1 + exp(-g)).  GELU: g Phi(g), Phi the normal distribution. */
+typedef enum { DISCO_SILU = 0, DISCO_GELU = 1 } disco_activation;
+
+/* Gated activation of x [B, 2 C, P], its gates in the first C channels:
+     y[b,c,p] = act(x[b,c,p]) * x[b,C+c,p]
+   with up to three outputs: y itself; y in 8 bits (q, scale: the operand of the
+   product that follows; taken from the unrounded y, so next to the middle of two
+   integers either may be stored); and x in 8 bits (xq, xscale: exactly what
+   disco_quant_i8 gives for x, one scale for gates and values of a token), which
+   a training program keeps in place of x for disco_glu_bwd.
+   y: [B, C, P] of `dtype`; q: [B, C, P] int8, scale: [B, P]; xq: [B, 2 C, P]
+   int8, xscale: [B, P].  NULL outputs are not written: at least one of y and q
+   is given, q comes with scale and xq with xscale.  No buffers may overlap.
+   Asynchronous; no workspace. */
+DISCO_API int disco_glu(const void* x, void* y, void* q, float* scale, void* xq, float* xscale, disco_activation act,
+                        int32_t B, int32_t C, int64_t P, disco_dtype dtype, void* stream);
+
+/* Gradient of the gated activation at the kept 8-bit input, g = xscale xq[:, :C]
+   and v = xscale xq[:, C:]:
+     dx[b,c,p] = dy[b,c,p] v act'(g),  dx[b,C+c,p] = dy[b,c,p] act(g)
+   in fp32, rounded once.  dy: [B, C, P], dx: [B, 2 C, P] of `dtype`.  No buffers
+   may overlap.  Asynchronous; no workspace. */
+DISCO_API int disco_glu_bwd(const void* dy, const void* xq, const float* xscale, void* dx, disco_activation act,
+                            int32_t B, int32_t C, int64_t P, disco_dtype dtype, void* stream);
+
 /* Diagnostics; BLOCKS the host (synchronises the current device).  Reads
    the device status word into *flags (0 = no fault; bit 0 = an mbarrier wait
    of the fused forward timed out, bit 1 = one of the dX GEMM timed out,

@@ -30,11 +30,17 @@ __all__ = [
     "DISCO_F32", "DISCO_BF16", "DISCO_F16", "dtype_code", "disco_rms_norm", "disco_rms_norm_bwd_workspace_bytes",
     "disco_rms_norm_bwd", "disco_dequant_e4m3", "disco_grad_tensor", "disco_grads", "disco_grad_plan", "GradPlan",
     "disco_grad_workspace_bytes", "disco_grad_norm", "disco_grad_clip", "disco_grad_norm_clip",
+    "DISCO_SILU", "DISCO_GELU",
+    "disco_quant_i8", "disco_matmul_i8_workspace_bytes", "disco_matmul_i8",
+    "disco_matmul_i8_bwd_input_workspace_bytes", "disco_matmul_i8_bwd_input",
+    "disco_matmul_i8_bwd_weight_workspace_bytes", "disco_matmul_i8_bwd_weight", "disco_glu", "disco_glu_bwd",
 ]
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 DISCO_F32, DISCO_BF16, DISCO_F16 = 0, 1, 2
+
+DISCO_SILU, DISCO_GELU = 0, 1
 
 EXPORTED_SYMBOLS = [
     "disco_version", "disco_last_error", "disco_psi_workspace_bytes", "disco_psi_plan",
@@ -46,6 +52,9 @@ EXPORTED_SYMBOLS = [
     "disco_check_sched_takeover", "disco_build_flags", "disco_rms_norm", "disco_rms_norm_bwd_workspace_bytes",
     "disco_rms_norm_bwd", "disco_dequant_e4m3", "disco_grad_plan", "disco_grad_workspace_bytes", "disco_grad_norm",
     "disco_grad_clip", "disco_grad_norm_clip",
+    "disco_quant_i8", "disco_matmul_i8_workspace_bytes", "disco_matmul_i8",
+    "disco_matmul_i8_bwd_input_workspace_bytes", "disco_matmul_i8_bwd_input",
+    "disco_matmul_i8_bwd_weight_workspace_bytes", "disco_matmul_i8_bwd_weight", "disco_glu", "disco_glu_bwd",
 ]
 
 
@@ -177,6 +186,17 @@ def load_library():
     lib.disco_grad_clip.argtypes = [PGR, F32, F32, P, P]
     lib.disco_grad_norm_clip.restype = ctypes.c_int
     lib.disco_grad_norm_clip.argtypes = [PGR, F32, F32, P, P, SZ, P]
+    lib.disco_quant_i8.restype = ctypes.c_int
+    lib.disco_quant_i8.argtypes = [P, P, P, I32, I32, I64, ctypes.c_int, P]
+    for nm, ptrs in (("disco_matmul_i8", 5), ("disco_matmul_i8_bwd_input", 4), ("disco_matmul_i8_bwd_weight", 4)):
+        getattr(lib, nm + "_workspace_bytes").restype = SZ
+        getattr(lib, nm + "_workspace_bytes").argtypes = [I32, I32, I32, I64, ctypes.c_int]
+        getattr(lib, nm).restype = ctypes.c_int
+        getattr(lib, nm).argtypes = [P] * ptrs + [I32, I32, I32, I64, ctypes.c_int, P, SZ, P]
+    lib.disco_glu.restype = ctypes.c_int
+    lib.disco_glu.argtypes = [P, P, P, P, P, P, ctypes.c_int, I32, I32, I64, ctypes.c_int, P]
+    lib.disco_glu_bwd.restype = ctypes.c_int
+    lib.disco_glu_bwd.argtypes = [P, P, P, P, ctypes.c_int, I32, I32, I64, ctypes.c_int, P]
     lib.disco_device_status.restype = ctypes.c_int
     lib.disco_device_status.argtypes = [ctypes.POINTER(I32), I32]
     _lib = lib
@@ -587,6 +607,82 @@ def disco_grad_norm_clip(grads: disco_grads, max_norm: float, norm, workspace, g
     wp, wn = _bytes(workspace, "workspace", dev)
     _check((_lib or load_library()).disco_grad_norm_clip(grads, grad_scale, max_norm, np_, wp, wn,
                                                          _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_quant_i8(x, q, scale, B: int, C: int, P: int, stream=None) -> None:
+    """The tokens of x in 8-bit integers q with a scale for each; see include/disco.h."""
+    n, dev = B * C * P, _on(x, "x")
+    _check((_lib or load_library()).disco_quant_i8(
+        _in(x, "x", n, x.dtype, dev), _in(q, "q", n, _torch.int8, dev), _in(scale, "scale", B * P, _torch.float32, dev),
+        B, C, P, dtype_code(x.dtype), _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_matmul_i8_workspace_bytes(B: int, Cin: int, Cout: int, P: int, dtype=DISCO_BF16) -> int:
+    return load_library().disco_matmul_i8_workspace_bytes(B, Cin, Cout, P, dtype)
+
+
+def disco_matmul_i8(q, scale, W, wscale, y, B: int, Cin: int, Cout: int, P: int, workspace=None, stream=None) -> None:
+    """y = scale wscale (W q), products of 8-bit integers over the channels of each token."""
+    T, dev = B * P, _on(y, "y")
+    f32, i8 = _torch.float32, _torch.int8
+    wp, wn = _bytes(workspace, "workspace", dev)
+    _check((_lib or load_library()).disco_matmul_i8(
+        _in(q, "q", T * Cin, i8, dev), _in(scale, "scale", T, f32, dev), _in(W, "W", Cout * Cin, i8, dev),
+        _in(wscale, "wscale", Cout, f32, dev), _in(y, "y", T * Cout, y.dtype, dev), B, Cin, Cout, P, dtype_code(y.dtype),
+        wp, wn, _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_matmul_i8_bwd_input_workspace_bytes(B: int, Cin: int, Cout: int, P: int, dtype=DISCO_BF16) -> int:
+    return load_library().disco_matmul_i8_bwd_input_workspace_bytes(B, Cin, Cout, P, dtype)
+
+
+def disco_matmul_i8_bwd_input(dy, W, wscale, dx, B: int, Cin: int, Cout: int, P: int, workspace=None,
+                              stream=None) -> None:
+    """dx = (wscale W)^T dy, the gradient of disco_matmul_i8's activation."""
+    T, dev = B * P, _on(dy, "dy")
+    dt = dy.dtype
+    wp, wn = _bytes(workspace, "workspace", dev)
+    _check((_lib or load_library()).disco_matmul_i8_bwd_input(
+        _in(dy, "dy", T * Cout, dt, dev), _in(W, "W", Cout * Cin, _torch.int8, dev),
+        _in(wscale, "wscale", Cout, _torch.float32, dev), _in(dx, "dx", T * Cin, dt, dev), B, Cin, Cout, P, dtype_code(dt),
+        wp, wn, _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_matmul_i8_bwd_weight_workspace_bytes(B: int, Cin: int, Cout: int, P: int, dtype=DISCO_BF16) -> int:
+    return load_library().disco_matmul_i8_bwd_weight_workspace_bytes(B, Cin, Cout, P, dtype)
+
+
+def disco_matmul_i8_bwd_weight(dy, q, scale, dW, B: int, Cin: int, Cout: int, P: int, workspace=None,
+                               stream=None) -> None:
+    """dW = dy (scale q)^T summed over tokens, from the kept 8-bit activation."""
+    T, dev = B * P, _on(dy, "dy")
+    dt = dy.dtype
+    wp, wn = _bytes(workspace, "workspace", dev)
+    _check((_lib or load_library()).disco_matmul_i8_bwd_weight(
+        _in(dy, "dy", T * Cout, dt, dev), _in(q, "q", T * Cin, _torch.int8, dev),
+        _in(scale, "scale", T, _torch.float32, dev), _in(dW, "dW", Cout * Cin, dt, dev), B, Cin, Cout, P, dtype_code(dt),
+        wp, wn, _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_glu(x, y, act: int, B: int, C: int, P: int, q=None, scale=None, xq=None, xscale=None, stream=None) -> None:
+    """y = act(x[:, :C]) x[:, C:] for x [B, 2 C, P], y in 8 bits (q, scale) and x
+    in 8 bits (xq, xscale, what disco_glu_bwd needs); y, or either pair, may be None."""
+    n, T, dev = B * C * P, B * P, _on(x, "x")
+    dt = x.dtype
+    f32, i8 = _torch.float32, _torch.int8
+    _check((_lib or load_library()).disco_glu(
+        _in(x, "x", 2 * n, dt, dev), _in(y, "y", n, dt, dev), _in(q, "q", n, i8, dev), _in(scale, "scale", T, f32, dev),
+        _in(xq, "xq", 2 * n, i8, dev), _in(xscale, "xscale", T, f32, dev), act, B, C, P, dtype_code(dt),
+        _raw_stream(dev) if stream is None else _stream(stream)))
+
+
+def disco_glu_bwd(dy, xq, xscale, dx, act: int, B: int, C: int, P: int, stream=None) -> None:
+    """dx of disco_glu for the gradient dy of y, from the kept 8-bit input."""
+    n, dev = B * C * P, _on(dy, "dy")
+    dt = dy.dtype
+    _check((_lib or load_library()).disco_glu_bwd(
+        _in(dy, "dy", n, dt, dev), _in(xq, "xq", 2 * n, _torch.int8, dev), _in(xscale, "xscale", B * P, _torch.float32, dev),
+        _in(dx, "dx", 2 * n, dt, dev), act, B, C, P, dtype_code(dt), _raw_stream(dev) if stream is None else _stream(stream)))
 
 
 def disco_device_status(clear: bool = True) -> int:

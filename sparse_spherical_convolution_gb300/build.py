@@ -30,7 +30,8 @@ LIB_BOUNDS = os.path.join(BUILD, f"libdisco_gb300_{platform.machine()}_bounds.so
 SOURCES = ["disco_capi.cu", "disco_psi.cu", "disco_contract.cu", "disco_fused.cu",
            "disco_fwd_tc.cu", "disco_bwd_tc.cu", "disco_gemm_tc.cu", "disco_host.cu",
            "disco_norm.cu", "disco_norm_tile.cu", "disco_norm_q.cu", "disco_norm_q_any.cu", "disco_norm_bwd.cu",
-           "disco_norm_rows.cu", "disco_dequant.cu", "disco_grad.cu"]
+           "disco_norm_rows.cu", "disco_dequant.cu", "disco_grad.cu",
+           "disco_tokens.cu", "disco_i8_mm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

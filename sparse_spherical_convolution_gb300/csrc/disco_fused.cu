@@ -840,7 +840,7 @@ extern "C" int disco_device_status(int32_t* flags, int32_t clear) {
   int32_t bounds = 0;
   for (auto fn : {contract_bounds, psi_bounds, tc_bounds, btc_bounds, gemm_bounds, fused_bounds, norm_bounds,
                   norm_tile_bounds, norm_q_bounds, norm_q_any_bounds, norm_bwd_bounds, norm_rows_bounds,
-                  dequant_bounds, grad_bounds})
+                  dequant_bounds, grad_bounds, tokens_bounds, i8_mm_bounds})
     if (e == cudaSuccess) e = fn(&bounds, clear != 0);
   *flags |= bounds;
   if (e != cudaSuccess) return fail(DISCO_ERR_CUDA, "device status: %s", cudaGetErrorString(e));

@@ -1,0 +1,114 @@
+// disco_i8.cuh -- what the operators on 8-bit integer activations share: the
+// magnitudes and the rounding of a token's 8-bit form (disco_tokens.cuh), and how
+// the integer products are described (disco_i8_mm.cuh).  Not part of the ABI.
+//
+// A token is one pixel of one sample (P = 1: one row of features).  Its 8-bit form:
+//   a = max(1e-30, max_c |x_c|),  scale = a / 127,  q_c = round(127 x_c / a)
+#pragma once
+
+#include "disco_norm.cuh"
+
+namespace disco {
+namespace i8 {
+
+using norm::check_buffers;
+using norm::check_shape;
+using norm::Buffer;
+using norm::elem_bytes;
+using norm::kSMs;
+
+constexpr float kQMax = 127.0f;
+constexpr float kAmaxFloor = 1e-30f;
+
+// The largest magnitude as the bits of |x|: integers order them like the values,
+// infinities above all finite ones and NaN above infinities, so a NaN is kept.
+__device__ __forceinline__ uint32_t max16(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t max32(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+
+// What a token's values are multiplied by.  For 16-bit inputs the quotient
+// 127 x / a is rounded correctly: k x is exact (11 + 7 bits), inv is the correctly
+// rounded reciprocal of b = a f (f a power of two that keeps all steps within
+// fp32's normal range), and one remainder step t + (k x - t b) inv then gives
+// the correctly rounded quotient (P. Markstein, IBM J. Res. Dev. 34, 1990).  A
+// quotient that is not half of an odd integer lies further from one than fp32's
+// rounding moves it (2^-19 against 2^-24 relative), so q is the definition's, ties included.
+struct Quantizer {
+  float k, b, inv, scale;
+  __device__ __forceinline__ explicit Quantizer(float amax) {  // amax >= 0, or infinite or NaN
+    const float a = amax < kAmaxFloor ? kAmaxFloor : amax;     // keeps NaN
+    const float f = a > 1e30f ? 0x1p-64f : a < 1e-20f ? 0x1p64f : 1.0f;
+    b = a * f;
+    k = kQMax * f;
+    inv = __frcp_rn(b);
+    scale = a / kQMax;
+  }
+};
+
+// round(t) of |t| < 2^22, to nearest even, as the low bits of a float's pattern
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+
+// The low byte of the result is q of one value of a token.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize(float x, const Quantizer& z) {
+  const float kx = z.k * x;
+  float t = kx * z.inv;
+  t = fmaf(fmaf(-t, z.b, kx), z.inv, t);
+  if (!(fabsf(t) < 128.0f)) t = 0.0f;  // a token with an infinity or a NaN: its scale says so
+  return __float_as_uint(t + kRound);
+}
+// fp32 inputs: 127 x takes 31 bits.  Within 2^-14 of a border (the error of t is
+// below 2^-15) the quotient is taken in 64 bits, where it cannot reach the wrong side.
+template <>
+__device__ __forceinline__ uint32_t quantize<float>(float x, const Quantizer& z) {
+  float t = (z.k * x) * z.inv;
+  if (!(fabsf(t) < 128.0f)) t = 0.0f;
+  const float r = (t + kRound) - kRound;
+  if (fabsf(fabsf(t - r) - 0.5f) < 0x1p-14f) t = (float)rint((double)z.k * (double)x / (double)z.b);
+  return __float_as_uint(t + kRound);
+}
+
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The same for a value that is no 16-bit input (the gated activation, in fp32):
+// within a few units of 2^-24 of the quotient, so next to a border either may come out.
+__device__ __forceinline__ uint32_t quantize_near(float y, const Quantizer& z) {
+  float t = (z.k * y) * z.inv;
+  if (!(fabsf(t) < 128.0f)) t = 0.0f;
+  return __float_as_uint(t + kRound);
+}
+
+// act(g) and act'(g).  SiLU: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).
+// GELU: g Phi, Phi + g phi with the normal distribution Phi and its density phi.
+// T: the tensors' type; 16-bit ones take the approximate exponential and
+// division (2^-21 relative, below their rounding of 2^-9 or 2^-12).
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-g));
+  return __fdividef(1.0f, 1.0f + __expf(-g));
+}
+template <typename T>
+__device__ __forceinline__ float act(float g, int kind) {
+  if (kind == DISCO_GELU) return g * (0.5f * erfcf(-0.70710678f * g));
+  return g * sigmoid<T>(g);
+}
+template <typename T>
+__device__ __forceinline__ float act_grad(float g, int kind, float* value) {
+  if (kind == DISCO_GELU) {
+    const float cdf = 0.5f * erfcf(-0.70710678f * g);
+    *value = g * cdf;
+    return fmaf(0.39894228f * g, sizeof(T) == 4 ? expf(-0.5f * g * g) : __expf(-0.5f * g * g), cdf);
+  }
+  const float s = sigmoid<T>(g);
+  *value = g * s;
+  return s * fmaf(g, 1.0f - s, 1.0f);
+}
+
+// The float that a byte of a word of 8-bit integers stands for (E = 0 .. 3), exactly.
+__device__ __forceinline__ float from_byte(uint32_t flipped, int e) {  // flipped: word ^ 0x80808080
+  return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 + e)) - 8388736.0f;
+}
+
+}  // namespace i8
+}  // namespace disco

@@ -111,6 +111,8 @@ cudaError_t norm_rows_bounds(int32_t* v, bool clear);
 cudaError_t norm_bwd_bounds(int32_t* v, bool clear);
 cudaError_t dequant_bounds(int32_t* v, bool clear);
 cudaError_t grad_bounds(int32_t* v, bool clear);
+cudaError_t tokens_bounds(int32_t* v, bool clear);
+cudaError_t i8_mm_bounds(int32_t* v, bool clear);
 // Weight gradient dW[o][j] = sum_b sum_p dy[b][o][p] X[b][j][p] (split reduction
 // through fp32 partials of dw_partial_bytes bytes, then rounded to bf16).
 bool dw_tensor_core_supported(int B, int Cout, int CK, int64_t P);

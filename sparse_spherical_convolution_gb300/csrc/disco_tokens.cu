@@ -1,0 +1,186 @@
+// disco_tokens.cu -- the 8-bit form of an activation's tokens (disco_quant_i8) and
+// the gated activation (disco_glu), on activations [B, C, P]: checks, the choice
+// of a kernel, and the general one.
+//
+//   y = act(x[:, :C]) x[:, C:]                    (disco_glu)
+//   a = max(1e-30, max_c |v_c|), scale = a / 127, q_c = round(127 v_c / a)
+//   for v = x (disco_quant_i8, and the checkpoint of disco_glu) and v = y (disco_glu)
+//
+// The general kernel below takes every shape and reads its inputs once for the
+// largest magnitude and once more for the rounding.
+
+#include "disco_tokens.cuh"
+
+namespace disco {
+
+DISCO_BOUNDS_READER(tokens_bounds)
+
+namespace {
+
+using namespace i8;
+
+constexpr int kAnyThreads = 256;
+
+// ROW: a block takes one token (P = 1), its threads the channels.  Else 32 pixels by 8 lanes of channels.
+template <typename T, bool ROW, bool GLU>
+__global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs a, const long long tiles) {
+  __shared__ float part[2][kAnyThreads];
+  const int lx = ROW ? 0 : threadIdx.x & 31, j0 = ROW ? threadIdx.x : threadIdx.x >> 5, step = ROW ? kAnyThreads : kAnyThreads / 32;
+  const long long per_sample = ROW ? 1 : (a.P + 31) / 32;
+  const int NC = GLU ? 2 * a.C : a.C;
+  const T* x = (const T*)a.x;
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const long long b = t / per_sample, p = (t - b * per_sample) * 32 * !ROW + lx;
+    const bool live = p < a.P;
+    const long long x0 = b * NC * a.P + p, y0 = b * a.C * a.P + p;
+    auto value = [&](int c) { return act<T>(to_f32(x[x0 + c * a.P]), a.act) * to_f32(x[x0 + (c + a.C) * a.P]); };
+    // the largest of all threads of a token, NaN above all
+    auto join = [&](float m, float* buf) {
+      buf[threadIdx.x] = m;
+      __syncthreads();
+      uint32_t r = 0;
+      if (ROW) {
+        for (int k = 0; k < kAnyThreads; ++k) r = max(r, __float_as_uint(buf[k]));
+      } else {
+        for (int k = 0; k < kAnyThreads / 32; ++k) r = max(r, __float_as_uint(buf[lx + 32 * k]));
+      }
+      return __uint_as_float(r);
+    };
+    float mx = 0.0f, my = 0.0f;
+    if (live) {
+      if (a.xq)
+        for (int c = j0; c < NC; c += step) mx = __uint_as_float(max32(__float_as_uint(mx), __float_as_uint(to_f32(x[x0 + c * a.P]))));
+      if (GLU && (a.q || a.y))
+        for (int c = j0; c < a.C; c += step) {
+          const float v = value(c);
+          my = __uint_as_float(max32(__float_as_uint(my), __float_as_uint(v)));
+          if (a.y) ((T*)a.y)[y0 + c * a.P] = from_f32<T>(v);
+        }
+    }
+    if (a.xq) {
+      const Quantizer z(join(mx, part[0]));
+      if (live) {
+        if (j0 == 0) a.xscale[b * a.P + p] = z.scale;
+        for (int c = j0; c < NC; c += step) a.xq[x0 + c * a.P] = (int8_t)quantize<T>(to_f32(x[x0 + c * a.P]), z);
+      }
+    }
+    if (GLU && a.q) {
+      const Quantizer z(join(my, part[1]));
+      if (live) {
+        if (j0 == 0) a.scale[b * a.P + p] = z.scale;
+        for (int c = j0; c < a.C; c += step) a.q[y0 + c * a.P] = (int8_t)quantize_near(value(c), z);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, bool GLU>
+int tokens(const TokenArgs& a, cudaStream_t st) {
+  const long long tiles = a.P == 1 ? a.B : a.B * ((a.P + 31) / 32);
+  const int grid = (int)min(tiles, (long long)kSMs * 8);
+  if (a.P == 1) tokens_any_kernel<T, true, GLU><<<grid, kAnyThreads, 0, st>>>(a, tiles);
+  else tokens_any_kernel<T, false, GLU><<<grid, kAnyThreads, 0, st>>>(a, tiles);
+  return check_launch("tokens_any_kernel");
+}
+
+// ---- gradient of the gated activation at the checkpoint --------------------
+
+struct GluBwdArgs {
+  const void* dy;
+  const int8_t* xq;
+  const float* xscale;
+  void* dx;
+  int act, C;
+  long long P, n;  // n = B C P elements of dy
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) glu_bwd_kernel(const GluBwdArgs a) {
+  const T* dy = (const T*)a.dy;
+  T* dx = (T*)a.dx;
+  const long long CP = a.C * a.P;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < a.n; i += gridDim.x * 256LL) {
+    const long long b = i / CP, r = i - b * CP, p = r % a.P, g0 = 2 * b * CP + r;
+    const float s = a.xscale[b * a.P + p];
+    const float g = (float)a.xq[g0] * s, v = (float)a.xq[g0 + CP] * s, d = to_f32(dy[i]);
+    float val;
+    const float der = act_grad<T>(g, a.act, &val);
+    dx[g0] = from_f32<T>(d * v * der);
+    dx[g0 + CP] = from_f32<T>(d * val);
+  }
+}
+
+int check_act(int32_t kind) {
+  if (kind != DISCO_SILU && kind != DISCO_GELU) return fail(DISCO_ERR_UNSUPPORTED, "activation");
+  return DISCO_OK;
+}
+
+}  // namespace
+}  // namespace disco
+
+using namespace disco;
+using namespace disco::i8;
+
+extern "C" int disco_quant_i8(const void* x, void* q, float* scale, int32_t B, int32_t C, int64_t P, disco_dtype dtype,
+                              void* stream) {
+  disco::NvtxScope nvtx_scope("disco_quant_i8");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype))) return rc;
+  if (!x || !q || !scale) return fail(DISCO_ERR_INVALID_ARG, "x, q or scale is null");
+  if ((rc = check_device())) return rc;
+  const size_t n = (size_t)B * C * P;
+  const Buffer in[] = {{x, n * elem_bytes(dtype), "x"}};
+  const Buffer out[] = {{q, n, "q"}, {scale, (size_t)B * P * 4, "scale"}};
+  const unsigned in_place[] = {0};
+  if ((rc = check_buffers(in, in_place, 1, out, 2))) return rc;
+  const TokenArgs a{x, nullptr, nullptr, nullptr, (int8_t*)q, scale, DISCO_SILU, B, C, P};
+#define CALL(T) rc = tokens<T, false>(a, (cudaStream_t)stream)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return rc;
+}
+
+extern "C" int disco_glu(const void* x, void* y, void* q, float* scale, void* xq, float* xscale, disco_activation act,
+                         int32_t B, int32_t C, int64_t P, disco_dtype dtype, void* stream) {
+  disco::NvtxScope nvtx_scope("disco_glu");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype)) || (rc = check_act(act))) return rc;
+  if (C > 1 << 29) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^29 channels");
+  if (!x) return fail(DISCO_ERR_INVALID_ARG, "x is null");
+  if (!y && !q) return fail(DISCO_ERR_INVALID_ARG, "neither y nor q is given");
+  if (!q != !scale) return fail(DISCO_ERR_INVALID_ARG, "q and scale come together");
+  if (!xq != !xscale) return fail(DISCO_ERR_INVALID_ARG, "xq and xscale come together");
+  if ((rc = check_device())) return rc;
+  const size_t n = (size_t)B * C * P, e = elem_bytes(dtype), t = (size_t)B * P * 4;
+  const Buffer in[] = {{x, 2 * n * e, "x"}};
+  const Buffer out[] = {{y, n * e, "y"}, {q, n, "q"}, {scale, t, "scale"}, {xq, 2 * n, "xq"}, {xscale, t, "xscale"}};
+  const unsigned in_place[] = {0};
+  if ((rc = check_buffers(in, in_place, 1, out, 5))) return rc;
+  const TokenArgs a{x, y, (int8_t*)q, scale, (int8_t*)xq, xscale, act, B, C, P};
+#define CALL(T) rc = tokens<T, true>(a, (cudaStream_t)stream)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return rc;
+}
+
+extern "C" int disco_glu_bwd(const void* dy, const void* xq, const float* xscale, void* dx, disco_activation act, int32_t B,
+                             int32_t C, int64_t P, disco_dtype dtype, void* stream) {
+  disco::NvtxScope nvtx_scope("disco_glu_bwd");
+  int rc;
+  if ((rc = check_shape(B, C, P, dtype)) || (rc = check_act(act))) return rc;
+  if (C > 1 << 29) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^29 channels");
+  if (!dy || !xq || !xscale || !dx) return fail(DISCO_ERR_INVALID_ARG, "dy, xq, xscale or dx is null");
+  if ((rc = check_device())) return rc;
+  const size_t n = (size_t)B * C * P, e = elem_bytes(dtype);
+  const Buffer in[] = {{dy, n * e, "dy"}, {xq, 2 * n, "xq"}, {xscale, (size_t)B * P * 4, "xscale"}};
+  const Buffer out[] = {{dx, 2 * n * e, "dx"}};
+  const unsigned in_place[] = {0, 0, 0};
+  if ((rc = check_buffers(in, in_place, 3, out, 1))) return rc;
+  const GluBwdArgs a{dy, (const int8_t*)xq, xscale, dx, act, C, P, (long long)n};
+  const int grid = (int)min((a.n + 255) / 256, (long long)kSMs * 16);
+#define CALL(T) glu_bwd_kernel<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return check_launch("glu_bwd_kernel");
+}
