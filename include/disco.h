@@ -591,7 +591,8 @@ DISCO_API int disco_glu_bwd(const void* dy, const void* xq, const float* xscale,
    input-row group reading more output rows than it can hold, bit 4 = the
    wait of disco_check_wait_timeout ran out, bit 5 = in the bounds-checked
    build, a gather index or a TMA or bulk-copy coordinate fell outside the
-   tensor it addresses; a kernel that times out stops issuing work, frees its
+   tensor it addresses, bit 6 = a wait of an 8-bit integer product or gradient
+   timed out; a kernel that times out stops issuing work, frees its
    tensor memory and returns, leaving its outputs incomplete).  clear != 0
    resets the word.  Returns DISCO_ERR_DEVICE_BOUNDS (with *flags filled in)
    when bit 5 is set, else DISCO_OK or a CUDA error. */

@@ -837,10 +837,13 @@ extern "C" int disco_device_status(int32_t* flags, int32_t clear) {
   if (e == cudaSuccess) e = tc_status(flags, clear != 0);
   if (e == cudaSuccess) e = btc_status(flags, clear != 0);
   if (e == cudaSuccess) e = gemm_status(flags, clear != 0);
+  for (auto fn : {i8_fwd_status, i8_dx_status, i8_dw_status})
+    if (e == cudaSuccess) e = fn(flags, clear != 0);
   int32_t bounds = 0;
   for (auto fn : {contract_bounds, psi_bounds, tc_bounds, btc_bounds, gemm_bounds, fused_bounds, norm_bounds,
                   norm_tile_bounds, norm_q_bounds, norm_q_any_bounds, norm_bwd_bounds, norm_rows_bounds,
-                  dequant_bounds, grad_bounds, tokens_bounds, i8_mm_bounds})
+                  dequant_bounds, grad_bounds, tokens_bounds, i8_mm_bounds,
+                  i8_fwd_bounds, i8_dx_bounds, i8_dw_bounds})
     if (e == cudaSuccess) e = fn(&bounds, clear != 0);
   *flags |= bounds;
   if (e != cudaSuccess) return fail(DISCO_ERR_CUDA, "device status: %s", cudaGetErrorString(e));

@@ -19,69 +19,69 @@ namespace {
 
 using namespace i8;
 
-constexpr int kTile = 32, kAnyThreads = 256;
+constexpr int kAnyThreads = 256;
 
-__device__ __forceinline__ float element(const Operand& o, long long i, int f16) {
-  if (o.bits == 8) return (float)((const int8_t*)o.p)[i];
-  return f16 ? __half2float(((const __half*)o.p)[i]) : __bfloat162float(((const __nv_bfloat16*)o.p)[i]);
-}
-
-// 32 x 32 outputs to a block, four to a thread; 32 k at a time through shared memory.
+// The parts' sums in their order, scaled and rounded.
 template <typename TO>
-__global__ void __launch_bounds__(kAnyThreads) mm_any_kernel(const MmArgs a) {
-  __shared__ float sa[kTile][kTile + 1], sb[kTile][kTile + 1];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const long long mt = (a.M + kTile - 1) / kTile, nt = (a.N + kTile - 1) / kTile;
-  const int f16 = a.f16;
-  for (long long t = blockIdx.x; t < mt * nt * a.Z; t += gridDim.x) {
-    const long long n0 = t % nt * kTile, m0 = t / nt % mt * kTile, z = t / (nt * mt);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = 0; r < a.R; ++r)
-      for (long long k0 = 0; k0 < a.K; k0 += kTile) {
-        // neighbouring threads read neighbouring elements: of a row, or of 32 rows' k
-        auto fill = [&](const Operand& o, long long i0, long long I, float (*s)[kTile + 1]) {
-          for (int u = ty; u < kTile; u += 8) {
-            const int i = o.k_major ? u : tx, k = o.k_major ? tx : u;
-            float v = 0.0f;
-            if (i0 + i < I && k0 + k < a.K) {
-              const long long zr = z * o.z + r * o.r;
-              v = element(o, zr + (o.k_major ? (i0 + i) * o.ld + k0 + k : (k0 + k) * o.ld + i0 + i), f16);
-              if (o.ks) v *= o.ks[r * o.ks_r + k0 + k];
-            }
-            s[k][i] = v;
-          }
-        };
-        fill(a.A, m0, a.M, sa);
-        fill(a.B, n0, a.N, sb);
-        __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < kTile; ++k) {
-          const float w = sb[k][tx];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[u] = fmaf(sa[k][ty + 8 * u], w, acc[u]);
-        }
-        __syncthreads();
-      }
-    const long long n = n0 + tx;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const long long m = m0 + ty + 8 * u;
-      if (m >= a.M || n >= a.N) continue;
-      float v = acc[u];
-      if (a.cs) v *= a.cs[z * a.cs_z + n];
-      if (a.rs) v *= a.rs[m];
-      ((TO*)a.out)[(z * a.M + m) * a.N + n] = from_f32<TO>(v);
-    }
+__global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, const float* part, int nsplit, long long n) {
+  for (long long i = (long long)blockIdx.x * kAnyThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kAnyThreads) {
+    float v = 0.0f;
+    for (int s = 0; s < nsplit; ++s) v += part[s * n + i];
+    const long long r = i / a.N, c = i - r * a.N;
+    if (a.cs) v *= a.cs[r / a.M * a.cs_z + c];
+    if (a.rs) v *= a.rs[r % a.M];
+    ((TO*)a.out)[i] = from_f32<TO>(v);
   }
 }
 
-int run(const MmArgs& a, disco_dtype dtype, cudaStream_t st) {
-  const long long tiles = (a.M + kTile - 1) / kTile * ((a.N + kTile - 1) / kTile) * a.Z;
-  const int grid = (int)min(tiles, (long long)kSMs * 16);
-#define CALL(T) mm_any_kernel<T><<<grid, kAnyThreads, 0, st>>>(a)
+// The cut of a product by its sizes alone (the workspace's bytes follow from it).
+// Tiles of 256 n; where they do not fill the SMs, the reduction is split into
+// parts of 8 steps at least, and where that leaves half of the SMs idle, tiles get narrower.
+struct Cut {
+  int NB, nsplit;
+  long long mt, nt, nkp, steps;
+  Cut(long long M, long long N, long long K, int Z, int R) {
+    mt = (M + 127) / 128;
+    nkp = (K + 63) / 64;
+    steps = nkp * R;
+    NB = N >= 256 ? 256 : (int)((N + 63) / 64 * 64);
+    for (;;) {
+      nt = (N + NB - 1) / NB;
+      const long long tiles = mt * nt * Z;
+      nsplit = (int)max(1LL, min(steps / 8, kSMs / tiles));
+      if (tiles * nsplit >= kSMs / 2 || NB == 64) break;
+      NB = NB > 128 ? 128 : 64;
+    }
+  }
+  size_t bytes(long long M, long long N, int Z) const { return nsplit > 1 ? (size_t)nsplit * Z * M * N * 4 : 16; }
+};
+
+bool rows_aligned(const Operand& o) {
+  const int es = o.bits / 8;
+  return o.ld * es % 16 == 0 && o.z * es % 16 == 0 && o.r * es % 16 == 0;
+}
+
+int run(const MmArgs& m, disco_dtype dtype, void* ws, int (*tc)(const TcArgs&, bool, cudaStream_t), cudaStream_t st) {
+  const Cut c(m.M, m.N, m.K, m.Z, m.R);
+  TcArgs a = {};
+  a.m = m;
+  a.enda = (const uint8_t*)m.A.p + m.A.n * (m.A.bits / 8);
+  a.endb = (const uint8_t*)m.B.p + m.B.n * (m.B.bits / 8);
+  a.NB = c.NB, a.nsplit = c.nsplit, a.mt = c.mt, a.nt = c.nt, a.nkp = c.nkp, a.steps = c.steps;
+  a.part = c.nsplit > 1 ? (float*)ws : nullptr;
+  a.out_type = dtype;
+  a.vec = m.N * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
+  a.tiles = c.mt * c.nt * m.Z * c.nsplit;
+  // the copy engine's coordinates are 32-bit
+  const bool aligned = rows_aligned(m.A) && rows_aligned(m.B) && max(max(m.M, m.N), m.K) < 1LL << 31 && max(m.A.n, m.B.n) < 1LL << 38;
+  int rc = tc(a, aligned, st);
+  if (rc || !a.part) return rc;
+  const long long n = m.Z * m.M * m.N;
+  const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
+#define CALL(T) mm_join_kernel<T><<<grid, kAnyThreads, 0, st>>>(m, a.part, c.nsplit, n)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
-  return check_launch("mm_any_kernel");
+  return check_launch("mm_join_kernel");
 }
 
 // Sizes of a product; 16-bit types only for the gradients.
@@ -107,17 +107,17 @@ using namespace disco::i8;
 
 extern "C" size_t disco_matmul_i8_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, false)) return 0;
-  return 16;
+  return P == 1 ? Cut(B, Cout, Cin, 1, 1).bytes(B, Cout, 1) : Cut(Cout, P, Cin, B, 1).bytes(Cout, P, B);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return 16;
+  return P == 1 ? Cut(B, Cin, Cout, 1, 1).bytes(B, Cin, 1) : Cut(Cin, P, Cout, B, 1).bytes(Cin, P, B);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return 16;
+  return P == 1 ? Cut(Cout, Cin, B, 1, 1).bytes(Cout, Cin, 1) : Cut(Cout, Cin, P, 1, B).bytes(Cout, Cin, 1);
 }
 
 extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W, const float* wscale, void* y, int32_t B,
@@ -139,17 +139,17 @@ extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W,
   a.K = Cin;
   a.R = 1;
   if (P == 1) {  // rows: m = token, n = output channel
-    a.A = {q, nullptr, 0, 0, Cin, 0, 8, true};
-    a.B = {W, nullptr, 0, 0, Cin, 0, 8, true};
+    a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)T * Cin};
+    a.B = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
     a.rs = scale, a.cs = wscale;
     a.M = B, a.N = Cout, a.Z = 1;
   } else {  // m = output channel, n = pixel
-    a.A = {W, nullptr, 0, 0, Cin, 0, 8, true};
-    a.B = {q, nullptr, Cin * P, 0, P, 0, 8, false};
+    a.A = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
+    a.B = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)T * Cin};
     a.rs = wscale, a.cs = scale, a.cs_z = P;
     a.M = Cout, a.N = P, a.Z = B;
   }
-  return run(a, dtype, (cudaStream_t)stream);
+  return run(a, dtype, workspace, tc_fwd, (cudaStream_t)stream);
 }
 
 extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const float* wscale, void* dx, int32_t B, int32_t Cin,
@@ -172,15 +172,15 @@ extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const fl
   a.K = Cout;
   a.R = 1;
   if (P == 1) {  // m = token, n = input channel
-    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, true};
-    a.B = {W, wscale, 0, 0, Cin, 0, 8, false};
+    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, true, (long long)T * Cout};
+    a.B = {W, wscale, 0, 0, Cin, 0, 8, false, (long long)w};
     a.M = B, a.N = Cin, a.Z = 1;
   } else {  // m = input channel, n = pixel
-    a.A = {W, wscale, 0, 0, Cin, 0, 8, false};
-    a.B = {dy, nullptr, Cout * P, 0, P, 0, 16, false};
+    a.A = {W, wscale, 0, 0, Cin, 0, 8, false, (long long)w};
+    a.B = {dy, nullptr, Cout * P, 0, P, 0, 16, false, (long long)T * Cout};
     a.M = Cin, a.N = P, a.Z = B;
   }
-  return run(a, dtype, (cudaStream_t)stream);
+  return run(a, dtype, workspace, tc_dx, (cudaStream_t)stream);
 }
 
 extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const float* scale, void* dW, int32_t B, int32_t Cin,
@@ -202,13 +202,13 @@ extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const f
   a.f16 = dtype == DISCO_F16;
   a.M = Cout, a.N = Cin, a.Z = 1;
   if (P == 1) {  // k = token
-    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, false};
-    a.B = {q, scale, 0, 0, Cin, 0, 8, false};
+    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, false, (long long)T * Cout};
+    a.B = {q, scale, 0, 0, Cin, 0, 8, false, (long long)T * Cin};
     a.K = B, a.R = 1;
   } else {  // k = pixel, summed over the samples too
-    a.A = {dy, nullptr, 0, Cout * P, P, 0, 16, true};
-    a.B = {q, scale, 0, Cin * P, P, P, 8, true};
+    a.A = {dy, nullptr, 0, Cout * P, P, 0, 16, true, (long long)T * Cout};
+    a.B = {q, scale, 0, Cin * P, P, P, 8, true, (long long)T * Cin};
     a.K = P, a.R = B;
   }
-  return run(a, dtype, (cudaStream_t)stream);
+  return run(a, dtype, workspace, tc_dw, (cudaStream_t)stream);
 }

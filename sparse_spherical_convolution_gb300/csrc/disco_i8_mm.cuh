@@ -15,6 +15,7 @@ struct Operand {
   long long z, r, ld, ks_r;
   int bits;  // 8: integers, 16: fp16 or bf16
   bool k_major;
+  long long n;  // elements of the tensor
 };
 
 // out[z][m][n] = rs[m] cs[z cs_z + n] sum_{r < R, k < K} A(m, k) B(n, k); rs and cs may be null.
@@ -25,6 +26,21 @@ struct MmArgs {
   long long cs_z, M, N, K;
   int Z, R, f16;
 };
+
+// How the tensor-core kernel cuts a product (disco_i8_tc.cuh): tiles of 128 m x NB n
+// of each z, their reduction of `steps` chunks of 64 k in nsplit parts.
+struct TcArgs {
+  MmArgs m;
+  const uint8_t *enda, *endb;  // ends of the operands' tensors
+  float* part;                 // fp32 sums of the parts [nsplit][Z][M][N], or null
+  int NB, nsplit, out_type, vec;        // vec: rows of what it writes start on 16 bytes
+  long long mt, nt, tiles, nkp, steps;  // tiles of the call (with parts); 64-k chunks of a slice r, of all
+};
+
+// aligned: every row of every operand starts on 16 bytes
+int tc_fwd(const TcArgs& a, bool aligned, cudaStream_t st);
+int tc_dx(const TcArgs& a, bool aligned, cudaStream_t st);
+int tc_dw(const TcArgs& a, bool aligned, cudaStream_t st);
 
 }  // namespace i8
 }  // namespace disco

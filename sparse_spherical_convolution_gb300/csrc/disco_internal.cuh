@@ -113,6 +113,13 @@ cudaError_t dequant_bounds(int32_t* v, bool clear);
 cudaError_t grad_bounds(int32_t* v, bool clear);
 cudaError_t tokens_bounds(int32_t* v, bool clear);
 cudaError_t i8_mm_bounds(int32_t* v, bool clear);
+cudaError_t i8_fwd_bounds(int32_t* v, bool clear);
+cudaError_t i8_dx_bounds(int32_t* v, bool clear);
+cudaError_t i8_dw_bounds(int32_t* v, bool clear);
+// Status words of the integer products' tensor-core units.
+cudaError_t i8_fwd_status(int32_t* v, bool clear);
+cudaError_t i8_dx_status(int32_t* v, bool clear);
+cudaError_t i8_dw_status(int32_t* v, bool clear);
 // Weight gradient dW[o][j] = sum_b sum_p dy[b][o][p] X[b][j][p] (split reduction
 // through fp32 partials of dw_partial_bytes bytes, then rounded to bf16).
 bool dw_tensor_core_supported(int B, int Cout, int CK, int64_t P);
