@@ -6,8 +6,9 @@
 //   a = max(1e-30, max_c |v_c|), scale = a / 127, q_c = round(127 v_c / a)
 //   for v = x (disco_quant_i8, and the checkpoint of disco_glu) and v = y (disco_glu)
 //
-// The general kernel below takes every shape and reads its inputs once for the
-// largest magnitude and once more for the rounding.
+// Tokens that a CTA holds in registers go by disco_tokens.cuh.  The general kernel
+// below takes every other one and reads its inputs once for the largest magnitude
+// and once more for the rounding.
 
 #include "disco_tokens.cuh"
 
@@ -75,8 +76,29 @@ __global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs
   }
 }
 
+// J words to a thread: few while the channels leave a tile rows of 64 bytes (many
+// CTAs to an SM), else twice as many.
+template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
+int held(const TokenArgs& a, cudaStream_t st) {
+  constexpr int most = kTokenThreads / (V > 1 ? 4 : 16) * J;  // channels
+  if (a.P == 1 ? a.C <= kTokenThreads * J * V : a.C <= most) return tokens_held<T, V, J, GLU, XQ, YQ>(a, st);
+  return tokens_held<T, V, 2 * J, GLU, XQ, YQ>(a, st);
+}
+template <typename T, int V>
+int held(const TokenArgs& a, bool glu, cudaStream_t st) {
+  constexpr int M = V == 1 ? 2 : 1;
+  if (!glu) return held<T, V, 8 * M, false, true, false>(a, st);
+  if (a.xq && a.q) return held<T, V, 2 * M, true, true, true>(a, st);
+  if (a.xq) return held<T, V, 4 * M, true, true, false>(a, st);
+  if (a.q) return held<T, V, 4 * M, true, false, true>(a, st);
+  return tokens_held<T, V, 4, true, false, false>(a, st);
+}
+
 template <typename T, bool GLU>
 int tokens(const TokenArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int rc = (a.P == 1 ? a.C : a.P) % V == 0 ? held<T, V>(a, GLU, st) : held<T, 1>(a, GLU, st);
+  if (rc != DISCO_ERR_UNSUPPORTED) return rc;
   const long long tiles = a.P == 1 ? a.B : a.B * ((a.P + 31) / 32);
   const int grid = (int)min(tiles, (long long)kSMs * 8);
   if (a.P == 1) tokens_any_kernel<T, true, GLU><<<grid, kAnyThreads, 0, st>>>(a, tiles);
@@ -95,20 +117,57 @@ struct GluBwdArgs {
   long long P, n;  // n = B C P elements of dy
 };
 
-template <typename T>
+// Words of V neighbouring elements; a word is inside one channel's pixels (grids:
+// V divides P) or one row's gates (rows: V divides C).  ROW: P = 1.
+template <typename T, int V, bool ROW>
 __global__ void __launch_bounds__(256) glu_bwd_kernel(const GluBwdArgs a) {
-  const T* dy = (const T*)a.dy;
-  T* dx = (T*)a.dx;
+  using WQ = typename Word<V>::type;
+  const long long i = (blockIdx.x * 256LL + threadIdx.x) * V;
+  if (i >= a.n) return;
   const long long CP = a.C * a.P;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < a.n; i += gridDim.x * 256LL) {
-    const long long b = i / CP, r = i - b * CP, p = r % a.P, g0 = 2 * b * CP + r;
-    const float s = a.xscale[b * a.P + p];
-    const float g = (float)a.xq[g0] * s, v = (float)a.xq[g0 + CP] * s, d = to_f32(dy[i]);
+  const long long b = a.n <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)CP) : i / CP;
+  const long long r = i - b * CP, g0 = 2 * b * CP + r;
+  float s[V];
+  const WQ wg = load_stream<WQ>(a.xq + g0), wv = load_stream<WQ>(a.xq + g0 + CP);
+  const F<V> d = unpack<T, V>(load_stream<Raw<T, V>>((const T*)a.dy + i));
+  if constexpr (ROW) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = a.xscale[b];
+  } else {
+    const long long p = r <= 0xffffffffLL && a.P <= 0xffffffffLL ? (long long)((uint32_t)r % (uint32_t)a.P) : r % a.P;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(a.xscale + b * a.P + p + e);
+        s[e] = f.x, s[e + 1] = f.y, s[e + 2] = f.z, s[e + 3] = f.w;
+      }
+    } else {
+      s[0] = a.xscale[b * a.P + p];
+    }
+  }
+  uint32_t qg[(V + 3) / 4] = {}, qv[(V + 3) / 4] = {};
+  memcpy(qg, &wg, V);
+  memcpy(qv, &wv, V);
+  F<V> dg, dv;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float g = from_byte(qg[e / 4] ^ 0x80808080u, e & 3) * s[e], v = from_byte(qv[e / 4] ^ 0x80808080u, e & 3) * s[e];
     float val;
     const float der = act_grad<T>(g, a.act, &val);
-    dx[g0] = from_f32<T>(d * v * der);
-    dx[g0 + CP] = from_f32<T>(d * val);
+    dg.v[e] = d.v[e] * v * der;
+    dv.v[e] = d.v[e] * val;
   }
+  store_stream((T*)a.dx + g0, packed<T, V>(dg));
+  store_stream((T*)a.dx + g0 + CP, packed<T, V>(dv));
+}
+
+template <typename T, int V>
+int glu_bwd(const GluBwdArgs& a, cudaStream_t st) {
+  const long long grid = (a.n / V + 255) / 256;
+  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^39 elements");
+  if (a.P == 1) glu_bwd_kernel<T, V, true><<<(unsigned)grid, 256, 0, st>>>(a);
+  else glu_bwd_kernel<T, V, false><<<(unsigned)grid, 256, 0, st>>>(a);
+  return check_launch("glu_bwd_kernel");
 }
 
 int check_act(int32_t kind) {
@@ -178,9 +237,10 @@ extern "C" int disco_glu_bwd(const void* dy, const void* xq, const float* xscale
   const unsigned in_place[] = {0, 0, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 1))) return rc;
   const GluBwdArgs a{dy, (const int8_t*)xq, xscale, dx, act, C, P, (long long)n};
-  const int grid = (int)min((a.n + 255) / 256, (long long)kSMs * 16);
-#define CALL(T) glu_bwd_kernel<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a)
+#define CALL(T)                                                                          \
+  if ((P == 1 ? C : P) % (16 / (int)sizeof(T)) == 0) rc = glu_bwd<T, 16 / (int)sizeof(T)>(a, (cudaStream_t)stream); \
+  else rc = glu_bwd<T, 1>(a, (cudaStream_t)stream)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
-  return check_launch("glu_bwd_kernel");
+  return rc;
 }
