@@ -10,16 +10,15 @@ DISCO_I8_STATUS_READER(i8_dx_status)
 
 namespace i8 {
 
-template <bool HALF, bool ALN>
+template <bool HALF>
 int dx(const TcArgs& a, cudaStream_t st) {
-  if (a.m.A.bits == 16) return tc_launch<Form<2, true, 0>, Form<1, false, 1>, HALF, ALN>(a, st);  // rows
-  return tc_launch<Form<1, false, 1>, Form<2, false, 0>, HALF, ALN>(a, st);
+  using Rows = Form<2, true, 0>;
+  using Grid = Form<2, false, 0>;
+  if (a.m.A.k_major) return a.ala ? tc_launch<Rows, false, HALF, true, true, false>(a, st) : tc_launch<Rows, false, HALF, false, true, false>(a, st);
+  return a.ala ? tc_launch<Grid, false, HALF, true, true, true>(a, st) : tc_launch<Grid, false, HALF, false, true, true>(a, st);
 }
 
-int tc_dx(const TcArgs& a, bool aligned, cudaStream_t st) {
-  if (a.m.f16) return aligned ? dx<true, true>(a, st) : dx<true, false>(a, st);
-  return aligned ? dx<false, true>(a, st) : dx<false, false>(a, st);
-}
+int tc_dx(const TcArgs& a, cudaStream_t st) { return a.m.f16 ? dx<true>(a, st) : dx<false>(a, st); }
 
 }  // namespace i8
 }  // namespace disco

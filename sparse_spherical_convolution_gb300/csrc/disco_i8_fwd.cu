@@ -9,11 +9,11 @@ DISCO_I8_STATUS_READER(i8_fwd_status)
 
 namespace i8 {
 
-int tc_fwd(const TcArgs& a, bool aligned, cudaStream_t st) {
-  using K8 = Form<1, true, 0>;
-  using N8 = Form<1, false, 0>;
-  if (a.m.B.k_major) return aligned ? tc_launch<K8, K8, true, true>(a, st) : tc_launch<K8, K8, true, false>(a, st);
-  return aligned ? tc_launch<K8, N8, true, true>(a, st) : tc_launch<K8, N8, true, false>(a, st);
+int tc_fwd(const TcArgs& a, cudaStream_t st) {
+  using Rows = Form<1, true, 0>;
+  using Grid = Form<1, false, 0>;
+  if (a.m.A.k_major) return a.ala ? tc_launch<Rows, true, true, true, true, false>(a, st) : tc_launch<Rows, true, true, false, true, false>(a, st);
+  return a.ala ? tc_launch<Grid, true, true, true, true, true>(a, st) : tc_launch<Grid, true, true, false, true, true>(a, st);
 }
 
 }  // namespace i8

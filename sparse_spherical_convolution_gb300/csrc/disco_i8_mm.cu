@@ -6,8 +6,8 @@
 //   dx[b,c,p] = sum_o wscale[o] W[o,c] dy[b,o,p]                (disco_matmul_i8_bwd_input)
 //   dW[o,c]   = sum_{b,p} dy[b,o,p] scale[b,p] q[b,c,p]         (disco_matmul_i8_bwd_weight)
 //
-// Each is out[z][m][n] = rs[m] cs[n] sum_k ks[k] A(m, k) B(n, k), row-major with n
-// the contiguous direction of the output: pixels (grids) or channels (rows).
+// Each is a product sum_k A(m, k) B(n, k) with scales on m, n or A's k, A the
+// activation (m = token; the channel of its weight's gradient).
 
 #include "disco_i8_mm.cuh"
 
@@ -27,11 +27,29 @@ __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, co
   for (long long i = (long long)blockIdx.x * kAnyThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kAnyThreads) {
     float v = 0.0f;
     for (int s = 0; s < nsplit; ++s) v += part[s * n + i];
-    const long long r = i / a.N, c = i - r * a.N;
-    if (a.cs) v *= a.cs[r / a.M * a.cs_z + c];
-    if (a.rs) v *= a.rs[r % a.M];
+    if (a.cs) {
+      const long long cols = a.transposed ? a.M : a.N, rows = a.transposed ? a.N : a.M;
+      const long long r = i / cols, c = i - r * cols, z = r / rows, rr = r - z * rows;
+      v *= a.cs[a.transposed ? rr : c];
+      v *= a.rs[z * a.rs_z + (a.transposed ? c : rr)];
+    }
     ((TO*)a.out)[i] = from_f32<TO>(v);
   }
+}
+
+// A weight [Cout][Cin] as the 16-bit operand: the integers in fp16, or times their
+// channel's scale rounded to the type; rows padded to `ld` elements with zeros.
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads) mm_weight_kernel(const int8_t* W, const float* wscale, T* w16, int Cin, int ld, long long n) {
+  const long long i = ((long long)blockIdx.x * kAnyThreads + threadIdx.x) * 8;
+  if (i >= n) return;
+  const long long o = i / ld;
+  const int c = (int)(i - o * ld);
+  const float f = wscale ? wscale[o] : 1.0f;
+  T v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(c + e < Cin ? (float)W[o * Cin + c + e] * f : 0.0f);
+  *reinterpret_cast<uint4*>(w16 + i) = *reinterpret_cast<const uint4*>(v);
 }
 
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).
@@ -44,37 +62,44 @@ struct Cut {
     mt = (M + 127) / 128;
     nkp = (K + 63) / 64;
     steps = nkp * R;
-    NB = N >= 256 ? 256 : (int)((N + 63) / 64 * 64);
+    NB = N >= 256 ? 256 : (int)((N + 15) / 16 * 16);
     for (;;) {
       nt = (N + NB - 1) / NB;
       const long long tiles = mt * nt * Z;
       nsplit = (int)max(1LL, min(steps / 8, kSMs / tiles));
-      if (tiles * nsplit >= kSMs / 2 || NB == 64) break;
+      if (tiles * nsplit >= kSMs / 2 || NB <= 64) break;
       NB = NB > 128 ? 128 : 64;
     }
   }
-  size_t bytes(long long M, long long N, int Z) const { return nsplit > 1 ? (size_t)nsplit * Z * M * N * 4 : 16; }
+  size_t part_bytes(long long M, long long N, int Z) const { return nsplit > 1 ? (size_t)nsplit * Z * M * N * 4 : 0; }
 };
+
+// What a call needs of the workspace: the 16-bit weight, then the parts' sums.
+size_t weight_bytes(int32_t Cin, int32_t Cout) { return ((size_t)Cout * (((size_t)Cin + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+
+Cut cut_fwd(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(B, Cout, Cin, 1, 1) : Cut(P, Cout, Cin, B, 1); }
+Cut cut_dx(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(B, Cin, Cout, 1, 1) : Cut(P, Cin, Cout, B, 1); }
+Cut cut_dw(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(Cin, Cout, B, 1, 1) : Cut(Cin, Cout, P, 1, B); }
 
 bool rows_aligned(const Operand& o) {
   const int es = o.bits / 8;
   return o.ld * es % 16 == 0 && o.z * es % 16 == 0 && o.r * es % 16 == 0;
 }
 
-int run(const MmArgs& m, disco_dtype dtype, void* ws, int (*tc)(const TcArgs&, bool, cudaStream_t), cudaStream_t st) {
-  const Cut c(m.M, m.N, m.K, m.Z, m.R);
+int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) {
   TcArgs a = {};
   a.m = m;
   a.enda = (const uint8_t*)m.A.p + m.A.n * (m.A.bits / 8);
   a.endb = (const uint8_t*)m.B.p + m.B.n * (m.B.bits / 8);
   a.NB = c.NB, a.nsplit = c.nsplit, a.mt = c.mt, a.nt = c.nt, a.nkp = c.nkp, a.steps = c.steps;
-  a.part = c.nsplit > 1 ? (float*)ws : nullptr;
+  a.part = c.nsplit > 1 ? (float*)part : nullptr;
   a.out_type = dtype;
-  a.vec = m.N * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
+  a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
   a.tiles = c.mt * c.nt * m.Z * c.nsplit;
-  // the copy engine's coordinates are 32-bit
-  const bool aligned = rows_aligned(m.A) && rows_aligned(m.B) && max(max(m.M, m.N), m.K) < 1LL << 31 && max(m.A.n, m.B.n) < 1LL << 38;
-  int rc = tc(a, aligned, st);
+  // the copy engine's coordinates are 32-bit, its strides below 2^40 bytes
+  const bool small = max(max(m.M, m.N), m.K) < 1LL << 31 && max(m.A.n, m.B.n) < 1LL << 38;
+  a.ala = small && rows_aligned(m.A), a.alb = small && rows_aligned(m.B);
+  int rc = tc(a, st);
   if (rc || !a.part) return rc;
   const long long n = m.Z * m.M * m.N;
   const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
@@ -82,6 +107,14 @@ int run(const MmArgs& m, disco_dtype dtype, void* ws, int (*tc)(const TcArgs&, b
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
   return check_launch("mm_join_kernel");
+}
+
+int weight_16(const void* W, const float* wscale, void* w16, int32_t Cin, int32_t Cout, bool f16, cudaStream_t st) {
+  const int ld = (int)(((long long)Cin + 7) / 8 * 8);
+  const long long n = (long long)Cout * ld, grid = (n / 8 + kAnyThreads - 1) / kAnyThreads;
+  if (f16) mm_weight_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)W, wscale, (__half*)w16, Cin, ld, n);
+  else mm_weight_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)W, wscale, (__nv_bfloat16*)w16, Cin, ld, n);
+  return check_launch("mm_weight_kernel");
 }
 
 // Sizes of a product; 16-bit types only for the gradients.
@@ -107,17 +140,17 @@ using namespace disco::i8;
 
 extern "C" size_t disco_matmul_i8_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, false)) return 0;
-  return P == 1 ? Cut(B, Cout, Cin, 1, 1).bytes(B, Cout, 1) : Cut(Cout, P, Cin, B, 1).bytes(Cout, P, B);
+  return weight_bytes(Cin, Cout) + cut_fwd(B, Cin, Cout, P).part_bytes((long long)B * P, Cout, 1);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return P == 1 ? Cut(B, Cin, Cout, 1, 1).bytes(B, Cin, 1) : Cut(Cin, P, Cout, B, 1).bytes(Cin, P, B);
+  return weight_bytes(Cin, Cout) + cut_dx(B, Cin, Cout, P).part_bytes((long long)B * P, Cin, 1);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return P == 1 ? Cut(Cout, Cin, B, 1, 1).bytes(Cout, Cin, 1) : Cut(Cout, Cin, P, 1, B).bytes(Cout, Cin, 1);
+  return max((size_t)16, cut_dw(B, Cin, Cout, P).part_bytes(Cin, Cout, 1));
 }
 
 extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W, const float* wscale, void* y, int32_t B,
@@ -134,22 +167,22 @@ extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W,
   const Buffer out[] = {{y, T * Cout * elem_bytes(dtype), "y"}, {workspace, need, "workspace"}};
   const unsigned in_place[] = {0, 0, 0, 0};
   if ((rc = check_buffers(in, in_place, 4, out, 2))) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = weight_16(W, nullptr, workspace, Cin, Cout, true, st))) return rc;
+  const long long ld = ((long long)Cin + 7) / 8 * 8;
   MmArgs a = {};
   a.out = y;
-  a.K = Cin;
-  a.R = 1;
-  if (P == 1) {  // rows: m = token, n = output channel
-    a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)T * Cin};
-    a.B = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
-    a.rs = scale, a.cs = wscale;
-    a.M = B, a.N = Cout, a.Z = 1;
-  } else {  // m = output channel, n = pixel
-    a.A = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
-    a.B = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)T * Cin};
-    a.rs = wscale, a.cs = scale, a.cs_z = P;
-    a.M = Cout, a.N = P, a.Z = B;
+  a.rs = scale, a.cs = wscale;
+  a.N = Cout, a.K = Cin, a.R = 1;
+  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, true, Cout * ld};
+  if (P == 1) {  // m = row
+    a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)(T * Cin)};
+    a.M = B, a.Z = 1;
+  } else {  // m = pixel
+    a.A = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)(T * Cin)};
+    a.M = P, a.Z = B, a.rs_z = P, a.transposed = true;
   }
-  return run(a, dtype, workspace, tc_fwd, (cudaStream_t)stream);
+  return run(a, cut_fwd(B, Cin, Cout, P), dtype, (char*)workspace + weight_bytes(Cin, Cout), tc_fwd, st);
 }
 
 extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const float* wscale, void* dx, int32_t B, int32_t Cin,
@@ -166,21 +199,22 @@ extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const fl
   const Buffer out[] = {{dx, T * Cin * 2, "dx"}, {workspace, need, "workspace"}};
   const unsigned in_place[] = {0, 0, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 2))) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = weight_16(W, wscale, workspace, Cin, Cout, dtype == DISCO_F16, st))) return rc;
+  const long long ld = ((long long)Cin + 7) / 8 * 8;
   MmArgs a = {};
   a.out = dx;
   a.f16 = dtype == DISCO_F16;
-  a.K = Cout;
-  a.R = 1;
-  if (P == 1) {  // m = token, n = input channel
-    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, true, (long long)T * Cout};
-    a.B = {W, wscale, 0, 0, Cin, 0, 8, false, (long long)w};
-    a.M = B, a.N = Cin, a.Z = 1;
-  } else {  // m = input channel, n = pixel
-    a.A = {W, wscale, 0, 0, Cin, 0, 8, false, (long long)w};
-    a.B = {dy, nullptr, Cout * P, 0, P, 0, 16, false, (long long)T * Cout};
-    a.M = Cin, a.N = P, a.Z = B;
+  a.N = Cin, a.K = Cout, a.R = 1;
+  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, false, Cout * ld};
+  if (P == 1) {  // m = row
+    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, true, (long long)(T * Cout)};
+    a.M = B, a.Z = 1;
+  } else {  // m = pixel
+    a.A = {dy, nullptr, Cout * P, 0, P, 0, 16, false, (long long)(T * Cout)};
+    a.M = P, a.Z = B, a.transposed = true;
   }
-  return run(a, dtype, workspace, tc_dx, (cudaStream_t)stream);
+  return run(a, cut_dx(B, Cin, Cout, P), dtype, (char*)workspace + weight_bytes(Cin, Cout), tc_dx, st);
 }
 
 extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const float* scale, void* dW, int32_t B, int32_t Cin,
@@ -200,15 +234,15 @@ extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const f
   MmArgs a = {};
   a.out = dW;
   a.f16 = dtype == DISCO_F16;
-  a.M = Cout, a.N = Cin, a.Z = 1;
-  if (P == 1) {  // k = token
-    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, false, (long long)T * Cout};
-    a.B = {q, scale, 0, 0, Cin, 0, 8, false, (long long)T * Cin};
+  a.M = Cin, a.N = Cout, a.Z = 1, a.transposed = true;  // m = input channel
+  if (P == 1) {  // k = row
+    a.A = {q, scale, 0, 0, Cin, 0, 8, false, (long long)(T * Cin)};
+    a.B = {dy, nullptr, 0, 0, Cout, 0, 16, false, (long long)(T * Cout)};
     a.K = B, a.R = 1;
   } else {  // k = pixel, summed over the samples too
-    a.A = {dy, nullptr, 0, Cout * P, P, 0, 16, true, (long long)T * Cout};
-    a.B = {q, scale, 0, Cin * P, P, P, 8, true, (long long)T * Cin};
+    a.A = {q, scale, 0, Cin * P, P, P, 8, true, (long long)(T * Cin)};
+    a.B = {dy, nullptr, 0, Cout * P, P, 0, 16, true, (long long)(T * Cout)};
     a.K = P, a.R = B;
   }
-  return run(a, dtype, workspace, tc_dw, (cudaStream_t)stream);
+  return run(a, cut_dw(B, Cin, Cout, P), dtype, workspace, tc_dw, (cudaStream_t)stream);
 }

@@ -18,13 +18,15 @@ struct Operand {
   long long n;  // elements of the tensor
 };
 
-// out[z][m][n] = rs[m] cs[z cs_z + n] sum_{r < R, k < K} A(m, k) B(n, k); rs and cs may be null.
+// out[z][m][n] = rs[z rs_z + m] cs[n] sum_{r < R, k < K} A(m, k) B(n, k), or with
+// `transposed` out[z][n][m]; rs and cs may both be null.
 struct MmArgs {
   Operand A, B;
   const float *rs, *cs;
   void* out;
-  long long cs_z, M, N, K;
+  long long rs_z, M, N, K;
   int Z, R, f16;
+  bool transposed;
 };
 
 // How the tensor-core kernel cuts a product (disco_i8_tc.cuh): tiles of 128 m x NB n
@@ -32,15 +34,15 @@ struct MmArgs {
 struct TcArgs {
   MmArgs m;
   const uint8_t *enda, *endb;  // ends of the operands' tensors
-  float* part;                 // fp32 sums of the parts [nsplit][Z][M][N], or null
+  float* part;                 // fp32 sums of the parts, each laid out as out, or null
   int NB, nsplit, out_type, vec;        // vec: rows of what it writes start on 16 bytes
+  bool ala, alb;                        // rows of A, of B start on 16 bytes
   long long mt, nt, tiles, nkp, steps;  // tiles of the call (with parts); 64-k chunks of a slice r, of all
 };
 
-// aligned: every row of every operand starts on 16 bytes
-int tc_fwd(const TcArgs& a, bool aligned, cudaStream_t st);
-int tc_dx(const TcArgs& a, bool aligned, cudaStream_t st);
-int tc_dw(const TcArgs& a, bool aligned, cudaStream_t st);
+int tc_fwd(const TcArgs& a, cudaStream_t st);
+int tc_dx(const TcArgs& a, cudaStream_t st);
+int tc_dw(const TcArgs& a, cudaStream_t st);
 
 }  // namespace i8
 }  // namespace disco

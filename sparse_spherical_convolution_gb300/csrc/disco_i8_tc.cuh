@@ -4,19 +4,24 @@
 //   out[z][m][n] = rs[m] cs[n] sum_{r, k} A(m, k) B(n, k)
 //
 // sm_103a's tensor cores have no 8-bit integer form worth the name, so integers
-// become fp16 (or the tensors' 16-bit type, where a scale belongs to k) on the way into shared
-// memory: fp16 holds -128 .. 127, their products are exact, and sums are fp32.
-// Persistent kernel of tiles of 128 m x NB n (NB <= 256), 64 k to a stage, four stages:
-//   warps 0-3    epilogue: tcgen05.ld, scales, rounding, stores coalesced along n
-//   warps 4-11   loaders: 16 bytes of integers from memory to a thread and unit, one
-//                step ahead in registers, to 16 bits, into the swizzled stage
-//   warp 12      MMA issuer (one thread); two accumulators of NB TMEM columns, so
+// become fp16 (or the tensors' 16-bit type, where a scale belongs to k): fp16 holds -128 .. 127,
+// their products are exact, and sums are fp32.  A is the activation (8-bit integers,
+// converted on the way into shared memory, or 16-bit); B is 16-bit: a weight converted
+// once a call into the workspace, or dy.  A tile is 128 m x NB n (NB <= 256), 64 k to a
+// stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
+// converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
+// Persistent kernel:
+//   warps 0-3    epilogue: tcgen05.ld, scales, rounding, stores along the output's rows
+//   warps 4-11   converters: integers from the raw ring (aligned rows) or from memory, to
+//                16 bits, into the stage.  All of them take every step in order: a waiter on
+//                a ring's barrier then is never two phases ahead of it, where a wait by parity would pass at once
+//   warp 12      MMA issuer (one thread); two accumulators of 256 TMEM columns, so
 //                the epilogue of a tile overlaps the main loop of the next
-//   warp 13      TMA of an operand that is 16-bit in memory
+//   warp 13      TMA of B, and warp 14 of A: into the stage (16-bit) or the raw ring (integers)
 // Both operands lie in the stage as lines of 64 elements (128 bytes, 128-byte
 // swizzle): element k .. k + 63 of one m or n where k is the contiguous direction
 // in memory, else (MN-major) 64 neighbouring m or n of one k.  So no operand is ever transposed.
-// Rows off 16-byte alignment (ALN false) are read in aligned 16-byte words and
+// Rows off 16-byte alignment are read by the converters in aligned 16-byte words and
 // shifted in registers; a thread's shift stays the same over a tile.
 // All mbarrier waits are bounded (time-out -> status flag, abort).
 #pragma once
@@ -29,30 +34,29 @@
 namespace disco {
 namespace i8 {
 
-constexpr int kEpiWarps = 4, kLoadWarps = 8;  // 14 warps: up to 128 registers a thread
-constexpr int kMmaWarp = kEpiWarps + kLoadWarps, kTmaWarp = kMmaWarp + 1;
-constexpr int kTcThreads = 32 * (kTmaWarp + 1);
-constexpr int kLoaders = 32 * kLoadWarps;
-constexpr int kBM = 128, kBK = 64, kStages = 4, kNBMax = 256;
-constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2;
-constexpr uint32_t kStagePitch = 80;                       // bytes of a row of the epilogue's staging: 64 and 16 against bank conflicts
-constexpr uint32_t kEpiBytes = 32 * kStagePitch;           // of a warp
-constexpr size_t kTcSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * (kEpiBytes + 128) + 256;
+constexpr int kEpiWarps = 4, kConvWarps = 8;
+constexpr int kMmaWarp = kEpiWarps + kConvWarps, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2;
+constexpr int kTcThreads = 32 * (kTmaAWarp + 1);
+constexpr int kConverters = 32 * kConvWarps;
+constexpr int kBM = 128, kBK = 64, kStages = 4, kNBMax = 256, kRaws = 3;
+constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2, kRawBytes = kBM * kBK;
+constexpr uint32_t kEpiBytes = 32 * 64;  // staging of an epilogue warp: 64 bytes of 32 rows
+constexpr size_t kTcSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kRawBytes + kEpiWarps * (kEpiBytes + 128) + 256;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr int kStatusI8Timeout = 1 << 6;
 
 static __device__ int g_i8_status = 0;  // one per translation unit
 __device__ __forceinline__ void i8_flag() { atomicOr(&g_i8_status, kStatusI8Timeout); }
 
-// How an operand lies in memory and what becomes of it.
+// How A lies in memory and what becomes of it.
 //   ES: bytes of an element; KM: k is the contiguous direction
 //   SC: 0 no scale; else integers times ks[k], in the tensors' type
 template <int ES_, bool KM_, int SC_>
 struct Form {
   static constexpr int ES = ES_, SC = SC_;
   static constexpr bool KM = KM_;
-  static constexpr int UPL = ES == 1 ? 4 : 8;    // 16-byte units of a line of 64 elements
-  static constexpr int LPI = kLoaders / UPL;     // lines that the loaders take at a time
+  static constexpr int UPL = ES == 1 ? 4 : 8;         // 16-byte units of a line of 64 elements
+  static constexpr int LPI = kConverters / UPL;       // lines that the converters take at a time
 };
 
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
@@ -147,24 +151,23 @@ __device__ __forceinline__ uint2 to_scaled4(uint32_t w, float s0, float s1, floa
                     pack2_16(from_byte(w, 2) * s2, from_byte(w, 3) * s3, HALF));
 }
 
-// One operand's share of a loader thread.
-template <class F, bool ALN, int LINES>
+// One operand's share of a converter thread.
+template <class F>
 struct Loader {
-  static constexpr int NU = LINES / F::LPI;  // units of this thread in a stage, at most
-  const uint8_t *base, *end, *row;           // the tensor; this slice's
-  long long ld;
-  int u, l0;           // unit of a line, first line
-  long long i0;        // first m or n of the tile
-  int ileft;           // m or n of the tile inside the tensor
+  const uint8_t *base, *end, *row;  // the tensor; this slice's
+  const float* ks;                  // the slice's scales on k
+  long long ld, i0;                 // first m or n of the tile
+  int u, l0, ileft;                 // unit of a line, first line; m or n of the tile inside the tensor
 
   __device__ __forceinline__ void init(const Operand& o, const uint8_t* e, int t) {
     base = (const uint8_t*)o.p, end = e, ld = o.ld * F::ES;
     u = t % F::UPL, l0 = t / F::UPL;
   }
-  __device__ __forceinline__ void tile(const Operand& o, long long z, long long r, long long first, long long I) {
+  __device__ __forceinline__ void tile(const Operand& o, long long z, long long r, long long first, long long I, int lines) {
     row = base + (z * o.z + r * o.r) * F::ES;
+    ks = F::SC ? o.ks + r * o.ks_r : nullptr;
     i0 = first;
-    ileft = (int)min(I - first, (long long)LINES);
+    ileft = (int)min(I - first, (long long)lines);
   }
   // where unit j of the step lies, and how many of its bytes are inside
   __device__ __forceinline__ const uint8_t* at(int j, long long k0, int kleft, int* nb) const {
@@ -178,63 +181,69 @@ struct Loader {
       return row + (k0 + kk) * ld + (i0 + 64 * box) * F::ES + 16 * u;
     }
   }
-  // units j0 .. j0 + N - 1 of the thread
-  template <int N>
-  __device__ __forceinline__ void fetch(Unit<ALN> (&w)[N], int j0, long long k0, int kleft, int lines) const {
+  // the scales of this thread's units of a step: of 16 k (k contiguous), or of its lines
+  static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 64 / F::LPI;
+  __device__ __forceinline__ void scales(float (&s)[NS], long long k0, int kleft) const {
+    if constexpr (F::SC && F::KM) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if ((j0 + j) * F::LPI < lines) {
-        int nb;
-        const uint8_t* p = at(j0 + j, k0, kleft, &nb);
-        load_unit<ALN>(w[j], p, nb, base, end);
-      }
+      for (int i = 0; i < 16; ++i) s[i] = 16 * u + i < kleft ? __ldg(ks + k0 + 16 * u + i) : 0.0f;
+    } else if constexpr (F::SC) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) s[i] = l0 + i * F::LPI < kleft ? __ldg(ks + k0 + l0 + i * F::LPI) : 0.0f;
+    }
   }
-  // all units, four at a time
+  // 16 bytes of unit j into the stage
   template <bool HALF>
-  __device__ __forceinline__ void copy(uint8_t* stage, const float* ks, long long k0, int kleft, int lines) const {
-    constexpr int N = NU < 4 ? NU : 4;
-#pragma unroll 1
-    for (int j0 = 0; j0 * F::LPI < lines; j0 += N) {
-      Unit<ALN> w[N];
-      fetch(w, j0, k0, kleft, lines);
-      put<HALF>(w, j0, stage, ks, k0, kleft, lines);
+  __device__ __forceinline__ void put(const uint4& v, int j, const float (&s)[NS], uint8_t* stage) const {
+    const int line = l0 + j * F::LPI, x = line & 7;
+    uint8_t* d = stage + line * 128;
+    if constexpr (F::ES == 2) {
+      *reinterpret_cast<uint4*>(d + ((u ^ x) << 4)) = v;
+    } else {
+      uint2 a, b, c, e;
+      if constexpr (F::SC == 0) {
+        a = to_half4(v.x), b = to_half4(v.y), c = to_half4(v.z), e = to_half4(v.w);
+      } else if constexpr (F::KM) {
+        a = to_scaled4<HALF>(v.x, s[0], s[1], s[2], s[3]), b = to_scaled4<HALF>(v.y, s[4], s[5], s[6], s[7]);
+        c = to_scaled4<HALF>(v.z, s[8], s[9], s[10], s[11]), e = to_scaled4<HALF>(v.w, s[12], s[13], s[14], s[15]);
+      } else {
+        const float f = s[j % NS];
+        a = to_scaled4<HALF>(v.x, f, f, f, f), b = to_scaled4<HALF>(v.y, f, f, f, f);
+        c = to_scaled4<HALF>(v.z, f, f, f, f), e = to_scaled4<HALF>(v.w, f, f, f, f);
+      }
+      *reinterpret_cast<uint4*>(d + (((2 * u) ^ x) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(d + (((2 * u + 1) ^ x) << 4)) = make_uint4(c.x, c.y, e.x, e.y);
+    }
+  }
+  // a step's lines from memory, up to four units at a time
+  template <bool HALF>
+  __device__ __forceinline__ void copy(uint8_t* stage, const float (&s)[NS], long long k0, int kleft, int lines) const {
+    constexpr int N = F::ES == 1 ? 2 : 4;
+    if (F::ES == 2 && lines % (N * F::LPI)) {  // 64 lines more
+      copy_units<HALF, 2>(stage, s, 0, 2, k0, kleft);
+      copy_units<HALF, N>(stage, s, 2, lines / F::LPI, k0, kleft);
+    } else {
+      copy_units<HALF, N>(stage, s, 0, lines / F::LPI, k0, kleft);
     }
   }
   template <bool HALF, int N>
-  __device__ __forceinline__ void put(const Unit<ALN> (&w)[N], int j0, uint8_t* stage, const float* ks, long long k0, int kleft, int lines) const {
-    float s[16];
-    if constexpr (F::SC && F::KM) {  // all lines share the step's scales
+  __device__ __forceinline__ void copy_units(uint8_t* stage, const float (&s)[NS], int first, int last, long long k0, int kleft) const {
+#pragma unroll 1
+    for (int j0 = first; j0 < last; j0 += N) {
+      Unit<false> w[N];
+      int nb[N], sh = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 16 * u + i < kleft ? __ldg(ks + k0 + 16 * u + i) : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if ((j0 + j) * F::LPI < lines) {
-        const int line = l0 + (j0 + j) * F::LPI;
-        int nb = 16, sh = 0;
-        if constexpr (!ALN) sh = (int)(reinterpret_cast<uintptr_t>(at(j0 + j, k0, kleft, &nb)) & 15);
-        const uint4 v = unit_bytes<ALN>(w[j], sh, nb);
-        uint8_t* d = stage + line * 128;
-        const int x = line & 7;
-        if constexpr (F::ES == 2) {
-          *reinterpret_cast<uint4*>(d + ((u ^ x) << 4)) = v;
-        } else {
-          uint2 a, b, c, e;
-          if constexpr (F::SC == 0) {
-            a = to_half4(v.x), b = to_half4(v.y), c = to_half4(v.z), e = to_half4(v.w);
-          } else if constexpr (F::KM) {
-            a = to_scaled4<HALF>(v.x, s[0], s[1], s[2], s[3]), b = to_scaled4<HALF>(v.y, s[4], s[5], s[6], s[7]);
-            c = to_scaled4<HALF>(v.z, s[8], s[9], s[10], s[11]), e = to_scaled4<HALF>(v.w, s[12], s[13], s[14], s[15]);
-          } else {
-            const int kk = line & 63;
-            const float f = kk < kleft ? __ldg(ks + k0 + kk) : 0.0f;
-            a = to_scaled4<HALF>(v.x, f, f, f, f), b = to_scaled4<HALF>(v.y, f, f, f, f);
-            c = to_scaled4<HALF>(v.z, f, f, f, f), e = to_scaled4<HALF>(v.w, f, f, f, f);
-          }
-          *reinterpret_cast<uint4*>(d + (((2 * u) ^ x) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(d + (((2 * u + 1) ^ x) << 4)) = make_uint4(c.x, c.y, e.x, e.y);
-        }
+      for (int j = 0; j < N; ++j) {
+        const uint8_t* p = at(j0 + j, k0, kleft, &nb[j]);
+        sh = (int)(reinterpret_cast<uintptr_t>(p) & 15);  // the same for all of them
+        load_unit<false>(w[j], p, nb[j], base, end);
       }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint4 v = unit_bytes<false>(w[j], sh, nb[j]);
+        put<HALF>(v, j0 + j, s, stage);
+      }
+    }
   }
 };
 
@@ -249,30 +258,37 @@ __device__ __forceinline__ void tc_tma_3d(void* dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// FA, FB: the operands' forms; HALF: 16-bit operands are fp16; ALN: every row of
-// every operand starts on 16 bytes.  `map`: the 16-bit operand's (ALN only).
-template <class FA, class FB, bool HALF, bool ALN>
-__global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_constant__ CUtensorMap map, const TcArgs a) {
-  constexpr bool kTma = ALN && (FA::ES == 2 || FB::ES == 2);
-  constexpr bool kLoadA = !(kTma && FA::ES == 2), kLoadB = !(kTma && FB::ES == 2);
+// FA: A's form; BKM: B is K-major; HALF: 16-bit operands are fp16; ALA, ALB: the
+// rows of A, of B start on 16 bytes (by TMA); TR: out[z][n][m] instead of [m][n].
+template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
+  using FB = Form<2, BKM, 0>;
+  constexpr bool kRaw = ALA && FA::ES == 1, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
+  constexpr bool kConv = !kTmaA || !ALB;                                 // the converters have work
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = smem + kStages * kStageBytes;
+  uint8_t* raws = smem + kStages * kStageBytes;
+  uint8_t* staging = raws + kRaws * kRawBytes;
   float* colscale = reinterpret_cast<float*>(staging + kEpiWarps * kEpiBytes);  // [kEpiWarps][32]
   uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * 32);
-  uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2, *rawf = acce + 2, *rawe = rawf + kRaws;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + kRaws);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], kLoadWarps + (kTma ? 1 : 0));
+      mbar_init(&full[s], (kConv ? kConvWarps : 0) + (kTmaA ? 1 : 0) + (ALB ? 1 : 0));
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
       mbar_init(&acce[b], kEpiWarps);
+    }
+    for (int r = 0; r < kRaws; ++r) {
+      mbar_init(&rawf[r], 1);
+      mbar_init(&rawe[r], kConvWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -286,17 +302,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = *tslot;
 
-  // tile t: m fastest (CTAs side by side share the n tile in L2), then n, z and the split
+  // tile t: n fastest (CTAs side by side share A's tile in L2), then m, z and the part
   struct Tile {
     long long m0, n0, z, q0, q1;
     int sp;
   };
   auto tile_of = [&](long long t) {
     Tile c;
-    c.m0 = t % a.mt * kBM;
-    t /= a.mt;
     c.n0 = t % a.nt * a.NB;
     t /= a.nt;
+    c.m0 = t % a.mt * kBM;
+    t /= a.mt;
     c.z = t % a.m.Z;
     c.sp = (int)(t / a.m.Z);
     c.q0 = a.steps * c.sp / a.nsplit;
@@ -305,137 +321,125 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
   };
 
   if (warp >= kEpiWarps && warp < kMmaWarp) {
-    // ------------------------------------------------------------ loaders --
-    Loader<FA, ALN, kBM> la;
-    Loader<FB, ALN, kNBMax> lb;
-    la.init(a.m.A, a.enda, tid - 32 * kEpiWarps);
-    lb.init(a.m.B, a.endb, tid - 32 * kEpiWarps);
-    // rows off alignment are not held a step ahead: two words to a unit would not fit the registers
-    constexpr bool kAheadA = kLoadA && ALN, kAheadB = kLoadB && ALN;
-    using UA = Unit<ALN>[Loader<FA, ALN, kBM>::NU];
-    using UB = Unit<ALN>[Loader<FB, ALN, kNBMax>::NU];
-    struct Pos {
-      long long t, q, k0;
-      long long q1;
-      const float *ksa, *ksb;  // the slice's scales on k
-      int kleft;
-    };
-    auto place = [&](Pos& p, bool fresh) {  // loaders at step p.q of tile p.t
-      const long long r = a.m.R == 1 ? 0 : p.q / a.nkp, kc = p.q - r * a.nkp;
-      p.k0 = kc * kBK;
-      p.kleft = (int)min(a.m.K - p.k0, (long long)kBK);
-      if (fresh || kc == 0) {
-        const Tile c = tile_of(p.t);
-        la.tile(a.m.A, c.z, r, c.m0, a.m.M);
-        lb.tile(a.m.B, c.z, r, c.n0, a.m.N);
-        p.ksa = FA::SC ? a.m.A.ks + r * a.m.A.ks_r : nullptr;
-        p.ksb = FB::SC ? a.m.B.ks + r * a.m.B.ks_r : nullptr;
-      }
-    };
-    auto start = [&](Pos& p, long long t) {
-      p.t = t;
-      if (t >= a.tiles) return;
-      const Tile c = tile_of(t);
-      p.q = c.q0, p.q1 = c.q1;
-      place(p, true);
-    };
-    auto advance = [&](Pos& p) {
-      if (++p.q == p.q1) start(p, p.t + gridDim.x);
-      else place(p, false);
-    };
-    int i = 0;
-    bool ok = true;
-    auto store = [&](const Pos& p, const UA& ua, const UB& ub) {  // step p, whose units were fetched before
-      const int s = i % kStages;
-      if (i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
-      ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
-      if (!ok) return;
-      uint8_t* sa = smem + s * kStageBytes;
-      if constexpr (kAheadA) la.template put<HALF>(ua, 0, sa, p.ksa, p.k0, p.kleft, kBM);
-      if constexpr (kAheadB) lb.template put<HALF>(ub, 0, sa + kABytes, p.ksb, p.k0, p.kleft, a.NB);
-      if constexpr (kLoadA && !kAheadA) la.template copy<HALF>(sa, p.ksa, p.k0, p.kleft, kBM);
-      if constexpr (kLoadB && !kAheadB) lb.template copy<HALF>(sa + kABytes, p.ksb, p.k0, p.kleft, a.NB);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-      ++i;
-    };
-    auto fetch = [&](const Pos& p, UA& ua, UB& ub) {
-      if constexpr (kAheadA) la.fetch(ua, 0, p.k0, p.kleft, kBM);
-      if constexpr (kAheadB) lb.fetch(ub, 0, p.k0, p.kleft, a.NB);
-    };
-    Pos cur, nxt;
-    UA ua0, ua1;
-    UB ub0, ub1;
-    start(cur, blockIdx.x);
-    if constexpr (ALN) {
-      if (cur.t < a.tiles) fetch(cur, ua0, ub0);
-      while (ok && cur.t < a.tiles) {
-        nxt = cur;
-        advance(nxt);
-        if (nxt.t < a.tiles) fetch(nxt, ua1, ub1);
-        store(cur, ua0, ub0);
-        if (!ok || nxt.t >= a.tiles) break;
-        cur = nxt;
-        advance(cur);
-        if (cur.t < a.tiles) fetch(cur, ua0, ub0);
-        store(nxt, ua1, ub1);
-      }
-    } else {
-      for (; ok && cur.t < a.tiles; advance(cur)) store(cur, ua0, ub0);
-    }
-    if (!ok) {
-      i8_flag();
-      *abort_flag = 1;
-    }
-  } else if (warp == kTmaWarp) {
-    // ---------------------------------------------- TMA of a 16-bit operand --
-    if constexpr (kTma) {
-      if (lane == 0) {
-        constexpr bool kIsA = FA::ES == 2;
-        constexpr bool kKM = kIsA ? FA::KM : FB::KM;
-        const int lines = kIsA ? kBM : a.NB;
-        int i = 0;
-        bool ok = true;
-        for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-          const Tile c = tile_of(t);
-          const long long i0 = kIsA ? c.m0 : c.n0, I = kIsA ? a.m.M : a.m.N;
-          for (long long q = c.q0; q < c.q1; ++q, ++i) {
-            const int s = i % kStages;
-            if ((i >= kStages && !mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit)) || *abort_flag) {
-              ok = false;
-              break;
-            }
-            const long long r = q / a.nkp, k0 = (q - r * a.nkp) * kBK, zr = a.m.R == 1 ? c.z : r;
-            uint8_t* d = smem + s * kStageBytes + (kIsA ? 0 : kABytes);
-            tc_expect_tx(&full[s], (uint32_t)lines * 128);
-            // boxes start inside the operand; past its ends the copy engine writes zeros
-            if (!DISCO_IN_BOUNDS(i0 >= 0 && i0 < I && k0 >= 0 && k0 < a.m.K && zr >= 0 && zr < (long long)a.m.Z * a.m.R)) {
-              mbar_complete_tx(&full[s], (uint32_t)lines * 128);
-              continue;
-            }
-            if (kKM) {
-              tc_tma_3d(d, &map, (int)k0, (int)i0, (int)zr, &full[s]);
+    // --------------------------------------------------------- converters --
+    if constexpr (kConv) {
+      constexpr int kUnits = kBM / Form<1, true, 0>::LPI;  // of a thread in a step
+      const int t0 = tid - 32 * kEpiWarps;
+      Loader<FA> la;
+      Loader<FB> lb;
+      la.init(a.m.A, a.enda, t0);
+      lb.init(a.m.B, a.endb, t0);
+      const int blines = (a.NB + 63) / 64 * 64;
+      int i = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+        const Tile c = tile_of(t);
+        long long r = a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
+        bool fresh = true;
+        for (long long q = c.q0; q < c.q1; ++q, ++i, ++kc) {
+          if (kc == a.nkp) kc = 0, ++r, fresh = true;
+          if (fresh) {  // of a slice
+            la.tile(a.m.A, c.z, r, c.m0, a.m.M, kBM);
+            if constexpr (!ALB) lb.tile(a.m.B, c.z, r, c.n0, a.m.N, blines);
+            fresh = false;
+          }
+          const long long k0 = kc * kBK;
+          const int kleft = (int)min(a.m.K - k0, (long long)kBK);
+          float sc[Loader<FA>::NS];
+          la.scales(sc, k0, kleft);
+          const int s = i % kStages, w = i % kRaws;
+          uint4 v[kUnits];
+          if constexpr (kRaw) {
+            ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
+            if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+              const uint4* src = reinterpret_cast<const uint4*>(raws + w * kRawBytes) + t0;
+#pragma unroll
+              for (int j = 0; j < kUnits; ++j) v[j] = src[j * kConverters];
             } else {
-              for (int b = 0; b < lines / 64; ++b) tc_tma_3d(d + b * 8192, &map, (int)i0 + 64 * b, (int)k0, (int)zr, &full[s]);
+              ok = false;
             }
           }
+          if (ok && i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
+          ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+          if (!ok) break;
+          uint8_t* sa = smem + s * kStageBytes;
+          if constexpr (kRaw) {
+            __syncwarp();  // every lane has read its units
+            if (lane == 0) mbar_arrive(&rawe[w]);
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) la.template put<HALF>(v[j], j, sc, sa);
+          } else if constexpr (!kTmaA) {
+            la.template copy<HALF>(sa, sc, k0, kleft, kBM);
+          }
+          if constexpr (!ALB) {
+            float none[1];
+            lb.template copy<HALF>(sa + kABytes, none, k0, kleft, blines);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
         }
-        if (!ok) {
-          i8_flag();
-          *abort_flag = 1;
+      }
+      if (!ok) {
+        i8_flag();
+        *abort_flag = 1;
+      }
+    }
+  } else if (warp == kTmaAWarp || warp == kTmaBWarp) {
+    // ------------------------------------------------------------ TMA --
+    const bool is_a = warp == kTmaAWarp;
+    if (lane == 0 && (is_a ? ALA : ALB)) {
+      // A's integers go into the raw ring, 16-bit lines into the stage
+      const bool ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
+      const int slots = ring ? kRaws : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
+      uint64_t *f = ring ? rawf : full, *e = ring ? rawe : empty;
+      uint8_t* base = ring ? raws : smem + (is_a ? 0 : kABytes);
+      const uint32_t pitch = ring ? kRawBytes : kStageBytes, line = ring ? 64 : 128;
+      const CUtensorMap* map = is_a ? &amap : &bmap;
+      [[maybe_unused]] const long long I = is_a ? a.m.M : a.m.N;
+      // a weight has one slice for all z
+      const bool sliced = is_a ? a.m.A.z || a.m.A.r : a.m.B.z || a.m.B.r;
+      int i = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+        const Tile c = tile_of(t);
+        const long long i0 = is_a ? c.m0 : c.n0;
+        long long r = a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
+        for (long long q = c.q0; q < c.q1; ++q, ++i, ++kc) {
+          if (kc == a.nkp) kc = 0, ++r;
+          const int s = i % slots;
+          if ((i >= slots && !mbar_wait(&e[s], ((i / slots) - 1) & 1, kWaitLimit)) || *abort_flag) {
+            ok = false;
+            break;
+          }
+          const long long k0 = kc * kBK, zr = !sliced ? 0 : a.m.R == 1 ? c.z : r;
+          uint8_t* d = base + s * pitch;
+          tc_expect_tx(&f[s], lines * line);
+          // boxes start inside the operand; past its ends the copy engine writes zeros
+          if (!DISCO_IN_BOUNDS(i0 >= 0 && i0 < I && k0 >= 0 && k0 < a.m.K && zr >= 0 && zr < (long long)a.m.Z * a.m.R)) {
+            mbar_complete_tx(&f[s], lines * line);
+            continue;
+          }
+          if (km) {
+            tc_tma_3d(d, map, (int)k0, (int)i0, (int)zr, &f[s]);
+          } else {
+            for (int b = 0; b < lines / 64; ++b) tc_tma_3d(d + b * 64 * line, map, (int)i0 + 64 * b, (int)k0, (int)zr, &f[s]);
+          }
         }
+      }
+      if (!ok) {
+        i8_flag();
+        *abort_flag = 1;
         // the copies in flight end before the CTA does
-        for (int back = 1; back <= kStages && i - back >= 0 && !ok; ++back)
-          mbar_wait(&full[(i - back) % kStages], ((i - back) / kStages) & 1, 1u << 16);
+        for (int back = 1; back <= slots && i - back >= 0; ++back)
+          mbar_wait(&f[(i - back) % slots], ((i - back) / slots) & 1, 1u << 16);
       }
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------- MMA issuer --
     if (lane == 0) {
-      // without scales on k both operands are fp16 whatever the output
-      constexpr bool kHalfOp = HALF || (FA::ES == 1 && FB::ES == 1);
-      const uint32_t idesc = idesc_16_f32(kBM, a.NB, kHalfOp) | (FA::KM ? 0u : 1u << 15) | (FB::KM ? 0u : 1u << 16);
+      const int nmma = (a.NB + 15) / 16 * 16;
+      const uint32_t idesc = idesc_16_f32(kBM, nmma, HALF) | (FA::KM ? 0u : 1u << 15) | (BKM ? 0u : 1u << 16);
       int i = 0, tl = 0;
       bool ok = true;
       for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++tl) {
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
           for (int ks = 0; ks < kBK / 16; ++ks) {
             // 16 k: 32 bytes of every line (k contiguous), or 16 lines; boxes of 64 m or n are 8 KB apart
             const uint64_t ad = FA::KM ? tc_desc(sa + ks * 32, 16) : tc_desc(sa + ks * 2048, 8192);
-            const uint64_t bd = FB::KM ? tc_desc(sb + ks * 32, 16) : tc_desc(sb + ks * 2048, 8192);
+            const uint64_t bd = BKM ? tc_desc(sb + ks * 32, 16) : tc_desc(sb + ks * 2048, 8192);
             umma_bf16(tmem + ab * kNBMax, ad, bd, idesc, (q > c.q0 || ks > 0) ? 1u : 0u);
           }
           umma_commit(&empty[s]);
@@ -474,21 +478,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
     }
   } else if (warp < kEpiWarps) {
     // ----------------------------------------------------------- epilogue --
-    const int q4 = warp;  // TMEM lanes 32 q4 ..
-    uint8_t* stg = staging + warp * kEpiBytes;
+    uint8_t* stg = staging + warp * kEpiBytes;  // 16-byte piece s of row r at piece s ^ (r / 2 % 4): no bank conflicts
+    float* cs = colscale + warp * 32;
     const bool split = a.part != nullptr;
     const int type = split ? DISCO_F32 : a.out_type, eb = type == DISCO_F32 ? 4 : 2;
+    const bool scaled = !split && a.m.cs, h16 = type == DISCO_F16;
     int tl = 0;
     for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
       const Tile c = tile_of(t);
       const int ab = tl & 1;
-      float* cs = colscale + warp * 32;
-      const bool scaled = !split && a.m.cs;
       // scale of column c0 + lane, fetched a chunk ahead
-      auto column = [&](int col) { return scaled && c.n0 + col < a.m.N ? __ldg(a.m.cs + c.z * a.m.cs_z + c.n0 + col) : 0.0f; };
+      auto column = [&](int col) { return scaled && c.n0 + col < a.m.N ? __ldg(a.m.cs + c.n0 + col) : 0.0f; };
       float next = column(lane);
-      const long long row0 = c.m0 + q4 * 32;
-      const float rs = !split && a.m.rs && row0 + lane < a.m.M ? a.m.rs[row0 + lane] : 1.0f;
+      const long long row0 = c.m0 + warp * 32;  // TMEM lanes 32 warp ..: m of this warp
+      const float rs = scaled && row0 + lane < a.m.M ? __ldg(a.m.rs + c.z * a.m.rs_z + row0 + lane) : 1.0f;
       bool fin = mbar_wait(&accf[ab], (tl >> 1) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
       if (!fin) {
@@ -497,14 +500,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const int rows = (int)min(a.m.M - row0, 32LL);  // of this warp, may be negative
-      uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) +
-                     (((c.sp * (long long)a.m.Z + c.z) * a.m.M + row0) * a.m.N + c.n0) * eb;
-      const long long pitch = a.m.N * eb;
+      const int rows = (int)min(a.m.M - row0, 32LL);  // may be negative
       const int cols = (int)min(a.m.N - c.n0, (long long)a.NB);
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+      const long long slice = (c.sp * (long long)a.m.Z + c.z) * a.m.M * a.m.N;
+      // first of this warp's outputs; rows of the output are n (TR) or m
+      uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) + (slice + (TR ? c.n0 * a.m.M + row0 : row0 * a.m.N + c.n0)) * eb;
+      const long long pitch = (TR ? a.m.M : a.m.N) * eb;
+      for (int c0 = 0; c0 < cols && rows > 0; c0 += 32) {
         uint32_t v[32];
-        tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(q4 * 32) << 16) + c0, v);
+        tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(warp * 32) << 16) + c0, v);
         if (scaled) {
           cs[lane] = next;
           __syncwarp();
@@ -517,49 +521,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
             v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f.z * rs);
             v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f.w * rs);
           }
-        }
-        // 64 bytes of each of the warp's 32 rows at a time through shared memory
-        auto emit = [&](int w0, int n) {  // n columns from c0 + w0 are staged
           __syncwarp();
-          const int left = min(n, cols - c0 - w0);
-          uint8_t* o = out + (long long)(c0 + w0) * eb;
-          if (a.vec) {
+        }
+        const int left = min(32, cols - c0);
+        if constexpr (TR) {
+          // the warp's lanes are neighbours in memory
+          if (type == DISCO_F32) {
+            uint8_t* o = out + (long long)c0 * pitch + lane * 4;
+            if (lane < rows)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < left) *reinterpret_cast<uint32_t*>(o + e * pitch) = v[e];
+          } else if (!a.vec) {
+            uint8_t* o = out + (long long)c0 * pitch + lane * 2;
+            if (lane < rows)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < left) *reinterpret_cast<uint16_t*>(o + e * pitch) = round_16(__uint_as_float(v[e]), h16);
+          } else {
+            // 64 bytes of 32 n through shared memory, then 16 bytes to a lane
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              *reinterpret_cast<uint16_t*>(stg + e * 64 + ((((lane >> 3) ^ (e >> 1)) & 3) << 4) + (lane & 7) * 2) = round_16(__uint_as_float(v[e]), h16);
+            __syncwarp();
+            uint8_t* o = out + (long long)c0 * pitch;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               const int idx = lane + 32 * h, row = idx >> 2, seg = idx & 3;
-              if (row < rows && seg * 16 < left * eb)
-                *reinterpret_cast<uint4*>(o + row * pitch + seg * 16) = *reinterpret_cast<const uint4*>(stg + row * kStagePitch + seg * 16);
+              if (row < left && seg * 8 < rows)
+                *reinterpret_cast<uint4*>(o + row * pitch + seg * 16) = *reinterpret_cast<const uint4*>(stg + row * 64 + ((seg ^ (row >> 1)) & 3) * 16);
             }
-          } else if (eb == 2) {
-            if (lane < left)
-#pragma unroll 4
-              for (int row = 0; row < rows; ++row)
-                *reinterpret_cast<uint16_t*>(o + row * pitch + lane * 2) = *reinterpret_cast<const uint16_t*>(stg + row * kStagePitch + lane * 2);
-          } else {
-            if ((lane & 15) < left)
-#pragma unroll 4
-              for (int row = lane >> 4; row < rows; row += 2)
-                *reinterpret_cast<uint32_t*>(o + row * pitch + (lane & 15) * 4) =
-                    *reinterpret_cast<const uint32_t*>(stg + row * kStagePitch + (lane & 15) * 4);
-          }
-          __syncwarp();
-        };
-        uint4* d = reinterpret_cast<uint4*>(stg + lane * kStagePitch);
-        if (type == DISCO_F32) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) d[g] = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-          emit(0, 16);
-          if (c0 + 16 < cols) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) d[g] = make_uint4(v[16 + 4 * g], v[17 + 4 * g], v[18 + 4 * g], v[19 + 4 * g]);
-            emit(16, 16);
+            __syncwarp();
           }
         } else {
-          const bool h16 = type == DISCO_F16;
-          auto two = [&](int e) { return pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16); };
+          // 64 bytes of each of the warp's 32 rows at a time through shared memory
+          auto emit = [&](int w0, int n) {  // n columns from c0 + w0 are staged
+            __syncwarp();
+            const int some = min(n, left - w0);
+            uint8_t* o = out + (long long)(c0 + w0) * eb;
+            if (a.vec) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) d[g] = make_uint4(two(8 * g), two(8 * g + 2), two(8 * g + 4), two(8 * g + 6));
-          emit(0, 32);
+              for (int h = 0; h < 4; ++h) {
+                const int idx = lane + 32 * h, row = idx >> 2, seg = idx & 3;
+                if (row < rows && seg * 16 < some * eb)
+                  *reinterpret_cast<uint4*>(o + row * pitch + seg * 16) = *reinterpret_cast<const uint4*>(stg + row * 64 + ((seg ^ (row >> 1)) & 3) * 16);
+              }
+            } else {
+              const int step = 64 / eb, col = lane & (step - 1);  // 32 lanes over one row of 2-byte or two of 4-byte elements
+              if (col < some)
+#pragma unroll 4
+                for (int row = lane / step; row < rows; row += 32 / step) {
+                  const uint8_t* s = stg + row * 64 + (((col * eb >> 4) ^ (row >> 1)) & 3) * 16 + (col * eb & 15);
+                  if (eb == 2) *reinterpret_cast<uint16_t*>(o + row * pitch + col * 2) = *reinterpret_cast<const uint16_t*>(s);
+                  else *reinterpret_cast<uint32_t*>(o + row * pitch + col * 4) = *reinterpret_cast<const uint32_t*>(s);
+                }
+            }
+            __syncwarp();
+          };
+          auto stage = [&](int g, uint4 x) { *reinterpret_cast<uint4*>(stg + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) = x; };
+          if (type == DISCO_F32) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) stage(g, make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
+            emit(0, 16);
+            if (left > 16) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) stage(g, make_uint4(v[16 + 4 * g], v[17 + 4 * g], v[18 + 4 * g], v[19 + 4 * g]));
+              emit(16, 16);
+            }
+          } else {
+            auto two = [&](int e) { return pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16); };
+#pragma unroll
+            for (int g = 0; g < 4; ++g) stage(g, make_uint4(two(8 * g), two(8 * g + 2), two(8 * g + 4), two(8 * g + 6)));
+            emit(0, 32);
+          }
         }
       }
       tc_fence_before();
@@ -577,6 +611,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) i8_tc_kernel(const __grid_const
 
 // ---- host --------------------------------------------------------------------
 
+// `lines` of 64 elements to a copy: of 64 k, or (MN-major) 64 of them, of 64 m or n.
 inline int tc_encode(CUtensorMap* map, const Operand& o, long long I, long long K, int ZR, int lines, bool f16) {
   static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
     void* p = nullptr;
@@ -587,30 +622,30 @@ inline int tc_encode(CUtensorMap* map, const Operand& o, long long I, long long 
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }();
   if (!enc) return fail(DISCO_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const int es = o.bits / 8;
   const long long slice = max(o.z, o.r);
-  const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : I), (cuuint64_t)(o.k_major ? I : K), (cuuint64_t)ZR};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)(slice ? slice : o.ld * dims[1]) * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : I), (cuuint64_t)(o.k_major ? I : K), (cuuint64_t)(slice ? ZR : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * es, (cuuint64_t)(slice ? slice : o.ld * dims[1]) * es};
   const cuuint32_t box[3] = {64, (cuuint32_t)(o.k_major ? lines : 64), 1}, estr[3] = {1, 1, 1};
-  const CUresult cr = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p),
-                          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapDataType type = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                           : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult cr = enc(map, type, 3, const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          es == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return fail(DISCO_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)cr);
   return DISCO_OK;
 }
 
-template <class FA, class FB, bool HALF, bool ALN>
+template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
 int tc_launch(const TcArgs& a, cudaStream_t st) {
-  CUtensorMap map = {};
-  if constexpr (ALN && (FA::ES == 2 || FB::ES == 2)) {
-    int rc;
-    if (FA::ES == 2) rc = tc_encode(&map, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF);
-    else rc = tc_encode(&map, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF);
-    if (rc) return rc;
-  }
-  auto kern = i8_tc_kernel<FA, FB, HALF, ALN>;
+  CUtensorMap amap = {}, bmap = {};
+  int rc;
+  if (ALA && (rc = tc_encode(&amap, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF))) return rc;
+  if (ALB && (rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
+  auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem) != cudaSuccess)
     return check_launch("i8_tc_kernel attribute");
-  kern<<<(int)min(a.tiles, (long long)kSMs), kTcThreads, kTcSmem, st>>>(map, a);
+  kern<<<(int)min(a.tiles, (long long)kSMs), kTcThreads, kTcSmem, st>>>(amap, bmap, a);
   return check_launch("i8_tc_kernel");
 }
 

@@ -141,6 +141,39 @@ def test_matmul_gradients(lib, shape, dtype):
     assert lib.disco_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("shape", [(2, 128, 256, 16400), (2, 128, 256, 16401), (6000, 512, 384, 1), (6001, 515, 391, 1), (1, 1024, 520, 4112),
+                                   (3, 80, 77, 9999), (1, 4096, 1000, 1), (40, 8200, 136, 1)], ids=ids)
+def test_many_steps_and_tiles(lib, shape, dtype):
+    """Reductions of many steps, split or not, over many tiles: the rings of shared
+    memory go round often.  Five runs give the same bits."""
+    B, Cin, Cout, P = shape
+    q, scale, W, wscale, dy = [t.cuda() for t in _operands(shape, dtype)]
+    code = lib.dtype_code(dtype)
+    y, dx = torch.empty((B, Cout, P), dtype=dtype, device="cuda"), torch.empty((B, Cin, P), dtype=dtype, device="cuda")
+    dW = torch.empty((Cout, Cin), dtype=dtype, device="cuda")
+    ws = _ws(max(f(*shape, code) for f in (lib.disco_matmul_i8_workspace_bytes, lib.disco_matmul_i8_bwd_input_workspace_bytes,
+                                           lib.disco_matmul_i8_bwd_weight_workspace_bytes)))
+    first = None
+    for _ in range(5):
+        for t in (y, dx, dW):
+            t.fill_(float("nan"))
+        lib.disco_matmul_i8(q, scale, W, wscale, y, *shape, ws)
+        lib.disco_matmul_i8_bwd_input(dy, W, wscale, dx, *shape, ws)
+        lib.disco_matmul_i8_bwd_weight(dy, q, scale, dW, *shape, ws)
+        if first is None:
+            first = [t.clone() for t in (y, dx, dW)]
+        assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dW)))
+    assert lib.disco_device_status() == 0
+    cpu = lambda *ts: [t.cpu() for t in ts]  # noqa: E731
+    want, S = r.matmul64(q, scale, W, wscale)
+    r.assert_close(y, *cpu(want, r.matmul_bound(want, S, scale, wscale, Cin, dtype)), "y")
+    want, S, D = r.bwd_input64(dy, W, wscale)
+    r.assert_close(dx, *cpu(want, r.grad_bound(want, S, D, Cout, dtype)), "dx")
+    want, S, D = r.bwd_weight64(dy, q, scale)
+    r.assert_close(dW, *cpu(want, r.grad_bound(want, S, D, B * P, dtype)), "dW")
+
+
 @pytest.mark.parametrize("P", [1, 37, 64])
 def test_extreme_integers_and_scales(lib, P):
     """-128 and 127 everywhere (the sum is exact for Cin <= 1024), and scales that
