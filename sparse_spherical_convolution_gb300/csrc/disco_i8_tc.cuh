@@ -11,18 +11,20 @@
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
 // Persistent kernel:
-//   warps 0-3    epilogue: tcgen05.ld, scales, rounding, stores along the output's rows
-//   warps 4-11   converters: integers from the raw ring (aligned rows) or from memory, to
-//                16 bits, into the stage.  All of them take every step in order: a waiter on
-//                a ring's barrier then is never two phases ahead of it, where a wait by parity would pass at once
+//   epilogue     (8 warps; 4 where rows are off alignment): tcgen05.ld, scales, rounding,
+//                stores along the output's rows
+//   converters   (4 warps; 8): integers from the raw ring, to 16 bits, into the stage.  All of
+//                them take every step in order: a waiter on a ring's barrier then is never
+//                two phases ahead of it, where a wait by parity would pass at once
 //   warp 12      MMA issuer (one thread); two accumulators of 256 TMEM columns, so
 //                the epilogue of a tile overlaps the main loop of the next
 //   warp 13      TMA of B, and warp 14 of A: into the stage (16-bit) or the raw ring (integers)
 // Both operands lie in the stage as lines of 64 elements (128 bytes, 128-byte
 // swizzle): element k .. k + 63 of one m or n where k is the contiguous direction
 // in memory, else (MN-major) 64 neighbouring m or n of one k.  So no operand is ever transposed.
-// Rows off 16-byte alignment are read by the converters in aligned 16-byte words and
-// shifted in registers; a thread's shift stays the same over a tile.
+// Rows off 16-byte alignment the converters copy themselves, some steps ahead with
+// cp.async, in aligned 16-byte words (one more than the line has), and shift in
+// registers; a thread's shift stays the same over a tile.
 // All mbarrier waits are bounded (time-out -> status flag, abort).
 #pragma once
 
@@ -34,14 +36,10 @@
 namespace disco {
 namespace i8 {
 
-constexpr int kEpiWarps = 4, kConvWarps = 8;
-constexpr int kMmaWarp = kEpiWarps + kConvWarps, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2;
-constexpr int kTcThreads = 32 * (kTmaAWarp + 1);
-constexpr int kConverters = 32 * kConvWarps;
-constexpr int kBM = 128, kBK = 64, kStages = 4, kNBMax = 256, kRaws = 3;
-constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2, kRawBytes = kBM * kBK;
+constexpr int kMmaWarp = 12, kTmaBWarp = 13, kTmaAWarp = 14, kTcThreads = 32 * 15;
+constexpr int kBM = 128, kBK = 64, kNBMax = 256;
+constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2;
 constexpr uint32_t kEpiBytes = 32 * 64;  // staging of an epilogue warp: 64 bytes of 32 rows
-constexpr size_t kTcSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kRawBytes + kEpiWarps * (kEpiBytes + 128) + 256;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr int kStatusI8Timeout = 1 << 6;
 
@@ -56,7 +54,22 @@ struct Form {
   static constexpr int ES = ES_, SC = SC_;
   static constexpr bool KM = KM_;
   static constexpr int UPL = ES == 1 ? 4 : 8;         // 16-byte units of a line of 64 elements
-  static constexpr int LPI = kConverters / UPL;       // lines that the converters take at a time
+};
+
+// What the kernel's parameters make of warps and shared memory (227 KB).
+//   raw ring, aligned: integers as they are; off alignment: words of each line and one more
+template <class FA, bool ALA, bool ALB>
+struct Plan {
+  static constexpr bool kAligned = ALA && ALB;
+  static constexpr int kEpi = kAligned ? 8 : 4, kConv = kMmaWarp - kEpi;
+  static constexpr bool kRaw = ALA && FA::ES == 1;  // A by TMA into the raw ring
+  static constexpr uint32_t kSlotA = kRaw ? kBM * kBK : ALA ? 0 : kBM * (64 * FA::ES + 16);
+  static constexpr uint32_t kSlot = kSlotA + (ALB ? 0 : kNBMax * (128 + 16));
+  static constexpr int kStages = kAligned ? (kRaw ? 3 : 4) : ALB ? 3 : 2;
+  static constexpr int kRaws = kAligned ? (kRaw ? 6 : 0) : ALB ? 4 : 2;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kEpiBytes + 128) + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(!kRaw || ALB, "the raw ring is filled by TMA or by the converters");
 };
 
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
@@ -69,70 +82,30 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
   return d;
 }
 
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// 16 bytes into shared memory, the first `bytes` (0 .. 16) of them from memory and zeros behind them
+__device__ __forceinline__ void cp16(void* d, const uint8_t* p, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(p), "r"(bytes) : "memory");
 }
 
-// The aligned word at p, zeros from `end` on.
-__device__ __forceinline__ uint4 ldg16_to(const uint8_t* p, const uint8_t* end) {
-  if (p + 16 <= end) return ldg16(p);
-  uint32_t w[4] = {0, 0, 0, 0};
+// The nb bytes from byte sh of two words on, zeros behind them.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int sh, int nb) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (sh & 8)
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (p + i < end) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Up to 16 bytes of a line as they come from memory.
-template <bool ALN>
-struct Unit {
-  uint4 lo, hi;
-};
-template <>
-struct Unit<true> {
-  uint4 lo;
-};
-
-template <bool ALN>
-__device__ __forceinline__ void load_unit(Unit<ALN>& u, const uint8_t* p, int nb, const uint8_t* base, const uint8_t* end) {
-  u.lo = make_uint4(0, 0, 0, 0);
-  if constexpr (ALN) {
-    if (nb > 0 && DISCO_IN_BOUNDS(p >= base && p + 16 <= end)) u.lo = ldg16(p);
-  } else {
-    u.hi = make_uint4(0, 0, 0, 0);
-    const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-    const uint8_t* c = p - sh;
-    if (nb > 0 && DISCO_IN_BOUNDS(c >= base && c < end)) {
-      u.lo = ldg16_to(c, end);
-      if (sh + nb > 16 && DISCO_IN_BOUNDS(c + 16 < end)) u.hi = ldg16_to(c + 16, end);
-    }
-  }
-}
-
-// Its nb bytes, zeros behind them.
-template <bool ALN>
-__device__ __forceinline__ uint4 unit_bytes(const Unit<ALN>& u, int sh, int nb) {
-  if constexpr (ALN) {
-    return u.lo;
-  } else {
-    uint32_t w[8] = {u.lo.x, u.lo.y, u.lo.z, u.lo.w, u.hi.x, u.hi.y, u.hi.z, u.hi.w};
-    if (sh & 8)
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (sh & 4)
 #pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    if (sh & 4)
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    uint32_t o[4];
+  for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (sh & 3));
+  if (nb < 16)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (sh & 3));
       const int left = nb - 4 * i;  // bytes of this word that belong to the line
       if (left < 4) o[i] = left <= 0 ? 0 : o[i] & (0xffffffffu >> (32 - 8 * left));
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // 4 integers to 4 fp16 values: 1024 + (q + 128) by the exponent's bits, less 1152; exact.
@@ -151,51 +124,40 @@ __device__ __forceinline__ uint2 to_scaled4(uint32_t w, float s0, float s1, floa
                     pack2_16(from_byte(w, 2) * s2, from_byte(w, 3) * s3, HALF));
 }
 
-// One operand's share of a converter thread.
-template <class F>
+// One operand's share of a converter thread: 16-byte units t, t + NT, ... of a step's lines.
+template <class F, int NT>
 struct Loader {
-  const uint8_t *base, *end, *row;  // the tensor; this slice's
-  const float* ks;                  // the slice's scales on k
-  long long ld, i0;                 // first m or n of the tile
-  int u, l0, ileft;                 // unit of a line, first line; m or n of the tile inside the tensor
+  static constexpr int LPI = NT / F::UPL;  // lines that the converters take at a time
+  const uint8_t *base, *end;        // the tensor
+  long long ld;
+  int u, l0;                        // unit of a line, first line
 
   __device__ __forceinline__ void init(const Operand& o, const uint8_t* e, int t) {
     base = (const uint8_t*)o.p, end = e, ld = o.ld * F::ES;
     u = t % F::UPL, l0 = t / F::UPL;
   }
-  __device__ __forceinline__ void tile(const Operand& o, long long z, long long r, long long first, long long I, int lines) {
-    row = base + (z * o.z + r * o.r) * F::ES;
-    ks = F::SC ? o.ks + r * o.ks_r : nullptr;
-    i0 = first;
-    ileft = (int)min(I - first, (long long)lines);
-  }
-  // where unit j of the step lies, and how many of its bytes are inside
-  __device__ __forceinline__ const uint8_t* at(int j, long long k0, int kleft, int* nb) const {
-    const int line = l0 + j * F::LPI;
-    if constexpr (F::KM) {
-      *nb = line < ileft ? min(16, kleft * F::ES - 16 * u) : 0;
-      return row + (i0 + line) * ld + k0 * F::ES + 16 * u;
-    } else {
-      const int box = line >> 6, kk = line & 63;
-      *nb = kk < kleft ? min(16, (ileft - 64 * box) * F::ES - 16 * u) : 0;
-      return row + (k0 + kk) * ld + (i0 + 64 * box) * F::ES + 16 * u;
-    }
-  }
-  // the scales of this thread's units of a step: of 16 k (k contiguous), or of its lines
-  static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 64 / F::LPI;
-  __device__ __forceinline__ void scales(float (&s)[NS], long long k0, int kleft) const {
-    if constexpr (F::SC && F::KM) {
+  // The scales of this thread's units of a step: of 16 k (k contiguous), or of its lines.
+  static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 64 / LPI > 1 ? 64 / LPI : 1;
+  template <bool ALN>
+  __device__ __forceinline__ void scales(float (&s)[NS], const float* ks, int kleft) const {  // ks: of the step's first k
+    if constexpr (F::SC && F::KM && ALN) {  // 16 k are inside or outside together
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 16 * u + i < kleft ? __ldg(ks + k0 + 16 * u + i) : 0.0f;
+      for (int i = 0; i < 16; i += 4) {
+        const float4 f = 16 * u < kleft ? __ldg(reinterpret_cast<const float4*>(ks + 16 * u + i)) : make_float4(0, 0, 0, 0);
+        s[i] = f.x, s[i + 1] = f.y, s[i + 2] = f.z, s[i + 3] = f.w;
+      }
+    } else if constexpr (F::SC && F::KM) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 16 * u + i < kleft ? __ldg(ks + 16 * u + i) : 0.0f;
     } else if constexpr (F::SC) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) s[i] = l0 + i * F::LPI < kleft ? __ldg(ks + k0 + l0 + i * F::LPI) : 0.0f;
+      for (int i = 0; i < NS; ++i) s[i] = ((l0 + i * LPI) & 63) < kleft ? __ldg(ks + ((l0 + i * LPI) & 63)) : 0.0f;
     }
   }
   // 16 bytes of unit j into the stage
   template <bool HALF>
   __device__ __forceinline__ void put(const uint4& v, int j, const float (&s)[NS], uint8_t* stage) const {
-    const int line = l0 + j * F::LPI, x = line & 7;
+    const int line = l0 + j * LPI, x = line & 7;
     uint8_t* d = stage + line * 128;
     if constexpr (F::ES == 2) {
       *reinterpret_cast<uint4*>(d + ((u ^ x) << 4)) = v;
@@ -215,36 +177,51 @@ struct Loader {
       *reinterpret_cast<uint4*>(d + (((2 * u + 1) ^ x) << 4)) = make_uint4(c.x, c.y, e.x, e.y);
     }
   }
-  // a step's lines from memory, up to four units at a time
+
+  // Rows off alignment.  `first`: the byte where line 0 of the step starts; unit (line, u)
+  // lies `line` storage rows further, in a box of 64 m or n where k is not contiguous.
+  __device__ __forceinline__ const uint8_t* line_at(const uint8_t* first, int line) const {
+    return F::KM ? first + line * ld : first + (line & 63) * ld + (line >> 6) * (64 * F::ES);
+  }
+  // bytes of a line that are inside the operand
+  __device__ __forceinline__ int line_bytes(int line, int ileft, int kleft) const {
+    if (F::KM) return line < ileft ? kleft * F::ES : 0;
+    return (line & 63) < kleft ? max(0, min(64, ileft - (line & ~63))) * F::ES : 0;
+  }
+  // The words of this thread's units into a slot of the ring: word u of a line at unit
+  // (line, u), and the one behind its last at `more`.
+  __device__ __forceinline__ void fetch(uint8_t* slot, int slot_lines, const uint8_t* first, int ileft, int kleft, int lines) const {
+    for (int line = l0; line < lines; line += LPI) {
+      const uint8_t* p = line_at(first, line);
+      const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15), len = line_bytes(line, ileft, kleft) + sh;
+      const uint8_t* w = p - sh + 16 * u;
+      const bool need = len > sh && 16 * u < len;
+      const int n = need && DISCO_IN_BOUNDS(w >= base && w < end) ? (int)min((long long)(end - w), 16LL) : 0;
+      cp16(slot + (line * F::UPL + u) * 16, n ? w : base, n);
+      if (u == F::UPL - 1) {
+        w += 16;
+        const int m = len > sh && 16 * F::UPL < len && DISCO_IN_BOUNDS(w >= base && w < end) ? (int)min((long long)(end - w), 16LL) : 0;
+        cp16(slot + (slot_lines * F::UPL + line) * 16, m ? w : base, m);
+      }
+    }
+  }
   template <bool HALF>
-  __device__ __forceinline__ void copy(uint8_t* stage, const float (&s)[NS], long long k0, int kleft, int lines) const {
-    constexpr int N = F::ES == 1 ? 2 : 4;
-    if (F::ES == 2 && lines % (N * F::LPI)) {  // 64 lines more
-      copy_units<HALF, 2>(stage, s, 0, 2, k0, kleft);
-      copy_units<HALF, N>(stage, s, 2, lines / F::LPI, k0, kleft);
-    } else {
-      copy_units<HALF, N>(stage, s, 0, lines / F::LPI, k0, kleft);
+  __device__ __forceinline__ void convert(const uint8_t* slot, int slot_lines, uint8_t* stage, const float (&s)[NS], const uint8_t* first,
+                                          int ileft, int kleft, int lines) const {
+    const int sh = (int)(reinterpret_cast<uintptr_t>(line_at(first, l0)) & 15);  // the same for all units of the thread
+    const uint4* w = reinterpret_cast<const uint4*>(slot);
+#pragma unroll 2
+    for (int j = 0; l0 + j * LPI < lines; ++j) {
+      const int line = l0 + j * LPI, at = line * F::UPL + u;
+      const uint4 lo = w[at], hi = w[u == F::UPL - 1 ? slot_lines * F::UPL + line : at + 1];
+      put<HALF>(shifted(lo, hi, sh, min(16, line_bytes(line, ileft, kleft) - 16 * u)), j, s, stage);
     }
   }
-  template <bool HALF, int N>
-  __device__ __forceinline__ void copy_units(uint8_t* stage, const float (&s)[NS], int first, int last, long long k0, int kleft) const {
-#pragma unroll 1
-    for (int j0 = first; j0 < last; j0 += N) {
-      Unit<false> w[N];
-      int nb[N], sh = 0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint8_t* p = at(j0 + j, k0, kleft, &nb[j]);
-        sh = (int)(reinterpret_cast<uintptr_t>(p) & 15);  // the same for all of them
-        load_unit<false>(w[j], p, nb[j], base, end);
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint4 v = unit_bytes<false>(w[j], sh, nb[j]);
-        put<HALF>(v, j0 + j, s, stage);
-      }
-    }
-  }
+};
+
+// Where a converter is: step q of tile t, slice r, chunk kc.
+struct Pos {
+  long long t, q, q1, r, kc, m0, n0, z;
 };
 
 __device__ __forceinline__ void tc_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -264,16 +241,18 @@ template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
 __global__ void __launch_bounds__(kTcThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
   using FB = Form<2, BKM, 0>;
-  constexpr bool kRaw = ALA && FA::ES == 1, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
-  constexpr bool kConv = !kTmaA || !ALB;                                 // the converters have work
+  using C = Plan<FA, ALA, ALB>;
+  constexpr int kEpiWarps = C::kEpi, kConvWarps = C::kConv, kConverters = 32 * kConvWarps, kStages = C::kStages, kRaws = C::kRaws;
+  constexpr bool kRaw = C::kRaw, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
+  constexpr bool kConv = !kTmaA || !ALB;                      // the converters have work
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* raws = smem + kStages * kStageBytes;
-  uint8_t* staging = raws + kRaws * kRawBytes;
+  uint8_t* staging = raws + kRaws * C::kSlot;
   float* colscale = reinterpret_cast<float*>(staging + kEpiWarps * kEpiBytes);  // [kEpiWarps][32]
   uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * 32);
-  uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2, *rawf = acce + 2, *rawe = rawf + kRaws;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + kRaws);
+  uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2, *rawf = acce + 2, *rawe = rawf + 8;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -286,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&accf[b], 1);
       mbar_init(&acce[b], kEpiWarps);
     }
-    for (int r = 0; r < kRaws; ++r) {
+    for (int r = 0; r < 8; ++r) {
       mbar_init(&rawf[r], 1);
       mbar_init(&rawe[r], kConvWarps);
     }
@@ -323,67 +302,104 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= kEpiWarps && warp < kMmaWarp) {
     // --------------------------------------------------------- converters --
     if constexpr (kConv) {
-      constexpr int kUnits = kBM / Form<1, true, 0>::LPI;  // of a thread in a step
       const int t0 = tid - 32 * kEpiWarps;
-      Loader<FA> la;
-      Loader<FB> lb;
+      Loader<FA, kConverters> la;
+      Loader<FB, kConverters> lb;
       la.init(a.m.A, a.enda, t0);
       lb.init(a.m.B, a.endb, t0);
       const int blines = (a.NB + 63) / 64 * 64;
-      int i = 0;
-      bool ok = true;
-      for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+      auto start = [&](Pos& p, long long t) {
+        p.t = t;
+        if (t >= a.tiles) return;
         const Tile c = tile_of(t);
-        long long r = a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
-        bool fresh = true;
-        for (long long q = c.q0; q < c.q1; ++q, ++i, ++kc) {
-          if (kc == a.nkp) kc = 0, ++r, fresh = true;
-          if (fresh) {  // of a slice
-            la.tile(a.m.A, c.z, r, c.m0, a.m.M, kBM);
-            if constexpr (!ALB) lb.tile(a.m.B, c.z, r, c.n0, a.m.N, blines);
-            fresh = false;
-          }
-          const long long k0 = kc * kBK;
-          const int kleft = (int)min(a.m.K - k0, (long long)kBK);
-          float sc[Loader<FA>::NS];
-          la.scales(sc, k0, kleft);
-          const int s = i % kStages, w = i % kRaws;
-          uint4 v[kUnits];
-          if constexpr (kRaw) {
-            ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
-            if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
-              const uint4* src = reinterpret_cast<const uint4*>(raws + w * kRawBytes) + t0;
-#pragma unroll
-              for (int j = 0; j < kUnits; ++j) v[j] = src[j * kConverters];
-            } else {
-              ok = false;
-            }
-          }
-          if (ok && i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
-          ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
-          if (!ok) break;
-          uint8_t* sa = smem + s * kStageBytes;
-          if constexpr (kRaw) {
-            __syncwarp();  // every lane has read its units
-            if (lane == 0) mbar_arrive(&rawe[w]);
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j) la.template put<HALF>(v[j], j, sc, sa);
-          } else if constexpr (!kTmaA) {
-            la.template copy<HALF>(sa, sc, k0, kleft, kBM);
-          }
-          if constexpr (!ALB) {
-            float none[1];
-            lb.template copy<HALF>(sa + kABytes, none, k0, kleft, blines);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
+        p.q = c.q0, p.q1 = c.q1, p.m0 = c.m0, p.n0 = c.n0, p.z = c.z;
+        p.r = a.m.R == 1 ? 0 : c.q0 / a.nkp;
+        p.kc = c.q0 - p.r * a.nkp;
+      };
+      auto advance = [&](Pos& p) {
+        if (++p.q == p.q1) return start(p, p.t + gridDim.x);
+        if (++p.kc == a.nkp) p.kc = 0, ++p.r;
+      };
+      auto kleft = [&](const Pos& p) { return (int)min(a.m.K - p.kc * kBK, (long long)kBK); };
+      auto scales = [&](const Pos& p, float (&s)[Loader<FA, kConverters>::NS]) {
+        if constexpr (FA::SC) la.template scales<ALA>(s, a.m.A.ks + p.r * a.m.A.ks_r + p.kc * kBK, kleft(p));
+      };
+      // the byte where a step's line 0 starts, m or n of the tile inside the operand
+      auto first_a = [&](const Pos& p) { return la.base + (p.z * a.m.A.z + p.r * a.m.A.r + (FA::KM ? p.m0 * a.m.A.ld + p.kc * kBK : p.kc * kBK * a.m.A.ld + p.m0)) * FA::ES; };
+      auto first_b = [&](const Pos& p) { return lb.base + (p.z * a.m.B.z + p.r * a.m.B.r + (BKM ? p.n0 * a.m.B.ld + p.kc * kBK : p.kc * kBK * a.m.B.ld + p.n0)) * 2; };
+      auto left_a = [&](const Pos& p) { return (int)min(a.m.M - p.m0, (long long)kBM); };
+      auto left_b = [&](const Pos& p) { return (int)min(a.m.N - p.n0, (long long)blines); };
+      auto fetch = [&](const Pos& p, int i) {  // rows off alignment: this thread's words of step i
+        if (p.t < a.tiles) {
+          uint8_t* slot = raws + (i % (kRaws ? kRaws : 1)) * C::kSlot;
+          if constexpr (!ALA) la.fetch(slot, kBM, first_a(p), left_a(p), kleft(p), kBM);
+          if constexpr (!ALB) lb.fetch(slot + C::kSlotA, kNBMax, first_b(p), left_b(p), kleft(p), blines);
         }
+        norm::copy_commit();
+      };
+      Pos cur, nxt, far;
+      start(cur, blockIdx.x);
+      far = cur;
+      if constexpr (!kRaw)
+        for (int d = 0; d < kRaws - 1; ++d) {
+          fetch(far, d);
+          if (far.t < a.tiles) advance(far);
+        }
+      float sc[Loader<FA, kConverters>::NS], scn[Loader<FA, kConverters>::NS];
+      if (cur.t < a.tiles) scales(cur, sc);
+      bool ok = true;
+      for (int i = 0; cur.t < a.tiles; ++i) {
+        nxt = cur;
+        advance(nxt);
+        if (nxt.t < a.tiles) scales(nxt, scn);  // a step ahead
+        const int s = i % kStages;
+        constexpr int kUnits = kBM * 4 / kConverters;
+        uint4 v[kUnits];
+        if constexpr (kRaw) {
+          const int w = i % kRaws;
+          ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
+          if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+            const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot) + t0;
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) v[j] = src[j * kConverters];
+          } else {
+            ok = false;
+          }
+        } else {
+          fetch(far, i + kRaws - 1);
+          if (far.t < a.tiles) advance(far);
+          norm::copy_wait<kRaws - 1>();
+          __syncwarp();  // a line's words are copied by lanes of one warp
+        }
+        if (ok && i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
+        ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+        if (!ok) break;
+        uint8_t* sa = smem + s * kStageBytes;
+        if constexpr (kRaw) {
+          __syncwarp();  // every lane has read its units
+          if (lane == 0) mbar_arrive(&rawe[i % kRaws]);
+#pragma unroll
+          for (int j = 0; j < kUnits; ++j) la.template put<HALF>(v[j], j, sc, sa);
+        } else {
+          const uint8_t* slot = raws + (i % kRaws) * C::kSlot;
+          if constexpr (!ALA) la.template convert<HALF>(slot, kBM, sa, sc, first_a(cur), left_a(cur), kleft(cur), kBM);
+          if constexpr (!ALB) {
+            const float none[1] = {0.0f};
+            lb.template convert<HALF>(slot + C::kSlotA, kNBMax, sa + kABytes, none, first_b(cur), left_b(cur), kleft(cur), blines);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        cur = nxt;
+#pragma unroll
+        for (int k = 0; k < Loader<FA, kConverters>::NS; ++k) sc[k] = scn[k];
       }
       if (!ok) {
         i8_flag();
         *abort_flag = 1;
       }
+      cp_async_wait_all();
     }
   } else if (warp == kTmaAWarp || warp == kTmaBWarp) {
     // ------------------------------------------------------------ TMA --
@@ -391,10 +407,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0 && (is_a ? ALA : ALB)) {
       // A's integers go into the raw ring, 16-bit lines into the stage
       const bool ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
-      const int slots = ring ? kRaws : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
+      const int slots = ring ? (kRaws ? kRaws : 1) : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
       uint64_t *f = ring ? rawf : full, *e = ring ? rawe : empty;
       uint8_t* base = ring ? raws : smem + (is_a ? 0 : kABytes);
-      const uint32_t pitch = ring ? kRawBytes : kStageBytes, line = ring ? 64 : 128;
+      const uint32_t pitch = ring ? C::kSlot : kStageBytes, line = ring ? 64 : 128;
       const CUtensorMap* map = is_a ? &amap : &bmap;
       [[maybe_unused]] const long long I = is_a ? a.m.M : a.m.N;
       // a weight has one slice for all z
@@ -478,6 +494,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp < kEpiWarps) {
     // ----------------------------------------------------------- epilogue --
+    const int q4 = warp & 3;                    // TMEM lanes 32 q4 ..: m of this warp
     uint8_t* stg = staging + warp * kEpiBytes;  // 16-byte piece s of row r at piece s ^ (r / 2 % 4): no bank conflicts
     float* cs = colscale + warp * 32;
     const bool split = a.part != nullptr;
@@ -487,10 +504,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
       const Tile c = tile_of(t);
       const int ab = tl & 1;
-      // scale of column c0 + lane, fetched a chunk ahead
+      // chunks of 32 columns, every second one where two warps share the lanes; the scale of a
+      // chunk's column `lane` is fetched a chunk ahead
+      constexpr int kStep = 8 * kEpiWarps;
+      const int c00 = (warp >> 2) * 32;
       auto column = [&](int col) { return scaled && c.n0 + col < a.m.N ? __ldg(a.m.cs + c.n0 + col) : 0.0f; };
-      float next = column(lane);
-      const long long row0 = c.m0 + warp * 32;  // TMEM lanes 32 warp ..: m of this warp
+      float next = column(c00 + lane);
+      const long long row0 = c.m0 + q4 * 32;
       const float rs = scaled && row0 + lane < a.m.M ? __ldg(a.m.rs + c.z * a.m.rs_z + row0 + lane) : 1.0f;
       bool fin = mbar_wait(&accf[ab], (tl >> 1) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
@@ -506,13 +526,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // first of this warp's outputs; rows of the output are n (TR) or m
       uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) + (slice + (TR ? c.n0 * a.m.M + row0 : row0 * a.m.N + c.n0)) * eb;
       const long long pitch = (TR ? a.m.M : a.m.N) * eb;
-      for (int c0 = 0; c0 < cols && rows > 0; c0 += 32) {
+      for (int c0 = c00; c0 < cols && rows > 0; c0 += kStep) {
         uint32_t v[32];
-        tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(warp * 32) << 16) + c0, v);
+        tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(q4 * 32) << 16) + c0, v);
         if (scaled) {
           cs[lane] = next;
           __syncwarp();
-          next = column(c0 + 32 + lane);
+          next = column(c0 + kStep + lane);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 f = *reinterpret_cast<const float4*>(cs + e);
@@ -539,17 +559,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (e < left) *reinterpret_cast<uint16_t*>(o + e * pitch) = round_16(__uint_as_float(v[e]), h16);
           } else {
-            // 64 bytes of 32 n through shared memory, then 16 bytes to a lane
+            // pairs of n of 32 m through shared memory, then 8 m of both n to a lane
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              *reinterpret_cast<uint16_t*>(stg + e * 64 + ((((lane >> 3) ^ (e >> 1)) & 3) << 4) + (lane & 7) * 2) = round_16(__uint_as_float(v[e]), h16);
+            for (int e = 0; e < 32; e += 2)
+              *reinterpret_cast<uint32_t*>(stg + (e / 2) * 128 + lane * 4) = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
             __syncwarp();
             uint8_t* o = out + (long long)c0 * pitch;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int idx = lane + 32 * h, row = idx >> 2, seg = idx & 3;
-              if (row < left && seg * 8 < rows)
-                *reinterpret_cast<uint4*>(o + row * pitch + seg * 16) = *reinterpret_cast<const uint4*>(stg + row * 64 + ((seg ^ (row >> 1)) & 3) * 16);
+            for (int h = 0; h < 2; ++h) {
+              const int pair = (lane >> 2) + 8 * h, seg = lane & 3;
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + pair * 128 + seg * 32), y = *reinterpret_cast<const uint4*>(stg + pair * 128 + seg * 32 + 16);
+              if (seg * 8 < rows) {
+                uint8_t* d = o + 2 * pair * pitch + seg * 16;
+                if (2 * pair < left)
+                  *reinterpret_cast<uint4*>(d) = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                                                            __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+                if (2 * pair + 1 < left)
+                  *reinterpret_cast<uint4*>(d + pitch) = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                                                                    __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
+              }
             }
             __syncwarp();
           }
@@ -642,10 +670,11 @@ int tc_launch(const TcArgs& a, cudaStream_t st) {
   int rc;
   if (ALA && (rc = tc_encode(&amap, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF))) return rc;
   if (ALB && (rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
+  constexpr size_t kSmem = Plan<FA, ALA, ALB>::kSmem;
   auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return check_launch("i8_tc_kernel attribute");
-  kern<<<(int)min(a.tiles, (long long)kSMs), kTcThreads, kTcSmem, st>>>(amap, bmap, a);
+  kern<<<(int)min(a.tiles, (long long)kSMs), kTcThreads, kSmem, st>>>(amap, bmap, a);
   return check_launch("i8_tc_kernel");
 }
 

@@ -94,10 +94,22 @@ int held(const TokenArgs& a, bool glu, cudaStream_t st) {
   return tokens_held<T, V, 4, true, false, false>(a, st);
 }
 
+template <typename T>
+int ring(const TokenArgs& a, bool glu, cudaStream_t st) {
+  if (!glu) return tokens_ring<T, false, true, false>(a, st);
+  if (a.xq && a.q) return tokens_ring<T, true, true, true>(a, st);
+  if (a.xq) return tokens_ring<T, true, true, false>(a, st);
+  if (a.q) return tokens_ring<T, true, false, true>(a, st);
+  return tokens_ring<T, true, false, false>(a, st);
+}
+
 template <typename T, bool GLU>
 int tokens(const TokenArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  const int rc = (a.P == 1 ? a.C : a.P) % V == 0 ? held<T, V>(a, GLU, st) : held<T, 1>(a, GLU, st);
+  int rc = DISCO_ERR_UNSUPPORTED;
+  if (a.P > 1 && a.P % V == 0) rc = ring<T>(a, GLU, st);
+  if (rc != DISCO_ERR_UNSUPPORTED) return rc;
+  rc = (a.P == 1 ? a.C : a.P) % V == 0 ? held<T, V>(a, GLU, st) : held<T, 1>(a, GLU, st);
   if (rc != DISCO_ERR_UNSUPPORTED) return rc;
   const long long tiles = a.P == 1 ? a.B : a.B * ((a.P + 31) / 32);
   const int grid = (int)min(tiles, (long long)kSMs * 8);

@@ -354,6 +354,257 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_rows_kernel(const TokenA
   }
 }
 
+// ---- grids: tiles of pixels in a ring of shared memory ----------------------
+
+// Persistent CTAs of NT threads take tiles of LX words of pixels by all channels.  A
+// thread copies its own words of the tiles ahead with cp.async, so the loads of `depth`
+// tiles are in flight while one is worked on, and no barrier orders the copies; it reads its
+// words twice (magnitudes, rounding).  y waits between the two in the words of its gate and value.
+struct RingCut {
+  int NT, LX, nj, depth;        // nj: words of a thread in a tile, of each half
+  long long per_sample, tiles;
+};
+constexpr int kRingMax = 512;
+
+// Reciprocal and magnitude of V tokens, as the words of a row of shared memory.
+// Tokens of ordinary magnitudes need no power of two (Quantizer's f is 1); of zeros
+// any magnitude gives 0.  A tile with any other token rounds one value at a time.
+__device__ __forceinline__ bool ordinary(float amax) { return amax == 0.0f || (amax >= 1e-20f && amax <= 1e30f); }
+
+// q of a word of V inputs of V tokens: quantize<T>, two values to an instruction
+template <typename T, int V>
+__device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, const F<V>& inv, const F<V>& minus_a, bool plain) {
+  if (plain && sizeof(T) == 2) {
+    const F<V> kx = norm::mul(norm::fill<V>(kQMax), x);
+    F<V> t = norm::mul(kx, inv);
+    t = norm::fma(norm::fma(t, minus_a, kx), inv, t);
+    t = norm::add(t, norm::fill<V>(kRound));
+#pragma unroll
+    for (int e = 0; e < V; ++e) r[e] = __float_as_uint(t.v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      Quantizer z(1.0f);
+      if (plain) z.k = kQMax, z.b = -minus_a.v[e], z.inv = inv.v[e];
+      else z = Quantizer(-minus_a.v[e]);
+      r[e] = quantize<T>(x.v[e], z);
+    }
+  }
+}
+
+template <typename T, bool GLU, bool XQ, bool YQ>
+__global__ void __launch_bounds__(kRingMax) tokens_ring_kernel(const TokenArgs a, const RingCut g) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0);
+  using R = Raw<T, V>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX, NL = g.NT / g.LX;
+  const int warps = g.NT / 32, warp = tid / 32;
+  const int slot_words = G * g.nj * g.NT;
+  uint4* ring = reinterpret_cast<uint4*>(smem) + tid;
+  float* scratch = reinterpret_cast<float*>(smem + (size_t)g.depth * slot_words * 16);  // of each warp: 1/a, -a of x, 127/a of y
+  uint8_t* sums = reinterpret_cast<uint8_t*>(scratch + warps * ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * g.LX * V);  // [2]: [warps][pixels] of x, of y
+  const long long half = a.C * a.P;
+  auto place = [&](long long t, long long* b, long long* p) {
+    *b = g.tiles <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)g.per_sample) : t / g.per_sample;
+    *p = (t - *b * g.per_sample) * (g.LX * V) + lx * V;
+  };
+  auto fetch = [&](long long t, int slot) {
+    if (t < g.tiles) {
+      long long b, p;
+      place(t, &b, &p);
+      if (p < a.P) {
+        const T* x = (const T*)a.x + b * G * half + p;
+        uint4* d = ring + slot * slot_words;
+        for (int i = 0; i < g.nj; ++i) {
+          const int c = j0 + i * NL;
+          if (c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) {
+#pragma unroll
+            for (int h = 0; h < G; ++h) norm::copy_async(d + (i * G + h) * g.NT, x + h * half + c * a.P);
+          }
+        }
+      }
+    }
+    norm::copy_commit();
+  };
+  for (int d = 0; d < g.depth - 1; ++d) fetch(blockIdx.x + (long long)d * gridDim.x, d);
+  int n = 0;
+  for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x, ++n) {
+    fetch(t + (long long)(g.depth - 1) * gridDim.x, (n + g.depth - 1) % g.depth);
+    if (g.depth == 3) norm::copy_wait<2>();
+    else norm::copy_wait<1>();
+    long long b, p;
+    place(t, &b, &p);
+    const bool live = p < a.P;
+    const long long y0 = b * half + p;
+    uint4* w = ring + (n % g.depth) * slot_words;
+    Mag<T, V> mx;
+    uint32_t my[V];
+    mx.clear();
+#pragma unroll
+    for (int e = 0; e < V; ++e) my[e] = 0;
+    const int nj = live ? (a.C - j0 + NL - 1) / NL : 0;
+#pragma unroll 2
+    for (int i = 0; i < nj; ++i) {
+      uint4* s = w + i * G * g.NT;
+      const uint4 w0 = s[0];
+      if constexpr (XQ) mx.add(w0);
+      if constexpr (GLU) {
+        const uint4 w1 = s[g.NT];
+        if constexpr (XQ) mx.add(w1);
+        R r0, r1;
+        memcpy(&r0, &w0, 16);
+        memcpy(&r1, &w1, 16);
+        const F<V> gate = unpack<T, V>(r0), val = unpack<T, V>(r1);
+        F<V> v;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
+        if constexpr (YQ) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) my[e] = max32(my[e], __float_as_uint(v.v[e]));
+          if constexpr (!XQ) {  // y over its gate and value
+            s[0] = *reinterpret_cast<const uint4*>(v.v);
+            if constexpr (V == 8) s[g.NT] = *reinterpret_cast<const uint4*>(v.v + 4);
+          }
+        }
+        if (a.y && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_stream((T*)a.y + y0 + (j0 + i * NL) * a.P, packed<T, V>(v));
+      }
+    }
+    const int TP = g.LX * V;
+    float* own = scratch + warp * ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * TP;
+    bool plain = true;
+    if constexpr (XQ || YQ) {
+      for (int o = g.LX; o < 32; o *= 2) {
+        if constexpr (XQ)
+#pragma unroll
+          for (int k = 0; k < Mag<T, V>::N; ++k) mx.join(__shfl_xor_sync(0xffffffffu, mx.m[k], o), k);
+        if constexpr (YQ)
+#pragma unroll
+          for (int k = 0; k < V; ++k) my[k] = max(my[k], __shfl_xor_sync(0xffffffffu, my[k], o));
+      }
+      // rows of the tile's pixels, one for each warp; two sets of them: one barrier a tile
+      uint8_t* part = sums + (n & 1) * warps * TP * kSum;
+      if ((tid & 31) < g.LX) {
+        if constexpr (XQ) memcpy(part + (warp * TP + lx * V) * ES, mx.m, V * ES);
+        if constexpr (YQ) memcpy(part + warps * TP * (XQ ? ES : 0) + (warp * TP + lx * V) * 4, my, V * 4);
+      }
+      __syncthreads();
+      // each warp joins them for itself, a pixel to a lane
+      for (int e = tid & 31; e < TP; e += 32) {
+        const long long at = b * a.P + p - lx * V + e;
+        const bool in = p - lx * V + e < a.P;
+        if constexpr (XQ) {
+          float amax;
+          if constexpr (ES == 2) {
+            uint32_t m = 0;
+            for (int o = 0; o < warps; ++o) m = max(m, (uint32_t)reinterpret_cast<const uint16_t*>(part)[o * TP + e]);
+            const uint16_t h = (uint16_t)m;
+            T v;
+            memcpy(&v, &h, 2);
+            amax = to_f32(v);
+          } else {
+            uint32_t m = 0;
+            for (int o = 0; o < warps; ++o) m = max(m, reinterpret_cast<const uint32_t*>(part)[o * TP + e]);
+            amax = __uint_as_float(m);
+          }
+          plain = plain && ordinary(amax);
+          if (warp == 0 && in) a.xscale[at] = Quantizer(amax).scale;
+          own[e] = __frcp_rn(amax == 0.0f ? 1.0f : amax);
+          own[TP + e] = amax == 0.0f ? -1.0f : -amax;
+        }
+        if constexpr (YQ) {
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(part + warps * TP * (XQ ? ES : 0));
+          uint32_t m = 0;
+          for (int o = 0; o < warps; ++o) m = max(m, q[o * TP + e]);
+          const Quantizer z(__uint_as_float(m));
+          if (warp == 0 && in) a.scale[at] = z.scale;
+          // a token with an infinity or a NaN: 0, and values that are NaN times it are cleared below
+          own[(XQ ? 2 * TP : 0) + e] = z.scale < __int_as_float(0x7f800000) ? z.k * z.inv : 0.0f;
+          plain = plain && z.scale < __int_as_float(0x7f800000);
+        }
+      }
+      plain = __all_sync(0xffffffffu, plain);
+      __syncwarp();
+    }
+    if (live) {
+      if constexpr (XQ) {
+        const F<V> inv = norm::load_row<V>(own + lx * V), minus_a = norm::load_row<V>(own + TP + lx * V);
+        int8_t* d = a.xq + G * b * half + p + j0 * a.P;
+#pragma unroll 2
+        for (int i = 0; i < nj; ++i, d += NL * a.P)
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            R r0;
+            memcpy(&r0, &w[(i * G + h) * g.NT], 16);
+            uint32_t r[V];
+            quantize_word<T, V>(r, unpack<T, V>(r0), inv, minus_a, plain);
+            if (DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_bytes<V>(d + h * half, r);
+          }
+      }
+      if constexpr (YQ) {
+        const F<V> f = norm::load_row<V>(own + (XQ ? 2 * TP : 0) + lx * V);
+        int8_t* d = a.q + y0 + j0 * a.P;
+#pragma unroll 2
+        for (int i = 0; i < nj; ++i, d += NL * a.P) {
+          uint4* s = w + i * G * g.NT;
+          F<V> v;
+          if constexpr (!XQ) {
+            *reinterpret_cast<uint4*>(v.v) = s[0];
+            if constexpr (V == 8) *reinterpret_cast<uint4*>(v.v + 4) = s[g.NT];
+          } else {
+            R r0, r1;
+            memcpy(&r0, &s[0], 16);
+            memcpy(&r1, &s[g.NT], 16);
+            const F<V> gate = unpack<T, V>(r0), val = unpack<T, V>(r1);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
+          }
+          v = norm::mul(v, f);
+          if (!plain)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v.v[e] = fabsf(v.v[e]) < 128.0f ? v.v[e] : 0.0f;
+          v = norm::add(v, norm::fill<V>(kRound));
+          uint32_t r[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) r[e] = __float_as_uint(v.v[e]);
+          if (DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_bytes<V>(d, r);
+        }
+      }
+    }
+    __syncwarp();  // `own` is read
+  }
+}
+
+template <typename T, bool GLU, bool XQ, bool YQ>
+int tokens_ring(const TokenArgs& a, cudaStream_t st) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0), kOwn = (XQ ? 2 : 0) + (YQ ? 1 : 0);
+  RingCut g;
+  size_t smem = 0;
+  // 128 bytes of a row to a tile, three tiles deep, while they fit
+  static const int shapes[][2] = {{8, 3}, {8, 2}, {4, 2}, {2, 2}};
+  bool fits = false;
+  for (const auto& s : shapes) {
+    g.LX = s[0], g.depth = s[1];
+    while (g.LX > 2 && (long long)g.LX / 2 * V >= a.P) g.LX /= 2;
+    // few channels: more pixels to a tile.  A thread has about 8 words of each half: what it does once a tile is divided by them
+    while (g.LX < 32 && a.C * g.LX < 1024 && g.LX * V < a.P) g.LX *= 2;
+    g.NT = 128;
+    while (g.NT < kRingMax && a.C * g.LX > 8 * g.NT) g.NT *= 2;
+    g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
+    smem = (size_t)g.depth * G * g.nj * g.NT * 16 + (size_t)(g.NT / 32) * g.LX * V * (4 * kOwn + 2 * kSum);
+    if ((fits = smem <= norm::kMaxSmem)) break;
+  }
+  if (!fits) return DISCO_ERR_UNSUPPORTED;
+  g.per_sample = (a.P + g.LX * V - 1) / (g.LX * V);
+  g.tiles = g.per_sample * a.B;
+  auto kern = tokens_ring_kernel<T, GLU, XQ, YQ>;
+  // one limit for all calls: host threads share it
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)norm::kMaxSmem) != cudaSuccess)
+    return check_launch("tokens_ring_kernel attribute");
+  const int ctas = (int)min((size_t)(1024 / g.NT), norm::kMaxSmem / (smem + 1024));
+  kern<<<(int)min(g.tiles, (long long)kSMs * max(1, ctas)), g.NT, smem, st>>>(a, g);
+  return check_launch("tokens_ring_kernel");
+}
+
 // Launches the kernels above; DISCO_ERR_UNSUPPORTED, without launching, for tokens
 // that no CTA holds.
 template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
