@@ -87,15 +87,16 @@ bool rows_aligned(const Operand& o) {
 }
 
 int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) {
+  if (c.mt * c.nt * m.Z * c.nsplit >= 1LL << 31) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 by %d", c.NB);
   TcArgs a = {};
   a.m = m;
   a.enda = (const uint8_t*)m.A.p + m.A.n * (m.A.bits / 8);
   a.endb = (const uint8_t*)m.B.p + m.B.n * (m.B.bits / 8);
-  a.NB = c.NB, a.nsplit = c.nsplit, a.mt = c.mt, a.nt = c.nt, a.nkp = c.nkp, a.steps = c.steps;
+  a.NB = c.NB, a.nsplit = c.nsplit, a.mt = (uint32_t)c.mt, a.nt = (uint32_t)c.nt, a.nkp = c.nkp, a.steps = c.steps;
   a.part = c.nsplit > 1 ? (float*)part : nullptr;
   a.out_type = dtype;
   a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
-  a.tiles = c.mt * c.nt * m.Z * c.nsplit;
+  a.tiles = (uint32_t)(c.mt * c.nt * m.Z * c.nsplit);
   // the copy engine's coordinates are 32-bit, its strides below 2^40 bytes
   const bool small = max(max(m.M, m.N), m.K) < 1LL << 31 && max(m.A.n, m.B.n) < 1LL << 38;
   a.ala = small && rows_aligned(m.A), a.alb = small && rows_aligned(m.B);

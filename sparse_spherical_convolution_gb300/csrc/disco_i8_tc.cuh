@@ -11,11 +11,13 @@
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
 // Persistent kernel:
-//   epilogue     (8 warps; 4 where rows are off alignment): tcgen05.ld, scales, rounding,
-//                stores along the output's rows
-//   converters   (4 warps; 8): integers from the raw ring, to 16 bits, into the stage.  All of
-//                them take every step in order: a waiter on a ring's barrier then is never
-//                two phases ahead of it, where a wait by parity would pass at once
+//   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few, and where rows are
+//                off alignment): tcgen05.ld, scales, rounding, stores along the output's rows
+//   converters   (the rest up to warp 11): integers from the raw ring, to 16 bits, into the
+//                stage.  Two groups take alternate steps, so that one's loads, conversion and
+//                fence overlap the other's.  The raw ring has an even number of slots, each always
+//                the same group's, and stages are released in order: no waiter is ever two
+//                phases ahead of a barrier, where a wait by parity would pass at once
 //   warp 12      MMA issuer (one thread); two accumulators of 256 TMEM columns, so
 //                the epilogue of a tile overlaps the main loop of the next
 //   warp 13      TMA of B, and warp 14 of A: into the stage (16-bit) or the raw ring (integers)
@@ -61,14 +63,16 @@ struct Form {
 template <class FA, bool ALA, bool ALB>
 struct Plan {
   static constexpr bool kAligned = ALA && ALB;
-  static constexpr int kEpi = kAligned ? 8 : 4, kConv = kMmaWarp - kEpi;
+  static constexpr int kEpi = kAligned && !FA::SC ? 8 : 4, kConv = kMmaWarp - kEpi;
   static constexpr bool kRaw = ALA && FA::ES == 1;  // A by TMA into the raw ring
+  static constexpr int kGroups = kRaw ? 2 : 1, kGroupWarps = kConv / kGroups;
   static constexpr uint32_t kSlotA = kRaw ? kBM * kBK : ALA ? 0 : kBM * (64 * FA::ES + 16);
   static constexpr uint32_t kSlot = kSlotA + (ALB ? 0 : kNBMax * (128 + 16));
   static constexpr int kStages = kAligned ? (kRaw ? 3 : 4) : ALB ? 3 : 2;
   static constexpr int kRaws = kAligned ? (kRaw ? 6 : 0) : ALB ? 4 : 2;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kEpiBytes + 128) + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kRaws % kGroups == 0, "a slot is always the same group's");
   static_assert(!kRaw || ALB, "the raw ring is filled by TMA or by the converters");
 };
 
@@ -221,7 +225,8 @@ struct Loader {
 
 // Where a converter is: step q of tile t, slice r, chunk kc.
 struct Pos {
-  long long t, q, q1, r, kc, m0, n0, z;
+  uint32_t t;
+  long long q, q1, r, kc, m0, n0, z;
 };
 
 __device__ __forceinline__ void tc_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
   using FB = Form<2, BKM, 0>;
   using C = Plan<FA, ALA, ALB>;
-  constexpr int kEpiWarps = C::kEpi, kConvWarps = C::kConv, kConverters = 32 * kConvWarps, kStages = C::kStages, kRaws = C::kRaws;
+  constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps, kStages = C::kStages, kRaws = C::kRaws;
   constexpr bool kRaw = C::kRaw, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
   constexpr bool kConv = !kTmaA || !ALB;                      // the converters have work
   extern __shared__ uint8_t smem_raw[];
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], (kConv ? kConvWarps : 0) + (kTmaA ? 1 : 0) + (ALB ? 1 : 0));
+      mbar_init(&full[s], (kConv ? kGroupWarps : 0) + (kTmaA ? 1 : 0) + (ALB ? 1 : 0));
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int r = 0; r < 8; ++r) {
       mbar_init(&rawf[r], 1);
-      mbar_init(&rawe[r], kConvWarps);
+      mbar_init(&rawe[r], kGroupWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -286,34 +291,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     long long m0, n0, z, q0, q1;
     int sp;
   };
-  auto tile_of = [&](long long t) {
+  auto tile_of = [&](uint32_t t) {  // 32-bit divisions: 64-bit ones took a third of a tile of four steps
     Tile c;
-    c.n0 = t % a.nt * a.NB;
-    t /= a.nt;
-    c.m0 = t % a.mt * kBM;
-    t /= a.mt;
-    c.z = t % a.m.Z;
-    c.sp = (int)(t / a.m.Z);
-    c.q0 = a.steps * c.sp / a.nsplit;
-    c.q1 = a.steps * (c.sp + 1) / a.nsplit;
+    uint32_t u = t / a.nt;
+    c.n0 = (long long)(t - u * a.nt) * a.NB;
+    t = u / a.mt;
+    c.m0 = (long long)(u - t * a.mt) * kBM;
+    u = t / (uint32_t)a.m.Z;
+    c.z = t - u * a.m.Z;
+    c.sp = (int)u;
+    c.q0 = 0, c.q1 = a.steps;
+    if (a.nsplit > 1) c.q0 = a.steps * c.sp / a.nsplit, c.q1 = a.steps * (c.sp + 1) / a.nsplit;
     return c;
   };
 
   if (warp >= kEpiWarps && warp < kMmaWarp) {
     // --------------------------------------------------------- converters --
     if constexpr (kConv) {
-      const int t0 = tid - 32 * kEpiWarps;
+      const int group = (warp - kEpiWarps) / kGroupWarps, t0 = tid - 32 * kEpiWarps - group * kConverters;
       Loader<FA, kConverters> la;
       Loader<FB, kConverters> lb;
       la.init(a.m.A, a.enda, t0);
       lb.init(a.m.B, a.endb, t0);
       const int blines = (a.NB + 63) / 64 * 64;
-      auto start = [&](Pos& p, long long t) {
+      auto start = [&](Pos& p, uint32_t t) {
         p.t = t;
         if (t >= a.tiles) return;
         const Tile c = tile_of(t);
         p.q = c.q0, p.q1 = c.q1, p.m0 = c.m0, p.n0 = c.n0, p.z = c.z;
-        p.r = a.m.R == 1 ? 0 : c.q0 / a.nkp;
+        p.r = c.q0 == 0 || a.m.R == 1 ? 0 : c.q0 / a.nkp;
         p.kc = c.q0 - p.r * a.nkp;
       };
       auto advance = [&](Pos& p) {
@@ -339,6 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       Pos cur, nxt, far;
       start(cur, blockIdx.x);
+      if (group == 1 && cur.t < a.tiles) advance(cur);
       far = cur;
       if constexpr (!kRaw)
         for (int d = 0; d < kRaws - 1; ++d) {
@@ -348,10 +355,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float sc[Loader<FA, kConverters>::NS], scn[Loader<FA, kConverters>::NS];
       if (cur.t < a.tiles) scales(cur, sc);
       bool ok = true;
-      for (int i = 0; cur.t < a.tiles; ++i) {
+      for (int i = group; cur.t < a.tiles; i += kGroups) {
         nxt = cur;
-        advance(nxt);
-        if (nxt.t < a.tiles) scales(nxt, scn);  // a step ahead
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k)
+          if (nxt.t < a.tiles) advance(nxt);
+        if (nxt.t < a.tiles) scales(nxt, scn);  // this group's next step's
         const int s = i % kStages;
         constexpr int kUnits = kBM * 4 / kConverters;
         uint4 v[kUnits];
@@ -417,10 +426,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool sliced = is_a ? a.m.A.z || a.m.A.r : a.m.B.z || a.m.B.r;
       int i = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+      for (uint32_t t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
         const Tile c = tile_of(t);
         const long long i0 = is_a ? c.m0 : c.n0;
-        long long r = a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
+        long long r = c.q0 == 0 || a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
         for (long long q = c.q0; q < c.q1; ++q, ++i, ++kc) {
           if (kc == a.nkp) kc = 0, ++r;
           const int s = i % slots;
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t idesc = idesc_16_f32(kBM, nmma, HALF) | (FA::KM ? 0u : 1u << 15) | (BKM ? 0u : 1u << 16);
       int i = 0, tl = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++tl) {
+      for (uint32_t t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++tl) {
         const Tile c = tile_of(t);
         const int ab = tl & 1;
         if (tl >= 2 && !mbar_wait(&acce[ab], ((tl >> 1) - 1) & 1, kWaitLimit)) {
@@ -501,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int type = split ? DISCO_F32 : a.out_type, eb = type == DISCO_F32 ? 4 : 2;
     const bool scaled = !split && a.m.cs, h16 = type == DISCO_F16;
     int tl = 0;
-    for (long long t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
+    for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
       const Tile c = tile_of(t);
       const int ab = tl & 1;
       // chunks of 32 columns, every second one where two warps share the lanes; the scale of a
@@ -674,7 +683,7 @@ int tc_launch(const TcArgs& a, cudaStream_t st) {
   auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return check_launch("i8_tc_kernel attribute");
-  kern<<<(int)min(a.tiles, (long long)kSMs), kTcThreads, kSmem, st>>>(amap, bmap, a);
+  kern<<<min(a.tiles, (uint32_t)kSMs), kTcThreads, kSmem, st>>>(amap, bmap, a);
   return check_launch("i8_tc_kernel");
 }
 
