@@ -110,5 +110,26 @@ __device__ __forceinline__ float from_byte(uint32_t flipped, int e) {  // flippe
   return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 + e)) - 8388736.0f;
 }
 
+// The nb bytes from byte sh of two words on, zeros behind them.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int sh, int nb) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (sh & 8)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (sh & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (sh & 3));
+  if (nb < 16)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = nb - 4 * i;  // bytes of this word that belong to the line
+      if (left < 4) o[i] = left <= 0 ? 0 : o[i] & (0xffffffffu >> (32 - 8 * left));
+    }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 }  // namespace i8
 }  // namespace disco

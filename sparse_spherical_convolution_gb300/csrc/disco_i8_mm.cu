@@ -10,6 +10,7 @@
 // activation (m = token; the channel of its weight's gradient).
 
 #include "disco_i8_mm.cuh"
+#include "disco_umma.cuh"
 
 namespace disco {
 
@@ -24,6 +25,7 @@ constexpr int kAnyThreads = 256;
 // The parts' sums in their order, scaled and rounded.
 template <typename TO>
 __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, const float* part, int nsplit, long long n) {
+  norm::wait_for_previous();
   for (long long i = (long long)blockIdx.x * kAnyThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kAnyThreads) {
     float v = 0.0f;
     for (int s = 0; s < nsplit; ++s) v += part[s * n + i];
@@ -37,19 +39,134 @@ __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, co
   }
 }
 
-// A weight [Cout][Cin] as the 16-bit operand: the integers in fp16, or times their
-// channel's scale rounded to the type; rows padded to `ld` elements with zeros.
+// Integers [rows][C] as the 16-bit operand: in fp16, or times their row's scale rounded
+// to the type; rows padded to `ld` elements with zeros.
 template <typename T>
-__global__ void __launch_bounds__(kAnyThreads) mm_weight_kernel(const int8_t* W, const float* wscale, T* w16, int Cin, int ld, long long n) {
+__global__ void __launch_bounds__(kAnyThreads) mm_operand_kernel(const int8_t* q, const float* scale, T* w16, int C, int ld, long long n) {
   const long long i = ((long long)blockIdx.x * kAnyThreads + threadIdx.x) * 8;
+  norm::let_next_begin();
   if (i >= n) return;
-  const long long o = i / ld;
+  const long long o = n <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)ld) : i / ld;
   const int c = (int)(i - o * ld);
-  const float f = wscale ? wscale[o] : 1.0f;
+  const float f = scale ? scale[o] : 1.0f;
+  uint32_t w[2];
+  if (C % 8 == 0) {
+    const uint2 u = *reinterpret_cast<const uint2*>(q + i);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < C) w[e / 4] |= (uint32_t)(uint8_t)q[o * C + c + e] << (8 * (e & 3));
+  }
   T v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(c + e < Cin ? (float)W[o * Cin + c + e] * f : 0.0f);
+  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(from_byte(w[e / 4] ^ 0x80808080u, e & 3) * f);
   *reinterpret_cast<uint4*>(w16 + i) = *reinterpret_cast<const uint4*>(v);
+}
+
+// ---- a few rows ----------------------------------------------------------------
+// Bound by the weight's bytes, or by the latency of one round to memory.  A warp takes O
+// output channels and all NB rows: a lane 16 input channels of each at a time, four
+// products and their sum to an instruction (dp4a), exact in 32 bits.  The rows lie in shared memory
+// from their first byte on, zeros behind them.
+constexpr int kFewThreads = 128, kFewRows = 16;
+constexpr size_t kFewSmem = 128 * 1024;
+
+__device__ __forceinline__ uint4 load16(const int8_t* p, const int8_t* end) {
+  if (p + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (p + i < end) w[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Word i (16 bytes) of a row of C bytes anywhere in a tensor that ends at `end`.
+template <bool ALN>
+__device__ __forceinline__ uint4 row_word(const int8_t* row, int i, int C, const int8_t* end) {
+  if (ALN) return __ldg(reinterpret_cast<const uint4*>(row) + i);
+  const int8_t* p = row + 16 * i;
+  const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15), nb = min(16, C - 16 * i);
+  if (nb <= 0) return make_uint4(0, 0, 0, 0);
+  const uint4 lo = load16(p - sh, end);
+  return shifted(lo, sh + nb > 16 ? load16(p - sh + 16, end) : make_uint4(0, 0, 0, 0), sh, nb);
+}
+
+struct FewArgs {
+  const int8_t *q, *W;
+  const float *scale, *wscale;
+  void* y;
+  int B, Cin, Cout, type;
+};
+
+template <int NB, int O, bool ALN>
+__global__ void __launch_bounds__(kFewThreads) mm_few_kernel(const FewArgs a) {
+  extern __shared__ __align__(16) uint4 rows[];  // [NB][words]
+  const int lane = threadIdx.x & 31, words = (a.Cin + 15) / 16;
+  const int o0 = (blockIdx.x * (kFewThreads / 32) + threadIdx.x / 32) * O;
+  const int8_t *qend = a.q + (long long)a.B * a.Cin, *wend = a.W + (long long)a.Cout * a.Cin;
+  uint4 w[O];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < O; ++k)
+      w[k] = o0 + k < a.Cout && i < words ? row_word<ALN>(a.W + (long long)(o0 + k) * a.Cin, i, a.Cin, wend) : make_uint4(0, 0, 0, 0);
+  };
+  fetch(lane);
+  for (int i = threadIdx.x; i < NB * words; i += kFewThreads) {
+    const int b = i / words;
+    rows[i] = b < a.B ? row_word<ALN>(a.q + (long long)b * a.Cin, i - b * words, a.Cin, qend) : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  int acc[O][NB] = {};
+  for (int i = lane; i < words; i += 32) {
+    uint4 v[O];
+#pragma unroll
+    for (int k = 0; k < O; ++k) v[k] = w[k];
+    fetch(i + 32);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint4 x = rows[b * words + i];
+#pragma unroll
+      for (int k = 0; k < O; ++k)
+        acc[k][b] = __dp4a((int)v[k].w, (int)x.w, __dp4a((int)v[k].z, (int)x.z, __dp4a((int)v[k].y, (int)x.y, __dp4a((int)v[k].x, (int)x.x, acc[k][b]))));
+    }
+  }
+  int mine[(O * NB + 31) / 32] = {};  // output k NB + b goes to lane (k NB + b) % 32
+#pragma unroll
+  for (int k = 0; k < O; ++k)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[k][b]), at = k * NB + b;
+      if (lane == at % 32) mine[at / 32] = s;
+    }
+#pragma unroll
+  for (int m = 0; m < (O * NB + 31) / 32; ++m) {
+    const int at = lane + 32 * m, b = at % NB, o = o0 + at / NB;
+    if (at < O * NB && b < a.B && o < a.Cout) {
+      const float v = (float)mine[m] * a.wscale[o] * a.scale[b];
+      const long long i = (long long)b * a.Cout + o;
+      if (a.type == DISCO_F32) ((float*)a.y)[i] = v;
+      else ((uint16_t*)a.y)[i] = round_16(v, a.type == DISCO_F16);
+    }
+  }
+}
+
+template <int NB, int O>
+int few(const FewArgs& a, cudaStream_t st) {
+  const int grid = (a.Cout + kFewThreads / 32 * O - 1) / (kFewThreads / 32 * O);
+  const size_t smem = (size_t)NB * ((a.Cin + 15) / 16) * 16;
+  if (a.Cin % 16 == 0) return norm::launch(mm_few_kernel<NB, O, true>, grid, kFewThreads, 1, false, smem, kFewSmem, st, "mm_few_kernel", a);
+  return norm::launch(mm_few_kernel<NB, O, false>, grid, kFewThreads, 1, false, smem, kFewSmem, st, "mm_few_kernel", a);
+}
+template <int NB>
+int few(const FewArgs& a, cudaStream_t st) {
+  // several channels to a warp share its reads of the rows, while every SM keeps some warps
+  return a.Cout >= 8 * 4 * kSMs ? few<NB, 4>(a, st) : few<NB, 1>(a, st);
+}
+bool takes_few(int32_t B, int32_t Cin, int64_t P) {
+  const int NB = B == 1 ? 1 : B <= 4 ? 4 : 16;
+  // 32 bits hold the sum of 2^16 products
+  return P == 1 && B <= kFewRows && Cin <= 1 << 16 && (size_t)NB * ((Cin + 15) / 16) * 16 <= kFewSmem;
 }
 
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).
@@ -74,10 +191,14 @@ struct Cut {
   size_t part_bytes(long long M, long long N, int Z) const { return nsplit > 1 ? (size_t)nsplit * Z * M * N * 4 : 0; }
 };
 
-// What a call needs of the workspace: the 16-bit weight, then the parts' sums.
-size_t weight_bytes(int32_t Cin, int32_t Cout) { return ((size_t)Cout * (((size_t)Cin + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+// What a call needs of the workspace: the 16-bit operand, then the parts' sums.
+size_t operand_bytes(long long rows, int32_t C) { return ((size_t)rows * (((size_t)C + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+// Of the product of rows, the smaller operand is converted once a call, the other one in the main loop.
+bool rows_are_b(int32_t B, int32_t Cout, int64_t P) { return P == 1 && B < Cout; }
 
-Cut cut_fwd(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(B, Cout, Cin, 1, 1) : Cut(P, Cout, Cin, B, 1); }
+Cut cut_fwd(int32_t B, int32_t Cin, int32_t Cout, int64_t P) {
+  return rows_are_b(B, Cout, P) ? Cut(Cout, B, Cin, 1, 1) : P == 1 ? Cut(B, Cout, Cin, 1, 1) : Cut(P, Cout, Cin, B, 1);
+}
 Cut cut_dx(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(B, Cin, Cout, 1, 1) : Cut(P, Cin, Cout, B, 1); }
 Cut cut_dw(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(Cin, Cout, B, 1, 1) : Cut(Cin, Cout, P, 1, B); }
 
@@ -86,7 +207,8 @@ bool rows_aligned(const Operand& o) {
   return o.ld * es % 16 == 0 && o.z * es % 16 == 0 && o.r * es % 16 == 0;
 }
 
-int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) {
+// after: an operand was converted just before
+int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, bool after, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) {
   if (c.mt * c.nt * m.Z * c.nsplit >= 1LL << 31) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 by %d", c.NB);
   TcArgs a = {};
   a.m = m;
@@ -95,6 +217,7 @@ int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, int (*tc)(
   a.NB = c.NB, a.nsplit = c.nsplit, a.mt = (uint32_t)c.mt, a.nt = (uint32_t)c.nt, a.nkp = c.nkp, a.steps = c.steps;
   a.part = c.nsplit > 1 ? (float*)part : nullptr;
   a.out_type = dtype;
+  a.after = after;
   a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
   a.tiles = (uint32_t)(c.mt * c.nt * m.Z * c.nsplit);
   // the copy engine's coordinates are 32-bit, its strides below 2^40 bytes
@@ -104,18 +227,18 @@ int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, int (*tc)(
   if (rc || !a.part) return rc;
   const long long n = m.Z * m.M * m.N;
   const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
-#define CALL(T) mm_join_kernel<T><<<grid, kAnyThreads, 0, st>>>(m, a.part, c.nsplit, n)
+#define CALL(T) rc = norm::launch(mm_join_kernel<T>, grid, kAnyThreads, 1, true, 0, 0, st, "mm_join_kernel", m, (const float*)a.part, c.nsplit, n)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
-  return check_launch("mm_join_kernel");
+  return rc;
 }
 
-int weight_16(const void* W, const float* wscale, void* w16, int32_t Cin, int32_t Cout, bool f16, cudaStream_t st) {
-  const int ld = (int)(((long long)Cin + 7) / 8 * 8);
-  const long long n = (long long)Cout * ld, grid = (n / 8 + kAnyThreads - 1) / kAnyThreads;
-  if (f16) mm_weight_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)W, wscale, (__half*)w16, Cin, ld, n);
-  else mm_weight_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)W, wscale, (__nv_bfloat16*)w16, Cin, ld, n);
-  return check_launch("mm_weight_kernel");
+int operand_16(const void* q, const float* scale, void* w16, int32_t C, int32_t rows, bool f16, cudaStream_t st) {
+  const int ld = (int)(((long long)C + 7) / 8 * 8);
+  const long long n = (long long)rows * ld, grid = (n / 8 + kAnyThreads - 1) / kAnyThreads;
+  if (f16) mm_operand_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)q, scale, (__half*)w16, C, ld, n);
+  else mm_operand_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)q, scale, (__nv_bfloat16*)w16, C, ld, n);
+  return check_launch("mm_operand_kernel");
 }
 
 // Sizes of a product; 16-bit types only for the gradients.
@@ -141,12 +264,13 @@ using namespace disco::i8;
 
 extern "C" size_t disco_matmul_i8_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, false)) return 0;
-  return weight_bytes(Cin, Cout) + cut_fwd(B, Cin, Cout, P).part_bytes((long long)B * P, Cout, 1);
+  if (takes_few(B, Cin, P)) return 16;
+  return operand_bytes(rows_are_b(B, Cout, P) ? B : Cout, Cin) + cut_fwd(B, Cin, Cout, P).part_bytes((long long)B * P, Cout, 1);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return weight_bytes(Cin, Cout) + cut_dx(B, Cin, Cout, P).part_bytes((long long)B * P, Cin, 1);
+  return operand_bytes(Cout, Cin) + cut_dx(B, Cin, Cout, P).part_bytes((long long)B * P, Cin, 1);
 }
 
 extern "C" size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
@@ -169,21 +293,33 @@ extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W,
   const unsigned in_place[] = {0, 0, 0, 0};
   if ((rc = check_buffers(in, in_place, 4, out, 2))) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
-  if ((rc = weight_16(W, nullptr, workspace, Cin, Cout, true, st))) return rc;
-  const long long ld = ((long long)Cin + 7) / 8 * 8;
+  if (takes_few(B, Cin, P)) {
+    const FewArgs a{(const int8_t*)q, (const int8_t*)W, scale, wscale, y, B, Cin, Cout, dtype};
+    return B == 1 ? few<1>(a, st) : B <= 4 ? few<4>(a, st) : few<16>(a, st);
+  }
+  const bool swap = rows_are_b(B, Cout, P);
+  const long long ld = ((long long)Cin + 7) / 8 * 8, rows16 = swap ? B : Cout;
+  if ((rc = operand_16(swap ? q : W, nullptr, workspace, Cin, (int32_t)rows16, true, st))) return rc;
   MmArgs a = {};
   a.out = y;
-  a.rs = scale, a.cs = wscale;
-  a.N = Cout, a.K = Cin, a.R = 1;
-  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, true, Cout * ld};
-  if (P == 1) {  // m = row
-    a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)(T * Cin)};
-    a.M = B, a.Z = 1;
-  } else {  // m = pixel
-    a.A = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)(T * Cin)};
-    a.M = P, a.Z = B, a.rs_z = P, a.transposed = true;
+  a.K = Cin, a.R = 1, a.Z = 1;
+  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, true, rows16 * ld};
+  if (swap) {  // m = output channel, n = row
+    a.A = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
+    a.rs = wscale, a.cs = scale;
+    a.M = Cout, a.N = B, a.transposed = true;
+  } else {  // n = output channel
+    a.rs = scale, a.cs = wscale;
+    a.N = Cout;
+    if (P == 1) {  // m = row
+      a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)(T * Cin)};
+      a.M = B;
+    } else {  // m = pixel
+      a.A = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)(T * Cin)};
+      a.M = P, a.Z = B, a.rs_z = P, a.transposed = true;
+    }
   }
-  return run(a, cut_fwd(B, Cin, Cout, P), dtype, (char*)workspace + weight_bytes(Cin, Cout), tc_fwd, st);
+  return run(a, cut_fwd(B, Cin, Cout, P), dtype, (char*)workspace + operand_bytes(rows16, Cin), true, tc_fwd, st);
 }
 
 extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const float* wscale, void* dx, int32_t B, int32_t Cin,
@@ -201,7 +337,7 @@ extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const fl
   const unsigned in_place[] = {0, 0, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 2))) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
-  if ((rc = weight_16(W, wscale, workspace, Cin, Cout, dtype == DISCO_F16, st))) return rc;
+  if ((rc = operand_16(W, wscale, workspace, Cin, Cout, dtype == DISCO_F16, st))) return rc;
   const long long ld = ((long long)Cin + 7) / 8 * 8;
   MmArgs a = {};
   a.out = dx;
@@ -215,7 +351,7 @@ extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const fl
     a.A = {dy, nullptr, Cout * P, 0, P, 0, 16, false, (long long)(T * Cout)};
     a.M = P, a.Z = B, a.transposed = true;
   }
-  return run(a, cut_dx(B, Cin, Cout, P), dtype, (char*)workspace + weight_bytes(Cin, Cout), tc_dx, st);
+  return run(a, cut_dx(B, Cin, Cout, P), dtype, (char*)workspace + operand_bytes(Cout, Cin), true, tc_dx, st);
 }
 
 extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const float* scale, void* dW, int32_t B, int32_t Cin,
@@ -245,5 +381,5 @@ extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const f
     a.B = {dy, nullptr, 0, Cout * P, P, 0, 16, true, (long long)(T * Cout)};
     a.K = P, a.R = B;
   }
-  return run(a, cut_dw(B, Cin, Cout, P), dtype, workspace, tc_dw, (cudaStream_t)stream);
+  return run(a, cut_dw(B, Cin, Cout, P), dtype, workspace, false, tc_dw, (cudaStream_t)stream);
 }

@@ -37,6 +37,7 @@ struct TcArgs {
   float* part;                 // fp32 sums of the parts, each laid out as out, or null
   int NB, nsplit, out_type, vec;        // vec: rows of what it writes start on 16 bytes
   bool ala, alb;                        // rows of A, of B start on 16 bytes
+  bool after;                           // the launch before it wrote an operand: begin while that one ends
   uint32_t mt, nt, tiles;               // of a z, of the call (with parts); below 2^31
   long long nkp, steps;                 // 64-k chunks of a slice r, of all
 };

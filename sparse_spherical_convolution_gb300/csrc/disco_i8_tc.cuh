@@ -91,27 +91,6 @@ __device__ __forceinline__ void cp16(void* d, const uint8_t* p, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(p), "r"(bytes) : "memory");
 }
 
-// The nb bytes from byte sh of two words on, zeros behind them.
-__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int sh, int nb) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (sh & 8)
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  if (sh & 4)
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (sh & 3));
-  if (nb < 16)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int left = nb - 4 * i;  // bytes of this word that belong to the line
-      if (left < 4) o[i] = left <= 0 ? 0 : o[i] & (0xffffffffu >> (32 - 8 * left));
-    }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // 4 integers to 4 fp16 values: 1024 + (q + 128) by the exponent's bits, less 1152; exact.
 __device__ __forceinline__ uint2 to_half4(uint32_t w) {
   w ^= 0x80808080u;
@@ -285,6 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  norm::wait_for_previous();  // the operand that was converted into the workspace
 
   // tile t: n fastest (CTAs side by side share A's tile in L2), then m, z and the part
   struct Tile {
@@ -571,13 +551,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // pairs of n of 32 m through shared memory, then 8 m of both n to a lane
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-              *reinterpret_cast<uint32_t*>(stg + (e / 2) * 128 + lane * 4) = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
+              *reinterpret_cast<uint32_t*>(stg + (e / 2) * 128 + (lane ^ (e / 2 & 1) << 2) * 4) = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
             __syncwarp();
             uint8_t* o = out + (long long)c0 * pitch;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int pair = (lane >> 2) + 8 * h, seg = lane & 3;
-              const uint4 x = *reinterpret_cast<const uint4*>(stg + pair * 128 + seg * 32), y = *reinterpret_cast<const uint4*>(stg + pair * 128 + seg * 32 + 16);
+              const uint8_t* row = stg + pair * 128;  // the 16-byte words of odd pairs are swapped: no bank conflicts
+              const uint4 x = *reinterpret_cast<const uint4*>(row + ((2 * seg ^ (pair & 1)) << 4)), y = *reinterpret_cast<const uint4*>(row + (((2 * seg + 1) ^ (pair & 1)) << 4));
               if (seg * 8 < rows) {
                 uint8_t* d = o + 2 * pair * pitch + seg * 16;
                 if (2 * pair < left)
@@ -681,10 +662,7 @@ int tc_launch(const TcArgs& a, cudaStream_t st) {
   if (ALB && (rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
   constexpr size_t kSmem = Plan<FA, ALA, ALB>::kSmem;
   auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
-    return check_launch("i8_tc_kernel attribute");
-  kern<<<min(a.tiles, (uint32_t)kSMs), kTcThreads, kSmem, st>>>(amap, bmap, a);
-  return check_launch("i8_tc_kernel");
+  return norm::launch(kern, (int)min(a.tiles, (uint32_t)kSMs), kTcThreads, 1, a.after, kSmem, kSmem, st, "i8_tc_kernel", amap, bmap, a);
 }
 
 // This unit's status word (ORed into *v, and optionally cleared).

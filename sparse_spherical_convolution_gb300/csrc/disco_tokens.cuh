@@ -585,10 +585,12 @@ int tokens_ring(const TokenArgs& a, cudaStream_t st) {
   for (const auto& s : shapes) {
     g.LX = s[0], g.depth = s[1];
     while (g.LX > 2 && (long long)g.LX / 2 * V >= a.P) g.LX /= 2;
-    // few channels: more pixels to a tile.  A thread has about 8 words of each half: what it does once a tile is divided by them
+    // few channels: more pixels to a tile, over which what a thread does once a tile is spread
     while (g.LX < 32 && a.C * g.LX < 1024 && g.LX * V < a.P) g.LX *= 2;
-    g.NT = 128;
-    while (g.NT < kRingMax && a.C * g.LX > 8 * g.NT) g.NT *= 2;
+    // about 512 threads to an SM, whose shared memory holds so many rings
+    const int rings = (int)max(1LL, (long long)(norm::kMaxSmem / ((size_t)g.depth * G * a.C * g.LX * 16 + 4096)));
+    g.NT = kRingMax;
+    while (g.NT > 128 && (g.NT * rings > 640 || a.C * g.LX < g.NT)) g.NT /= 2;
     g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
     smem = (size_t)g.depth * G * g.nj * g.NT * 16 + (size_t)(g.NT / 32) * g.LX * V * (4 * kOwn + 2 * kSum);
     if ((fits = smem <= norm::kMaxSmem)) break;
@@ -600,7 +602,7 @@ int tokens_ring(const TokenArgs& a, cudaStream_t st) {
   // one limit for all calls: host threads share it
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)norm::kMaxSmem) != cudaSuccess)
     return check_launch("tokens_ring_kernel attribute");
-  const int ctas = (int)min((size_t)(1024 / g.NT), norm::kMaxSmem / (smem + 1024));
+  const int ctas = (int)min((size_t)(1024 / g.NT), (norm::kMaxSmem + 1024) / (smem + 1024));
   kern<<<(int)min(g.tiles, (long long)kSMs * max(1, ctas)), g.NT, smem, st>>>(a, g);
   return check_launch("tokens_ring_kernel");
 }

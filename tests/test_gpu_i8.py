@@ -88,7 +88,7 @@ def test_quant_of_special_tokens(lib, P, dtype):
 
 # products: one token, few, more than a tile, odd channel counts; grids whole, odd, with more than one sample
 SHAPES = [(1, 1, 1, 1), (1, 512, 2048, 1), (3, 17, 5, 1), (8, 256, 64, 1), (16, 1024, 33, 1), (33, 100, 77, 1), (130, 64, 257, 1), (200, 130, 48, 1),
-          (17, 2048, 96, 1), (129, 1030, 300, 1),
+          (17, 2048, 96, 1), (129, 1030, 300, 1), (2, 48, 5000, 1), (5, 33, 4900, 1), (16, 100, 4871, 1), (1, 4100, 4865, 1),
           (1, 3, 5, 2), (2, 5, 3, 7), (1, 16, 16, 64), (3, 64, 48, 128), (2, 80, 77, 181), (1, 64, 48, 33 * 65), (2, 130, 140, 1000), (4, 9, 300, 272),
           (1, 300, 9, 16), (1, 520, 136, 304)]
 
