@@ -81,17 +81,28 @@ __device__ __forceinline__ uint32_t quantize_near(float y, const Quantizer& z) {
 
 // act(g) and act'(g).  SiLU: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).
 // GELU: g Phi, Phi + g phi with the normal distribution Phi and its density phi.
-// T: the tensors' type; 16-bit ones take the approximate exponential and
-// division (2^-21 relative, below their rounding of 2^-9 or 2^-12).
+// T: the tensors' type.  16-bit ones take the approximate exponential and
+// reciprocal (2^-22 relative and 2^-23 |g| of the exponent, below their rounding of
+// 2^-9 or 2^-12) of t = e^-|g|, s = (1 or t) / (1 + t): gates below -87 give 0.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-g));
-  return __fdividef(1.0f, 1.0f + __expf(-g));
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-1.44269504f * fabsf(g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return (g < 0.0f ? t : 1.0f) * r;
 }
-template <typename T>
-__device__ __forceinline__ float act(float g, int kind) {
-  if (kind == DISCO_GELU) return g * (0.5f * erfcf(-0.70710678f * g));
-  return g * sigmoid<T>(g);
+template <typename T, int V>
+__device__ __forceinline__ norm::F<V> gated(const norm::F<V>& g, const norm::F<V>& v, int kind) {
+  norm::F<V> y;
+  if (kind == DISCO_GELU) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y.v[e] = g.v[e] * (0.5f * erfcf(-0.70710678f * g.v[e])) * v.v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y.v[e] = g.v[e] * sigmoid<T>(g.v[e]) * v.v[e];
+  }
+  return y;
 }
 template <typename T>
 __device__ __forceinline__ float act_grad(float g, int kind, float* value) {
@@ -103,6 +114,13 @@ __device__ __forceinline__ float act_grad(float g, int kind, float* value) {
   const float s = sigmoid<T>(g);
   *value = g * s;
   return s * fmaf(g, 1.0f - s, 1.0f);
+}
+
+// The larger of m and |v|, NaN where one is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
 }
 
 // The float that a byte of a word of 8-bit integers stands for (E = 0 .. 3), exactly.

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs
     const long long b = t / per_sample, p = (t - b * per_sample) * 32 * !ROW + lx;
     const bool live = p < a.P;
     const long long x0 = b * NC * a.P + p, y0 = b * a.C * a.P + p;
-    auto value = [&](int c) { return act<T>(to_f32(x[x0 + c * a.P]), a.act) * to_f32(x[x0 + (c + a.C) * a.P]); };
+    auto value = [&](int c) { return gated<T, 1>({{to_f32(x[x0 + c * a.P])}}, {{to_f32(x[x0 + (c + a.C) * a.P])}}, a.act).v[0]; };
     // the largest of all threads of a token, NaN above all
     auto join = [&](float m, float* buf) {
       buf[threadIdx.x] = m;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs
       if (GLU && (a.q || a.y))
         for (int c = j0; c < a.C; c += step) {
           const float v = value(c);
-          my = __uint_as_float(max32(__float_as_uint(my), __float_as_uint(v)));
+          my = max_abs(my, v);
           if (a.y) ((T*)a.y)[y0 + c * a.P] = from_f32<T>(v);
         }
     }
@@ -95,26 +95,28 @@ int held(const TokenArgs& a, bool glu, cudaStream_t st) {
 }
 
 template <typename T>
-int ring(const TokenArgs& a, bool glu, cudaStream_t st) {
-  if (!glu) return tokens_ring<T, false, true, false>(a, st);
-  if (a.xq && a.q) return tokens_ring<T, true, true, true>(a, st);
-  if (a.xq) return tokens_ring<T, true, true, false>(a, st);
-  if (a.q) return tokens_ring<T, true, false, true>(a, st);
-  return tokens_ring<T, true, false, false>(a, st);
+int grid(const TokenArgs& a, bool glu, cudaStream_t st) {
+  if (!glu) return tokens_tiles<T, false, true, false>(a, st);
+  if (a.xq && a.q) return tokens_tiles<T, true, true, true>(a, st);
+  if (a.xq) return tokens_tiles<T, true, true, false>(a, st);
+  if (a.q) return tokens_tiles<T, true, false, true>(a, st);
+  return tokens_tiles<T, true, false, false>(a, st);
 }
 
 template <typename T, bool GLU>
 int tokens(const TokenArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  int rc = DISCO_ERR_UNSUPPORTED;
-  if (a.P > 1 && a.P % V == 0) rc = ring<T>(a, GLU, st);
-  if (rc != DISCO_ERR_UNSUPPORTED) return rc;
-  rc = (a.P == 1 ? a.C : a.P) % V == 0 ? held<T, V>(a, GLU, st) : held<T, 1>(a, GLU, st);
+  const bool whole = (a.P == 1 ? a.C : a.P) % V == 0;
+  if (!whole && a.P > 1 && !GLU) {
+    const int rc = tokens_skewed<T>(a, st);
+    if (rc != DISCO_ERR_UNSUPPORTED) return rc;
+  }
+  const int rc = !whole ? held<T, 1>(a, GLU, st) : a.P == 1 ? held<T, V>(a, GLU, st) : grid<T>(a, GLU, st);
   if (rc != DISCO_ERR_UNSUPPORTED) return rc;
   const long long tiles = a.P == 1 ? a.B : a.B * ((a.P + 31) / 32);
-  const int grid = (int)min(tiles, (long long)kSMs * 8);
-  if (a.P == 1) tokens_any_kernel<T, true, GLU><<<grid, kAnyThreads, 0, st>>>(a, tiles);
-  else tokens_any_kernel<T, false, GLU><<<grid, kAnyThreads, 0, st>>>(a, tiles);
+  const int ctas = (int)min(tiles, (long long)kSMs * 8);
+  if (a.P == 1) tokens_any_kernel<T, true, GLU><<<ctas, kAnyThreads, 0, st>>>(a, tiles);
+  else tokens_any_kernel<T, false, GLU><<<ctas, kAnyThreads, 0, st>>>(a, tiles);
   return check_launch("tokens_any_kernel");
 }
 

@@ -2,13 +2,18 @@
 // in registers between the join of the largest magnitude and the rounding
 // (disco_quant_i8, disco_glu).  Not part of the ABI.
 //
-// A token's C values are dealt over the threads of one CTA.  On grids a thread
-// takes V neighbouring pixels (one 16-byte word, or one pixel where V does not
-// divide P) of J channels, NL channels apart; LX threads lie side by side along
-// the pixels.  In rows (P = 1) V neighbouring channels, J words.  All loads of a thread
-// are in flight at once, many CTAs share an SM, and the largest magnitude crosses the
-// CTA by one row of shared memory for each warp: one barrier a tile.
+// A token's C values are dealt over the threads of one CTA.
+//   tokens_tile_kernel   grids, V pixels (16 bytes) to a word, V divides P: words in shared memory
+//   tokens_rows_kernel   rows (P = 1), J words of neighbouring channels to a thread, in registers
+//   tokens_skew_kernel   the same where V does not divide P (quantisation): aligned words,
+//                        which are not pixels
+//   tokens_pixel_kernel  what these do not take: one pixel of J channels to a thread
+// Bound by HBM where a thread has 16 to 32 words and three CTAs or more share an SM: one
+// loads while another rounds.  Measured (GB300, bf16): quantisation of [1,512,360x720]
+// 76 us, 5.2 TB/s; the same tile three deep in one CTA of 512 threads 117.
 #pragma once
+
+#include <type_traits>
 
 #include "disco_i8.cuh"
 
@@ -36,8 +41,8 @@ struct TokenArgs {
 };
 
 struct TokenCut {
-  int LX, NL, TP;       // threads along pixels, along channels; pixels of a tile
-  long long per_sample; // tiles of a sample (grids)
+  int LX, NL;           // threads along pixels, along channels
+  long long per_sample; // tiles of a sample
 };
 
 constexpr int kTokenThreads = 512;
@@ -111,151 +116,75 @@ __device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&r)[V]) {
 
 // GLU: x holds gates and values, 2 C channels; y = act(gate) value.  XQ: the 8-bit
 // form of x; YQ: that of y.
-template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
-__global__ void __launch_bounds__(kTokenThreads) tokens_tile_kernel(const TokenArgs a, const TokenCut g) {
-  constexpr int G = GLU ? 2 : 1;
-  using R = Raw<T, V>;
-  using MX = Mag<T, V>;
-  using MY = Mag<float, V>;
-  constexpr int NM = (XQ ? MX::N : 0) + (YQ ? MY::N : 0);
-  extern __shared__ uint32_t sums[];  // [warps][NM][LX], or the 32 lanes' where a row of lanes is wider
+template <typename T, int J, bool GLU, bool XQ, bool YQ>
+__global__ void __launch_bounds__(kTokenThreads) tokens_pixel_kernel(const TokenArgs a, const TokenCut g) {
+  constexpr int G = GLU ? 2 : 1, NM = (XQ ? 1 : 0) + (YQ ? 1 : 0);
+  extern __shared__ uint32_t part[];  // [warps][NM][LX]
   const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX;
-  const long long t = blockIdx.x, b = t / g.per_sample, p = (t - b * g.per_sample) * g.TP + lx * V;
-  const bool live = p < a.P;
-  const T* x = (const T*)a.x + b * G * a.C * a.P + p;
-  const long long half = a.C * a.P, y0 = b * a.C * a.P + p;
-  R w[G][J];
-  float y[YQ ? J : 1][V];
+  const long long t = blockIdx.x, b = t / g.per_sample, p = (t - b * g.per_sample) * g.LX + lx;
+  const bool live = p < a.P && DISCO_IN_BOUNDS(b < a.B);
+  const long long half = a.C * a.P, y0 = b * half + p, x0 = b * G * half + p;
+  float w[G][J], y[YQ ? J : 1];
 #pragma unroll
   for (int i = 0; i < J; ++i) {
     const int c = j0 + i * g.NL;
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      memset(&w[h][i], 0, sizeof(R));
-      if (live && c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) w[h][i] = load_stream<R>(x + h * half + c * a.P);
-    }
+    for (int h = 0; h < G; ++h) w[h][i] = live && c < a.C ? to_f32(((const T*)a.x)[x0 + h * half + c * a.P]) : 0.0f;
   }
-  MX mx;
-  MY my;
-  mx.clear(), my.clear();
+  uint32_t m[2] = {0, 0};  // magnitudes of x, of y
 #pragma unroll
   for (int i = 0; i < J; ++i) {
     const int c = j0 + i * g.NL;
     if constexpr (XQ)
 #pragma unroll
-      for (int h = 0; h < G; ++h) mx.add(w[h][i]);
+      for (int h = 0; h < G; ++h) m[0] = max32(m[0], __float_as_uint(w[h][i]));
     if constexpr (GLU) {
-      if (!XQ && !YQ && !(live && c < a.C)) continue;
-      const F<V> gate = unpack<T, V>(w[0][i]), val = unpack<T, V>(w[1][i]);
-      F<V> v;
-#pragma unroll
-      for (int e = 0; e < V; ++e) v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
-      if constexpr (YQ)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          y[i][e] = v.v[e];
-          my.m[e] = max32(my.m[e], __float_as_uint(v.v[e]));
-        }
-      if (a.y && live && c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_stream((T*)a.y + y0 + c * a.P, packed<T, V>(v));
+      const float v = gated<T, 1>({{w[0][i]}}, {{w[1][i]}}, a.act).v[0];
+      if constexpr (YQ) {
+        y[i] = v;
+        m[1] = __float_as_uint(max_abs(__uint_as_float(m[1]), v));
+      }
+      if (a.y && live && c < a.C) ((T*)a.y)[y0 + c * a.P] = from_f32<T>(v);
     }
   }
   if constexpr (NM > 0) {
-    // the largest over all threads of the same pixels: by shuffles inside the warp, then over the warps
-    for (int o = g.LX; o < 32; o *= 2) {
-      if constexpr (XQ)
+    // the largest over all threads of the same pixel: by shuffles inside the warp, then over the warps
+    for (int o = g.LX; o < 32; o *= 2)
 #pragma unroll
-        for (int k = 0; k < MX::N; ++k) mx.join(__shfl_xor_sync(0xffffffffu, mx.m[k], o), k);
-      if constexpr (YQ)
-#pragma unroll
-        for (int k = 0; k < MY::N; ++k) my.join(__shfl_xor_sync(0xffffffffu, my.m[k], o), k);
-    }
-    const int warps = blockDim.x / 32, warp = tid / 32, row = NM * g.LX;
+      for (int k = 0; k < 2; ++k)
+        if (k ? YQ : XQ) m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+    const int warps = blockDim.x / 32;
     if (warps > 1) {
-      if ((tid & 31) < g.LX) {
-        uint32_t* d = sums + warp * row + lx;
-        if constexpr (XQ)
+      if ((tid & 31) < g.LX)
 #pragma unroll
-          for (int k = 0; k < MX::N; ++k) d[k * g.LX] = mx.m[k];
-        if constexpr (YQ)
-#pragma unroll
-          for (int k = 0; k < MY::N; ++k) d[(NM - MY::N + k) * g.LX] = my.m[k];
-      }
+        for (int k = 0; k < 2; ++k)
+          if (k ? YQ : XQ) part[(tid / 32 * NM + (k && XQ)) * g.LX + lx] = m[k];
       __syncthreads();
-      for (int o = 0; o < warps; ++o) {
-        const uint32_t* d = sums + o * row + lx;
-        if constexpr (XQ)
+      for (int o = 0; o < warps; ++o)
 #pragma unroll
-          for (int k = 0; k < MX::N; ++k) mx.join(d[k * g.LX], k);
-        if constexpr (YQ)
-#pragma unroll
-          for (int k = 0; k < MY::N; ++k) my.join(d[(NM - MY::N + k) * g.LX], k);
-      }
+        for (int k = 0; k < 2; ++k)
+          if (k ? YQ : XQ) m[k] = max(m[k], part[(o * NM + (k && XQ)) * g.LX + lx]);
     }
   }
   if (!live) return;
   if constexpr (XQ) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const Quantizer z(mx.value(e));
-      if (j0 == 0) a.xscale[b * a.P + p + e] = z.scale;
-#pragma unroll
-      for (int i = 0; i < J; ++i)
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          // the value's place takes its integer
-          T v[V];
-          memcpy(v, &w[h][i], sizeof(R));
-          const uint32_t n = quantize<T>(to_f32(v[e]), z);
-          if constexpr (sizeof(T) == 4) {
-            uint32_t u[V];
-            memcpy(u, &w[h][i], sizeof(R));
-            u[e] = n;
-            memcpy(&w[h][i], u, sizeof(R));
-          } else {
-            uint16_t u[V];
-            memcpy(u, &w[h][i], sizeof(R));
-            u[e] = (uint16_t)n;
-            memcpy(&w[h][i], u, sizeof(R));
-          }
-        }
-    }
+    const Quantizer z(__uint_as_float(m[0]));
+    if (j0 == 0) a.xscale[b * a.P + p] = z.scale;
 #pragma unroll
     for (int i = 0; i < J; ++i) {
       const int c = j0 + i * g.NL;
-      if (c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P))
+      if (c < a.C)
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          int8_t* d = a.xq + G * y0 - (G - 1) * p + h * half + c * a.P;
-          uint32_t r[V];
-          if constexpr (sizeof(T) == 4) {
-            memcpy(r, &w[h][i], sizeof(R));
-          } else {
-            uint16_t u[V];
-            memcpy(u, &w[h][i], sizeof(R));
-#pragma unroll
-            for (int e = 0; e < V; ++e) r[e] = u[e];
-          }
-          store_bytes<V>(d, r);
-        }
+        for (int h = 0; h < G; ++h) a.xq[x0 + h * half + c * a.P] = (int8_t)quantize<T>(w[h][i], z);
     }
   }
   if constexpr (YQ) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const Quantizer z(my.value(e));
-      if (j0 == 0) a.scale[b * a.P + p + e] = z.scale;
-#pragma unroll
-      for (int i = 0; i < J; ++i) y[i][e] = __uint_as_float(quantize_near(y[i][e], z));
-    }
+    const Quantizer z(__uint_as_float(m[1]));
+    if (j0 == 0) a.scale[b * a.P + p] = z.scale;
 #pragma unroll
     for (int i = 0; i < J; ++i) {
       const int c = j0 + i * g.NL;
-      if (c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) {
-        uint32_t r[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) r[e] = __float_as_uint(y[i][e]);
-        store_bytes<V>(a.q + y0 + c * a.P, r);
-      }
+      if (c < a.C) a.q[y0 + c * a.P] = (int8_t)quantize_near(y[i], z);
     }
   }
 }
@@ -293,15 +222,13 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_rows_kernel(const TokenA
       for (int h = 0; h < G; ++h) mx.add(w[h][i]);
     if constexpr (GLU) {
       const F<V> gate = unpack<T, V>(w[0][i]), val = unpack<T, V>(w[1][i]);
-      F<V> v;
+      const F<V> v = gated<T, V>(gate, val, a.act);
+      if constexpr (YQ)
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
-        if constexpr (YQ) {
+        for (int e = 0; e < V; ++e) {
           y[i][e] = v.v[e];
-          my = __uint_as_float(max32(__float_as_uint(my), __float_as_uint(v.v[e])));
+          my = max_abs(my, v.v[e]);
         }
-      }
       if (a.y && live && c < a.C && DISCO_IN_BOUNDS(c + V <= a.C)) store_stream((T*)a.y + y0 + c, packed<T, V>(v));
     }
   }
@@ -354,17 +281,16 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_rows_kernel(const TokenA
   }
 }
 
-// ---- grids: tiles of pixels in a ring of shared memory ----------------------
+// ---- grids: tiles of pixels in shared memory --------------------------------
 
 // Persistent CTAs of NT threads take tiles of LX words of pixels by all channels.  A
-// thread copies its own words of the tiles ahead with cp.async, so the loads of `depth`
-// tiles are in flight while one is worked on, and no barrier orders the copies; it reads its
-// words twice (magnitudes, rounding).  y waits between the two in the words of its gate and value.
-struct RingCut {
-  int NT, LX, nj, depth;        // nj: words of a thread in a tile, of each half
+// thread copies its own words of a tile with cp.async and reads them twice (magnitudes,
+// rounding).  y waits between the two in the words of its gate and value.
+struct TileCut {
+  int NT, LX, nj;  // nj: words of a thread in a tile, of each half
   long long per_sample, tiles;
 };
-constexpr int kRingMax = 512;
+constexpr int kTileThreads = 512;
 
 // Reciprocal and magnitude of V tokens, as the words of a row of shared memory.
 // Tokens of ordinary magnitudes need no power of two (Quantizer's f is 1); of zeros
@@ -372,9 +298,9 @@ constexpr int kRingMax = 512;
 __device__ __forceinline__ bool ordinary(float amax) { return amax == 0.0f || (amax >= 1e-20f && amax <= 1e30f); }
 
 // q of a word of V inputs of V tokens: quantize<T>, two values to an instruction
-template <typename T, int V>
-__device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, const F<V>& inv, const F<V>& minus_a, bool plain) {
-  if (plain && sizeof(T) == 2) {
+template <typename T, int V, bool PLAIN>
+__device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, const F<V>& inv, const F<V>& minus_a) {
+  if constexpr (PLAIN && sizeof(T) == 2) {
     const F<V> kx = norm::mul(norm::fill<V>(kQMax), x);
     F<V> t = norm::mul(kx, inv);
     t = norm::fma(norm::fma(t, minus_a, kx), inv, t);
@@ -385,7 +311,7 @@ __device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, c
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       Quantizer z(1.0f);
-      if (plain) z.k = kQMax, z.b = -minus_a.v[e], z.inv = inv.v[e];
+      if (PLAIN) z.k = kQMax, z.b = -minus_a.v[e], z.inv = inv.v[e];
       else z = Quantizer(-minus_a.v[e]);
       r[e] = quantize<T>(x.v[e], z);
     }
@@ -393,84 +319,67 @@ __device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, c
 }
 
 template <typename T, bool GLU, bool XQ, bool YQ>
-__global__ void __launch_bounds__(kRingMax) tokens_ring_kernel(const TokenArgs a, const RingCut g) {
-  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0);
+__global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenArgs a, const TileCut g) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1;
   using R = Raw<T, V>;
   extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX, NL = g.NT / g.LX;
-  const int warps = g.NT / 32, warp = tid / 32;
-  const int slot_words = G * g.nj * g.NT;
-  uint4* ring = reinterpret_cast<uint4*>(smem) + tid;
-  float* scratch = reinterpret_cast<float*>(smem + (size_t)g.depth * slot_words * 16);  // of each warp: 1/a, -a of x, 127/a of y
-  uint8_t* sums = reinterpret_cast<uint8_t*>(scratch + warps * ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * g.LX * V);  // [2]: [warps][pixels] of x, of y
-  const long long half = a.C * a.P;
-  auto place = [&](long long t, long long* b, long long* p) {
-    *b = g.tiles <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)g.per_sample) : t / g.per_sample;
-    *p = (t - *b * g.per_sample) * (g.LX * V) + lx * V;
-  };
-  auto fetch = [&](long long t, int slot) {
-    if (t < g.tiles) {
-      long long b, p;
-      place(t, &b, &p);
-      if (p < a.P) {
-        const T* x = (const T*)a.x + b * G * half + p;
-        uint4* d = ring + slot * slot_words;
-        for (int i = 0; i < g.nj; ++i) {
-          const int c = j0 + i * NL;
-          if (c < a.C && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) {
-#pragma unroll
-            for (int h = 0; h < G; ++h) norm::copy_async(d + (i * G + h) * g.NT, x + h * half + c * a.P);
-          }
-        }
+  const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX, NL = g.NT / g.LX, NT = g.NT, TP = g.LX * V;
+  const int warps = NT / 32, warp = tid / 32;
+  uint4* w = reinterpret_cast<uint4*>(smem) + tid;
+  float* own = reinterpret_cast<float*>(smem + (size_t)G * g.nj * NT * 16);  // of each pixel: 1/a, -a of x, 127/a of y
+  uint8_t* sums = reinterpret_cast<uint8_t*>(own + ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * TP);  // [warps][pixels] of x, of y
+  const int nj = j0 < a.C ? (a.C - j0 + NL - 1) / NL : 0;       // channels of this thread
+  const long long P = a.P, half = a.C * P, step = NL * P, row0 = j0 * P;  // from one of its channels to the next; its first
+  for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x) {
+    const long long b = g.tiles <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)g.per_sample) : t / g.per_sample;
+    const long long p = (t - b * g.per_sample) * TP + lx * V, y0 = b * half + p;
+    const int n = p < P && DISCO_IN_BOUNDS(b < a.B && p + V <= P) ? nj : 0;
+    {
+      const T* x = (const T*)a.x + b * G * half + p + row0;
+      uint4* d = w;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i, x += step, d += G * NT) {
+        norm::copy_async(d, x);
+        if constexpr (GLU) norm::copy_async(d + NT, x + half);
       }
+      norm::copy_commit();
+      norm::copy_wait<0>();
     }
-    norm::copy_commit();
-  };
-  for (int d = 0; d < g.depth - 1; ++d) fetch(blockIdx.x + (long long)d * gridDim.x, d);
-  int n = 0;
-  for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x, ++n) {
-    fetch(t + (long long)(g.depth - 1) * gridDim.x, (n + g.depth - 1) % g.depth);
-    if (g.depth == 3) norm::copy_wait<2>();
-    else norm::copy_wait<1>();
-    long long b, p;
-    place(t, &b, &p);
-    const bool live = p < a.P;
-    const long long y0 = b * half + p;
-    uint4* w = ring + (n % g.depth) * slot_words;
     Mag<T, V> mx;
     uint32_t my[V];
     mx.clear();
 #pragma unroll
     for (int e = 0; e < V; ++e) my[e] = 0;
-    const int nj = live ? (a.C - j0 + NL - 1) / NL : 0;
-#pragma unroll 2
-    for (int i = 0; i < nj; ++i) {
-      uint4* s = w + i * G * g.NT;
-      const uint4 w0 = s[0];
-      if constexpr (XQ) mx.add(w0);
-      if constexpr (GLU) {
-        const uint4 w1 = s[g.NT];
-        if constexpr (XQ) mx.add(w1);
-        R r0, r1;
-        memcpy(&r0, &w0, 16);
-        memcpy(&r1, &w1, 16);
-        const F<V> gate = unpack<T, V>(r0), val = unpack<T, V>(r1);
-        F<V> v;
+    {
+      uint4* s = w;
+      T* yo = (T*)a.y + y0 + row0;
+      auto first = [&](auto kind) {  // the activation's kind is known in the loop
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, s += G * NT) {
+          const uint4 w0 = s[0];
+          if constexpr (XQ) mx.add(w0);
+          if constexpr (GLU) {
+            const uint4 w1 = s[NT];
+            if constexpr (XQ) mx.add(w1);
+            R r0, r1;
+            memcpy(&r0, &w0, 16);
+            memcpy(&r1, &w1, 16);
+            const F<V> v = gated<T, V>(unpack<T, V>(r0), unpack<T, V>(r1), decltype(kind)::value);
+            if constexpr (YQ) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
-        if constexpr (YQ) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) my[e] = max32(my[e], __float_as_uint(v.v[e]));
-          if constexpr (!XQ) {  // y over its gate and value
-            s[0] = *reinterpret_cast<const uint4*>(v.v);
-            if constexpr (V == 8) s[g.NT] = *reinterpret_cast<const uint4*>(v.v + 4);
+              for (int e = 0; e < V; ++e) my[e] = __float_as_uint(max_abs(__uint_as_float(my[e]), v.v[e]));
+              if constexpr (!XQ) {  // y over its gate and value
+                s[0] = *reinterpret_cast<const uint4*>(v.v);
+                if constexpr (V == 8) s[NT] = *reinterpret_cast<const uint4*>(v.v + 4);
+              }
+            }
+            if (a.y) store_stream(yo, packed<T, V>(v)), yo += step;
           }
         }
-        if (a.y && DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_stream((T*)a.y + y0 + (j0 + i * NL) * a.P, packed<T, V>(v));
-      }
+      };
+      if (GLU && a.act == DISCO_GELU) first(std::integral_constant<int, DISCO_GELU>());
+      else first(std::integral_constant<int, DISCO_SILU>());
     }
-    const int TP = g.LX * V;
-    float* own = scratch + warp * ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * TP;
     bool plain = true;
     if constexpr (XQ || YQ) {
       for (int o = g.LX; o < 32; o *= 2) {
@@ -481,137 +390,235 @@ __global__ void __launch_bounds__(kRingMax) tokens_ring_kernel(const TokenArgs a
 #pragma unroll
           for (int k = 0; k < V; ++k) my[k] = max(my[k], __shfl_xor_sync(0xffffffffu, my[k], o));
       }
-      // rows of the tile's pixels, one for each warp; two sets of them: one barrier a tile
-      uint8_t* part = sums + (n & 1) * warps * TP * kSum;
+      // rows of the tile's pixels, one for each warp
+      uint8_t* ysums = sums + (XQ ? warps * TP * ES : 0);
       if ((tid & 31) < g.LX) {
-        if constexpr (XQ) memcpy(part + (warp * TP + lx * V) * ES, mx.m, V * ES);
-        if constexpr (YQ) memcpy(part + warps * TP * (XQ ? ES : 0) + (warp * TP + lx * V) * 4, my, V * 4);
+        if constexpr (XQ) memcpy(sums + (warp * TP + lx * V) * ES, mx.m, V * ES);
+        if constexpr (YQ) memcpy(ysums + (warp * TP + lx * V) * 4, my, V * 4);
       }
       __syncthreads();
-      // each warp joins them for itself, a pixel to a lane
-      for (int e = tid & 31; e < TP; e += 32) {
+      // S neighbouring threads to a pixel join them
+      const int S = g.NT > TP ? g.NT / TP : 1, sub = tid & (S - 1);
+      for (int e = tid / S; e < TP; e += g.NT / S) {
         const long long at = b * a.P + p - lx * V + e;
-        const bool in = p - lx * V + e < a.P;
+        const bool first = sub == 0, in = first && p - lx * V + e < a.P;
         if constexpr (XQ) {
-          float amax;
+          uint32_t m = 0;
+          for (int o = sub; o < warps; o += S)
+            m = max(m, ES == 2 ? (uint32_t)reinterpret_cast<const uint16_t*>(sums)[o * TP + e] : reinterpret_cast<const uint32_t*>(sums)[o * TP + e]);
+          for (int o = 1; o < S; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float amax = __uint_as_float(m);
           if constexpr (ES == 2) {
-            uint32_t m = 0;
-            for (int o = 0; o < warps; ++o) m = max(m, (uint32_t)reinterpret_cast<const uint16_t*>(part)[o * TP + e]);
             const uint16_t h = (uint16_t)m;
             T v;
             memcpy(&v, &h, 2);
             amax = to_f32(v);
-          } else {
-            uint32_t m = 0;
-            for (int o = 0; o < warps; ++o) m = max(m, reinterpret_cast<const uint32_t*>(part)[o * TP + e]);
-            amax = __uint_as_float(m);
           }
           plain = plain && ordinary(amax);
-          if (warp == 0 && in) a.xscale[at] = Quantizer(amax).scale;
-          own[e] = __frcp_rn(amax == 0.0f ? 1.0f : amax);
-          own[TP + e] = amax == 0.0f ? -1.0f : -amax;
+          if (in) a.xscale[at] = Quantizer(amax).scale;
+          if (first) {
+            own[e] = __frcp_rn(amax == 0.0f ? 1.0f : amax);
+            own[TP + e] = amax == 0.0f ? -1.0f : -amax;
+          }
         }
         if constexpr (YQ) {
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(part + warps * TP * (XQ ? ES : 0));
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(ysums);
           uint32_t m = 0;
-          for (int o = 0; o < warps; ++o) m = max(m, q[o * TP + e]);
+          for (int o = sub; o < warps; o += S) m = max(m, q[o * TP + e]);
+          for (int o = 1; o < S; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
           const Quantizer z(__uint_as_float(m));
-          if (warp == 0 && in) a.scale[at] = z.scale;
+          const bool finite = z.scale < __int_as_float(0x7f800000);
+          if (in) a.scale[at] = z.scale;
           // a token with an infinity or a NaN: 0, and values that are NaN times it are cleared below
-          own[(XQ ? 2 * TP : 0) + e] = z.scale < __int_as_float(0x7f800000) ? z.k * z.inv : 0.0f;
-          plain = plain && z.scale < __int_as_float(0x7f800000);
+          if (first) own[(XQ ? 2 * TP : 0) + e] = finite ? z.k * z.inv : 0.0f;
+          plain = plain && finite;
         }
       }
-      plain = __all_sync(0xffffffffu, plain);
-      __syncwarp();
+      plain = __syncthreads_and(plain);
     }
-    if (live) {
-      if constexpr (XQ) {
-        const F<V> inv = norm::load_row<V>(own + lx * V), minus_a = norm::load_row<V>(own + TP + lx * V);
-        int8_t* d = a.xq + G * b * half + p + j0 * a.P;
-#pragma unroll 2
-        for (int i = 0; i < nj; ++i, d += NL * a.P)
+    if constexpr (XQ) {
+      const F<V> inv = norm::load_row<V>(own + lx * V), minus_a = norm::load_row<V>(own + TP + lx * V);
+      auto second = [&](auto is_plain) {
+        const uint4* s = w;
+        int8_t* d = a.xq + G * b * half + p + row0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, s += G * NT, d += step)
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             R r0;
-            memcpy(&r0, &w[(i * G + h) * g.NT], 16);
+            const uint4 w0 = s[h * NT];
+            memcpy(&r0, &w0, 16);
             uint32_t r[V];
-            quantize_word<T, V>(r, unpack<T, V>(r0), inv, minus_a, plain);
-            if (DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_bytes<V>(d + h * half, r);
+            quantize_word<T, V, decltype(is_plain)::value>(r, unpack<T, V>(r0), inv, minus_a);
+            store_bytes<V>(d + h * half, r);
           }
-      }
-      if constexpr (YQ) {
-        const F<V> f = norm::load_row<V>(own + (XQ ? 2 * TP : 0) + lx * V);
-        int8_t* d = a.q + y0 + j0 * a.P;
-#pragma unroll 2
-        for (int i = 0; i < nj; ++i, d += NL * a.P) {
-          uint4* s = w + i * G * g.NT;
+      };
+      if (plain) second(std::true_type());
+      else second(std::false_type());
+    }
+    if constexpr (YQ) {
+      const F<V> f = norm::load_row<V>(own + (XQ ? 2 * TP : 0) + lx * V);
+      auto third = [&](auto is_plain, auto kind) {
+        const uint4* s = w;
+        int8_t* d = a.q + y0 + row0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, s += G * NT, d += step) {
           F<V> v;
           if constexpr (!XQ) {
             *reinterpret_cast<uint4*>(v.v) = s[0];
-            if constexpr (V == 8) *reinterpret_cast<uint4*>(v.v + 4) = s[g.NT];
+            if constexpr (V == 8) *reinterpret_cast<uint4*>(v.v + 4) = s[NT];
           } else {
             R r0, r1;
             memcpy(&r0, &s[0], 16);
-            memcpy(&r1, &s[g.NT], 16);
-            const F<V> gate = unpack<T, V>(r0), val = unpack<T, V>(r1);
-#pragma unroll
-            for (int e = 0; e < V; ++e) v.v[e] = act<T>(gate.v[e], a.act) * val.v[e];
+            memcpy(&r1, &s[NT], 16);
+            v = gated<T, V>(unpack<T, V>(r0), unpack<T, V>(r1), decltype(kind)::value);
           }
           v = norm::mul(v, f);
-          if (!plain)
+          if constexpr (!decltype(is_plain)::value)
 #pragma unroll
             for (int e = 0; e < V; ++e) v.v[e] = fabsf(v.v[e]) < 128.0f ? v.v[e] : 0.0f;
           v = norm::add(v, norm::fill<V>(kRound));
           uint32_t r[V];
 #pragma unroll
           for (int e = 0; e < V; ++e) r[e] = __float_as_uint(v.v[e]);
-          if (DISCO_IN_BOUNDS(b < a.B && p + V <= a.P)) store_bytes<V>(d, r);
+          store_bytes<V>(d, r);
         }
-      }
+      };
+      using Silu = std::integral_constant<int, DISCO_SILU>;
+      using Gelu = std::integral_constant<int, DISCO_GELU>;
+      if (XQ && a.act == DISCO_GELU) third(std::false_type(), Gelu());
+      else if (plain) third(std::true_type(), Silu());
+      else third(std::false_type(), Silu());
     }
-    __syncwarp();  // `own` is read
   }
 }
 
 template <typename T, bool GLU, bool XQ, bool YQ>
-int tokens_ring(const TokenArgs& a, cudaStream_t st) {
+int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
   constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0), kOwn = (XQ ? 2 : 0) + (YQ ? 1 : 0);
-  RingCut g;
-  size_t smem = 0;
-  // 128 bytes of a row to a tile, three tiles deep, while they fit
-  static const int shapes[][2] = {{8, 3}, {8, 2}, {4, 2}, {2, 2}};
-  bool fits = false;
-  for (const auto& s : shapes) {
-    g.LX = s[0], g.depth = s[1];
-    while (g.LX > 2 && (long long)g.LX / 2 * V >= a.P) g.LX /= 2;
-    // few channels: more pixels to a tile, over which what a thread does once a tile is spread
-    while (g.LX < 32 && a.C * g.LX < 1024 && g.LX * V < a.P) g.LX *= 2;
-    // about 512 threads to an SM, whose shared memory holds so many rings
-    const int rings = (int)max(1LL, (long long)(norm::kMaxSmem / ((size_t)g.depth * G * a.C * g.LX * 16 + 4096)));
-    g.NT = kRingMax;
-    while (g.NT > 128 && (g.NT * rings > 640 || a.C * g.LX < g.NT)) g.NT /= 2;
-    g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
-    smem = (size_t)g.depth * G * g.nj * g.NT * 16 + (size_t)(g.NT / 32) * g.LX * V * (4 * kOwn + 2 * kSum);
-    if ((fits = smem <= norm::kMaxSmem)) break;
-  }
-  if (!fits) return DISCO_ERR_UNSUPPORTED;
+  TileCut g;
+  // 128 bytes of a row to a tile, more for few channels, less for many, so that three tiles share an SM
+  g.LX = 8;
+  while (g.LX < 32 && G * a.C * g.LX < 1024 && g.LX * V < a.P) g.LX *= 2;
+  while (g.LX > 2 && ((size_t)G * a.C * g.LX * 16 * 3 > norm::kMaxSmem - 12 * 1024 || (long long)g.LX / 2 * V >= a.P)) g.LX /= 2;
+  const int share = (int)(norm::kMaxSmem / ((size_t)G * a.C * g.LX * 16 + 4096));
+  g.NT = share >= 3 ? (G * a.C * g.LX <= 1024 ? 64 : 128) : share == 2 ? 256 : kTileThreads;
+  g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
+  const size_t smem = (size_t)G * g.nj * g.NT * 16 + (size_t)g.LX * V * (4 * kOwn + g.NT / 32 * kSum);
+  if (smem > norm::kMaxSmem) return DISCO_ERR_UNSUPPORTED;
   g.per_sample = (a.P + g.LX * V - 1) / (g.LX * V);
   g.tiles = g.per_sample * a.B;
-  auto kern = tokens_ring_kernel<T, GLU, XQ, YQ>;
+  auto kern = tokens_tile_kernel<T, GLU, XQ, YQ>;
   // one limit for all calls: host threads share it
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)norm::kMaxSmem) != cudaSuccess)
-    return check_launch("tokens_ring_kernel attribute");
+    return check_launch("tokens_tile_kernel attribute");
   const int ctas = (int)min((size_t)(1024 / g.NT), (norm::kMaxSmem + 1024) / (smem + 1024));
   kern<<<(int)min(g.tiles, (long long)kSMs * max(1, ctas)), g.NT, smem, st>>>(a, g);
-  return check_launch("tokens_ring_kernel");
+  return check_launch("tokens_tile_kernel");
+}
+
+// Quantisation of grids where V does not divide P: a row of pixels starts m = 0 .. V - 1
+// elements past a word.  Words stay aligned, LX of them cover TP = (LX - 1) V pixels and
+// parts of two neighbouring tiles'; a thread's channels are a multiple of V apart, so its rows
+// have one skew, and only its magnitudes and factors are realigned, once a tile.
+template <typename T>
+__global__ void __launch_bounds__(128) tokens_skew_kernel(const TokenArgs a, const TileCut g) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES;
+  using R = Raw<T, V>;
+  using M = typename Word<ES>::type;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX, NL = g.NT / g.LX, TP = (g.LX - 1) * V, row = TP + 2 * V;
+  uint4* w = reinterpret_cast<uint4*>(smem) + tid;
+  float* own = reinterpret_cast<float*>(smem + (size_t)g.nj * g.NT * 16);  // 1/a and -a of pixels -V .. TP + V
+  M* sums = reinterpret_cast<M*>(own + 2 * row);                           // [NL][pixels -V .. TP + V]
+  const int nj = j0 < a.C ? (a.C - j0 + NL - 1) / NL : 0;
+  const long long P = a.P, step = NL * P, total = (long long)a.B * a.C * P;
+  for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x) {
+    const long long b = g.tiles <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)g.per_sample) : t / g.per_sample;
+    const long long pos = (t - b * g.per_sample) * TP, e0 = (b * a.C + j0) * P + pos;
+    const int N = (int)min((long long)TP, P - pos), m = (int)e0 & (V - 1), px = lx * V - m;  // this thread's first pixel
+    const int n = px < N ? nj : 0;
+    const long long at = e0 + px;  // its first element
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const long long k = at + i * step;
+      const int left = DISCO_IN_BOUNDS(k >= 0 && k < total) ? (int)min((long long)V, total - k) : 0;
+      norm::copy_async(w + i * g.NT, (const T*)a.x + (left ? k : 0), left * ES);
+    }
+    norm::copy_commit();
+    norm::copy_wait<0>();
+    Mag<T, V> mx;
+    mx.clear();
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) mx.add(w[i * g.NT]);
+    M part[V];
+    memcpy(part, mx.m, sizeof(part));
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[j0 * row + V + px + e] = part[e];
+    __syncthreads();
+    bool plain = true;
+    for (int e = tid; e < N; e += g.NT) {
+      uint32_t u = 0;
+      for (int o = 0; o < NL; ++o) u = max(u, (uint32_t)sums[o * row + V + e]);
+      const M h = (M)u;
+      T v;
+      memcpy(&v, &h, ES);
+      const float amax = to_f32(v);
+      plain = plain && ordinary(amax);
+      a.xscale[b * P + pos + e] = Quantizer(amax).scale;
+      own[V + e] = __frcp_rn(amax == 0.0f ? 1.0f : amax);
+      own[row + V + e] = amax == 0.0f ? -1.0f : -amax;
+    }
+    plain = __syncthreads_and(plain);
+    F<V> inv, minus_a;
+#pragma unroll
+    for (int e = 0; e < V; ++e) inv.v[e] = own[V + px + e], minus_a.v[e] = own[row + V + px + e];
+    const bool full = px >= 0 && px + V <= N;
+    auto second = [&](auto is_plain) {
+      int8_t* d = a.xq + at;
+#pragma unroll 2
+      for (int i = 0; i < n; ++i, d += step) {
+        R r0;
+        const uint4 w0 = w[i * g.NT];
+        memcpy(&r0, &w0, 16);
+        uint32_t r[V];
+        quantize_word<T, V, decltype(is_plain)::value>(r, unpack<T, V>(r0), inv, minus_a);
+        if (full) {
+          store_bytes<V>(d, r);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (px + e >= 0 && px + e < N) d[e] = (int8_t)r[e];
+        }
+      }
+    };
+    if (plain) second(std::true_type());
+    else second(std::false_type());
+  }
+}
+
+template <typename T>
+int tokens_skewed(const TokenArgs& a, cudaStream_t st) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES;
+  TileCut g;
+  g.NT = 128, g.LX = 16;  // a multiple of 8 channels side by side
+  while (g.LX > 4 && ((size_t)a.C * g.LX * 16 * 3 > norm::kMaxSmem - 12 * 1024 || (g.LX / 2 - 1) * V >= a.P)) g.LX /= 2;
+  const int TP = (g.LX - 1) * V, NL = g.NT / g.LX;
+  g.nj = (a.C + NL - 1) / NL;
+  const size_t smem = (size_t)g.nj * g.NT * 16 + (size_t)(TP + 2 * V) * (8 + NL * ES);
+  if (smem > norm::kMaxSmem / 2) return DISCO_ERR_UNSUPPORTED;
+  g.per_sample = (a.P + TP - 1) / TP;
+  g.tiles = g.per_sample * a.B;
+  const int ctas = (int)min((size_t)(1024 / g.NT), (norm::kMaxSmem + 1024) / (smem + 1024));
+  return norm::launch(tokens_skew_kernel<T>, (int)min(g.tiles, (long long)kSMs * ctas), g.NT, 1, false, smem, norm::kMaxSmem / 2, st,
+                      "tokens_skew_kernel", a, g);
 }
 
 // Launches the kernels above; DISCO_ERR_UNSUPPORTED, without launching, for tokens
 // that no CTA holds.
 template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
 int tokens_held(const TokenArgs& a, cudaStream_t st) {
-  constexpr int NM = (XQ ? Mag<T, V>::N : 0) + (YQ ? Mag<float, V>::N : 0);
+  [[maybe_unused]] constexpr int NM = (XQ ? 1 : 0) + (YQ ? 1 : 0);
   if (a.P == 1) {
     const int words = (a.C + V - 1) / V;
     int TR = 32;
@@ -621,20 +628,22 @@ int tokens_held(const TokenArgs& a, cudaStream_t st) {
     tokens_rows_kernel<T, V, J, GLU, XQ, YQ><<<(a.B + rows - 1) / rows, TR * rows, 0, st>>>(a, TR);
     return check_launch("tokens_rows_kernel");
   }
-  TokenCut g;
-  // 128 bytes of a row to a tile, less where the channels need the threads or there are few pixels
-  g.LX = V > 1 ? 8 : 32;
-  g.NL = (a.C + J - 1) / J;
-  while (g.LX > 1 && (long long)g.LX * g.NL > kTokenThreads) g.LX /= 2;
-  while (g.LX > 1 && (long long)g.LX / 2 * V >= a.P) g.LX /= 2;
-  if ((long long)g.LX * g.NL > kTokenThreads) return DISCO_ERR_UNSUPPORTED;
-  const int threads = (g.LX * g.NL + 31) / 32 * 32;
-  g.TP = g.LX * V;
-  g.per_sample = (a.P + g.TP - 1) / g.TP;
-  const long long tiles = g.per_sample * a.B;
-  if (tiles > 0x7fffffffLL) return DISCO_ERR_UNSUPPORTED;
-  tokens_tile_kernel<T, V, J, GLU, XQ, YQ><<<(unsigned)tiles, threads, (size_t)threads / 32 * NM * g.LX * 4, st>>>(a, g);
-  return check_launch("tokens_tile_kernel");
+  if constexpr (V > 1) {
+    return DISCO_ERR_UNSUPPORTED;
+  } else {
+    TokenCut g;
+    // 32 pixels of a row to a tile, fewer where the channels need the threads or there are few pixels
+    g.LX = 32;
+    g.NL = (a.C + J - 1) / J;
+    while (g.LX > 1 && (long long)g.LX * g.NL > kTokenThreads) g.LX /= 2;
+    while (g.LX > 1 && g.LX / 2 >= a.P) g.LX /= 2;
+    const int threads = (g.LX * g.NL + 31) / 32 * 32;
+    g.per_sample = (a.P + g.LX - 1) / g.LX;
+    const long long tiles = g.per_sample * a.B;
+    if ((long long)g.LX * g.NL > kTokenThreads || tiles > 0x7fffffffLL) return DISCO_ERR_UNSUPPORTED;
+    tokens_pixel_kernel<T, J, GLU, XQ, YQ><<<(unsigned)tiles, threads, (size_t)threads / 32 * NM * g.LX * 4, st>>>(a, g);
+    return check_launch("tokens_pixel_kernel");
+  }
 }
 
 }  // namespace i8
