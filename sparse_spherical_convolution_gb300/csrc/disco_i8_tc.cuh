@@ -13,14 +13,14 @@
 // Persistent kernel:
 //   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few, and where rows are
 //                off alignment): tcgen05.ld, scales, rounding, stores along the output's rows
-//   converters   (the rest up to warp 11): integers from the raw ring, to 16 bits, into the
+//   converters   (8 warps, idle where both operands are 16-bit): integers from the raw ring, to 16 bits, into the
 //                stage.  Two groups take alternate steps, so that one's loads, conversion and
 //                fence overlap the other's.  The raw ring has an even number of slots, each always
 //                the same group's, and stages are released in order: no waiter is ever two
 //                phases ahead of a barrier, where a wait by parity would pass at once
-//   warp 12      MMA issuer (one thread); two accumulators of 256 TMEM columns, so
+//   one warp     MMA issuer (one thread); two accumulators of 256 TMEM columns, so
 //                the epilogue of a tile overlaps the main loop of the next
-//   warp 13      TMA of B, and warp 14 of A: into the stage (16-bit) or the raw ring (integers)
+//   two warps    TMA of B and of A: into the stage (16-bit) or the raw ring (integers)
 // Both operands lie in the stage as lines of 64 elements (128 bytes, 128-byte
 // swizzle): element k .. k + 63 of one m or n where k is the contiguous direction
 // in memory, else (MN-major) 64 neighbouring m or n of one k.  So no operand is ever transposed.
@@ -38,10 +38,8 @@
 namespace disco {
 namespace i8 {
 
-constexpr int kMmaWarp = 12, kTmaBWarp = 13, kTmaAWarp = 14, kTcThreads = 32 * 15;
 constexpr int kBM = 128, kBK = 64, kNBMax = 256;
 constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2;
-constexpr uint32_t kEpiBytes = 32 * 64;  // staging of an epilogue warp: 64 bytes of 32 rows
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr int kStatusI8Timeout = 1 << 6;
 
@@ -60,17 +58,20 @@ struct Form {
 
 // What the kernel's parameters make of warps and shared memory (227 KB).
 //   raw ring, aligned: integers as they are; off alignment: words of each line and one more
-template <class FA, bool ALA, bool ALB>
+template <class FA, bool ALA, bool ALB, bool TR>
 struct Plan {
   static constexpr bool kAligned = ALA && ALB;
-  static constexpr int kEpi = kAligned && !FA::SC ? 8 : 4, kConv = kMmaWarp - kEpi;
   static constexpr bool kRaw = ALA && FA::ES == 1;  // A by TMA into the raw ring
+  static constexpr int kEpi = kAligned && !FA::SC ? 8 : 4, kConv = kAligned && !kRaw ? 4 : 8;
+  static constexpr int kMmaWarp = kEpi + kConv, kThreads = 32 * (kMmaWarp + 3);
   static constexpr int kGroups = kRaw ? 2 : 1, kGroupWarps = kConv / kGroups;
   static constexpr uint32_t kSlotA = kRaw ? kBM * kBK : ALA ? 0 : kBM * (64 * FA::ES + 16);
   static constexpr uint32_t kSlot = kSlotA + (ALB ? 0 : kNBMax * (128 + 16));
   static constexpr int kStages = kAligned ? (kRaw ? 3 : 4) : ALB ? 3 : 2;
   static constexpr int kRaws = kAligned ? (kRaw ? 6 : 0) : ALB ? 4 : 2;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kEpiBytes + 128) + 256;
+  // of an epilogue warp: 64 bytes of 32 rows on their way out, the scales of a tile's columns
+  static constexpr uint32_t kStaging = 32 * 64, kCols = FA::ES == 1 && !FA::SC ? kNBMax * 4 : 0;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kRaws % kGroups == 0, "a slot is always the same group's");
   static_assert(!kRaw || ALB, "the raw ring is filled by TMA or by the converters");
@@ -219,13 +220,17 @@ __device__ __forceinline__ void tc_tma_3d(void* dst, const CUtensorMap* map, int
       : "memory");
 }
 
+// One row on; opaque to the compiler, which would keep 32 rows' addresses in registers.
+__device__ __forceinline__ void next_row(uint8_t*& o, long long pitch) { asm volatile("add.s64 %0, %0, %1;" : "+l"(o) : "l"(pitch)); }
+
 // FA: A's form; BKM: B is K-major; HALF: 16-bit operands are fp16; ALA, ALB: the
 // rows of A, of B start on 16 bytes (by TMA); TR: out[z][n][m] instead of [m][n].
 template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
   using FB = Form<2, BKM, 0>;
-  using C = Plan<FA, ALA, ALB>;
+  using C = Plan<FA, ALA, ALB, TR>;
+  constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2;
   constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps, kStages = C::kStages, kRaws = C::kRaws;
   constexpr bool kRaw = C::kRaw, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
   constexpr bool kConv = !kTmaA || !ALB;                      // the converters have work
@@ -233,8 +238,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* raws = smem + kStages * kStageBytes;
   uint8_t* staging = raws + kRaws * C::kSlot;
-  float* colscale = reinterpret_cast<float*>(staging + kEpiWarps * kEpiBytes);  // [kEpiWarps][32]
-  uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * 32);
+  uint8_t* colscale = staging + kEpiWarps * C::kStaging;
+  uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * C::kCols);
   uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2, *rawf = acce + 2, *rawe = rawf + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -484,23 +489,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp < kEpiWarps) {
     // ----------------------------------------------------------- epilogue --
     const int q4 = warp & 3;                    // TMEM lanes 32 q4 ..: m of this warp
-    uint8_t* stg = staging + warp * kEpiBytes;  // 16-byte piece s of row r at piece s ^ (r / 2 % 4): no bank conflicts
-    float* cs = colscale + warp * 32;
-    const bool split = a.part != nullptr;
+    uint8_t* stg = staging + warp * C::kStaging;  // 16-byte piece s of row r at piece s ^ (r / 2 % 4): no bank conflicts
+    float* cs = reinterpret_cast<float*>(colscale + warp * C::kCols);
+    const bool split = a.part != nullptr, scaled = C::kCols && !split;
     const int type = split ? DISCO_F32 : a.out_type, eb = type == DISCO_F32 ? 4 : 2;
-    const bool scaled = !split && a.m.cs, h16 = type == DISCO_F16;
+    const bool h16 = type == DISCO_F16;
     int tl = 0;
     for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
       const Tile c = tile_of(t);
       const int ab = tl & 1;
-      // chunks of 32 columns, every second one where two warps share the lanes; the scale of a
-      // chunk's column `lane` is fetched a chunk ahead
-      constexpr int kStep = 8 * kEpiWarps;
-      const int c00 = (warp >> 2) * 32;
-      auto column = [&](int col) { return scaled && c.n0 + col < a.m.N ? __ldg(a.m.cs + c.n0 + col) : 0.0f; };
-      float next = column(c00 + lane);
       const long long row0 = c.m0 + q4 * 32;
-      const float rs = scaled && row0 + lane < a.m.M ? __ldg(a.m.rs + c.z * a.m.rs_z + row0 + lane) : 1.0f;
+      // chunks of 32 columns, every second one where two warps share the lanes
+      constexpr int kStep = 8 * kEpiWarps;
+      float rs = 1.0f;
+      if (scaled) {
+        for (int n = lane; n < a.NB; n += 32) cs[n] = c.n0 + n < a.m.N ? __ldg(a.m.cs + c.n0 + n) : 0.0f;
+        if (row0 + lane < a.m.M) rs = __ldg(a.m.rs + c.z * a.m.rs_z + row0 + lane);
+        __syncwarp();
+      }
       bool fin = mbar_wait(&accf[ab], (tl >> 1) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
       if (!fin) {
@@ -515,45 +521,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // first of this warp's outputs; rows of the output are n (TR) or m
       uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) + (slice + (TR ? c.n0 * a.m.M + row0 : row0 * a.m.N + c.n0)) * eb;
       const long long pitch = (TR ? a.m.M : a.m.N) * eb;
-      for (int c0 = c00; c0 < cols && rows > 0; c0 += kStep) {
+      for (int c0 = (warp >> 2) * 32; c0 < cols && rows > 0; c0 += kStep) {
         uint32_t v[32];
         tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(q4 * 32) << 16) + c0, v);
         if (scaled) {
-          cs[lane] = next;
-          __syncwarp();
-          next = column(c0 + kStep + lane);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(cs + e);
-            v[e] = __float_as_uint(__uint_as_float(v[e]) * f.x * rs);
-            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * f.y * rs);
-            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f.z * rs);
-            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f.w * rs);
+            const float4 f = *reinterpret_cast<const float4*>(cs + c0 + e);
+            const norm::F<4> x = norm::mul(norm::mul(norm::F<4>{{f.x, f.y, f.z, f.w}}, norm::fill<4>(rs)),
+                                           norm::F<4>{{__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])}});
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[e + k] = __float_as_uint(x.v[k]);
           }
-          __syncwarp();
         }
         const int left = min(32, cols - c0);
         if constexpr (TR) {
-          // the warp's lanes are neighbours in memory
-          if (type == DISCO_F32) {
-            uint8_t* o = out + (long long)c0 * pitch + lane * 4;
-            if (lane < rows)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e < left) *reinterpret_cast<uint32_t*>(o + e * pitch) = v[e];
-          } else if (!a.vec) {
-            uint8_t* o = out + (long long)c0 * pitch + lane * 2;
-            if (lane < rows)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e < left) *reinterpret_cast<uint16_t*>(o + e * pitch) = round_16(__uint_as_float(v[e]), h16);
-          } else {
-            // pairs of n of 32 m through shared memory, then 8 m of both n to a lane
+          uint8_t* o = out + (long long)c0 * pitch;
+          // pixels of aligned rows make whole words of the output too
+          constexpr bool kWhole = ALA && !FA::KM && !FA::SC;
+          if (eb == 2 && (kWhole || a.vec)) {
+            // pairs of n of 32 m through shared memory, then 8 m of both n to a lane (2-byte
+            // stores straight from the registers took 141 us instead of 71 for dx of 2 x 256 -> 128 channels)
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
               *reinterpret_cast<uint32_t*>(stg + (e / 2) * 128 + (lane ^ (e / 2 & 1) << 2) * 4) = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
             __syncwarp();
-            uint8_t* o = out + (long long)c0 * pitch;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int pair = (lane >> 2) + 8 * h, seg = lane & 3;
@@ -570,6 +562,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
             __syncwarp();
+          } else if (lane < rows) {  // the warp's lanes are neighbours in memory
+            o += lane * eb;
+            if (type == DISCO_F32) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (e < left) *reinterpret_cast<uint32_t*>(o) = v[e];
+                next_row(o, pitch);
+              }
+            } else if (!kWhole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint32_t two = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
+                if (e < left) *reinterpret_cast<uint16_t*>(o) = (uint16_t)two;
+                next_row(o, pitch);
+                if (e + 1 < left) *reinterpret_cast<uint16_t*>(o) = (uint16_t)(two >> 16);
+                next_row(o, pitch);
+              }
+            }
           }
         } else {
           // 64 bytes of each of the warp's 32 rows at a time through shared memory
@@ -660,9 +670,9 @@ int tc_launch(const TcArgs& a, cudaStream_t st) {
   int rc;
   if (ALA && (rc = tc_encode(&amap, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF))) return rc;
   if (ALB && (rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
-  constexpr size_t kSmem = Plan<FA, ALA, ALB>::kSmem;
+  constexpr size_t kSmem = Plan<FA, ALA, ALB, TR>::kSmem;
   auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
-  return norm::launch(kern, (int)min(a.tiles, (uint32_t)kSMs), kTcThreads, 1, a.after, kSmem, kSmem, st, "i8_tc_kernel", amap, bmap, a);
+  return norm::launch(kern, (int)min(a.tiles, (uint32_t)kSMs), Plan<FA, ALA, ALB, TR>::kThreads, 1, a.after, kSmem, kSmem, st, "i8_tc_kernel", amap, bmap, a);
 }
 
 // This unit's status word (ORed into *v, and optionally cleared).
