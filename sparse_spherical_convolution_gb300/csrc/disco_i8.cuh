@@ -71,10 +71,13 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// The same for a value that is no 16-bit input (the gated activation, in fp32):
-// within a few units of 2^-24 of the quotient, so next to a border either may come out.
-__device__ __forceinline__ uint32_t quantize_near(float y, const Quantizer& z) {
-  float t = (z.k * y) * z.inv;
+// The same for the gated activation y, in fp32.  For tensors of 16 bits within a few units
+// of 2^-24 of the quotient; of 32 bits by the formula's own steps, each rounded correctly.
+// Next to the middle of two integers either may come out.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize_y(float y, const Quantizer& z) {
+  const float ky = __fmul_rn(z.k, y);
+  float t = sizeof(T) == 4 ? __fdiv_rn(ky, z.b) : ky * z.inv;
   if (!(fabsf(t) < 128.0f)) t = 0.0f;
   return __float_as_uint(t + kRound);
 }
@@ -86,7 +89,7 @@ __device__ __forceinline__ uint32_t quantize_near(float y, const Quantizer& z) {
 // 2^-9 or 2^-12) of t = e^-|g|, s = (1 or t) / (1 + t): gates below -87 give 0.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-g));
+  if constexpr (sizeof(T) == 4) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-g)));
   float t, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-1.44269504f * fabsf(g)));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
@@ -97,10 +100,10 @@ __device__ __forceinline__ norm::F<V> gated(const norm::F<V>& g, const norm::F<V
   norm::F<V> y;
   if (kind == DISCO_GELU) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) y.v[e] = g.v[e] * (0.5f * erfcf(-0.70710678f * g.v[e])) * v.v[e];
+    for (int e = 0; e < V; ++e) y.v[e] = __fmul_rn(__fmul_rn(g.v[e], __fmul_rn(0.5f, erfcf(-0.70710678f * g.v[e]))), v.v[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) y.v[e] = g.v[e] * sigmoid<T>(g.v[e]) * v.v[e];
+    for (int e = 0; e < V; ++e) y.v[e] = __fmul_rn(__fmul_rn(g.v[e], sigmoid<T>(g.v[e])), v.v[e]);
   }
   return y;
 }

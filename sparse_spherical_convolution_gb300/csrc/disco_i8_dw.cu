@@ -10,16 +10,11 @@ DISCO_I8_STATUS_READER(i8_dw_status)
 
 namespace i8 {
 
-template <bool HALF, bool KM>
-int dw(const TcArgs& a, cudaStream_t st) {
-  using F = Form<1, KM, 1>;
-  if (a.ala && a.alb) return tc_launch<F, KM, HALF, true, true, true>(a, st);
-  return a.alb ? tc_launch<F, KM, HALF, false, true, true>(a, st) : tc_launch<F, KM, HALF, false, false, true>(a, st);
-}
-
 int tc_dw(const TcArgs& a, cudaStream_t st) {
-  if (a.m.f16) return a.m.A.k_major ? dw<true, true>(a, st) : dw<true, false>(a, st);
-  return a.m.A.k_major ? dw<false, true>(a, st) : dw<false, false>(a, st);
+  using Grid = Form<1, true, 1>;
+  using Rows = Form<1, false, 1>;
+  if (a.m.A.k_major) return a.m.f16 ? tc_launch<Grid, true, true, true>(a, st) : tc_launch<Grid, true, false, true>(a, st);
+  return a.m.f16 ? tc_launch<Rows, false, true, true>(a, st) : tc_launch<Rows, false, false, true>(a, st);
 }
 
 }  // namespace i8

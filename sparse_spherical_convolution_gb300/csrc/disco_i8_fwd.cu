@@ -10,12 +10,9 @@ DISCO_I8_STATUS_READER(i8_fwd_status)
 namespace i8 {
 
 int tc_fwd(const TcArgs& a, cudaStream_t st) {
-  using Rows = Form<1, true, 0>;
-  using Grid = Form<1, false, 0>;
-  if (a.m.A.k_major && a.m.transposed)  // rows, A the weight
-    return a.ala ? tc_launch<Rows, true, true, true, true, true>(a, st) : tc_launch<Rows, true, true, false, true, true>(a, st);
-  if (a.m.A.k_major) return a.ala ? tc_launch<Rows, true, true, true, true, false>(a, st) : tc_launch<Rows, true, true, false, true, false>(a, st);
-  return a.ala ? tc_launch<Grid, true, true, true, true, true>(a, st) : tc_launch<Grid, true, true, false, true, true>(a, st);
+  if (!a.m.A.k_major) return tc_launch<Form<1, false, 0>, true, true, true>(a, st);  // grids
+  if (a.m.transposed) return tc_launch<Form<1, true, 0>, true, true, true>(a, st);   // rows, A the weight
+  return tc_launch<Form<1, true, 0>, true, true, false>(a, st);
 }
 
 }  // namespace i8

@@ -39,30 +39,61 @@ __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, co
   }
 }
 
-// Integers [rows][C] as the 16-bit operand: in fp16, or times their row's scale rounded
-// to the type; rows padded to `ld` elements with zeros.
-template <typename T>
-__global__ void __launch_bounds__(kAnyThreads) mm_operand_kernel(const int8_t* q, const float* scale, T* w16, int C, int ld, long long n) {
-  const long long i = ((long long)blockIdx.x * kAnyThreads + threadIdx.x) * 8;
+// ---- operands laid out once a call --------------------------------------------
+// Bound by HBM, or by a launch: a thread writes one 16-byte word of a row, from two aligned
+// words shifted together where the source's rows start anywhere.
+
+__device__ __forceinline__ uint4 load16(const uint8_t* p, const uint8_t* end) {
+  if (p + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (p + i < end) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// `rows` rows of `len` elements of es bytes, to rows of `words` words, zeros at their
+// end.  Kinds: 0 as they are; else integers to fp16 (1), or times their row's scale, rounded, to fp16 (2) or bf16 (3).
+struct Layout {
+  const uint8_t *src, *end;
+  uint4* dst;
+  const float* scale;
+  long long len, words, total;
+  int es, kind;
+  uint32_t block0;  // the first block that works on it
+};
+struct Layouts {
+  Layout t[3];
+  int n;
+};
+
+__global__ void __launch_bounds__(kAnyThreads) mm_layout_kernel(const Layouts a) {
   norm::let_next_begin();
-  if (i >= n) return;
-  const long long o = n <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)ld) : i / ld;
-  const int c = (int)(i - o * ld);
-  const float f = scale ? scale[o] : 1.0f;
-  uint32_t w[2];
-  if (C % 8 == 0) {
-    const uint2 u = *reinterpret_cast<const uint2*>(q + i);
-    w[0] = u.x, w[1] = u.y;
-  } else {
-    w[0] = w[1] = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < C) w[e / 4] |= (uint32_t)(uint8_t)q[o * C + c + e] << (8 * (e & 3));
+  int k = 0;
+  if (a.n > 1 && blockIdx.x >= a.t[1].block0) k = 1;
+  if (a.n > 2 && blockIdx.x >= a.t[2].block0) k = 2;
+  const Layout& t = a.t[k];
+  const long long i = (long long)(blockIdx.x - t.block0) * kAnyThreads + threadIdx.x;
+  if (i >= t.total) return;
+  const long long row = t.total <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)t.words) : i / t.words;
+  const int step = t.kind ? 8 : 16;  // source bytes of a word
+  const long long at = (i - row * t.words) * step;
+  const int nb = (int)max(0LL, min((long long)step, t.len * t.es - at));
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (nb > 0) {
+    const uint8_t* p = t.src + row * t.len * t.es + at;
+    const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    if (DISCO_IN_BOUNDS(p - sh >= t.src && p + nb <= t.end)) {
+      const uint4 lo = load16(p - sh, t.end);
+      v = shifted(lo, sh + nb > 16 ? load16(p - sh + 16, t.end) : v, sh, nb);
+    }
   }
-  T v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(from_byte(w[e / 4] ^ 0x80808080u, e & 3) * f);
-  *reinterpret_cast<uint4*>(w16 + i) = *reinterpret_cast<const uint4*>(v);
+  if (t.kind) {
+    const uint32_t w[2] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u};
+    const float f = t.kind > 1 ? t.scale[row] : 1.0f;
+    auto two = [&](int e) { return pack2_16(from_byte(w[e / 4], e & 3) * f, from_byte(w[e / 4], (e & 3) + 1) * f, t.kind < 3); };
+    v = make_uint4(two(0), two(2), two(4), two(6));
+  }
+  t.dst[i] = v;
 }
 
 // ---- a few rows ----------------------------------------------------------------
@@ -73,19 +104,11 @@ __global__ void __launch_bounds__(kAnyThreads) mm_operand_kernel(const int8_t* q
 constexpr int kFewThreads = 128, kFewRows = 16;
 constexpr size_t kFewSmem = 128 * 1024;
 
-__device__ __forceinline__ uint4 load16(const int8_t* p, const int8_t* end) {
-  if (p + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (p + i < end) w[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // Word i (16 bytes) of a row of C bytes anywhere in a tensor that ends at `end`.
 template <bool ALN>
-__device__ __forceinline__ uint4 row_word(const int8_t* row, int i, int C, const int8_t* end) {
+__device__ __forceinline__ uint4 row_word(const uint8_t* row, int i, int C, const uint8_t* end) {
   if (ALN) return __ldg(reinterpret_cast<const uint4*>(row) + i);
-  const int8_t* p = row + 16 * i;
+  const uint8_t* p = row + 16 * i;
   const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15), nb = min(16, C - 16 * i);
   if (nb <= 0) return make_uint4(0, 0, 0, 0);
   const uint4 lo = load16(p - sh, end);
@@ -93,7 +116,7 @@ __device__ __forceinline__ uint4 row_word(const int8_t* row, int i, int C, const
 }
 
 struct FewArgs {
-  const int8_t *q, *W;
+  const uint8_t *q, *W;
   const float *scale, *wscale;
   void* y;
   int B, Cin, Cout, type;
@@ -104,7 +127,7 @@ __global__ void __launch_bounds__(kFewThreads) mm_few_kernel(const FewArgs a) {
   extern __shared__ __align__(16) uint4 rows[];  // [NB][words]
   const int lane = threadIdx.x & 31, words = (a.Cin + 15) / 16;
   const int o0 = (blockIdx.x * (kFewThreads / 32) + threadIdx.x / 32) * O;
-  const int8_t *qend = a.q + (long long)a.B * a.Cin, *wend = a.W + (long long)a.Cout * a.Cin;
+  const uint8_t *qend = a.q + (long long)a.B * a.Cin, *wend = a.W + (long long)a.Cout * a.Cin;
   uint4 w[O];
   auto fetch = [&](int i) {
 #pragma unroll
@@ -170,8 +193,8 @@ bool takes_few(int32_t B, int32_t Cin, int64_t P) {
 }
 
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).
-// Tiles of 256 n; where they do not fill the SMs, the reduction is split into
-// parts of 8 steps at least, and where that leaves half of the SMs idle, tiles get narrower.
+// Tiles of 256 n; where they do not fill the SMs, the reduction is split into parts of 8 steps
+// at least (2 where the sums are few), and where that leaves half of the SMs idle, tiles get narrower.
 struct Cut {
   int NB, nsplit;
   long long mt, nt, nkp, steps;
@@ -183,62 +206,133 @@ struct Cut {
     for (;;) {
       nt = (N + NB - 1) / NB;
       const long long tiles = mt * nt * Z;
-      nsplit = (int)max(1LL, min(steps / 8, kSMs / tiles));
+      nsplit = (int)max(1LL, min(steps / (M * N * Z <= 1 << 16 ? 2 : 8), kSMs / tiles));
       if (tiles * nsplit >= kSMs / 2 || NB <= 64) break;
       NB = NB > 128 ? 128 : 64;
     }
   }
-  size_t part_bytes(long long M, long long N, int Z) const { return nsplit > 1 ? (size_t)nsplit * Z * M * N * 4 : 0; }
 };
 
-// What a call needs of the workspace: the 16-bit operand, then the parts' sums.
-size_t operand_bytes(long long rows, int32_t C) { return ((size_t)rows * (((size_t)C + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
-// Of the product of rows, the smaller operand is converted once a call, the other one in the main loop.
-bool rows_are_b(int32_t B, int32_t Cout, int64_t P) { return P == 1 && B < Cout; }
+// A product ready to launch: its arguments, the operands that are laid out first, and the bytes of
+// the workspace it takes.  Made from the sizes alone where `ws` is null.
+struct Product {
+  MmArgs m = {};
+  Cut cut;
+  Layouts lay = {};
+  char* ws;
+  size_t bytes = 0;
+  uint32_t blocks = 0;
 
-Cut cut_fwd(int32_t B, int32_t Cin, int32_t Cout, int64_t P) {
-  return rows_are_b(B, Cout, P) ? Cut(Cout, B, Cin, 1, 1) : P == 1 ? Cut(B, Cout, Cin, 1, 1) : Cut(P, Cout, Cin, B, 1);
-}
-Cut cut_dx(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(B, Cin, Cout, 1, 1) : Cut(P, Cin, Cout, B, 1); }
-Cut cut_dw(int32_t B, int32_t Cin, int32_t Cout, int64_t P) { return P == 1 ? Cut(Cin, Cout, B, 1, 1) : Cut(Cin, Cout, P, 1, B); }
+  Product(void* workspace, long long M, long long N, long long K, int Z, int R, bool transposed) : cut(M, N, K, Z, R), ws((char*)workspace) {
+    m.M = M, m.N = N, m.K = K, m.Z = Z, m.R = R, m.transposed = transposed;
+  }
+  void* take(size_t n) {
+    void* p = ws ? ws + bytes : nullptr;
+    bytes += (n + 255) / 256 * 256;
+    return p;
+  }
+  void* add(const void* src, const float* scale, long long rows, long long len, long long words, int es, int kind) {
+    Layout& t = lay.t[lay.n++];
+    t.src = (const uint8_t*)src, t.end = t.src + rows * len * es;
+    t.scale = scale, t.len = len, t.words = words, t.total = rows * words, t.es = es, t.kind = kind;
+    t.block0 = blocks;
+    blocks += (uint32_t)((t.total + kAnyThreads - 1) / kAnyThreads);
+    t.dst = (uint4*)take((size_t)t.total * 16);
+    return t.dst;
+  }
+  // [rows][ld] as it is where rows start on 16 bytes, else a copy that does
+  Operand rows(Operand o, long long rows) {
+    const int es = o.bits / 8;
+    if (o.ld * es % 16 == 0) return o;
+    const long long words = (o.ld * es + 15) / 16, pitch = words * 16 / es;
+    o.p = add(o.p, nullptr, rows, o.ld, words, es, 0);
+    o.z = o.z / o.ld * pitch, o.r = o.r / o.ld * pitch, o.ld = pitch;
+    return o;
+  }
+  // integers [rows][C] in 16 bits; scaled: times their row's scale
+  Operand halves(const void* q, bool scaled, const float* scale, long long rows, long long C, bool f16, bool k_major) {
+    const long long words = (C + 7) / 8;
+    return {add(q, scale, rows, C, words, 1, !scaled ? 1 : f16 ? 2 : 3), nullptr, 0, 0, words * 8, 0, 16, k_major};
+  }
+  float* parts() { return cut.nsplit > 1 ? (float*)take((size_t)cut.nsplit * m.Z * m.M * m.N * 4) : nullptr; }
 
-bool rows_aligned(const Operand& o) {
-  const int es = o.bits / 8;
-  return o.ld * es % 16 == 0 && o.z * es % 16 == 0 && o.r * es % 16 == 0;
-}
-
-// after: an operand was converted just before
-int run(const MmArgs& m, const Cut& c, disco_dtype dtype, void* part, bool after, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) {
-  if (c.mt * c.nt * m.Z * c.nsplit >= 1LL << 31) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 by %d", c.NB);
-  TcArgs a = {};
-  a.m = m;
-  a.enda = (const uint8_t*)m.A.p + m.A.n * (m.A.bits / 8);
-  a.endb = (const uint8_t*)m.B.p + m.B.n * (m.B.bits / 8);
-  a.NB = c.NB, a.nsplit = c.nsplit, a.mt = (uint32_t)c.mt, a.nt = (uint32_t)c.nt, a.nkp = c.nkp, a.steps = c.steps;
-  a.part = c.nsplit > 1 ? (float*)part : nullptr;
-  a.out_type = dtype;
-  a.after = after;
-  a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
-  a.tiles = (uint32_t)(c.mt * c.nt * m.Z * c.nsplit);
-  // the copy engine's coordinates are 32-bit, its strides below 2^40 bytes
-  const bool small = max(max(m.M, m.N), m.K) < 1LL << 31 && max(m.A.n, m.B.n) < 1LL << 38;
-  a.ala = small && rows_aligned(m.A), a.alb = small && rows_aligned(m.B);
-  int rc = tc(a, st);
-  if (rc || !a.part) return rc;
-  const long long n = m.Z * m.M * m.N;
-  const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
-#define CALL(T) rc = norm::launch(mm_join_kernel<T>, grid, kAnyThreads, 1, true, 0, 0, st, "mm_join_kernel", m, (const float*)a.part, c.nsplit, n)
-  DISCO_BY_DTYPE(dtype, CALL)
+  int run(float* part, disco_dtype dtype, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) const {
+    if (cut.mt * cut.nt * m.Z * cut.nsplit >= 1LL << 31) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 by %d", cut.NB);
+    if (lay.n) {
+      mm_layout_kernel<<<blocks, kAnyThreads, 0, st>>>(lay);
+      if (int rc = check_launch("mm_layout_kernel")) return rc;
+    }
+    TcArgs a = {};
+    a.m = m;
+    a.NB = cut.NB, a.nsplit = cut.nsplit, a.mt = (uint32_t)cut.mt, a.nt = (uint32_t)cut.nt, a.nkp = cut.nkp, a.steps = cut.steps;
+    a.part = cut.nsplit > 1 ? part : nullptr;
+    a.out_type = dtype;
+    a.after = lay.n > 0;
+    a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
+    a.tiles = (uint32_t)(cut.mt * cut.nt * m.Z * cut.nsplit);
+    int rc = tc(a, st);
+    if (rc || !a.part) return rc;
+    const long long n = m.Z * m.M * m.N;
+    const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
+#define CALL(T) rc = norm::launch(mm_join_kernel<T>, grid, kAnyThreads, 1, true, 0, 0, st, "mm_join_kernel", m, (const float*)part, cut.nsplit, n)
+    DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
-  return rc;
-}
+    return rc;
+  }
+};
 
-int operand_16(const void* q, const float* scale, void* w16, int32_t C, int32_t rows, bool f16, cudaStream_t st) {
-  const int ld = (int)(((long long)C + 7) / 8 * 8);
-  const long long n = (long long)rows * ld, grid = (n / 8 + kAnyThreads - 1) / kAnyThreads;
-  if (f16) mm_operand_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)q, scale, (__half*)w16, C, ld, n);
-  else mm_operand_kernel<<<(unsigned)grid, kAnyThreads, 0, st>>>((const int8_t*)q, scale, (__nv_bfloat16*)w16, C, ld, n);
-  return check_launch("mm_operand_kernel");
+// Of the product of rows, the smaller operand is converted once a call, the other one in the main loop.
+Product product(const void* q, const float* scale, const void* W, const float* wscale, void* y, int32_t B, int32_t Cin, int32_t Cout,
+                int64_t P, void* ws, float** part) {
+  const bool swap = P == 1 && B < Cout;
+  Product p = swap ? Product(ws, Cout, B, Cin, 1, 1, true) : P == 1 ? Product(ws, B, Cout, Cin, 1, 1, false) : Product(ws, P, Cout, Cin, B, 1, true);
+  p.m.out = y;
+  p.m.rs = swap ? wscale : scale, p.m.cs = swap ? scale : wscale;
+  if (swap) {  // m = output channel, n = row
+    p.m.A = p.rows({W, nullptr, 0, 0, Cin, 0, 8, true}, Cout);
+    p.m.B = p.halves(q, false, nullptr, B, Cin, true, true);
+  } else {
+    p.m.B = p.halves(W, false, nullptr, Cout, Cin, true, true);
+    if (P == 1) {  // m = row
+      p.m.A = p.rows({q, nullptr, 0, 0, Cin, 0, 8, true}, B);
+    } else {  // m = pixel
+      p.m.A = p.rows({q, nullptr, Cin * P, 0, P, 0, 8, false}, (long long)B * Cin);
+      p.m.rs_z = P;
+    }
+  }
+  *part = p.parts();
+  return p;
+}
+Product product_dx(const void* dy, const void* W, const float* wscale, void* dx, int32_t B, int32_t Cin, int32_t Cout, int64_t P, bool f16,
+                   void* ws, float** part) {
+  Product p = P == 1 ? Product(ws, B, Cin, Cout, 1, 1, false) : Product(ws, P, Cin, Cout, B, 1, true);
+  p.m.out = dx;
+  p.m.f16 = f16;
+  p.m.B = p.halves(W, true, wscale, Cout, Cin, f16, false);
+  if (P == 1) p.m.A = p.rows({dy, nullptr, 0, 0, Cout, 0, 16, true}, B);  // m = row
+  else p.m.A = p.rows({dy, nullptr, Cout * P, 0, P, 0, 16, false}, (long long)B * Cout);  // m = pixel
+  *part = p.parts();
+  return p;
+}
+Product product_dw(const void* dy, const void* q, const float* scale, void* dW, int32_t B, int32_t Cin, int32_t Cout, int64_t P, bool f16,
+                   void* ws, float** part) {
+  Product p = P == 1 ? Product(ws, Cin, Cout, B, 1, 1, true) : Product(ws, Cin, Cout, P, 1, B, true);  // m = input channel
+  p.m.out = dW;
+  p.m.f16 = f16;
+  if (P == 1) {  // k = row
+    p.m.A = p.rows({q, scale, 0, 0, Cin, 0, 8, false}, B);
+    p.m.B = p.rows({dy, nullptr, 0, 0, Cout, 0, 16, false}, B);
+  } else {  // k = pixel, summed over the samples too
+    p.m.A = p.rows({q, scale, 0, Cin * P, P, P, 8, true}, (long long)B * Cin);
+    p.m.B = p.rows({dy, nullptr, 0, Cout * P, P, 0, 16, true}, (long long)B * Cout);
+    if (P % 16) {  // rows of scales that go on in zeros
+      const long long words = (P + 15) / 16 * 4;
+      p.m.A.ks = (const float*)p.add(scale, nullptr, B, P, words, 4, 0);
+      p.m.A.ks_r = words * 4;
+    }
+  }
+  *part = p.parts();
+  return p;
 }
 
 // Sizes of a product; 16-bit types only for the gradients.
@@ -247,6 +341,9 @@ int check_mm(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype,
   if ((rc = check_shape(B, Cin, P, dtype)) || (rc = check_shape(B, Cout, P, dtype))) return rc;
   if (grad && dtype == DISCO_F32) return fail(DISCO_ERR_UNSUPPORTED, "gradients take bf16 or fp16");
   if ((double)Cin * Cout > 1e12) return fail(DISCO_ERR_UNSUPPORTED, "more than 1e12 weights");
+  // the copy engine's coordinates are 32-bit, its strides below 2^40 bytes
+  if (P >= 1LL << 31 || (double)max(Cin, Cout) * (double)P * 2 >= 1099511627776.0)
+    return fail(DISCO_ERR_UNSUPPORTED, "2^31 pixels or more, or 2^40 bytes of a sample");
   return DISCO_OK;
 }
 
@@ -265,17 +362,20 @@ using namespace disco::i8;
 extern "C" size_t disco_matmul_i8_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, false)) return 0;
   if (takes_few(B, Cin, P)) return 16;
-  return operand_bytes(rows_are_b(B, Cout, P) ? B : Cout, Cin) + cut_fwd(B, Cin, Cout, P).part_bytes((long long)B * P, Cout, 1);
+  float* part;
+  return product(nullptr, nullptr, nullptr, nullptr, nullptr, B, Cin, Cout, P, nullptr, &part).bytes;
 }
 
 extern "C" size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return operand_bytes(Cout, Cin) + cut_dx(B, Cin, Cout, P).part_bytes((long long)B * P, Cin, 1);
+  float* part;
+  return product_dx(nullptr, nullptr, nullptr, nullptr, B, Cin, Cout, P, false, nullptr, &part).bytes;
 }
 
 extern "C" size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype) {
   if (check_mm(B, Cin, Cout, P, dtype, true)) return 0;
-  return max((size_t)16, cut_dw(B, Cin, Cout, P).part_bytes(Cin, Cout, 1));
+  float* part;
+  return max((size_t)16, product_dw(nullptr, nullptr, nullptr, nullptr, B, Cin, Cout, P, false, nullptr, &part).bytes);
 }
 
 extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W, const float* wscale, void* y, int32_t B,
@@ -294,32 +394,12 @@ extern "C" int disco_matmul_i8(const void* q, const float* scale, const void* W,
   if ((rc = check_buffers(in, in_place, 4, out, 2))) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
   if (takes_few(B, Cin, P)) {
-    const FewArgs a{(const int8_t*)q, (const int8_t*)W, scale, wscale, y, B, Cin, Cout, dtype};
+    const FewArgs a{(const uint8_t*)q, (const uint8_t*)W, scale, wscale, y, B, Cin, Cout, dtype};
     return B == 1 ? few<1>(a, st) : B <= 4 ? few<4>(a, st) : few<16>(a, st);
   }
-  const bool swap = rows_are_b(B, Cout, P);
-  const long long ld = ((long long)Cin + 7) / 8 * 8, rows16 = swap ? B : Cout;
-  if ((rc = operand_16(swap ? q : W, nullptr, workspace, Cin, (int32_t)rows16, true, st))) return rc;
-  MmArgs a = {};
-  a.out = y;
-  a.K = Cin, a.R = 1, a.Z = 1;
-  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, true, rows16 * ld};
-  if (swap) {  // m = output channel, n = row
-    a.A = {W, nullptr, 0, 0, Cin, 0, 8, true, (long long)w};
-    a.rs = wscale, a.cs = scale;
-    a.M = Cout, a.N = B, a.transposed = true;
-  } else {  // n = output channel
-    a.rs = scale, a.cs = wscale;
-    a.N = Cout;
-    if (P == 1) {  // m = row
-      a.A = {q, nullptr, 0, 0, Cin, 0, 8, true, (long long)(T * Cin)};
-      a.M = B;
-    } else {  // m = pixel
-      a.A = {q, nullptr, Cin * P, 0, P, 0, 8, false, (long long)(T * Cin)};
-      a.M = P, a.Z = B, a.rs_z = P, a.transposed = true;
-    }
-  }
-  return run(a, cut_fwd(B, Cin, Cout, P), dtype, (char*)workspace + operand_bytes(rows16, Cin), true, tc_fwd, st);
+  float* part;
+  const Product p = product(q, scale, W, wscale, y, B, Cin, Cout, P, workspace, &part);
+  return p.run(part, dtype, tc_fwd, st);
 }
 
 extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const float* wscale, void* dx, int32_t B, int32_t Cin,
@@ -336,22 +416,9 @@ extern "C" int disco_matmul_i8_bwd_input(const void* dy, const void* W, const fl
   const Buffer out[] = {{dx, T * Cin * 2, "dx"}, {workspace, need, "workspace"}};
   const unsigned in_place[] = {0, 0, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 2))) return rc;
-  const cudaStream_t st = (cudaStream_t)stream;
-  if ((rc = operand_16(W, wscale, workspace, Cin, Cout, dtype == DISCO_F16, st))) return rc;
-  const long long ld = ((long long)Cin + 7) / 8 * 8;
-  MmArgs a = {};
-  a.out = dx;
-  a.f16 = dtype == DISCO_F16;
-  a.N = Cin, a.K = Cout, a.R = 1;
-  a.B = {workspace, nullptr, 0, 0, ld, 0, 16, false, Cout * ld};
-  if (P == 1) {  // m = row
-    a.A = {dy, nullptr, 0, 0, Cout, 0, 16, true, (long long)(T * Cout)};
-    a.M = B, a.Z = 1;
-  } else {  // m = pixel
-    a.A = {dy, nullptr, Cout * P, 0, P, 0, 16, false, (long long)(T * Cout)};
-    a.M = P, a.Z = B, a.transposed = true;
-  }
-  return run(a, cut_dx(B, Cin, Cout, P), dtype, (char*)workspace + operand_bytes(Cout, Cin), true, tc_dx, st);
+  float* part;
+  const Product p = product_dx(dy, W, wscale, dx, B, Cin, Cout, P, dtype == DISCO_F16, workspace, &part);
+  return p.run(part, dtype, tc_dx, (cudaStream_t)stream);
 }
 
 extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const float* scale, void* dW, int32_t B, int32_t Cin,
@@ -368,18 +435,7 @@ extern "C" int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const f
   const Buffer out[] = {{dW, (size_t)Cout * Cin * 2, "dW"}, {workspace, need, "workspace"}};
   const unsigned in_place[] = {0, 0, 0};
   if ((rc = check_buffers(in, in_place, 3, out, 2))) return rc;
-  MmArgs a = {};
-  a.out = dW;
-  a.f16 = dtype == DISCO_F16;
-  a.M = Cin, a.N = Cout, a.Z = 1, a.transposed = true;  // m = input channel
-  if (P == 1) {  // k = row
-    a.A = {q, scale, 0, 0, Cin, 0, 8, false, (long long)(T * Cin)};
-    a.B = {dy, nullptr, 0, 0, Cout, 0, 16, false, (long long)(T * Cout)};
-    a.K = B, a.R = 1;
-  } else {  // k = pixel, summed over the samples too
-    a.A = {q, scale, 0, Cin * P, P, P, 8, true, (long long)(T * Cin)};
-    a.B = {dy, nullptr, 0, Cout * P, P, 0, 16, true, (long long)(T * Cout)};
-    a.K = P, a.R = B;
-  }
-  return run(a, cut_dw(B, Cin, Cout, P), dtype, workspace, false, tc_dw, (cudaStream_t)stream);
+  float* part;
+  const Product p = product_dw(dy, q, scale, dW, B, Cin, Cout, P, dtype == DISCO_F16, workspace, &part);
+  return p.run(part, dtype, tc_dw, (cudaStream_t)stream);
 }

@@ -15,7 +15,6 @@ struct Operand {
   long long z, r, ld, ks_r;
   int bits;  // 8: integers, 16: fp16 or bf16
   bool k_major;
-  long long n;  // elements of the tensor
 };
 
 // out[z][m][n] = rs[z rs_z + m] cs[n] sum_{r < R, k < K} A(m, k) B(n, k), or with
@@ -33,11 +32,9 @@ struct MmArgs {
 // of each z, their reduction of `steps` chunks of 64 k in nsplit parts.
 struct TcArgs {
   MmArgs m;
-  const uint8_t *enda, *endb;  // ends of the operands' tensors
   float* part;                 // fp32 sums of the parts, each laid out as out, or null
   int NB, nsplit, out_type, vec;        // vec: rows of what it writes start on 16 bytes
-  bool ala, alb;                        // rows of A, of B start on 16 bytes
-  bool after;                           // the launch before it wrote an operand: begin while that one ends
+  bool after;                           // the launch before it wrote operands: begin while that one ends
   uint32_t mt, nt, tiles;               // of a z, of the call (with parts); below 2^31
   long long nkp, steps;                 // 64-k chunks of a slice r, of all
 };

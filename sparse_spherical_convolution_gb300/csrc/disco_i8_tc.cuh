@@ -11,8 +11,8 @@
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
 // Persistent kernel:
-//   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few, and where rows are
-//                off alignment): tcgen05.ld, scales, rounding, stores along the output's rows
+//   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few): tcgen05.ld,
+//                scales, rounding, stores along the output's rows
 //   converters   (8 warps, idle where both operands are 16-bit): integers from the raw ring, to 16 bits, into the
 //                stage.  Two groups take alternate steps, so that one's loads, conversion and
 //                fence overlap the other's.  The raw ring has an even number of slots, each always
@@ -24,9 +24,9 @@
 // Both operands lie in the stage as lines of 64 elements (128 bytes, 128-byte
 // swizzle): element k .. k + 63 of one m or n where k is the contiguous direction
 // in memory, else (MN-major) 64 neighbouring m or n of one k.  So no operand is ever transposed.
-// Rows off 16-byte alignment the converters copy themselves, some steps ahead with
-// cp.async, in aligned 16-byte words (one more than the line has), and shift in
-// registers; a thread's shift stays the same over a tile.
+// Operands whose rows do not start on 16 bytes are laid out anew in the workspace first
+// (disco_i8_mm.cu): with the converters reading and shifting their words instead, dx of
+// [1,512,259199] took 326 us and dW 676; copy and product take less.
 // All mbarrier waits are bounded (time-out -> status flag, abort).
 #pragma once
 
@@ -53,28 +53,23 @@ template <int ES_, bool KM_, int SC_>
 struct Form {
   static constexpr int ES = ES_, SC = SC_;
   static constexpr bool KM = KM_;
-  static constexpr int UPL = ES == 1 ? 4 : 8;         // 16-byte units of a line of 64 elements
 };
 
-// What the kernel's parameters make of warps and shared memory (227 KB).
-//   raw ring, aligned: integers as they are; off alignment: words of each line and one more
-template <class FA, bool ALA, bool ALB, bool TR>
+
+// What the forms make of warps and shared memory (227 KB).
+template <class FA>
 struct Plan {
-  static constexpr bool kAligned = ALA && ALB;
-  static constexpr bool kRaw = ALA && FA::ES == 1;  // A by TMA into the raw ring
-  static constexpr int kEpi = kAligned && !FA::SC ? 8 : 4, kConv = kAligned && !kRaw ? 4 : 8;
+  static constexpr bool kRaw = FA::ES == 1;  // A by TMA into the raw ring
+  static constexpr int kEpi = FA::SC ? 4 : 8, kConv = kRaw ? 8 : 4;
   static constexpr int kMmaWarp = kEpi + kConv, kThreads = 32 * (kMmaWarp + 3);
-  static constexpr int kGroups = kRaw ? 2 : 1, kGroupWarps = kConv / kGroups;
-  static constexpr uint32_t kSlotA = kRaw ? kBM * kBK : ALA ? 0 : kBM * (64 * FA::ES + 16);
-  static constexpr uint32_t kSlot = kSlotA + (ALB ? 0 : kNBMax * (128 + 16));
-  static constexpr int kStages = kAligned ? (kRaw ? 3 : 4) : ALB ? 3 : 2;
-  static constexpr int kRaws = kAligned ? (kRaw ? 6 : 0) : ALB ? 4 : 2;
+  static constexpr int kGroups = 2, kGroupWarps = kConv / kGroups;
+  static constexpr int kStages = kRaw ? 3 : 4, kRaws = kRaw ? 6 : 0;
+  static constexpr uint32_t kSlot = kBM * kBK;
   // of an epilogue warp: 64 bytes of 32 rows on their way out, the scales of a tile's columns
-  static constexpr uint32_t kStaging = 32 * 64, kCols = FA::ES == 1 && !FA::SC ? kNBMax * 4 : 0;
+  static constexpr uint32_t kStaging = 32 * 64, kCols = kRaw && !FA::SC ? kNBMax * 4 : 0;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kRaws % kGroups == 0, "a slot is always the same group's");
-  static_assert(!kRaw || ALB, "the raw ring is filled by TMA or by the converters");
 };
 
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
@@ -85,11 +80,6 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-// 16 bytes into shared memory, the first `bytes` (0 .. 16) of them from memory and zeros behind them
-__device__ __forceinline__ void cp16(void* d, const uint8_t* p, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(p), "r"(bytes) : "memory");
 }
 
 // 4 integers to 4 fp16 values: 1024 + (q + 128) by the exponent's bits, less 1152; exact.
@@ -108,105 +98,53 @@ __device__ __forceinline__ uint2 to_scaled4(uint32_t w, float s0, float s1, floa
                     pack2_16(from_byte(w, 2) * s2, from_byte(w, 3) * s3, HALF));
 }
 
-// One operand's share of a converter thread: 16-byte units t, t + NT, ... of a step's lines.
+// A's share of a converter thread: 16-byte units t, t + NT, ... of a step's 128 lines.
 template <class F, int NT>
-struct Loader {
-  static constexpr int LPI = NT / F::UPL;  // lines that the converters take at a time
-  const uint8_t *base, *end;        // the tensor
-  long long ld;
-  int u, l0;                        // unit of a line, first line
+struct Units {
+  static constexpr int N = kBM * 4 / NT, LPI = NT / 4;  // units; lines that the converters take at a time
+  int u, l0;                                            // unit of a line, first line
 
-  __device__ __forceinline__ void init(const Operand& o, const uint8_t* e, int t) {
-    base = (const uint8_t*)o.p, end = e, ld = o.ld * F::ES;
-    u = t % F::UPL, l0 = t / F::UPL;
-  }
+  __device__ __forceinline__ explicit Units(int t) : u(t % 4), l0(t / 4) {}
   // The scales of this thread's units of a step: of 16 k (k contiguous), or of its lines.
+  // ks: of the step's first k; the row of scales goes on in zeros to a multiple of 16.
   static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 64 / LPI > 1 ? 64 / LPI : 1;
-  template <bool ALN>
-  __device__ __forceinline__ void scales(float (&s)[NS], const float* ks, int kleft) const {  // ks: of the step's first k
-    if constexpr (F::SC && F::KM && ALN) {  // 16 k are inside or outside together
+  __device__ __forceinline__ void scales(float (&s)[NS], const float* ks, int kleft) const {
+    if constexpr (F::SC && F::KM) {
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 f = 16 * u < kleft ? __ldg(reinterpret_cast<const float4*>(ks + 16 * u + i)) : make_float4(0, 0, 0, 0);
         s[i] = f.x, s[i + 1] = f.y, s[i + 2] = f.z, s[i + 3] = f.w;
       }
-    } else if constexpr (F::SC && F::KM) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 16 * u + i < kleft ? __ldg(ks + 16 * u + i) : 0.0f;
     } else if constexpr (F::SC) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) s[i] = ((l0 + i * LPI) & 63) < kleft ? __ldg(ks + ((l0 + i * LPI) & 63)) : 0.0f;
     }
   }
-  // 16 bytes of unit j into the stage
+  // unit j into the stage
   template <bool HALF>
   __device__ __forceinline__ void put(const uint4& v, int j, const float (&s)[NS], uint8_t* stage) const {
     const int line = l0 + j * LPI, x = line & 7;
     uint8_t* d = stage + line * 128;
-    if constexpr (F::ES == 2) {
-      *reinterpret_cast<uint4*>(d + ((u ^ x) << 4)) = v;
+    uint2 a, b, c, e;
+    if constexpr (F::SC == 0) {
+      a = to_half4(v.x), b = to_half4(v.y), c = to_half4(v.z), e = to_half4(v.w);
+    } else if constexpr (F::KM) {
+      a = to_scaled4<HALF>(v.x, s[0], s[1], s[2], s[3]), b = to_scaled4<HALF>(v.y, s[4], s[5], s[6], s[7]);
+      c = to_scaled4<HALF>(v.z, s[8], s[9], s[10], s[11]), e = to_scaled4<HALF>(v.w, s[12], s[13], s[14], s[15]);
     } else {
-      uint2 a, b, c, e;
-      if constexpr (F::SC == 0) {
-        a = to_half4(v.x), b = to_half4(v.y), c = to_half4(v.z), e = to_half4(v.w);
-      } else if constexpr (F::KM) {
-        a = to_scaled4<HALF>(v.x, s[0], s[1], s[2], s[3]), b = to_scaled4<HALF>(v.y, s[4], s[5], s[6], s[7]);
-        c = to_scaled4<HALF>(v.z, s[8], s[9], s[10], s[11]), e = to_scaled4<HALF>(v.w, s[12], s[13], s[14], s[15]);
-      } else {
-        const float f = s[j % NS];
-        a = to_scaled4<HALF>(v.x, f, f, f, f), b = to_scaled4<HALF>(v.y, f, f, f, f);
-        c = to_scaled4<HALF>(v.z, f, f, f, f), e = to_scaled4<HALF>(v.w, f, f, f, f);
-      }
-      *reinterpret_cast<uint4*>(d + (((2 * u) ^ x) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-      *reinterpret_cast<uint4*>(d + (((2 * u + 1) ^ x) << 4)) = make_uint4(c.x, c.y, e.x, e.y);
+      const float f = s[j % NS];
+      a = to_scaled4<HALF>(v.x, f, f, f, f), b = to_scaled4<HALF>(v.y, f, f, f, f);
+      c = to_scaled4<HALF>(v.z, f, f, f, f), e = to_scaled4<HALF>(v.w, f, f, f, f);
     }
-  }
-
-  // Rows off alignment.  `first`: the byte where line 0 of the step starts; unit (line, u)
-  // lies `line` storage rows further, in a box of 64 m or n where k is not contiguous.
-  __device__ __forceinline__ const uint8_t* line_at(const uint8_t* first, int line) const {
-    return F::KM ? first + line * ld : first + (line & 63) * ld + (line >> 6) * (64 * F::ES);
-  }
-  // bytes of a line that are inside the operand
-  __device__ __forceinline__ int line_bytes(int line, int ileft, int kleft) const {
-    if (F::KM) return line < ileft ? kleft * F::ES : 0;
-    return (line & 63) < kleft ? max(0, min(64, ileft - (line & ~63))) * F::ES : 0;
-  }
-  // The words of this thread's units into a slot of the ring: word u of a line at unit
-  // (line, u), and the one behind its last at `more`.
-  __device__ __forceinline__ void fetch(uint8_t* slot, int slot_lines, const uint8_t* first, int ileft, int kleft, int lines) const {
-    for (int line = l0; line < lines; line += LPI) {
-      const uint8_t* p = line_at(first, line);
-      const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15), len = line_bytes(line, ileft, kleft) + sh;
-      const uint8_t* w = p - sh + 16 * u;
-      const bool need = len > sh && 16 * u < len;
-      const int n = need && DISCO_IN_BOUNDS(w >= base && w < end) ? (int)min((long long)(end - w), 16LL) : 0;
-      cp16(slot + (line * F::UPL + u) * 16, n ? w : base, n);
-      if (u == F::UPL - 1) {
-        w += 16;
-        const int m = len > sh && 16 * F::UPL < len && DISCO_IN_BOUNDS(w >= base && w < end) ? (int)min((long long)(end - w), 16LL) : 0;
-        cp16(slot + (slot_lines * F::UPL + line) * 16, m ? w : base, m);
-      }
-    }
-  }
-  template <bool HALF>
-  __device__ __forceinline__ void convert(const uint8_t* slot, int slot_lines, uint8_t* stage, const float (&s)[NS], const uint8_t* first,
-                                          int ileft, int kleft, int lines) const {
-    const int sh = (int)(reinterpret_cast<uintptr_t>(line_at(first, l0)) & 15);  // the same for all units of the thread
-    const uint4* w = reinterpret_cast<const uint4*>(slot);
-#pragma unroll 2
-    for (int j = 0; l0 + j * LPI < lines; ++j) {
-      const int line = l0 + j * LPI, at = line * F::UPL + u;
-      const uint4 lo = w[at], hi = w[u == F::UPL - 1 ? slot_lines * F::UPL + line : at + 1];
-      put<HALF>(shifted(lo, hi, sh, min(16, line_bytes(line, ileft, kleft) - 16 * u)), j, s, stage);
-    }
+    *reinterpret_cast<uint4*>(d + (((2 * u) ^ x) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(d + (((2 * u + 1) ^ x) << 4)) = make_uint4(c.x, c.y, e.x, e.y);
   }
 };
 
 // Where a converter is: step q of tile t, slice r, chunk kc.
 struct Pos {
   uint32_t t;
-  long long q, q1, r, kc, m0, n0, z;
+  long long q, q1, r, kc;
 };
 
 __device__ __forceinline__ void tc_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -223,17 +161,15 @@ __device__ __forceinline__ void tc_tma_3d(void* dst, const CUtensorMap* map, int
 // One row on; opaque to the compiler, which would keep 32 rows' addresses in registers.
 __device__ __forceinline__ void next_row(uint8_t*& o, long long pitch) { asm volatile("add.s64 %0, %0, %1;" : "+l"(o) : "l"(pitch)); }
 
-// FA: A's form; BKM: B is K-major; HALF: 16-bit operands are fp16; ALA, ALB: the
-// rows of A, of B start on 16 bytes (by TMA); TR: out[z][n][m] instead of [m][n].
-template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
-__global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
+// FA: A's form; BKM: B is K-major; HALF: 16-bit operands are fp16; TR: out[z][n][m]
+// instead of [m][n].
+template <class FA, bool BKM, bool HALF, bool TR>
+__global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
-  using FB = Form<2, BKM, 0>;
-  using C = Plan<FA, ALA, ALB, TR>;
-  constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2;
-  constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps, kStages = C::kStages, kRaws = C::kRaws;
-  constexpr bool kRaw = C::kRaw, kTmaA = ALA && FA::ES == 2;  // A by the raw ring, or straight into the stage
-  constexpr bool kConv = !kTmaA || !ALB;                      // the converters have work
+  using C = Plan<FA>;
+  constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2, kStages = C::kStages, kRaws = C::kRaws;
+  constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps;
+  constexpr bool kRaw = C::kRaw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* raws = smem + kStages * kStageBytes;
@@ -247,7 +183,7 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], (kConv ? kGroupWarps : 0) + (kTmaA ? 1 : 0) + (ALB ? 1 : 0));
+      mbar_init(&full[s], (kRaw ? kGroupWarps : 1) + 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -292,18 +228,15 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
 
   if (warp >= kEpiWarps && warp < kMmaWarp) {
     // --------------------------------------------------------- converters --
-    if constexpr (kConv) {
+    if constexpr (kRaw) {
       const int group = (warp - kEpiWarps) / kGroupWarps, t0 = tid - 32 * kEpiWarps - group * kConverters;
-      Loader<FA, kConverters> la;
-      Loader<FB, kConverters> lb;
-      la.init(a.m.A, a.enda, t0);
-      lb.init(a.m.B, a.endb, t0);
-      const int blines = (a.NB + 63) / 64 * 64;
+      using U = Units<FA, kConverters>;
+      const U units(t0);
       auto start = [&](Pos& p, uint32_t t) {
         p.t = t;
         if (t >= a.tiles) return;
         const Tile c = tile_of(t);
-        p.q = c.q0, p.q1 = c.q1, p.m0 = c.m0, p.n0 = c.n0, p.z = c.z;
+        p.q = c.q0, p.q1 = c.q1;
         p.r = c.q0 == 0 || a.m.R == 1 ? 0 : c.q0 / a.nkp;
         p.kc = c.q0 - p.r * a.nkp;
       };
@@ -311,33 +244,13 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
         if (++p.q == p.q1) return start(p, p.t + gridDim.x);
         if (++p.kc == a.nkp) p.kc = 0, ++p.r;
       };
-      auto kleft = [&](const Pos& p) { return (int)min(a.m.K - p.kc * kBK, (long long)kBK); };
-      auto scales = [&](const Pos& p, float (&s)[Loader<FA, kConverters>::NS]) {
-        if constexpr (FA::SC) la.template scales<ALA>(s, a.m.A.ks + p.r * a.m.A.ks_r + p.kc * kBK, kleft(p));
+      auto scales = [&](const Pos& p, float (&s)[U::NS]) {
+        if constexpr (FA::SC) units.scales(s, a.m.A.ks + p.r * a.m.A.ks_r + p.kc * kBK, (int)min(a.m.K - p.kc * kBK, (long long)kBK));
       };
-      // the byte where a step's line 0 starts, m or n of the tile inside the operand
-      auto first_a = [&](const Pos& p) { return la.base + (p.z * a.m.A.z + p.r * a.m.A.r + (FA::KM ? p.m0 * a.m.A.ld + p.kc * kBK : p.kc * kBK * a.m.A.ld + p.m0)) * FA::ES; };
-      auto first_b = [&](const Pos& p) { return lb.base + (p.z * a.m.B.z + p.r * a.m.B.r + (BKM ? p.n0 * a.m.B.ld + p.kc * kBK : p.kc * kBK * a.m.B.ld + p.n0)) * 2; };
-      auto left_a = [&](const Pos& p) { return (int)min(a.m.M - p.m0, (long long)kBM); };
-      auto left_b = [&](const Pos& p) { return (int)min(a.m.N - p.n0, (long long)blines); };
-      auto fetch = [&](const Pos& p, int i) {  // rows off alignment: this thread's words of step i
-        if (p.t < a.tiles) {
-          uint8_t* slot = raws + (i % (kRaws ? kRaws : 1)) * C::kSlot;
-          if constexpr (!ALA) la.fetch(slot, kBM, first_a(p), left_a(p), kleft(p), kBM);
-          if constexpr (!ALB) lb.fetch(slot + C::kSlotA, kNBMax, first_b(p), left_b(p), kleft(p), blines);
-        }
-        norm::copy_commit();
-      };
-      Pos cur, nxt, far;
+      Pos cur, nxt;
       start(cur, blockIdx.x);
       if (group == 1 && cur.t < a.tiles) advance(cur);
-      far = cur;
-      if constexpr (!kRaw)
-        for (int d = 0; d < kRaws - 1; ++d) {
-          fetch(far, d);
-          if (far.t < a.tiles) advance(far);
-        }
-      float sc[Loader<FA, kConverters>::NS], scn[Loader<FA, kConverters>::NS];
+      float sc[U::NS], scn[U::NS];
       if (cur.t < a.tiles) scales(cur, sc);
       bool ok = true;
       for (int i = group; cur.t < a.tiles; i += kGroups) {
@@ -346,59 +259,37 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
         for (int k = 0; k < kGroups; ++k)
           if (nxt.t < a.tiles) advance(nxt);
         if (nxt.t < a.tiles) scales(nxt, scn);  // this group's next step's
-        const int s = i % kStages;
-        constexpr int kUnits = kBM * 4 / kConverters;
-        uint4 v[kUnits];
-        if constexpr (kRaw) {
-          const int w = i % kRaws;
-          ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
-          if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
-            const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot) + t0;
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j) v[j] = src[j * kConverters];
-          } else {
-            ok = false;
-          }
-        } else {
-          fetch(far, i + kRaws - 1);
-          if (far.t < a.tiles) advance(far);
-          norm::copy_wait<kRaws - 1>();
-          __syncwarp();  // a line's words are copied by lanes of one warp
-        }
-        if (ok && i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
+        const int s = i % kStages, w = i % kRaws;
+        uint4 v[U::N];
+        ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
         ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
         if (!ok) break;
-        uint8_t* sa = smem + s * kStageBytes;
-        if constexpr (kRaw) {
-          __syncwarp();  // every lane has read its units
-          if (lane == 0) mbar_arrive(&rawe[i % kRaws]);
+        const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot) + t0;
 #pragma unroll
-          for (int j = 0; j < kUnits; ++j) la.template put<HALF>(v[j], j, sc, sa);
-        } else {
-          const uint8_t* slot = raws + (i % kRaws) * C::kSlot;
-          if constexpr (!ALA) la.template convert<HALF>(slot, kBM, sa, sc, first_a(cur), left_a(cur), kleft(cur), kBM);
-          if constexpr (!ALB) {
-            const float none[1] = {0.0f};
-            lb.template convert<HALF>(slot + C::kSlotA, kNBMax, sa + kABytes, none, first_b(cur), left_b(cur), kleft(cur), blines);
-          }
-        }
+        for (int j = 0; j < U::N; ++j) v[j] = src[j * kConverters];
+        if (i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
+        ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+        if (!ok) break;
+        __syncwarp();  // every lane has read its units
+        if (lane == 0) mbar_arrive(&rawe[w]);
+#pragma unroll
+        for (int j = 0; j < U::N; ++j) units.template put<HALF>(v[j], j, sc, smem + s * kStageBytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
         cur = nxt;
 #pragma unroll
-        for (int k = 0; k < Loader<FA, kConverters>::NS; ++k) sc[k] = scn[k];
+        for (int k = 0; k < U::NS; ++k) sc[k] = scn[k];
       }
       if (!ok) {
         i8_flag();
         *abort_flag = 1;
       }
-      cp_async_wait_all();
     }
   } else if (warp == kTmaAWarp || warp == kTmaBWarp) {
     // ------------------------------------------------------------ TMA --
     const bool is_a = warp == kTmaAWarp;
-    if (lane == 0 && (is_a ? ALA : ALB)) {
+    if (lane == 0) {
       // A's integers go into the raw ring, 16-bit lines into the stage
       const bool ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
       const int slots = ring ? (kRaws ? kRaws : 1) : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
@@ -537,9 +428,7 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
         const int left = min(32, cols - c0);
         if constexpr (TR) {
           uint8_t* o = out + (long long)c0 * pitch;
-          // pixels of aligned rows make whole words of the output too
-          constexpr bool kWhole = ALA && !FA::KM && !FA::SC;
-          if (eb == 2 && (kWhole || a.vec)) {
+          if (eb == 2 && a.vec) {
             // pairs of n of 32 m through shared memory, then 8 m of both n to a lane (2-byte
             // stores straight from the registers took 141 us instead of 71 for dx of 2 x 256 -> 128 channels)
 #pragma unroll
@@ -570,7 +459,7 @@ __global__ void __launch_bounds__(Plan<FA, ALA, ALB, TR>::kThreads, 1)
                 if (e < left) *reinterpret_cast<uint32_t*>(o) = v[e];
                 next_row(o, pitch);
               }
-            } else if (!kWhole) {
+            } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const uint32_t two = pack2_16(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), h16);
@@ -664,15 +553,15 @@ inline int tc_encode(CUtensorMap* map, const Operand& o, long long I, long long 
   return DISCO_OK;
 }
 
-template <class FA, bool BKM, bool HALF, bool ALA, bool ALB, bool TR>
+template <class FA, bool BKM, bool HALF, bool TR>
 int tc_launch(const TcArgs& a, cudaStream_t st) {
   CUtensorMap amap = {}, bmap = {};
   int rc;
-  if (ALA && (rc = tc_encode(&amap, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF))) return rc;
-  if (ALB && (rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
-  constexpr size_t kSmem = Plan<FA, ALA, ALB, TR>::kSmem;
-  auto kern = i8_tc_kernel<FA, BKM, HALF, ALA, ALB, TR>;
-  return norm::launch(kern, (int)min(a.tiles, (uint32_t)kSMs), Plan<FA, ALA, ALB, TR>::kThreads, 1, a.after, kSmem, kSmem, st, "i8_tc_kernel", amap, bmap, a);
+  if ((rc = tc_encode(&amap, a.m.A, a.m.M, a.m.K, a.m.Z * a.m.R, kBM, HALF))) return rc;
+  if ((rc = tc_encode(&bmap, a.m.B, a.m.N, a.m.K, a.m.Z * a.m.R, a.NB, HALF))) return rc;
+  constexpr size_t kSmem = Plan<FA>::kSmem;
+  auto kern = i8_tc_kernel<FA, BKM, HALF, TR>;
+  return norm::launch(kern, (int)min(a.tiles, (uint32_t)kSMs), Plan<FA>::kThreads, 1, a.after, kSmem, kSmem, st, "i8_tc_kernel", amap, bmap, a);
 }
 
 // This unit's status word (ORed into *v, and optionally cleared).

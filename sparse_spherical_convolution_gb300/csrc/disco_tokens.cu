@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs
       const Quantizer z(join(my, part[1]));
       if (live) {
         if (j0 == 0) a.scale[b * a.P + p] = z.scale;
-        for (int c = j0; c < a.C; c += step) a.q[y0 + c * a.P] = (int8_t)quantize_near(value(c), z);
+        for (int c = j0; c < a.C; c += step) a.q[y0 + c * a.P] = (int8_t)quantize_y<T>(value(c), z);
       }
     }
     __syncthreads();

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_pixel_kernel(const Token
 #pragma unroll
     for (int i = 0; i < J; ++i) {
       const int c = j0 + i * g.NL;
-      if (c < a.C) a.q[y0 + c * a.P] = (int8_t)quantize_near(y[i], z);
+      if (c < a.C) a.q[y0 + c * a.P] = (int8_t)quantize_y<T>(y[i], z);
     }
   }
 }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_rows_kernel(const TokenA
       if (c < a.C && DISCO_IN_BOUNDS(c + V <= a.C)) {
         uint32_t r[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) r[e] = quantize_near(y[i][e], z);
+        for (int e = 0; e < V; ++e) r[e] = quantize_y<T>(y[i][e], z);
         store_bytes<V>(a.q + y0 + c, r);
       }
     }
@@ -320,14 +320,14 @@ __device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, c
 
 template <typename T, bool GLU, bool XQ, bool YQ>
 __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenArgs a, const TileCut g) {
-  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1;
+  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kOwnY = XQ ? 2 : 0, kOwn = kOwnY + (YQ ? 2 : 0);
   using R = Raw<T, V>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lx = tid & (g.LX - 1), j0 = tid / g.LX, NL = g.NT / g.LX, NT = g.NT, TP = g.LX * V;
   const int warps = NT / 32, warp = tid / 32;
   uint4* w = reinterpret_cast<uint4*>(smem) + tid;
-  float* own = reinterpret_cast<float*>(smem + (size_t)G * g.nj * NT * 16);  // of each pixel: 1/a, -a of x, 127/a of y
-  uint8_t* sums = reinterpret_cast<uint8_t*>(own + ((XQ ? 2 : 0) + (YQ ? 1 : 0)) * TP);  // [warps][pixels] of x, of y
+  float* own = reinterpret_cast<float*>(smem + (size_t)G * g.nj * NT * 16);  // of each pixel: 1/a, -a of x, a and 127/a of y
+  uint8_t* sums = reinterpret_cast<uint8_t*>(own + kOwn * TP);  // [warps][pixels] of x, of y
   const int nj = j0 < a.C ? (a.C - j0 + NL - 1) / NL : 0;       // channels of this thread
   const long long P = a.P, half = a.C * P, step = NL * P, row0 = j0 * P;  // from one of its channels to the next; its first
   for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x) {
@@ -426,12 +426,11 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
           uint32_t m = 0;
           for (int o = sub; o < warps; o += S) m = max(m, q[o * TP + e]);
           for (int o = 1; o < S; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const Quantizer z(__uint_as_float(m));
-          const bool finite = z.scale < __int_as_float(0x7f800000);
+          const float amax = __uint_as_float(m);
+          const Quantizer z(amax);
           if (in) a.scale[at] = z.scale;
-          // a token with an infinity or a NaN: 0, and values that are NaN times it are cleared below
-          if (first) own[(XQ ? 2 * TP : 0) + e] = finite ? z.k * z.inv : 0.0f;
-          plain = plain && finite;
+          if (first) own[kOwnY * TP + e] = amax, own[(kOwnY + 1) * TP + e] = z.k * z.inv;
+          plain = plain && ordinary(amax);
         }
       }
       plain = __syncthreads_and(plain);
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
       else second(std::false_type());
     }
     if constexpr (YQ) {
-      const F<V> f = norm::load_row<V>(own + (XQ ? 2 * TP : 0) + lx * V);
+      const F<V> amax = norm::load_row<V>(own + kOwnY * TP + lx * V), f = norm::load_row<V>(own + (kOwnY + 1) * TP + lx * V);
       auto third = [&](auto is_plain, auto kind) {
         const uint4* s = w;
         int8_t* d = a.q + y0 + row0;
@@ -473,14 +472,18 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
             memcpy(&r1, &s[NT], 16);
             v = gated<T, V>(unpack<T, V>(r0), unpack<T, V>(r1), decltype(kind)::value);
           }
-          v = norm::mul(v, f);
-          if constexpr (!decltype(is_plain)::value)
-#pragma unroll
-            for (int e = 0; e < V; ++e) v.v[e] = fabsf(v.v[e]) < 128.0f ? v.v[e] : 0.0f;
-          v = norm::add(v, norm::fill<V>(kRound));
           uint32_t r[V];
+          if constexpr (decltype(is_plain)::value && ES == 2) {
+            v = norm::add(norm::mul(v, f), norm::fill<V>(kRound));
 #pragma unroll
-          for (int e = 0; e < V; ++e) r[e] = __float_as_uint(v.v[e]);
+            for (int e = 0; e < V; ++e) r[e] = __float_as_uint(v.v[e]);
+          } else if constexpr (decltype(is_plain)::value) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) r[e] = __float_as_uint(__fdiv_rn(__fmul_rn(kQMax, v.v[e]), amax.v[e] == 0.0f ? 1.0f : amax.v[e]) + kRound);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) r[e] = quantize_y<T>(v.v[e], Quantizer(amax.v[e]));
+          }
           store_bytes<V>(d, r);
         }
       };
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
 
 template <typename T, bool GLU, bool XQ, bool YQ>
 int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
-  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0), kOwn = (XQ ? 2 : 0) + (YQ ? 1 : 0);
+  constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0), kOwn = (XQ ? 2 : 0) + (YQ ? 2 : 0);
   TileCut g;
   // 128 bytes of a row to a tile, more for few channels, less for many, so that three tiles share an SM
   g.LX = 8;
