@@ -100,8 +100,9 @@ struct Mag {
   }
 };
 
+// the low bytes of V words
 template <int V>
-__device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&r)[V]) {
+__device__ __forceinline__ typename Word<V>::type bytes_word(const uint32_t (&r)[V]) {
   typename Word<V>::type o;
   if constexpr (V == 1) {
     o = (uint8_t)r[0];
@@ -111,7 +112,11 @@ __device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&r)[V]) {
     for (int i = 0; i < V / 4; ++i) w[i] = bytes4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
     memcpy(&o, w, V);
   }
-  store_stream(p, o);
+  return o;
+}
+template <int V>
+__device__ __forceinline__ void store_bytes(int8_t* p, const uint32_t (&r)[V]) {
+  store_stream(p, bytes_word<V>(r));
 }
 
 // GLU: x holds gates and values, 2 C channels; y = act(gate) value.  XQ: the 8-bit
@@ -308,13 +313,19 @@ __device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, c
 #pragma unroll
     for (int e = 0; e < V; ++e) r[e] = __float_as_uint(t.v[e]);
   } else {
+    if constexpr (PLAIN) {  // fp32: one test for the word (quantize<float>)
+      const F<V> t = norm::mul(norm::mul(norm::fill<V>(kQMax), x), inv), u = norm::add(t, norm::fill<V>(kRound));
+      const F<V> d = norm::add(norm::add(u, norm::fill<V>(-kRound)), norm::mul(t, norm::fill<V>(-1.0f)));
+      float far = 0.0f;  // from the integers
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      Quantizer z(1.0f);
-      if (PLAIN) z.k = kQMax, z.b = -minus_a.v[e], z.inv = inv.v[e];
-      else z = Quantizer(-minus_a.v[e]);
-      r[e] = quantize<T>(x.v[e], z);
+      for (int e = 0; e < V; ++e) {
+        far = fmaxf(far, fabsf(d.v[e]));
+        r[e] = __float_as_uint(u.v[e]);
+      }
+      if (far < 0.5f - 0x1p-14f) return;
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) r[e] = quantize<T>(x.v[e], Quantizer(-minus_a.v[e]));
   }
 }
 
@@ -525,7 +536,7 @@ int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
 // parts of two neighbouring tiles'; a thread's channels are a multiple of V apart, so its rows
 // have one skew, and only its magnitudes and factors are realigned, once a tile.
 template <typename T>
-__global__ void __launch_bounds__(128) tokens_skew_kernel(const TokenArgs a, const TileCut g) {
+__global__ void __launch_bounds__(256) tokens_skew_kernel(const TokenArgs a, const TileCut g) {
   constexpr int ES = (int)sizeof(T), V = 16 / ES;
   using R = Raw<T, V>;
   using M = typename Word<ES>::type;
@@ -576,23 +587,21 @@ __global__ void __launch_bounds__(128) tokens_skew_kernel(const TokenArgs a, con
     F<V> inv, minus_a;
 #pragma unroll
     for (int e = 0; e < V; ++e) inv.v[e] = own[V + px + e], minus_a.v[e] = own[row + V + px + e];
-    const bool full = px >= 0 && px + V <= N;
     auto second = [&](auto is_plain) {
-      int8_t* d = a.xq + at;
+      using W = typename Word<V>::type;
+      long long k = e0 - m;  // the element where the row's word 0 starts
 #pragma unroll 2
-      for (int i = 0; i < n; ++i, d += step) {
-        R r0;
-        const uint4 w0 = w[i * g.NT];
-        memcpy(&r0, &w0, 16);
-        uint32_t r[V];
-        quantize_word<T, V, decltype(is_plain)::value>(r, unpack<T, V>(r0), inv, minus_a);
-        if (full) {
-          store_bytes<V>(d, r);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            if (px + e >= 0 && px + e < N) d[e] = (int8_t)r[e];
+      for (int i = 0; i < g.nj; ++i, k += step) {
+        W o = {};
+        if (i < n) {
+          R r0;
+          const uint4 w0 = w[i * g.NT];
+          memcpy(&r0, &w0, 16);
+          uint32_t r[V];
+          quantize_word<T, V, decltype(is_plain)::value>(r, unpack<T, V>(r0), inv, minus_a);
+          o = bytes_word<V>(r);
         }
+        norm::store_words<V>(a.xq + k, k, total, o, m, lx, g.LX, N, i < nj);  // all lanes
       }
     };
     if (plain) second(std::true_type());
@@ -604,16 +613,17 @@ template <typename T>
 int tokens_skewed(const TokenArgs& a, cudaStream_t st) {
   constexpr int ES = (int)sizeof(T), V = 16 / ES;
   TileCut g;
-  g.NT = 128, g.LX = 16;  // a multiple of 8 channels side by side
-  while (g.LX > 4 && ((size_t)a.C * g.LX * 16 * 3 > norm::kMaxSmem - 12 * 1024 || (g.LX / 2 - 1) * V >= a.P)) g.LX /= 2;
+  // 15 words of pixels to a tile while three tiles share an SM, else 7 (at 3, half of the words are shared with other tiles)
+  g.LX = (size_t)a.C * 16 * 16 * 3 <= norm::kMaxSmem - 24 * 1024 && 7 * V < a.P ? 16 : 8;
+  g.NT = (size_t)a.C * g.LX * 16 * 3 <= norm::kMaxSmem - 24 * 1024 ? 128 : 256;  // a multiple of 8 channels side by side
   const int TP = (g.LX - 1) * V, NL = g.NT / g.LX;
   g.nj = (a.C + NL - 1) / NL;
   const size_t smem = (size_t)g.nj * g.NT * 16 + (size_t)(TP + 2 * V) * (8 + NL * ES);
-  if (smem > norm::kMaxSmem / 2) return DISCO_ERR_UNSUPPORTED;
+  if (smem > norm::kMaxSmem) return DISCO_ERR_UNSUPPORTED;
   g.per_sample = (a.P + TP - 1) / TP;
   g.tiles = g.per_sample * a.B;
-  const int ctas = (int)min((size_t)(1024 / g.NT), (norm::kMaxSmem + 1024) / (smem + 1024));
-  return norm::launch(tokens_skew_kernel<T>, (int)min(g.tiles, (long long)kSMs * ctas), g.NT, 1, false, smem, norm::kMaxSmem / 2, st,
+  const int ctas = (int)max((size_t)1, min((size_t)(1024 / g.NT), (norm::kMaxSmem + 1024) / (smem + 1024)));
+  return norm::launch(tokens_skew_kernel<T>, (int)min(g.tiles, (long long)kSMs * ctas), g.NT, 1, false, smem, norm::kMaxSmem, st,
                       "tokens_skew_kernel", a, g);
 }
 
