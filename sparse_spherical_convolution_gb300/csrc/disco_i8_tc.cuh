@@ -19,7 +19,8 @@
 //                the same group's, and stages are released in order: no waiter is ever two
 //                phases ahead of a barrier, where a wait by parity would pass at once
 //   one warp     MMA issuer (one thread); two accumulators of 256 TMEM columns, so
-//                the epilogue of a tile overlaps the main loop of the next
+//                the epilogue of a tile overlaps the main loop of the next.  Of narrow tiles
+//                four or eight, and each half of eight epilogue warps takes every second tile
 //   two warps    TMA of B and of A: into the stage (16-bit) or the raw ring (integers)
 // Both operands lie in the stage as lines of 64 elements (128 bytes, 128-byte
 // swizzle): element k .. k + 63 of one m or n where k is the contiguous direction
@@ -67,7 +68,7 @@ struct Plan {
   static constexpr uint32_t kSlot = kBM * kBK;
   // of an epilogue warp: 64 bytes of 32 rows on their way out, the scales of a tile's columns
   static constexpr uint32_t kStaging = 32 * 64, kCols = kRaw && !FA::SC ? kNBMax * 4 : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 256;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kRaws % kGroups == 0, "a slot is always the same group's");
 };
@@ -141,9 +142,41 @@ struct Units {
   }
 };
 
+// A CTA's tiles: tile t has n fastest (CTAs side by side share A's tile in L2), then m, z
+// and the part; the next one is gridDim.x on, by additions (divisions for each tile took a
+// third of one of four steps).
+struct Walk {
+  uint32_t t;
+  int n, m, z, sp, dn, dm, dz, dsp;
+  __device__ __forceinline__ explicit Walk(const TcArgs& a) {
+    t = blockIdx.x;
+    split(a, t, &n, &m, &z, &sp);
+    split(a, gridDim.x, &dn, &dm, &dz, &dsp);
+  }
+  __device__ static __forceinline__ void split(const TcArgs& a, uint32_t t, int* n, int* m, int* z, int* sp) {
+    uint32_t u = t / a.nt;
+    *n = (int)(t - u * a.nt);
+    t = u / a.mt;
+    *m = (int)(u - t * a.mt);
+    u = t / (uint32_t)a.m.Z;
+    *z = (int)(t - u * a.m.Z);
+    *sp = (int)u;
+  }
+  __device__ __forceinline__ void next(const TcArgs& a) {
+    t += gridDim.x;
+    n += dn, m += dm, z += dz, sp += dsp;
+    if (n >= (int)a.nt) n -= a.nt, ++m;
+    if (m >= (int)a.mt) m -= a.mt, ++z;
+    if (z >= a.m.Z) z -= a.m.Z, ++sp;
+  }
+  __device__ __forceinline__ bool in(const TcArgs& a) const { return t < a.tiles; }
+  __device__ __forceinline__ long long m0() const { return (long long)m * kBM; }
+  __device__ __forceinline__ long long n0(const TcArgs& a) const { return (long long)n * a.NB; }
+};
+
 // Where a converter is: step q of tile t, slice r, chunk kc.
 struct Pos {
-  uint32_t t;
+  Walk w;
   long long q, q1, r, kc;
 };
 
@@ -176,19 +209,21 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
   uint8_t* staging = raws + kRaws * C::kSlot;
   uint8_t* colscale = staging + kEpiWarps * C::kStaging;
   uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * C::kCols);
-  uint64_t *empty = full + kStages, *accf = empty + kStages, *acce = accf + 2, *rawf = acce + 2, *rawe = rawf + 8;
+  uint64_t *empty = full + 4, *accf = empty + 4, *acce = accf + 8, *rawf = acce + 8, *rawe = rawf + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int accs = a.NB <= 64 ? 8 : a.NB <= 128 ? 4 : 2, acc_cols = 512 / accs;  // accumulators, their columns
+  const bool turns = kEpiWarps == 8 && accs > 2;                                 // the epilogue's halves take turns
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], (kRaw ? kGroupWarps : 1) + 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 8; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], kEpiWarps);
+      mbar_init(&acce[b], turns ? 4 : kEpiWarps);
     }
     for (int r = 0; r < 8; ++r) {
       mbar_init(&rawf[r], 1);
@@ -207,24 +242,9 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
   const uint32_t tmem = *tslot;
   norm::wait_for_previous();  // the operand that was converted into the workspace
 
-  // tile t: n fastest (CTAs side by side share A's tile in L2), then m, z and the part
-  struct Tile {
-    long long m0, n0, z, q0, q1;
-    int sp;
-  };
-  auto tile_of = [&](uint32_t t) {  // 32-bit divisions: 64-bit ones took a third of a tile of four steps
-    Tile c;
-    uint32_t u = t / a.nt;
-    c.n0 = (long long)(t - u * a.nt) * a.NB;
-    t = u / a.mt;
-    c.m0 = (long long)(u - t * a.mt) * kBM;
-    u = t / (uint32_t)a.m.Z;
-    c.z = t - u * a.m.Z;
-    c.sp = (int)u;
-    c.q0 = 0, c.q1 = a.steps;
-    if (a.nsplit > 1) c.q0 = a.steps * c.sp / a.nsplit, c.q1 = a.steps * (c.sp + 1) / a.nsplit;
-    return c;
-  };
+  // reduction steps of a tile's part
+  auto first_step = [&](int sp) { return a.nsplit > 1 ? a.steps * sp / a.nsplit : 0; };
+  auto last_step = [&](int sp) { return a.nsplit > 1 ? a.steps * (sp + 1) / a.nsplit : a.steps; };
 
   if (warp >= kEpiWarps && warp < kMmaWarp) {
     // --------------------------------------------------------- converters --
@@ -232,33 +252,33 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       const int group = (warp - kEpiWarps) / kGroupWarps, t0 = tid - 32 * kEpiWarps - group * kConverters;
       using U = Units<FA, kConverters>;
       const U units(t0);
-      auto start = [&](Pos& p, uint32_t t) {
-        p.t = t;
-        if (t >= a.tiles) return;
-        const Tile c = tile_of(t);
-        p.q = c.q0, p.q1 = c.q1;
-        p.r = c.q0 == 0 || a.m.R == 1 ? 0 : c.q0 / a.nkp;
-        p.kc = c.q0 - p.r * a.nkp;
+      auto start = [&](Pos& p) {
+        p.q = first_step(p.w.sp), p.q1 = last_step(p.w.sp);
+        p.r = p.q == 0 || a.m.R == 1 ? 0 : p.q / a.nkp;
+        p.kc = p.q - p.r * a.nkp;
       };
       auto advance = [&](Pos& p) {
-        if (++p.q == p.q1) return start(p, p.t + gridDim.x);
-        if (++p.kc == a.nkp) p.kc = 0, ++p.r;
+        if (++p.q == p.q1) {
+          p.w.next(a);
+          start(p);
+        } else if (++p.kc == a.nkp) {
+          p.kc = 0, ++p.r;
+        }
       };
       auto scales = [&](const Pos& p, float (&s)[U::NS]) {
         if constexpr (FA::SC) units.scales(s, a.m.A.ks + p.r * a.m.A.ks_r + p.kc * kBK, (int)min(a.m.K - p.kc * kBK, (long long)kBK));
       };
-      Pos cur, nxt;
-      start(cur, blockIdx.x);
-      if (group == 1 && cur.t < a.tiles) advance(cur);
+      Pos cur{Walk(a), 0, 0, 0, 0};
+      start(cur);
+      if (group == 1) advance(cur);
       float sc[U::NS], scn[U::NS];
-      if (cur.t < a.tiles) scales(cur, sc);
+      if (cur.w.in(a)) scales(cur, sc);
       bool ok = true;
-      for (int i = group; cur.t < a.tiles; i += kGroups) {
-        nxt = cur;
+      for (int i = group; cur.w.in(a); i += kGroups) {
+        Pos nxt = cur;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k)
-          if (nxt.t < a.tiles) advance(nxt);
-        if (nxt.t < a.tiles) scales(nxt, scn);  // this group's next step's
+        for (int k = 0; k < kGroups; ++k) advance(nxt);
+        if (nxt.w.in(a)) scales(nxt, scn);  // this group's next step's
         const int s = i % kStages, w = i % kRaws;
         uint4 v[U::N];
         ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
@@ -302,11 +322,10 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       const bool sliced = is_a ? a.m.A.z || a.m.A.r : a.m.B.z || a.m.B.r;
       int i = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-        const Tile c = tile_of(t);
-        const long long i0 = is_a ? c.m0 : c.n0;
-        long long r = c.q0 == 0 || a.m.R == 1 ? 0 : c.q0 / a.nkp, kc = c.q0 - r * a.nkp;
-        for (long long q = c.q0; q < c.q1; ++q, ++i, ++kc) {
+      for (Walk c(a); c.in(a) && ok; c.next(a)) {
+        const long long i0 = is_a ? c.m0() : c.n0(a), q0 = first_step(c.sp), q1 = last_step(c.sp);
+        long long r = q0 == 0 || a.m.R == 1 ? 0 : q0 / a.nkp, kc = q0 - r * a.nkp;
+        for (long long q = q0; q < q1; ++q, ++i, ++kc) {
           if (kc == a.nkp) kc = 0, ++r;
           const int s = i % slots;
           if ((i >= slots && !mbar_wait(&e[s], ((i / slots) - 1) & 1, kWaitLimit)) || *abort_flag) {
@@ -343,15 +362,15 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       const uint32_t idesc = idesc_16_f32(kBM, nmma, HALF) | (FA::KM ? 0u : 1u << 15) | (BKM ? 0u : 1u << 16);
       int i = 0, tl = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++tl) {
-        const Tile c = tile_of(t);
-        const int ab = tl & 1;
-        if (tl >= 2 && !mbar_wait(&acce[ab], ((tl >> 1) - 1) & 1, kWaitLimit)) {
+      for (Walk c(a); c.in(a) && ok; c.next(a), ++tl) {
+        const int ab = tl & (accs - 1), turn = tl / accs;
+        const long long q0 = first_step(c.sp), q1 = last_step(c.sp);
+        if (turn > 0 && !mbar_wait(&acce[ab], (turn - 1) & 1, kWaitLimit)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (long long q = c.q0; q < c.q1; ++q, ++i) {
+        for (long long q = q0; q < q1; ++q, ++i) {
           const int s = i % kStages;
           if (!mbar_wait(&full[s], (i / kStages) & 1, kWaitLimit) || *abort_flag) {
             ok = false;
@@ -364,7 +383,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
             // 16 k: 32 bytes of every line (k contiguous), or 16 lines; boxes of 64 m or n are 8 KB apart
             const uint64_t ad = FA::KM ? tc_desc(sa + ks * 32, 16) : tc_desc(sa + ks * 2048, 8192);
             const uint64_t bd = BKM ? tc_desc(sb + ks * 32, 16) : tc_desc(sb + ks * 2048, 8192);
-            umma_bf16(tmem + ab * kNBMax, ad, bd, idesc, (q > c.q0 || ks > 0) ? 1u : 0u);
+            umma_bf16(tmem + ab * acc_cols, ad, bd, idesc, (q > q0 || ks > 0) ? 1u : 0u);
           }
           umma_commit(&empty[s]);
         }
@@ -385,20 +404,31 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
     const bool split = a.part != nullptr, scaled = C::kCols && !split;
     const int type = split ? DISCO_F32 : a.out_type, eb = type == DISCO_F32 ? 4 : 2;
     const bool h16 = type == DISCO_F16;
+    // chunks of 32 columns; where two warps share the lanes, every second chunk, or all of every second tile
+    const int half = warp >> 2, c00 = turns ? 0 : half * 32, step = turns ? 32 : 8 * kEpiWarps;
     int tl = 0;
-    for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++tl) {
-      const Tile c = tile_of(t);
-      const int ab = tl & 1;
-      const long long row0 = c.m0 + q4 * 32;
-      // chunks of 32 columns, every second one where two warps share the lanes
-      constexpr int kStep = 8 * kEpiWarps;
-      float rs = 1.0f;
-      if (scaled) {
-        for (int n = lane; n < a.NB; n += 32) cs[n] = c.n0 + n < a.m.N ? __ldg(a.m.cs + c.n0 + n) : 0.0f;
-        if (row0 + lane < a.m.M) rs = __ldg(a.m.rs + c.z * a.m.rs_z + row0 + lane);
+    Walk c(a);
+    if (turns && half) c.next(a), ++tl;
+    auto row_scale = [&](const Walk& w) {
+      const long long row = w.m0() + q4 * 32 + lane;
+      return scaled && w.in(a) && row < a.m.M ? __ldg(a.m.rs + w.z * a.m.rs_z + row) : 1.0f;
+    };
+    float rs, rs_next = row_scale(c);
+    int cs_n = -1;  // the n tile whose scales are held
+    while (c.in(a)) {
+      const int ab = tl & (accs - 1);
+      const long long row0 = c.m0() + q4 * 32, n0 = c.n0(a);
+      Walk next = c;
+      next.next(a);
+      if (turns) next.next(a);
+      rs = rs_next;
+      rs_next = row_scale(next);  // a tile ahead
+      if (scaled && cs_n != c.n) {
+        for (int n = lane; n < a.NB; n += 32) cs[n] = n0 + n < a.m.N ? __ldg(a.m.cs + n0 + n) : 0.0f;
+        cs_n = c.n;
         __syncwarp();
       }
-      bool fin = mbar_wait(&accf[ab], (tl >> 1) & 1, kWaitLimit);
+      bool fin = mbar_wait(&accf[ab], (tl / accs) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
       if (!fin) {
         if (lane == 0) i8_flag();
@@ -407,14 +437,14 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       }
       tc_fence_after();
       const int rows = (int)min(a.m.M - row0, 32LL);  // may be negative
-      const int cols = (int)min(a.m.N - c.n0, (long long)a.NB);
+      const int cols = (int)min(a.m.N - n0, (long long)a.NB);
       const long long slice = (c.sp * (long long)a.m.Z + c.z) * a.m.M * a.m.N;
       // first of this warp's outputs; rows of the output are n (TR) or m
-      uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) + (slice + (TR ? c.n0 * a.m.M + row0 : row0 * a.m.N + c.n0)) * eb;
+      uint8_t* out = (uint8_t*)(split ? (void*)a.part : a.m.out) + (slice + (TR ? n0 * a.m.M + row0 : row0 * a.m.N + n0)) * eb;
       const long long pitch = (TR ? a.m.M : a.m.N) * eb;
-      for (int c0 = (warp >> 2) * 32; c0 < cols && rows > 0; c0 += kStep) {
+      for (int c0 = c00; c0 < cols && rows > 0; c0 += step) {
         uint32_t v[32];
-        tmem_ld32(tmem + ab * kNBMax + ((uint32_t)(q4 * 32) << 16) + c0, v);
+        tmem_ld32(tmem + ab * acc_cols + ((uint32_t)(q4 * 32) << 16) + c0, v);
         if (scaled) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -516,6 +546,8 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acce[ab]);
+      c = next;
+      tl += turns ? 2 : 1;
     }
   }
   tc_fence_before();
