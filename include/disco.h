@@ -506,7 +506,12 @@ DISCO_API int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, f
    Activations are kept in 8-bit integers with an fp32 scale for each token,
    weights W [Cout, Cin] with one for each output channel.  The 8-bit
    activation serves the product and, kept in place of the 16-bit one, the
-   gradients. */
+   gradients.
+   The products and gradients take up to 2^31 - 1 pixels and a sample of less
+   than 2^40 bytes in 16 bits (DISCO_ERR_UNSUPPORTED beyond).  Their workspace
+   holds the weight (or a few rows) in 16 bits, the sums of a split reduction,
+   and a copy of every operand whose rows do not start on 16 bytes (an odd
+   number of pixels, or of features for P = 1). */
 
 /* The tokens of an activation in 8-bit integers:
      a[b,p] = max(1e-30, max_c |x[b,c,p]|),  scale[b,p] = a / 127
@@ -558,7 +563,9 @@ DISCO_API int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const fl
                                          int32_t Cin, int32_t Cout, int64_t P, disco_dtype dtype, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
-/* SiLU: g / (1 + exp(-g)).  GELU: g Phi(g), Phi the normal distribution. */
+/* SiLU: g / (1 + exp(-g)).  GELU: g Phi(g), Phi the normal distribution.  With
+   bf16 and fp16 tensors the SiLU takes the approximate exponential and
+   reciprocal (2^-21 and 2^-23 |g| relative), and gates below -87 give 0. */
 typedef enum { DISCO_SILU = 0, DISCO_GELU = 1 } disco_activation;
 
 /* Gated activation of x [B, 2 C, P], its gates in the first C channels:

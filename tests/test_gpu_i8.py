@@ -33,7 +33,7 @@ def _randn(g, *shape):
 # tokens: one, rows with and without whole words, grids, odd grids, few and many channels
 TOKENS = [(1, 1, 1), (1, 512, 1), (3, 17, 1), (33, 100, 1), (130, 256, 1), (5, 1365, 1), (2, 4097, 1), (2, 9000, 1), (1, 16384, 1),
           (1, 1, 2), (2, 5, 7), (1, 3, 64), (3, 16, 128), (2, 80, 181), (1, 64, 33 * 65), (2, 130, 1000), (1, 700, 96), (1, 2050, 40), (4, 9, 4099),
-          (1, 5000, 24), (1, 520, 33)]
+          (1, 5000, 24), (1, 520, 33), (1, 900, 301), (1, 1700, 77), (2, 40, 1001), (1, 7500, 16), (1, 1200, 200), (2, 6, 1030)]
 
 
 def _x(shape, dtype, seed=0):
@@ -250,7 +250,7 @@ def test_gradients_are_those_of_differences(lib):
 # ------------------------------------------------------------------ gated activation
 
 GLU = [(1, 1, 1), (1, 512, 1), (3, 17, 1), (33, 100, 1), (130, 256, 1), (5, 1365, 1), (2, 4097, 1), (1, 12000, 1), (1, 1, 2), (2, 5, 7), (3, 16, 128), (2, 80, 181),
-       (2, 130, 1000), (1, 700, 96), (1, 3000, 24), (1, 300, 33)]
+       (2, 130, 1000), (1, 700, 96), (1, 3000, 24), (1, 300, 33), (1, 600, 200), (1, 1100, 40), (2, 6, 1032), (1, 4000, 16)]
 
 
 @pytest.mark.parametrize("dtype", ALL, ids=ids)
@@ -338,6 +338,24 @@ def test_glu_special_values(lib, dtype, P):
         assert torch.isnan(yc[1, 0, P - 1]) and torch.isnan(s[1, P - 1])
         if P > 1:
             assert bool((yc[:, :, 1:P - 1] == 0).all()) and bool((s[:, 1:P - 1] < 1e-30).all())
+
+
+@pytest.mark.parametrize("dtype", ALL, ids=ids)
+def test_masked_pixels_and_extreme_tokens_beside_ordinary_ones(lib, dtype):
+    """Pixels of zeros, of the largest and of the smallest magnitudes in one tile with ordinary ones."""
+    B, C, P = 2, 24, 136
+    x = _x((B, C, P), dtype, 7)
+    x[:, :, 3::7] = 0
+    x[0, :, 5] *= torch.finfo(dtype).max / 1e3 / x[0, :, 5].abs().max().clamp_min(1) if dtype != HF else 8
+    x[1, :, 9] = (x[1, :, 9].float() * 1e-25).to(dtype)
+    q, s = torch.empty((B, C, P), dtype=torch.int8, device="cuda"), torch.empty((B, P), device="cuda")
+    for pixels in (P, P - 3):
+        v = x[:, :, :pixels].contiguous()
+        qv, sv = q.view(-1)[:v.numel()].view(v.shape), s.view(-1)[:B * pixels].view(B, pixels)
+        lib.disco_quant_i8(v.cuda(), qv, sv, B, C, pixels)
+        want, scale = r.quant64(v)
+        assert torch.equal(qv.cpu().double(), want)
+        r.assert_close(sv, scale, scale * 2 * r.U32, "scale")
 
 
 # ------------------------------------------------------------------ calls

@@ -60,6 +60,15 @@ def test_types_and_pointers_are_checked_before_the_device(lib):
     assert so.disco_glu_bwd(P, P, P, P, -1, 2, 8, 4, 1, None) == -2
 
 
+def test_limits_of_the_products(lib):
+    so = lib.load_library()
+    for args in ((1, 8, 8, 1 << 31), (1, 1 << 20, 8, 1 << 21), (1, 1 << 21, 1 << 20, 1)):
+        assert set(_products(so, args, 1).values()) == {-2}
+        for name in ("disco_matmul_i8", "disco_matmul_i8_bwd_input", "disco_matmul_i8_bwd_weight"):
+            assert getattr(lib, name + "_workspace_bytes")(*args) == 0
+    assert lib.disco_matmul_i8_workspace_bytes(1, 8, 8, (1 << 31) - 1) > 0
+
+
 def test_workspace_is_checked_before_the_device(lib):
     so = lib.load_library()
     for args in ((1, 8, 8, 1), (3, 80, 77, 65341), (96, 2048, 2048, 1), (2, 128, 256, 259920)):
