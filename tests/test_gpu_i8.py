@@ -143,7 +143,8 @@ def test_matmul_gradients(lib, shape, dtype):
 
 @pytest.mark.parametrize("dtype", HALF, ids=ids)
 @pytest.mark.parametrize("shape", [(2, 128, 256, 16400), (2, 128, 256, 16401), (6000, 512, 384, 1), (6001, 515, 391, 1), (1, 1024, 520, 4112),
-                                   (3, 80, 77, 9999), (1, 4096, 1000, 1), (40, 8200, 136, 1)], ids=ids)
+                                   (3, 80, 77, 9999), (1, 4096, 1000, 1), (40, 8200, 136, 1), (20000, 512, 256, 1), (2, 515, 300, 9001),
+                                   (20001, 300, 520, 1)], ids=ids)
 def test_many_steps_and_tiles(lib, shape, dtype):
     """Reductions of many steps, split or not, over many tiles: the rings of shared
     memory go round often.  Five runs give the same bits."""
@@ -172,6 +173,17 @@ def test_many_steps_and_tiles(lib, shape, dtype):
     r.assert_close(dx, *cpu(want, r.grad_bound(want, S, D, Cout, dtype)), "dx")
     want, S, D = r.bwd_weight64(dy, q, scale)
     r.assert_close(dW, *cpu(want, r.grad_bound(want, S, D, B * P, dtype)), "dW")
+
+
+@pytest.mark.parametrize("shape", [(20000, 512, 256, 1), (20001, 100, 250, 1), (2, 128, 256, 16400), (2, 128, 256, 16401), (1, 64, 700, 7000)], ids=ids)
+def test_large_products_in_32_bits(lib, shape):
+    B, Cin, Cout, P = shape
+    q, scale, W, wscale, _ = [t.cuda() for t in _operands(shape, F32)]
+    y, ok = r.guarded((B, Cout, P), F32)
+    lib.disco_matmul_i8(q, scale, W, wscale, y, *shape, _ws(lib.disco_matmul_i8_workspace_bytes(*shape, lib.DISCO_F32)))
+    want, S = r.matmul64(q, scale, W, wscale)
+    r.assert_close(y, want.cpu(), r.matmul_bound(want, S, scale, wscale, Cin, F32).cpu(), "y")
+    ok()
 
 
 @pytest.mark.parametrize("P", [1, 37, 64])
