@@ -31,7 +31,8 @@ SOURCES = ["disco_capi.cu", "disco_psi.cu", "disco_contract.cu", "disco_fused.cu
            "disco_fwd_tc.cu", "disco_bwd_tc.cu", "disco_gemm_tc.cu", "disco_host.cu",
            "disco_norm.cu", "disco_norm_tile.cu", "disco_norm_q.cu", "disco_norm_q_any.cu", "disco_norm_bwd.cu",
            "disco_norm_rows.cu", "disco_dequant.cu", "disco_grad.cu",
-           "disco_tokens.cu", "disco_i8_mm.cu", "disco_i8_fwd.cu", "disco_i8_dx.cu", "disco_i8_dw.cu"]
+           "disco_tokens.cu", "disco_tokens_grid.cu", "disco_tokens_odd.cu", "disco_tokens_rows.cu",
+           "disco_i8_mm.cu", "disco_i8_fwd.cu", "disco_i8_dx.cu", "disco_i8_dw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -842,7 +842,8 @@ extern "C" int disco_device_status(int32_t* flags, int32_t clear) {
   int32_t bounds = 0;
   for (auto fn : {contract_bounds, psi_bounds, tc_bounds, btc_bounds, gemm_bounds, fused_bounds, norm_bounds,
                   norm_tile_bounds, norm_q_bounds, norm_q_any_bounds, norm_bwd_bounds, norm_rows_bounds,
-                  dequant_bounds, grad_bounds, tokens_bounds, i8_mm_bounds,
+                  dequant_bounds, grad_bounds, tokens_bounds, tokens_grid_bounds,
+                  tokens_grid_odd_bounds, tokens_rows_bounds, i8_mm_bounds,
                   i8_fwd_bounds, i8_dx_bounds, i8_dw_bounds})
     if (e == cudaSuccess) e = fn(&bounds, clear != 0);
   *flags |= bounds;

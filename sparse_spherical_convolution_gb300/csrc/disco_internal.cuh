@@ -112,6 +112,9 @@ cudaError_t norm_bwd_bounds(int32_t* v, bool clear);
 cudaError_t dequant_bounds(int32_t* v, bool clear);
 cudaError_t grad_bounds(int32_t* v, bool clear);
 cudaError_t tokens_bounds(int32_t* v, bool clear);
+cudaError_t tokens_grid_bounds(int32_t* v, bool clear);
+cudaError_t tokens_grid_odd_bounds(int32_t* v, bool clear);
+cudaError_t tokens_rows_bounds(int32_t* v, bool clear);
 cudaError_t i8_mm_bounds(int32_t* v, bool clear);
 cudaError_t i8_fwd_bounds(int32_t* v, bool clear);
 cudaError_t i8_dx_bounds(int32_t* v, bool clear);

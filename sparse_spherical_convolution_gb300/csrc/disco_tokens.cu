@@ -76,48 +76,24 @@ __global__ void __launch_bounds__(kAnyThreads) tokens_any_kernel(const TokenArgs
   }
 }
 
-// J words to a thread: few while the channels leave a tile rows of 64 bytes (many
-// CTAs to an SM), else twice as many.
-template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
-int held(const TokenArgs& a, cudaStream_t st) {
-  constexpr int most = kTokenThreads / (V > 1 ? 4 : 16) * J;  // channels
-  if (a.P == 1 ? a.C <= kTokenThreads * J * V : a.C <= most) return tokens_held<T, V, J, GLU, XQ, YQ>(a, st);
-  return tokens_held<T, V, 2 * J, GLU, XQ, YQ>(a, st);
-}
-template <typename T, int V>
-int held(const TokenArgs& a, bool glu, cudaStream_t st) {
-  constexpr int M = V == 1 ? 2 : 1;
-  if (!glu) return held<T, V, 8 * M, false, true, false>(a, st);
-  if (a.xq && a.q) return held<T, V, 2 * M, true, true, true>(a, st);
-  if (a.xq) return held<T, V, 4 * M, true, true, false>(a, st);
-  if (a.q) return held<T, V, 4 * M, true, false, true>(a, st);
-  return tokens_held<T, V, 4, true, false, false>(a, st);
-}
-
-template <typename T>
-int grid(const TokenArgs& a, bool glu, cudaStream_t st) {
-  if (!glu) return tokens_tiles<T, false, true, false>(a, st);
-  if (a.xq && a.q) return tokens_tiles<T, true, true, true>(a, st);
-  if (a.xq) return tokens_tiles<T, true, true, false>(a, st);
-  if (a.q) return tokens_tiles<T, true, false, true>(a, st);
-  return tokens_tiles<T, true, false, false>(a, st);
-}
-
 template <typename T, bool GLU>
-int tokens(const TokenArgs& a, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const bool whole = (a.P == 1 ? a.C : a.P) % V == 0;
-  if (!whole && a.P > 1 && !GLU) {
-    const int rc = tokens_skewed<T>(a, st);
-    if (rc != DISCO_ERR_UNSUPPORTED) return rc;
-  }
-  const int rc = !whole ? held<T, 1>(a, GLU, st) : a.P == 1 ? held<T, V>(a, GLU, st) : grid<T>(a, GLU, st);
-  if (rc != DISCO_ERR_UNSUPPORTED) return rc;
+int any(const TokenArgs& a, cudaStream_t st) {
   const long long tiles = a.P == 1 ? a.B : a.B * ((a.P + 31) / 32);
   const int ctas = (int)min(tiles, (long long)kSMs * 8);
   if (a.P == 1) tokens_any_kernel<T, true, GLU><<<ctas, kAnyThreads, 0, st>>>(a, tiles);
   else tokens_any_kernel<T, false, GLU><<<ctas, kAnyThreads, 0, st>>>(a, tiles);
   return check_launch("tokens_any_kernel");
+}
+
+int tokens(const TokenArgs& a, bool glu, disco_dtype dtype, cudaStream_t st) {
+  int rc = DISCO_ERR_UNSUPPORTED;
+  if (a.P > 1) rc = a.P % (16 / elem_bytes(dtype)) == 0 ? tokens_grid(a, glu, dtype, st) : tokens_grid_odd(a, glu, dtype, st);
+  if (rc == DISCO_ERR_UNSUPPORTED) rc = tokens_held(a, glu, dtype, st);
+  if (rc != DISCO_ERR_UNSUPPORTED) return rc;
+#define CALL(T) rc = glu ? any<T, true>(a, st) : any<T, false>(a, st)
+  DISCO_BY_DTYPE(dtype, CALL)
+#undef CALL
+  return rc;
 }
 
 // ---- gradient of the gated activation at the checkpoint --------------------
@@ -131,6 +107,33 @@ struct GluBwdArgs {
   long long P, n;  // n = B C P elements of dy
 };
 
+// The gradients of a word's gates and values.
+template <typename T, int V>
+__device__ __forceinline__ void glu_bwd_word(const typename Word<V>::type& wg, const typename Word<V>::type& wv, const Raw<T, V>& wd, const float (&s)[V],
+                                             int act, F<V>* dg, F<V>* dv) {
+  uint32_t qg[(V + 3) / 4] = {}, qv[(V + 3) / 4] = {};
+  memcpy(qg, &wg, V);
+  memcpy(qv, &wv, V);
+  const F<V> d = unpack<T, V>(wd);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float g = from_byte(qg[e / 4] ^ 0x80808080u, e & 3) * s[e], v = from_byte(qv[e / 4] ^ 0x80808080u, e & 3) * s[e];
+    float val;
+    const float der = act_grad<T>(g, act, &val);
+    dg->v[e] = d.v[e] * v * der;
+    dv->v[e] = d.v[e] * val;
+  }
+}
+
+// The word of V bytes at `at` of a tensor that ends within it.
+template <int V>
+__device__ __forceinline__ void memcpy_tail(void* w, const int8_t* x, long long at, long long total) {
+  uint8_t v[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = at + e < total ? (uint8_t)x[at + e] : 0;
+  memcpy(w, v, V);
+}
+
 // Words of V neighbouring elements; a word is inside one channel's pixels (grids:
 // V divides P) or one row's gates (rows: V divides C).  ROW: P = 1.
 template <typename T, int V, bool ROW>
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(256) glu_bwd_kernel(const GluBwdArgs a) {
   const long long r = i - b * CP, g0 = 2 * b * CP + r;
   float s[V];
   const WQ wg = load_stream<WQ>(a.xq + g0), wv = load_stream<WQ>(a.xq + g0 + CP);
-  const F<V> d = unpack<T, V>(load_stream<Raw<T, V>>((const T*)a.dy + i));
+  const Raw<T, V> wd = load_stream<Raw<T, V>>((const T*)a.dy + i);
   if constexpr (ROW) {
 #pragma unroll
     for (int e = 0; e < V; ++e) s[e] = a.xscale[b];
@@ -159,20 +162,60 @@ __global__ void __launch_bounds__(256) glu_bwd_kernel(const GluBwdArgs a) {
       s[0] = a.xscale[b * a.P + p];
     }
   }
-  uint32_t qg[(V + 3) / 4] = {}, qv[(V + 3) / 4] = {};
-  memcpy(qg, &wg, V);
-  memcpy(qv, &wv, V);
   F<V> dg, dv;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float g = from_byte(qg[e / 4] ^ 0x80808080u, e & 3) * s[e], v = from_byte(qv[e / 4] ^ 0x80808080u, e & 3) * s[e];
-    float val;
-    const float der = act_grad<T>(g, a.act, &val);
-    dg.v[e] = d.v[e] * v * der;
-    dv.v[e] = d.v[e] * val;
-  }
+  glu_bwd_word<T, V>(wg, wv, wd, s, a.act, &dg, &dv);
   store_stream((T*)a.dx + g0, packed<T, V>(dg));
   store_stream((T*)a.dx + g0 + CP, packed<T, V>(dv));
+}
+
+// Grids where V does not divide P: a warp takes 32 V pixels of a channel; aligned words are
+// shifted to pixels on the way in and back on the way out (disco_tokens.cuh).
+// [2,128,361x719] bf16: 176 us; one pixel to a thread 304.
+template <typename T>
+__global__ void __launch_bounds__(256) glu_bwd_odd_kernel(const GluBwdArgs a, const long long per_row, const long long units) {
+  constexpr int ES = (int)sizeof(T), V = 16 / ES;
+  using WQ = typename Word<V>::type;
+  const int lane = threadIdx.x & 31;
+  const long long unit = blockIdx.x * 8LL + threadIdx.x / 32;
+  if (unit >= units) return;  // the whole warp
+  const long long row = units <= 0xffffffffLL ? (long long)((uint32_t)unit / (uint32_t)per_row) : unit / per_row;
+  const long long b = row / a.C, pos = (unit - row * per_row) * (32 * V), half = a.C * a.P;
+  const int N = (int)min(32LL * V, a.P - pos), nv = min(V, N - lane * V);
+  const long long y0 = row * a.P + pos, g0 = y0 + b * half, p = pos + lane * V;  // dy's first element, the gate's
+  WQ wg = {}, wv = {};
+  uint4 wd = make_uint4(0, 0, 0, 0);
+  float s[V] = {};
+  if (nv > 0) {
+    auto q8 = [&](long long k) {  // V integers from element k on
+      const int m = (int)k & (V - 1);
+      const long long at = k - m;
+      WQ lo = {}, hi = {};
+      if (at + V <= 2 * a.n) lo = load_stream<WQ>(a.xq + at);
+      else memcpy_tail<V>(&lo, a.xq, at, 2 * a.n);
+      if (m + nv > V) {
+        if (at + 2 * V <= 2 * a.n) hi = load_stream<WQ>(a.xq + at + V);
+        else memcpy_tail<V>(&hi, a.xq, at + V, 2 * a.n);
+      }
+      uint32_t u[V / 2 + 1] = {};
+      memcpy(u, &lo, V);
+      memcpy(u + V / 4, &hi, V);
+      if (V == 8 && (m & 4)) u[0] = u[1], u[1] = u[2], u[2] = u[3];
+      uint32_t o[V / 4];
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], 8 * (m & 3));
+      WQ w;
+      memcpy(&w, o, V);
+      return w;
+    };
+    wg = q8(g0 + lane * V), wv = q8(g0 + half + lane * V);
+    wd = load_px<T, V>((const T*)a.dy, y0 + lane * V, nv, a.n);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = e < nv ? a.xscale[b * a.P + p + e] : 0.0f;
+  }
+  F<V> dg, dv;
+  glu_bwd_word<T, V>(wg, wv, wd, s, a.act, &dg, &dv);
+  store_px<V>(a.dx, g0, packed<T, V>(dg), lane, 32, N, true);
+  store_px<V>(a.dx, g0 + half, packed<T, V>(dv), lane, 32, N, true);
 }
 
 template <typename T, int V>
@@ -182,6 +225,15 @@ int glu_bwd(const GluBwdArgs& a, cudaStream_t st) {
   if (a.P == 1) glu_bwd_kernel<T, V, true><<<(unsigned)grid, 256, 0, st>>>(a);
   else glu_bwd_kernel<T, V, false><<<(unsigned)grid, 256, 0, st>>>(a);
   return check_launch("glu_bwd_kernel");
+}
+
+template <typename T>
+int glu_bwd_odd(const GluBwdArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const long long per_row = (a.P + 32 * V - 1) / (32 * V), units = a.n / a.P * per_row, grid = (units + 7) / 8;
+  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^39 elements");
+  glu_bwd_odd_kernel<T><<<(unsigned)grid, 256, 0, st>>>(a, per_row, units);
+  return check_launch("glu_bwd_odd_kernel");
 }
 
 int check_act(int32_t kind) {
@@ -208,10 +260,7 @@ extern "C" int disco_quant_i8(const void* x, void* q, float* scale, int32_t B, i
   const unsigned in_place[] = {0};
   if ((rc = check_buffers(in, in_place, 1, out, 2))) return rc;
   const TokenArgs a{x, nullptr, nullptr, nullptr, (int8_t*)q, scale, DISCO_SILU, B, C, P};
-#define CALL(T) rc = tokens<T, false>(a, (cudaStream_t)stream)
-  DISCO_BY_DTYPE(dtype, CALL)
-#undef CALL
-  return rc;
+  return tokens(a, false, dtype, (cudaStream_t)stream);
 }
 
 extern "C" int disco_glu(const void* x, void* y, void* q, float* scale, void* xq, float* xscale, disco_activation act,
@@ -231,10 +280,7 @@ extern "C" int disco_glu(const void* x, void* y, void* q, float* scale, void* xq
   const unsigned in_place[] = {0};
   if ((rc = check_buffers(in, in_place, 1, out, 5))) return rc;
   const TokenArgs a{x, y, (int8_t*)q, scale, (int8_t*)xq, xscale, act, B, C, P};
-#define CALL(T) rc = tokens<T, true>(a, (cudaStream_t)stream)
-  DISCO_BY_DTYPE(dtype, CALL)
-#undef CALL
-  return rc;
+  return tokens(a, true, dtype, (cudaStream_t)stream);
 }
 
 extern "C" int disco_glu_bwd(const void* dy, const void* xq, const float* xscale, void* dx, disco_activation act, int32_t B,
@@ -253,6 +299,7 @@ extern "C" int disco_glu_bwd(const void* dy, const void* xq, const float* xscale
   const GluBwdArgs a{dy, (const int8_t*)xq, xscale, dx, act, C, P, (long long)n};
 #define CALL(T)                                                                          \
   if ((P == 1 ? C : P) % (16 / (int)sizeof(T)) == 0) rc = glu_bwd<T, 16 / (int)sizeof(T)>(a, (cudaStream_t)stream); \
+  else if (P >= 64) rc = glu_bwd_odd<T>(a, (cudaStream_t)stream);                        \
   else rc = glu_bwd<T, 1>(a, (cudaStream_t)stream)
   DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL

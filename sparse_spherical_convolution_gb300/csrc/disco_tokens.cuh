@@ -3,11 +3,12 @@
 // (disco_quant_i8, disco_glu).  Not part of the ABI.
 //
 // A token's C values are dealt over the threads of one CTA.
-//   tokens_tile_kernel   grids, V pixels (16 bytes) to a word, V divides P: words in shared memory
+//   tokens_tile_kernel   grids, V pixels (16 bytes) to a word: words in shared memory.  Where V does not
+//                        divide P (ODD), aligned words are shifted on the way in and out
+//   tokens_skew_kernel   quantisation where V does not divide P: aligned words as they are, which
+//                        are not pixels ([1,512,259199] 118 us; shifted 192)
 //   tokens_rows_kernel   rows (P = 1), J words of neighbouring channels to a thread, in registers
-//   tokens_skew_kernel   the same where V does not divide P (quantisation): aligned words,
-//                        which are not pixels
-//   tokens_pixel_kernel  what these do not take: one pixel of J channels to a thread
+//   tokens_pixel_kernel  grids of more channels than the tiles hold: one pixel of J channels to a thread
 // Bound by HBM where a thread has 16 to 32 words and three CTAs or more share an SM: one
 // loads while another rounds.  Measured (GB300, bf16): quantisation of [1,512,360x720]
 // 76 us, 5.2 TB/s; the same tile three deep in one CTA of 512 threads 117.
@@ -329,7 +330,75 @@ __device__ __forceinline__ void quantize_word(uint32_t (&r)[V], const F<V>& x, c
   }
 }
 
-template <typename T, bool GLU, bool XQ, bool YQ>
+// V elements from element k on (nv of them wanted, zeros behind) of a tensor of `total`.
+template <typename T, int V>
+__device__ __forceinline__ uint4 load_px(const T* x, long long k, int nv, long long total) {
+  constexpr int ES = (int)sizeof(T);
+  const int m = (int)k & (V - 1);
+  auto word = [&](long long at) {
+    if (at + V <= total) return load_stream<uint4>(x + at);
+    T v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = at + e < total ? x[at + e] : from_f32<T>(0.0f);
+    uint4 w;
+    memcpy(&w, v, 16);
+    return w;
+  };
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  if (nv > 0 && DISCO_IN_BOUNDS(k - m >= 0 && k + nv <= total)) {
+    lo = word(k - m);
+    if (m + nv > V) hi = word(k - m + V);
+  }
+  return shifted(lo, hi, m * ES, nv * ES);
+}
+
+// The V pixels of each of LX lanes to a row that starts at element k, m past a word: N
+// pixels of the tile.  Lanes put together aligned words from their own and their neighbour's
+// pixels; the V pixels in words that another tile shares go out one to a lane.  All
+// lanes of the warp call it; `has`: the row is there.
+template <int V, typename W>
+__device__ __forceinline__ void store_px(void* base, long long k, W word, int lx, int LX, int N, bool has) {
+  constexpr int NW = (int)sizeof(W) / 4, ES = (int)sizeof(W) / V;
+  using E = typename Word<ES>::type;
+  const int m = (int)k & (V - 1);
+  uint32_t w[NW], u[2 * NW + 1];
+  memcpy(w, &word, sizeof(W));
+#pragma unroll
+  for (int i = 0; i < NW; ++i) u[i] = __shfl_up_sync(0xffffffffu, w[i], 1, LX), u[NW + i] = w[i];
+  u[2 * NW] = 0;
+  E* d = (E*)base + k;
+  if (N == LX * V) {
+    const int off = (V - m) * ES;  // where the aligned word starts in the neighbour's bytes and these
+    // by whole words, then by bytes
+#pragma unroll
+    for (int step = NW; step >= 1; step /= 2)
+      if (off / 4 & step) {
+#pragma unroll
+        for (int i = 0; i + step < 2 * NW + 1; ++i) u[i] = u[i + step];
+      }
+    uint32_t o[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) o[i] = ES % 4 ? __funnelshift_r(u[i], u[i + 1], 8 * (off & 3)) : u[i];
+    memcpy(&word, o, sizeof(W));
+    if (has && (lx > 0 || m == 0)) store_stream(d - m + lx * V, word);
+    const int e = lx & (V - 1), from = e < V - m ? 0 : LX - 1;
+    uint32_t one = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const uint32_t x = __shfl_sync(0xffffffffu, w[i], from, LX);
+      one = e * ES / 4 == i ? x : one;
+    }
+    if (has && m > 0 && lx < V) d[from * V + e] = (E)(one >> (8 * (e * ES & 3)));
+  } else if (has) {
+    E v[V];
+    memcpy(v, &word, sizeof(W));
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (lx * V + e < N) d[lx * V + e] = v[e];
+  }
+}
+
+template <typename T, bool GLU, bool XQ, bool YQ, bool ODD>
 __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenArgs a, const TileCut g) {
   constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kOwnY = XQ ? 2 : 0, kOwn = kOwnY + (YQ ? 2 : 0);
   using R = Raw<T, V>;
@@ -343,9 +412,42 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
   const long long P = a.P, half = a.C * P, step = NL * P, row0 = j0 * P;  // from one of its channels to the next; its first
   for (long long t = blockIdx.x; t < g.tiles; t += gridDim.x) {
     const long long b = g.tiles <= 0xffffffffLL ? (long long)((uint32_t)t / (uint32_t)g.per_sample) : t / g.per_sample;
-    const long long p = (t - b * g.per_sample) * TP + lx * V, y0 = b * half + p;
-    const int n = p < P && DISCO_IN_BOUNDS(b < a.B && p + V <= P) ? nj : 0;
-    {
+    const long long pos = (t - b * g.per_sample) * TP, p = pos + lx * V, y0 = b * half + p;
+    const int N = (int)min((long long)TP, P - pos);  // pixels of the tile
+    const bool live = p < P && DISCO_IN_BOUNDS(b < a.B);
+    const int n = live ? nj : 0;
+    const int loops = ODD ? g.nj : n;  // stores off alignment are the whole warp's
+    if constexpr (ODD) {
+      const long long k0 = b * G * half + p + row0, total = (long long)a.B * G * half;
+      const int nv = min(V, N - lx * V);
+      if (b + 1 < a.B || pos + TP + V <= P) {
+        // both words of every row end inside the tensor: no tests between the loads, eight of them in flight
+        constexpr int U = 4 / G;
+        for (int i0 = 0; i0 < n; i0 += U) {
+          uint4 lo[U][G], hi[U][G];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+              const long long k = k0 + min(i0 + u, n - 1) * step + h * half;
+              const T* x = (const T*)a.x + (k & ~(long long)(V - 1));
+              if (DISCO_IN_BOUNDS(k >= 0 && (k & ~(long long)(V - 1)) + 2 * V <= total)) lo[u][h] = load_stream<uint4>(x), hi[u][h] = load_stream<uint4>(x + V);
+            }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < G; ++h)
+              if (i0 + u < n) {
+                const int m = (int)(k0 + (i0 + u) * step + h * half) & (V - 1);
+                w[((i0 + u) * G + h) * NT] = shifted(lo[u][h], hi[u][h], m * ES, nv * ES);
+              }
+        }
+      } else {
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+          for (int h = 0; h < G; ++h) w[(i * G + h) * NT] = load_px<T, V>((const T*)a.x, k0 + i * step + h * half, nv, total);
+      }
+    } else {
       const T* x = (const T*)a.x + b * G * half + p + row0;
       uint4* d = w;
 #pragma unroll 4
@@ -363,14 +465,15 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
     for (int e = 0; e < V; ++e) my[e] = 0;
     {
       uint4* s = w;
-      T* yo = (T*)a.y + y0 + row0;
+      long long yo = y0 - lx * V * ODD + row0;
       auto first = [&](auto kind) {  // the activation's kind is known in the loop
 #pragma unroll 4
-        for (int i = 0; i < n; ++i, s += G * NT) {
-          const uint4 w0 = s[0];
+        for (int i = 0; i < loops; ++i, s += G * NT) {
+          const bool has = !ODD || i < n;
+          const uint4 zero = make_uint4(0, 0, 0, 0), w0 = has ? s[0] : zero;
           if constexpr (XQ) mx.add(w0);
           if constexpr (GLU) {
-            const uint4 w1 = s[NT];
+            const uint4 w1 = has ? s[NT] : zero;
             if constexpr (XQ) mx.add(w1);
             R r0, r1;
             memcpy(&r0, &w0, 16);
@@ -380,11 +483,17 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
 #pragma unroll
               for (int e = 0; e < V; ++e) my[e] = __float_as_uint(max_abs(__uint_as_float(my[e]), v.v[e]));
               if constexpr (!XQ) {  // y over its gate and value
-                s[0] = *reinterpret_cast<const uint4*>(v.v);
-                if constexpr (V == 8) s[NT] = *reinterpret_cast<const uint4*>(v.v + 4);
+                if (has) {
+                  s[0] = *reinterpret_cast<const uint4*>(v.v);
+                  if constexpr (V == 8) s[NT] = *reinterpret_cast<const uint4*>(v.v + 4);
+                }
               }
             }
-            if (a.y) store_stream(yo, packed<T, V>(v)), yo += step;
+            if (a.y) {
+              if constexpr (ODD) store_px<V>(a.y, yo, packed<T, V>(v), lx, g.LX, N, i < nj);
+              else store_stream((T*)a.y + yo, packed<T, V>(v));
+              yo += step;
+            }
           }
         }
       };
@@ -450,17 +559,18 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
       const F<V> inv = norm::load_row<V>(own + lx * V), minus_a = norm::load_row<V>(own + TP + lx * V);
       auto second = [&](auto is_plain) {
         const uint4* s = w;
-        int8_t* d = a.xq + G * b * half + p + row0;
+        long long d = G * b * half + (ODD ? pos : p) + row0;
 #pragma unroll 4
-        for (int i = 0; i < n; ++i, s += G * NT, d += step)
+        for (int i = 0; i < loops; ++i, s += G * NT, d += step)
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             R r0;
-            const uint4 w0 = s[h * NT];
+            const uint4 w0 = !ODD || i < n ? s[h * NT] : make_uint4(0, 0, 0, 0);
             memcpy(&r0, &w0, 16);
             uint32_t r[V];
             quantize_word<T, V, decltype(is_plain)::value>(r, unpack<T, V>(r0), inv, minus_a);
-            store_bytes<V>(d + h * half, r);
+            if constexpr (ODD) store_px<V>(a.xq, d + h * half, bytes_word<V>(r), lx, g.LX, N, i < nj);
+            else store_bytes<V>(a.xq + d + h * half, r);
           }
       };
       if (plain) second(std::true_type());
@@ -470,17 +580,20 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
       const F<V> amax = norm::load_row<V>(own + kOwnY * TP + lx * V), f = norm::load_row<V>(own + (kOwnY + 1) * TP + lx * V);
       auto third = [&](auto is_plain, auto kind) {
         const uint4* s = w;
-        int8_t* d = a.q + y0 + row0;
+        long long d = b * half + (ODD ? pos : p) + row0;
 #pragma unroll 4
-        for (int i = 0; i < n; ++i, s += G * NT, d += step) {
+        for (int i = 0; i < loops; ++i, s += G * NT, d += step) {
           F<V> v;
+          const bool has = !ODD || i < n;
+          const uint4 zero = make_uint4(0, 0, 0, 0), w0 = has ? s[0] : zero;
+          [[maybe_unused]] const uint4 w1 = (XQ || V == 8) && has ? s[NT] : zero;
           if constexpr (!XQ) {
-            *reinterpret_cast<uint4*>(v.v) = s[0];
-            if constexpr (V == 8) *reinterpret_cast<uint4*>(v.v + 4) = s[NT];
+            *reinterpret_cast<uint4*>(v.v) = w0;
+            if constexpr (V == 8) *reinterpret_cast<uint4*>(v.v + 4) = w1;
           } else {
             R r0, r1;
-            memcpy(&r0, &s[0], 16);
-            memcpy(&r1, &s[NT], 16);
+            memcpy(&r0, &w0, 16);
+            memcpy(&r1, &w1, 16);
             v = gated<T, V>(unpack<T, V>(r0), unpack<T, V>(r1), decltype(kind)::value);
           }
           uint32_t r[V];
@@ -495,7 +608,8 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
 #pragma unroll
             for (int e = 0; e < V; ++e) r[e] = quantize_y<T>(v.v[e], Quantizer(amax.v[e]));
           }
-          store_bytes<V>(d, r);
+          if constexpr (ODD) store_px<V>(a.q, d, bytes_word<V>(r), lx, g.LX, N, i < nj);
+          else store_bytes<V>(a.q + d, r);
         }
       };
       using Silu = std::integral_constant<int, DISCO_SILU>;
@@ -507,14 +621,15 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
   }
 }
 
-template <typename T, bool GLU, bool XQ, bool YQ>
+template <typename T, bool GLU, bool XQ, bool YQ, bool ODD>
 int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
   constexpr int ES = (int)sizeof(T), V = 16 / ES, G = GLU ? 2 : 1, kSum = (XQ ? ES : 0) + (YQ ? 4 : 0), kOwn = (XQ ? 2 : 0) + (YQ ? 2 : 0);
   TileCut g;
   // 128 bytes of a row to a tile, more for few channels, less for many, so that three tiles share an SM
   g.LX = 8;
   while (g.LX < 32 && G * a.C * g.LX < 1024 && g.LX * V < a.P) g.LX *= 2;
-  while (g.LX > 2 && ((size_t)G * a.C * g.LX * 16 * 3 > norm::kMaxSmem - 12 * 1024 || (long long)g.LX / 2 * V >= a.P)) g.LX /= 2;
+  // (shifted words want V lanes side by side)
+  while (g.LX > (ODD ? V : 2) && ((size_t)G * a.C * g.LX * 16 * 3 > norm::kMaxSmem - 12 * 1024 || (long long)g.LX / 2 * V >= a.P)) g.LX /= 2;
   const int share = (int)(norm::kMaxSmem / ((size_t)G * a.C * g.LX * 16 + 4096));
   g.NT = share >= 3 ? (G * a.C * g.LX <= 1024 ? 64 : 128) : share == 2 ? 256 : kTileThreads;
   g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
@@ -522,7 +637,7 @@ int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
   if (smem > norm::kMaxSmem) return DISCO_ERR_UNSUPPORTED;
   g.per_sample = (a.P + g.LX * V - 1) / (g.LX * V);
   g.tiles = g.per_sample * a.B;
-  auto kern = tokens_tile_kernel<T, GLU, XQ, YQ>;
+  auto kern = tokens_tile_kernel<T, GLU, XQ, YQ, ODD>;
   // one limit for all calls: host threads share it
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)norm::kMaxSmem) != cudaSuccess)
     return check_launch("tokens_tile_kernel attribute");
@@ -630,13 +745,12 @@ int tokens_skewed(const TokenArgs& a, cudaStream_t st) {
 // Launches the kernels above; DISCO_ERR_UNSUPPORTED, without launching, for tokens
 // that no CTA holds.
 template <typename T, int V, int J, bool GLU, bool XQ, bool YQ>
-int tokens_held(const TokenArgs& a, cudaStream_t st) {
+int held_as(const TokenArgs& a, cudaStream_t st) {
   [[maybe_unused]] constexpr int NM = (XQ ? 1 : 0) + (YQ ? 1 : 0);
   if (a.P == 1) {
     const int words = (a.C + V - 1) / V;
-    int TR = 32;
-    while (TR < kTokenThreads && TR * J < words) TR *= 2;
-    if (TR * J < words) return DISCO_ERR_UNSUPPORTED;
+    const int TR = ((words + J - 1) / J + 31) / 32 * 32;
+    if (TR > kTokenThreads) return DISCO_ERR_UNSUPPORTED;
     const int rows = max(1, 128 / TR);  // of a CTA
     tokens_rows_kernel<T, V, J, GLU, XQ, YQ><<<(a.B + rows - 1) / rows, TR * rows, 0, st>>>(a, TR);
     return check_launch("tokens_rows_kernel");
@@ -657,6 +771,24 @@ int tokens_held(const TokenArgs& a, cudaStream_t st) {
     tokens_pixel_kernel<T, J, GLU, XQ, YQ><<<(unsigned)tiles, threads, (size_t)threads / 32 * NM * g.LX * 4, st>>>(a, g);
     return check_launch("tokens_pixel_kernel");
   }
+}
+
+// By the element type, for tokens that the kernels hold (DISCO_ERR_UNSUPPORTED else): grids
+// whose P words divide, other grids, and rows or single pixels.  glu: gates and values.
+int tokens_grid(const TokenArgs& a, bool glu, disco_dtype dtype, cudaStream_t st);
+int tokens_grid_odd(const TokenArgs& a, bool glu, disco_dtype dtype, cudaStream_t st);
+int tokens_held(const TokenArgs& a, bool glu, disco_dtype dtype, cudaStream_t st);
+
+template <typename T, bool ODD>
+int tiles_of(const TokenArgs& a, bool glu, cudaStream_t st) {
+  if (!glu) {
+    if constexpr (ODD) return tokens_skewed<T>(a, st);
+    else return tokens_tiles<T, false, true, false, false>(a, st);
+  }
+  if (a.xq && a.q) return tokens_tiles<T, true, true, true, ODD>(a, st);
+  if (a.xq) return tokens_tiles<T, true, true, false, ODD>(a, st);
+  if (a.q) return tokens_tiles<T, true, false, true, ODD>(a, st);
+  return tokens_tiles<T, true, false, false, ODD>(a, st);
 }
 
 }  // namespace i8

@@ -262,7 +262,8 @@ def test_gradients_are_those_of_differences(lib):
 # ------------------------------------------------------------------ gated activation
 
 GLU = [(1, 1, 1), (1, 512, 1), (3, 17, 1), (33, 100, 1), (130, 256, 1), (5, 1365, 1), (2, 4097, 1), (1, 12000, 1), (1, 1, 2), (2, 5, 7), (3, 16, 128), (2, 80, 181),
-       (2, 130, 1000), (1, 700, 96), (1, 3000, 24), (1, 300, 33), (1, 600, 200), (1, 1100, 40), (2, 6, 1032), (1, 4000, 16)]
+       (2, 130, 1000), (1, 700, 96), (1, 3000, 24), (1, 300, 33), (1, 600, 200), (1, 1100, 40), (2, 6, 1032), (1, 4000, 16),
+       (3, 20, 1001), (1, 9, 4099), (2, 33, 2145), (1, 1000, 137), (2, 7, 65), (1, 64, 66)]
 
 
 @pytest.mark.parametrize("dtype", ALL, ids=ids)
