@@ -10,6 +10,13 @@
 // once a call into the workspace, or dy.  A tile is 128 m x NB n (NB <= 256), 64 k to a
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
+// Measured (GB300, bf16): that product 108 us, 1.28 PFLOP/s, dx 109, dW 171; 512 -> 512
+// channels on 360x720 147 us, dx 125, dW 124; 2 x 128 -> 256 on 361x720 83, 69 and 72.
+// Large products are bound by shared memory (a step of 128 x 256 x 64 writes 56 KB of it and
+// reads as much), grids of
+// few channels by what a tile costs at least (1.3 us of an SM), between them by HBM.  Pairs
+// of CTAs (256 x 256 tiles, half of B each) gained nothing: 141, 126 and 136 us on 360x720, 134
+// and 118 for rows.
 // Persistent kernel:
 //   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few): tcgen05.ld,
 //                scales, rounding, stores along the output's rows
@@ -27,7 +34,7 @@
 // in memory, else (MN-major) 64 neighbouring m or n of one k.  So no operand is ever transposed.
 // Operands whose rows do not start on 16 bytes are laid out anew in the workspace first
 // (disco_i8_mm.cu): with the converters reading and shifting their words instead, dx of
-// [1,512,259199] took 326 us and dW 676; copy and product take less.
+// 512 -> 512 on 259199 pixels took 326 us and dW 676; copy and product take 242 and 284.
 // All mbarrier waits are bounded (time-out -> status flag, abort).
 #pragma once
 
@@ -42,6 +49,7 @@ namespace i8 {
 constexpr int kBM = 128, kBK = 64, kNBMax = 256;
 constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2;
 constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr int kReductionWaits = 16;  // of that limit, where one wait spans all steps of a tile
 constexpr int kStatusI8Timeout = 1 << 6;
 
 static __device__ int g_i8_status = 0;  // one per translation unit
@@ -428,7 +436,8 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         cs_n = c.n;
         __syncwarp();
       }
-      bool fin = mbar_wait(&accf[ab], (tl / accs) & 1, kWaitLimit);
+      bool fin = false;  // a whole reduction's wait
+      for (int k = 0; k < kReductionWaits && !fin && !*abort_flag; ++k) fin = mbar_wait(&accf[ab], (tl / accs) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
       if (!fin) {
         if (lane == 0) i8_flag();
@@ -449,8 +458,9 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 f = *reinterpret_cast<const float4*>(cs + c0 + e);
-            const norm::F<4> x = norm::mul(norm::mul(norm::F<4>{{f.x, f.y, f.z, f.w}}, norm::fill<4>(rs)),
-                                           norm::F<4>{{__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])}});
+            // the product of the scales may leave fp32's range where y does not
+            const norm::F<4> sum{{__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])}};
+            const norm::F<4> x = norm::mul(norm::mul(sum, norm::F<4>{{f.x, f.y, f.z, f.w}}), norm::fill<4>(rs));
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[e + k] = __float_as_uint(x.v[k]);
           }

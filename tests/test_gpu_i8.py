@@ -529,3 +529,71 @@ def test_offsets_past_32_bits(lib):
     want, S, D = r.bwd_weight64(keep(y), keep(q), keep(s))
     r.assert_close(dW, want, r.grad_bound(want, S, D, 8192, BF), "dW")
     assert lib.disco_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(3, 64, 40, 1), (70, 1024, 130, 1), (300, 96, 130, 1), (2, 64, 130, 64), (2, 1024, 24, 37)], ids=ids)
+def test_scales_whose_product_leaves_fp32(lib, shape):
+    """scale * wscale past both ends of fp32 where y is inside.  y takes three
+    roundings of 2^-24 (the exact sum's conversion among them) and a subnormal half step."""
+    B, Cin, Cout, P = shape
+    g = _gen("products", shape)
+    q = torch.randint(-127, 128, (B, Cin, P), generator=g, dtype=torch.int8)
+    W = torch.randint(-127, 128, (Cout, Cin), generator=g, dtype=torch.int8)
+    q[0] = 0
+    scale, wscale = torch.full((B, P), 1e-25), torch.full((Cout,), 1e-17)
+    scale[0], wscale[1] = 1e25, 1e25
+    y = torch.empty((B, Cout, P), device="cuda")
+    lib.disco_matmul_i8(q.cuda(), scale.cuda(), W.cuda(), wscale.cuda(), y, B, Cin, Cout, P,
+                        _ws(lib.disco_matmul_i8_workspace_bytes(B, Cin, Cout, P, lib.DISCO_F32)))
+    want, _ = r.matmul64(q, scale, W, wscale)
+    assert (y[0].cpu() == 0).all()
+    r.assert_close(y, want, 3 * 2.0 ** -24 * want.abs() + 2.0 ** -150, "y")
+
+
+def test_as_many_rows_as_fit_the_argument(lib):
+    """2^31 - 1 rows of one value: both ends."""
+    B = 2 ** 31 - 1
+    x = torch.full((B,), 3.0, dtype=BF, device="cuda")
+    x[-3:] = torch.tensor([-5.0, 0.0, 7.0])
+    q, s = torch.zeros(B, dtype=torch.int8, device="cuda"), torch.zeros(B, device="cuda")
+    lib.disco_quant_i8(x, q, s, B, 1, 1)
+    assert q[-5:].tolist() == [127, 127, -127, 0, 127] and q[:3].tolist() == [127] * 3
+    want, scale = r.quant64(torch.tensor([3.0, 3.0, -5.0, 0.0, 7.0])[:, None, None])
+    r.assert_close(s[-5:], scale[:, 0], 2.0 ** -24 * scale[:, 0], "scale")
+    assert lib.disco_device_status() == 0
+
+
+def test_host_threads_at_once(lib):
+    """Four threads, each with its own tensors, workspace and stream, give what one gives."""
+    import threading
+    shapes = [(40, 96, 160, 1), (2, 64, 96, 256), (2, 48, 72, 165), (1, 64, 80, 1)]
+    outs = ("nq", "gq", "uq", "y", "dW1", "dW2", "dn")
+    runs, errors = [], []
+    for B, C, F, P in shapes:
+        t, ws = _block_tensors(lib, B, C, F, P, BF)
+        _block(lib, B, C, F, P, BF, t, ws)
+        torch.cuda.synchronize()
+        want = {k: t[k].clone() for k in outs}
+        for k in outs:
+            t[k].zero_()
+        runs.append(((B, C, F, P, BF, t, ws), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(args, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    _block(lib, *args)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(args, stream)) for args, _, stream in runs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for args, want, _ in runs:
+        for k in outs:
+            assert torch.equal(args[5][k], want[k]), (args[:4], k)
+    assert lib.disco_device_status() == 0
