@@ -107,16 +107,22 @@ __device__ __forceinline__ uint2 to_scaled4(uint32_t w, float s0, float s1, floa
                     pack2_16(from_byte(w, 2) * s2, from_byte(w, 3) * s3, HALF));
 }
 
-// A's share of a converter thread: 16-byte units t, t + NT, ... of a step's 128 lines.
+// A's share of a converter thread: four 16-byte units of a step.  The raw slot holds 128 lines of
+// 64 k, or (MN-major) 64 k of 128 m: whole sectors to a copy's row.  There eight lanes take both
+// halves of neighbouring k, which the stage keeps 8 KB apart, so that neither side's
+// accesses meet in a bank.
 template <class F, int NT>
 struct Units {
-  static constexpr int N = kBM * 4 / NT, LPI = NT / 4;  // units; lines that the converters take at a time
-  int u, l0;                                            // unit of a line, first line
+  static_assert(NT == 128, "the units below");
+  static constexpr int N = 4;
+  int t, u, l0, h;  // unit of a line; first line (k contiguous) or k
 
-  __device__ __forceinline__ explicit Units(int t) : u(t % 4), l0(t / 4) {}
-  // The scales of this thread's units of a step: of 16 k (k contiguous), or of its lines.
+  __device__ __forceinline__ explicit Units(int t) : t(t), u(t % 4), l0(F::KM ? t / 4 : t / 8 * 2 + (t / 4 & 1)), h(t / 4 & 1) {}
+  __device__ __forceinline__ int line(int j) const { return F::KM ? l0 + 32 * j : l0 + 32 * (j >> 1) + 64 * (h ^ (j & 1)); }
+  __device__ __forceinline__ int raw(int j) const { return F::KM ? t + NT * j : (l0 + 32 * (j >> 1)) * 8 + 4 * (h ^ (j & 1)) + u; }
+  // The scales of this thread's units of a step: of 16 k (k contiguous), or of its two k.
   // ks: of the step's first k; the row of scales goes on in zeros to a multiple of 16.
-  static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 64 / LPI > 1 ? 64 / LPI : 1;
+  static constexpr int NS = F::SC == 0 ? 1 : F::KM ? 16 : 2;
   __device__ __forceinline__ void scales(float (&s)[NS], const float* ks, int kleft) const {
     if constexpr (F::SC && F::KM) {
 #pragma unroll
@@ -126,14 +132,14 @@ struct Units {
       }
     } else if constexpr (F::SC) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) s[i] = ((l0 + i * LPI) & 63) < kleft ? __ldg(ks + ((l0 + i * LPI) & 63)) : 0.0f;
+      for (int i = 0; i < NS; ++i) s[i] = l0 + 32 * i < kleft ? __ldg(ks + l0 + 32 * i) : 0.0f;
     }
   }
   // unit j into the stage
   template <bool HALF>
   __device__ __forceinline__ void put(const uint4& v, int j, const float (&s)[NS], uint8_t* stage) const {
-    const int line = l0 + j * LPI, x = line & 7;
-    uint8_t* d = stage + line * 128;
+    const int x = line(j) & 7;
+    uint8_t* d = stage + line(j) * 128;
     uint2 a, b, c, e;
     if constexpr (F::SC == 0) {
       a = to_half4(v.x), b = to_half4(v.y), c = to_half4(v.z), e = to_half4(v.w);
@@ -141,7 +147,7 @@ struct Units {
       a = to_scaled4<HALF>(v.x, s[0], s[1], s[2], s[3]), b = to_scaled4<HALF>(v.y, s[4], s[5], s[6], s[7]);
       c = to_scaled4<HALF>(v.z, s[8], s[9], s[10], s[11]), e = to_scaled4<HALF>(v.w, s[12], s[13], s[14], s[15]);
     } else {
-      const float f = s[j % NS];
+      const float f = s[j >> 1];
       a = to_scaled4<HALF>(v.x, f, f, f, f), b = to_scaled4<HALF>(v.y, f, f, f, f);
       c = to_scaled4<HALF>(v.z, f, f, f, f), e = to_scaled4<HALF>(v.w, f, f, f, f);
     }
@@ -292,9 +298,9 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         ok = mbar_wait(&rawf[w], (i / kRaws) & 1, kWaitLimit);
         ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
         if (!ok) break;
-        const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot) + t0;
+        const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot);
 #pragma unroll
-        for (int j = 0; j < U::N; ++j) v[j] = src[j * kConverters];
+        for (int j = 0; j < U::N; ++j) v[j] = src[units.raw(j)];
         if (i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
         ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
         if (!ok) break;
@@ -351,7 +357,8 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
           if (km) {
             tc_tma_3d(d, map, (int)k0, (int)i0, (int)zr, &f[s]);
           } else {
-            for (int b = 0; b < lines / 64; ++b) tc_tma_3d(d + b * 64 * line, map, (int)i0 + 64 * b, (int)k0, (int)zr, &f[s]);
+            const int wide = ring ? kBM : 64;  // m or n of a box
+            for (int b = 0; b < lines / wide; ++b) tc_tma_3d(d + b * 64 * line, map, (int)i0 + wide * b, (int)k0, (int)zr, &f[s]);
           }
         }
       }
@@ -570,7 +577,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
 
 // ---- host --------------------------------------------------------------------
 
-// `lines` of 64 elements to a copy: of 64 k, or (MN-major) 64 of them, of 64 m or n.
+// `lines` of 64 elements to a copy: of 64 k, or (MN-major) 64 of them, of 64 m or n (integers: 128).
 inline int tc_encode(CUtensorMap* map, const Operand& o, long long I, long long K, int ZR, int lines, bool f16) {
   static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
     void* p = nullptr;
@@ -585,7 +592,7 @@ inline int tc_encode(CUtensorMap* map, const Operand& o, long long I, long long 
   const long long slice = max(o.z, o.r);
   const cuuint64_t dims[3] = {(cuuint64_t)(o.k_major ? K : I), (cuuint64_t)(o.k_major ? I : K), (cuuint64_t)(slice ? ZR : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)o.ld * es, (cuuint64_t)(slice ? slice : o.ld * dims[1]) * es};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(o.k_major ? lines : 64), 1}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {o.k_major || es == 2 ? 64u : (cuuint32_t)kBM, (cuuint32_t)(o.k_major ? lines : 64), 1}, estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                            : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUresult cr = enc(map, type, 3, const_cast<void*>(o.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
