@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, co
 // ---- operands laid out once a call --------------------------------------------
 // Bound by HBM, or by a launch: a thread writes one 16-byte word of a row, from two aligned
 // words shifted together where the source's rows start anywhere.  With its
-// copies and its 2-byte stores a product of 512 by 512 channels takes 206 us on 259199
-// pixels and 147 on 259200.
+// copies and its 2-byte stores a product of 512 by 512 channels takes 184 us on 259199
+// pixels and 128 on 259200.
 
 __device__ __forceinline__ uint4 load16(const uint8_t* p, const uint8_t* end) {
   if (p + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(p));

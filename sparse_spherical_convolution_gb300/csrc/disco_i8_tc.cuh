@@ -10,13 +10,12 @@
 // once a call into the workspace, or dy.  A tile is 128 m x NB n (NB <= 256), 64 k to a
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
-// Measured (GB300, bf16): that product 108 us, 1.28 PFLOP/s, dx 109, dW 171; 512 -> 512
-// channels on 360x720 147 us, dx 125, dW 124; 2 x 128 -> 256 on 361x720 83, 69 and 72.
+// Measured (GB300, bf16): that product 108 us, 1.28 PFLOP/s, dx 109, dW 144; 512 -> 512
+// channels on 360x720 128 us, dx 125, dW 124; 2 x 128 -> 256 on 361x720 84, 69 and 73.
 // Large products are bound by shared memory (a step of 128 x 256 x 64 writes 56 KB of it and
-// reads as much), grids of
-// few channels by what a tile costs at least (1.3 us of an SM), between them by HBM.  Pairs
-// of CTAs (256 x 256 tiles, half of B each) gained nothing: 141, 126 and 136 us on 360x720, 134
-// and 118 for rows.
+// reads as much), grids of few channels by what a tile costs at least (1.3 us of an SM),
+// between them by HBM.  Dropped: pairs of CTAs (256 x 256 tiles, half of B each; rows 134 us and
+// dx 118), and prefetches to L2 four steps ahead (rows 119, dx 184, dW 246).
 // Persistent kernel:
 //   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few): tcgen05.ld,
 //                scales, rounding, stores along the output's rows
@@ -24,7 +23,8 @@
 //                stage.  Two groups take alternate steps, so that one's loads, conversion and
 //                fence overlap the other's.  The raw ring has an even number of slots, each always
 //                the same group's, and stages are released in order: no waiter is ever two
-//                phases ahead of a barrier, where a wait by parity would pass at once
+//                phases ahead of a barrier, where a wait by parity would pass at once.  They
+//                convert after the wait for the stage: before it, dW of 512 by 512 channels on 360x720 took 138 us (124)
 //   one warp     MMA issuer (one thread); two accumulators of 256 TMEM columns, so
 //                the epilogue of a tile overlaps the main loop of the next.  Of narrow tiles
 //                four or eight, and each half of eight epilogue warps takes every second tile
@@ -47,7 +47,7 @@ namespace disco {
 namespace i8 {
 
 constexpr int kBM = 128, kBK = 64, kNBMax = 256;
-constexpr uint32_t kABytes = kBM * kBK * 2, kStageBytes = kABytes + kNBMax * kBK * 2;
+constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kNBMax * kBK * 2;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr int kReductionWaits = 16;  // of that limit, where one wait spans all steps of a tile
 constexpr int kStatusI8Timeout = 1 << 6;
@@ -72,11 +72,16 @@ struct Plan {
   static constexpr int kEpi = FA::SC ? 4 : 8, kConv = kRaw ? 8 : 4;
   static constexpr int kMmaWarp = kEpi + kConv, kThreads = 32 * (kMmaWarp + 3);
   static constexpr int kGroups = 2, kGroupWarps = kConv / kGroups;
-  static constexpr int kStages = kRaw ? 3 : 4, kRaws = kRaw ? 6 : 0;
+  // Slots of B (and barriers of a step), of A, and of the raw ring.  A slot of A waits for the
+  // products of step i - kAs by that step's barrier; its waiter has seen step i - 2 - kAs
+  // end, so the barrier is never a phase behind.  B comes from memory or L2 and wants the
+  // lead: with 3, 3 and 6 slots dW of 16384 rows of 2048 by 2048 took 171 us (144), 512 -> 512 on 360x720
+  // 136 (128); with 4 of A and 2 raw dW 156.
+  static constexpr int kStages = 4, kAs = !kRaw ? 4 : FA::SC ? 3 : 2, kRaws = kRaw ? 4 : 0;
   static constexpr uint32_t kSlot = kBM * kBK;
   // of an epilogue warp: 64 bytes of 32 rows on their way out, the scales of a tile's columns
   static constexpr uint32_t kStaging = 32 * 64, kCols = kRaw && !FA::SC ? kNBMax * 4 : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 512;
+  static constexpr size_t kSmem = 1024 + (size_t)kAs * kABytes + (size_t)kStages * kBBytes + kRaws * kSlot + kEpi * (kStaging + kCols) + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kRaws % kGroups == 0, "a slot is always the same group's");
 };
@@ -214,12 +219,12 @@ template <class FA, bool BKM, bool HALF, bool TR>
 __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const TcArgs a) {
   using C = Plan<FA>;
-  constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2, kStages = C::kStages, kRaws = C::kRaws;
+  constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2, kStages = C::kStages, kAs = C::kAs, kRaws = C::kRaws;
   constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps;
   constexpr bool kRaw = C::kRaw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* raws = smem + kStages * kStageBytes;
+  uint8_t *bring = smem + kAs * kABytes, *raws = bring + kStages * kBBytes;
   uint8_t* staging = raws + kRaws * C::kSlot;
   uint8_t* colscale = staging + kEpiWarps * C::kStaging;
   uint64_t* full = reinterpret_cast<uint64_t*>(colscale + kEpiWarps * C::kCols);
@@ -301,13 +306,13 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         const uint4* src = reinterpret_cast<const uint4*>(raws + w * C::kSlot);
 #pragma unroll
         for (int j = 0; j < U::N; ++j) v[j] = src[units.raw(j)];
-        if (i >= kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitLimit);
+        if (i >= kAs) ok = mbar_wait(&empty[(i - kAs) % kStages], ((i - kAs) / kStages) & 1, kWaitLimit);
         ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
         if (!ok) break;
         __syncwarp();  // every lane has read its units
         if (lane == 0) mbar_arrive(&rawe[w]);
 #pragma unroll
-        for (int j = 0; j < U::N; ++j) units.template put<HALF>(v[j], j, sc, smem + s * kStageBytes);
+        for (int j = 0; j < U::N; ++j) units.template put<HALF>(v[j], j, sc, smem + i % kAs * kABytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
@@ -328,8 +333,8 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       const bool ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
       const int slots = ring ? (kRaws ? kRaws : 1) : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
       uint64_t *f = ring ? rawf : full, *e = ring ? rawe : empty;
-      uint8_t* base = ring ? raws : smem + (is_a ? 0 : kABytes);
-      const uint32_t pitch = ring ? C::kSlot : kStageBytes, line = ring ? 64 : 128;
+      uint8_t* base = ring ? raws : is_a ? smem : bring;
+      const uint32_t pitch = ring ? C::kSlot : is_a ? kABytes : kBBytes, line = ring ? 64 : 128;
       const CUtensorMap* map = is_a ? &amap : &bmap;
       [[maybe_unused]] const long long I = is_a ? a.m.M : a.m.N;
       // a weight has one slice for all z
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kABytes;
+          const uint32_t sa = smem_u32(smem + i % kAs * kABytes), sb = smem_u32(bring + s * kBBytes);
 #pragma unroll
           for (int ks = 0; ks < kBK / 16; ++ks) {
             // 16 k: 32 bytes of every line (k contiguous), or 16 lines; boxes of 64 m or n are 8 KB apart
