@@ -105,7 +105,10 @@ __global__ void __launch_bounds__(kAnyThreads) mm_layout_kernel(const Layouts a)
 // products and their sum to an instruction (dp4a), exact in 32 bits.  The rows lie in shared memory
 // from their first byte on, zeros behind them.
 constexpr int kFewThreads = 128, kFewRows = 16;
-constexpr size_t kFewSmem = 128 * 1024;
+// Rows beyond this leave too few warps to an SM: 12 rows of 8192 to 3079 channels (128 KB) took 58
+// us (16 on the tensor cores), of 4096 (64 KB) 15.5 (12.3); 4 rows of 8192 (32 KB) take 8.6 (16),
+// 12 of 2048 7.3 (10).  Its 2^15 products at most keep a sum in 32 bits.
+constexpr size_t kFewSmem = 32 * 1024;
 
 // Word i (16 bytes) of a row of C bytes anywhere in a tensor that ends at `end`.
 template <bool ALN>
@@ -191,8 +194,7 @@ int few(const FewArgs& a, cudaStream_t st) {
 }
 bool takes_few(int32_t B, int32_t Cin, int64_t P) {
   const int NB = B == 1 ? 1 : B <= 4 ? 4 : 16;
-  // 32 bits hold the sum of 2^16 products
-  return P == 1 && B <= kFewRows && Cin <= 1 << 16 && (size_t)NB * ((Cin + 15) / 16) * 16 <= kFewSmem;
+  return P == 1 && B <= kFewRows && (size_t)NB * ((Cin + 15) / 16) * 16 <= kFewSmem;
 }
 
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).

@@ -597,3 +597,17 @@ def test_host_threads_at_once(lib):
         for k in outs:
             assert torch.equal(args[5][k], want[k]), (args[:4], k)
     assert lib.disco_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(16, 2048, 70, 1), (16, 2049, 70, 1), (4, 8192, 40, 1), (4, 8193, 40, 1), (1, 32768, 40, 1), (1, 32769, 40, 1),
+                                   (12, 6929, 3079, 1)], ids=ids)
+def test_few_rows_up_to_the_kernels_limit(lib, shape):
+    """Both sides of where rows are too long for the kernel of a few rows."""
+    B, Cin, Cout, P = shape
+    q, scale, W, wscale, _ = _operands(shape, F32)
+    y = torch.empty((B, Cout, P), device="cuda")
+    lib.disco_matmul_i8(q.cuda(), scale.cuda(), W.cuda(), wscale.cuda(), y, B, Cin, Cout, P,
+                        _ws(lib.disco_matmul_i8_workspace_bytes(B, Cin, Cout, P, lib.DISCO_F32)))
+    want, S = r.matmul64(q, scale, W, wscale)
+    r.assert_close(y, want, r.matmul_bound(want, S, scale, wscale, Cin, F32), "y")
+    assert lib.disco_device_status() == 0
