@@ -210,6 +210,14 @@ __device__ __forceinline__ void tc_tma_3d(void* dst, const CUtensorMap* map, int
       : "memory");
 }
 
+// One thread of a whole warp.  Chosen this way, its loops' counters and addresses stay in the
+// warp's uniform registers, where the copy engine and the tensor cores take them from.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // One row on; opaque to the compiler, which would keep 32 rows' addresses in registers.
 __device__ __forceinline__ void next_row(uint8_t*& o, long long pitch) { asm volatile("add.s64 %0, %0, %1;" : "+l"(o) : "l"(pitch)); }
 
@@ -327,14 +335,14 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
     }
   } else if (warp == kTmaAWarp || warp == kTmaBWarp) {
     // ------------------------------------------------------------ TMA --
-    const bool is_a = warp == kTmaAWarp;
-    if (lane == 0) {
+    auto copies = [&](auto which) {
       // A's integers go into the raw ring, 16-bit lines into the stage
-      const bool ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
-      const int slots = ring ? (kRaws ? kRaws : 1) : kStages, lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
+      constexpr bool is_a = decltype(which)::value, ring = is_a && kRaw, km = is_a ? FA::KM : BKM;
+      constexpr int slots = ring ? kRaws : kStages;
+      const int lines = is_a ? kBM : km ? a.NB : (a.NB + 63) / 64 * 64;
       uint64_t *f = ring ? rawf : full, *e = ring ? rawe : empty;
       uint8_t* base = ring ? raws : is_a ? smem : bring;
-      const uint32_t pitch = ring ? C::kSlot : is_a ? kABytes : kBBytes, line = ring ? 64 : 128;
+      constexpr uint32_t pitch = ring ? C::kSlot : is_a ? kABytes : kBBytes, line = ring ? 64 : 128;
       const CUtensorMap* map = is_a ? &amap : &bmap;
       [[maybe_unused]] const long long I = is_a ? a.m.M : a.m.N;
       // a weight has one slice for all z
@@ -359,10 +367,10 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
             mbar_complete_tx(&f[s], lines * line);
             continue;
           }
-          if (km) {
+          if constexpr (km) {
             tc_tma_3d(d, map, (int)k0, (int)i0, (int)zr, &f[s]);
           } else {
-            const int wide = ring ? kBM : 64;  // m or n of a box
+            constexpr int wide = ring ? kBM : 64;  // m or n of a box
             for (int b = 0; b < lines / wide; ++b) tc_tma_3d(d + b * 64 * line, map, (int)i0 + wide * b, (int)k0, (int)zr, &f[s]);
           }
         }
@@ -374,10 +382,14 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         for (int back = 1; back <= slots && i - back >= 0; ++back)
           mbar_wait(&f[(i - back) % slots], ((i - back) / slots) & 1, 1u << 16);
       }
+    };
+    if (elected()) {
+      if (warp == kTmaAWarp) copies(std::true_type());
+      else copies(std::false_type());
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
+    if (elected()) {
       const int nmma = (a.NB + 15) / 16 * 16;
       const uint32_t idesc = idesc_16_f32(kBM, nmma, HALF) | (FA::KM ? 0u : 1u << 15) | (BKM ? 0u : 1u << 16);
       int i = 0, tl = 0;
