@@ -10,10 +10,10 @@
 // once a call into the workspace, or dy.  A tile is 128 m x NB n (NB <= 256), 64 k to a
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
-// Measured (GB300, bf16): that product 108 us, 1.28 PFLOP/s, dx 109, dW 144; 512 -> 512
-// channels on 360x720 128 us, dx 125, dW 124; 2 x 128 -> 256 on 361x720 84, 69 and 73.
+// Measured (GB300, bf16): that product 106 us, 1.30 PFLOP/s, dx 91, dW 132; 512 -> 512
+// channels on 360x720 128 us, dx 124, dW 126; 2 x 128 -> 256 on 361x720 85, 68 and 74.
 // Large products are bound by shared memory (a step of 128 x 256 x 64 writes 56 KB of it and
-// reads as much), grids of few channels by what a tile costs at least (1.3 us of an SM),
+// reads as much, 900 cycles; dx's 48 and 48 KB 770), grids of few channels by what a tile costs at least (1.3 us of an SM),
 // between them by HBM.  Dropped: pairs of CTAs (256 x 256 tiles, half of B each; rows 134 us and
 // dx 118), and prefetches to L2 four steps ahead (rows 119, dx 184, dW 246).
 // Persistent kernel:
@@ -75,7 +75,7 @@ struct Plan {
   // Slots of B (and barriers of a step), of A, and of the raw ring.  A slot of A waits for the
   // products of step i - kAs by that step's barrier; its waiter has seen step i - 2 - kAs
   // end, so the barrier is never a phase behind.  B comes from memory or L2 and wants the
-  // lead: with 3, 3 and 6 slots dW of 16384 rows of 2048 by 2048 took 171 us (144), 512 -> 512 on 360x720
+  // lead: with 3, 3 and 6 slots dW of 16384 rows of 2048 by 2048 took 171 us (144 then), 512 -> 512 on 360x720
   // 136 (128); with 4 of A and 2 raw dW 156.
   static constexpr int kStages = 4, kAs = !kRaw ? 4 : FA::SC ? 3 : 2, kRaws = kRaw ? 4 : 0;
   static constexpr uint32_t kSlot = kBM * kBK;
@@ -210,8 +210,9 @@ __device__ __forceinline__ void tc_tma_3d(void* dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// One thread of a whole warp.  Chosen this way, its loops' counters and addresses stay in the
-// warp's uniform registers, where the copy engine and the tensor cores take them from.
+// One thread of a whole warp, for the loops of copies and matrix instructions: the compiler
+// knows that it is one.  With lane 0 instead, and ring sizes taken at run time, their threads were
+// busy 1000 cycles a step: dx of 16384 rows of 2048 by 2048 took 109 us (91), dW 143 (132).
 __device__ __forceinline__ bool elected() {
   uint32_t p;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
