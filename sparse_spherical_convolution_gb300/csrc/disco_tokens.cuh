@@ -422,11 +422,12 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
     if constexpr (ODD) {
       const long long k0 = b * G * half + p + row0, total = (long long)a.B * G * half;
       const int nv = min(V, N - lx * V);
-      if (b + 1 < a.B || pos + TP + V <= P) {
+      const long long last = (b + 1) * G * half - P + pos + (N - 1) / V * V;  // the tile's last words start here, rounded down
+      if ((last & ~(long long)(V - 1)) + 2 * V <= total) {
         // both words of every row end inside the tensor: no tests between the loads, eight of them in flight
         constexpr int U = 4 / G;
         for (int i0 = 0; i0 < n; i0 += U) {
-          uint4 lo[U][G], hi[U][G];
+          uint4 lo[U][G] = {}, hi[U][G] = {};
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
