@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kTokenThreads) tokens_rows_kernel(const TokenA
 // rounding).  y waits between the two in the words of its gate and value.
 struct TileCut {
   int NT, LX, nj;  // nj: words of a thread in a tile, of each half
+  int roomy = 0;   // sample b < roomy - 1 is followed by two words of x, so its rows' last words end inside x
   long long per_sample, tiles;
 };
 constexpr int kTileThreads = 512;
@@ -422,12 +423,11 @@ __global__ void __launch_bounds__(kTileThreads) tokens_tile_kernel(const TokenAr
     if constexpr (ODD) {
       const long long k0 = b * G * half + p + row0, total = (long long)a.B * G * half;
       const int nv = min(V, N - lx * V);
-      const long long last = (b + 1) * G * half - P + pos + (N - 1) / V * V;  // the tile's last words start here, rounded down
-      if ((last & ~(long long)(V - 1)) + 2 * V <= total) {
+      if (b + 1 < g.roomy || pos + TP + V <= P) {
         // both words of every row end inside the tensor: no tests between the loads, eight of them in flight
         constexpr int U = 4 / G;
         for (int i0 = 0; i0 < n; i0 += U) {
-          uint4 lo[U][G] = {}, hi[U][G] = {};
+          uint4 lo[U][G], hi[U][G];
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -638,6 +638,7 @@ int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
   g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
   const size_t smem = (size_t)G * g.nj * g.NT * 16 + (size_t)g.LX * V * (4 * kOwn + g.NT / 32 * kSum);
   if (smem > norm::kMaxSmem) return DISCO_ERR_UNSUPPORTED;
+  g.roomy = (long long)G * a.C * a.P >= 2 * V ? a.B : 0;  // samples of one channel by two pixels are shorter: decided here, as in the kernel it cost registers (221 us became 257)
   g.per_sample = (a.P + g.LX * V - 1) / (g.LX * V);
   g.tiles = g.per_sample * a.B;
   auto kern = tokens_tile_kernel<T, GLU, XQ, YQ, ODD>;
