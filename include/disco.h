@@ -508,7 +508,10 @@ DISCO_API int disco_grad_norm_clip(const disco_grads* grads, float grad_scale, f
    activation serves the product and, kept in place of the 16-bit one, the
    gradients.
    The products and gradients take up to 2^31 - 1 pixels and a sample of less
-   than 2^40 bytes in 16 bits (DISCO_ERR_UNSUPPORTED beyond).  Their workspace
+   than 2^40 bytes in 16 bits (DISCO_ERR_UNSUPPORTED beyond).  The tensor cores
+   cut off what a sum's 24 bits do not hold, so no sum of theirs has more than
+   32768 terms (they lose some 4e-5 of it where all have one sign); the sums of
+   longer reductions are added in fp32, in their order.  The workspace
    holds the weight (or a few rows) in 16 bits, the sums of a split reduction,
    and a copy of every operand whose rows do not start on 16 bytes (an odd
    number of pixels, or of features for P = 1). */

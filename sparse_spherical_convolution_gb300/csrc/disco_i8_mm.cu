@@ -200,9 +200,10 @@ bool takes_few(int32_t B, int32_t Cin, int64_t P) {
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).
 // Tiles of 256 n; where they do not fill the SMs, the reduction is split into parts of 8 steps
 // at least (2 where the sums are few), and where that leaves half of the SMs idle, tiles get narrower.
+// No part has more than kPartSteps; where that decides, parts are added until they fill the SMs evenly.
 struct Cut {
-  int NB, nsplit;
-  long long mt, nt, nkp, steps;
+  int NB;
+  long long nsplit, mt, nt, nkp, steps;
   Cut(long long M, long long N, long long K, int Z, int R) {
     mt = (M + 127) / 128;
     nkp = (K + 63) / 64;
@@ -211,10 +212,12 @@ struct Cut {
     for (;;) {
       nt = (N + NB - 1) / NB;
       const long long tiles = mt * nt * Z;
-      nsplit = (int)max(1LL, min(steps / (M * N * Z <= 1 << 16 ? 2 : 8), kSMs / tiles));
+      nsplit = max(1LL, min(steps / (M * N * Z <= 1 << 16 ? 2 : 8), kSMs / tiles));
       if (tiles * nsplit >= kSMs / 2 || NB <= 64) break;
       NB = NB > 128 ? 128 : 64;
     }
+    const long long least = (steps + kPartSteps - 1) / kPartSteps, tiles = mt * nt * Z;
+    if (nsplit < least) nsplit = max(least, (least * tiles + kSMs - 1) / kSMs * kSMs / tiles);
   }
 };
 
@@ -269,7 +272,7 @@ struct Product {
     }
     TcArgs a = {};
     a.m = m;
-    a.NB = cut.NB, a.nsplit = cut.nsplit, a.mt = (uint32_t)cut.mt, a.nt = (uint32_t)cut.nt, a.nkp = cut.nkp, a.steps = cut.steps;
+    a.NB = cut.NB, a.nsplit = (int)cut.nsplit, a.mt = (uint32_t)cut.mt, a.nt = (uint32_t)cut.nt, a.nkp = cut.nkp, a.steps = cut.steps;
     a.part = cut.nsplit > 1 ? part : nullptr;
     a.out_type = dtype;
     a.after = lay.n > 0;
@@ -279,7 +282,7 @@ struct Product {
     if (rc || !a.part) return rc;
     const long long n = m.Z * m.M * m.N;
     const int grid = (int)min((n + kAnyThreads - 1) / kAnyThreads, (long long)kSMs * 8);
-#define CALL(T) rc = norm::launch(mm_join_kernel<T>, grid, kAnyThreads, 1, true, 0, 0, st, "mm_join_kernel", m, (const float*)part, cut.nsplit, n)
+#define CALL(T) rc = norm::launch(mm_join_kernel<T>, grid, kAnyThreads, 1, true, 0, 0, st, "mm_join_kernel", m, (const float*)part, (int)cut.nsplit, n)
     DISCO_BY_DTYPE(dtype, CALL)
 #undef CALL
     return rc;

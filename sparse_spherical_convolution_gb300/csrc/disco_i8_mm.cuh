@@ -28,6 +28,14 @@ struct MmArgs {
   bool transposed;
 };
 
+// The steps (of 64 k) of one sum in an accumulator, at most.  The tensor cores cut off what a sum's
+// 24 bits do not hold at each of the four instructions of a step, so a sum of one sign comes out too small: over 2
+// million tokens by 1.7e-3 of it, three times fp16's rounding.  2048 instructions lose 2.4e-4 of a sum
+// at a unit of 2^-23 each, and some 4e-5 where terms are alike and the sum grows evenly; and a wait for a
+// part's sums stays short.  Parts are joined in fp32 with rounding to nearest.  Times with and without:
+// dW of 400000 rows of 2048 by 1280 1.72 ms (3.04: its parts fill the SMs), 20 x 64 -> 64 on 360x720 320 us (307).
+constexpr long long kPartSteps = 512;
+
 // How the tensor-core kernel cuts a product (disco_i8_tc.cuh): tiles of 128 m x NB n
 // of each z, their reduction of `steps` chunks of 64 k in nsplit parts.
 struct TcArgs {

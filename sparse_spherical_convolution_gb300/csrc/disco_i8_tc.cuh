@@ -48,8 +48,7 @@ namespace i8 {
 
 constexpr int kBM = 128, kBK = 64, kNBMax = 256;
 constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kNBMax * kBK * 2;
-constexpr uint32_t kWaitLimit = 1u << 24;
-constexpr int kReductionWaits = 16;  // of that limit, where one wait spans all steps of a tile
+constexpr uint32_t kWaitLimit = 1u << 24;  // the longest wait spans the kPartSteps of a tile's part, below a millisecond
 constexpr int kStatusI8Timeout = 1 << 6;
 
 static __device__ int g_i8_status = 0;  // one per translation unit
@@ -461,8 +460,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         cs_n = c.n;
         __syncwarp();
       }
-      bool fin = false;  // a whole reduction's wait
-      for (int k = 0; k < kReductionWaits && !fin && !*abort_flag; ++k) fin = mbar_wait(&accf[ab], (tl / accs) & 1, kWaitLimit);
+      bool fin = mbar_wait(&accf[ab], (tl / accs) & 1, kWaitLimit);
       fin = __all_sync(0xffffffffu, fin) && !*abort_flag;
       if (!fin) {
         if (lane == 0) i8_flag();
