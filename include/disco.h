@@ -545,7 +545,11 @@ DISCO_API int disco_matmul_i8(const void* q, const float* scale, const void* W, 
 /* Gradient of the product with respect to the activation that q and scale stand
    for (the rounding to 8 bits counts as the identity):
      dx[b,c,p] = sum_o (wscale[o] W[o,c]) dy[b,o,p]
-   wscale[o] W[o,c] is rounded to `dtype`, sums are fp32, dx is rounded once.
+   wscale[o] W[o,c] is rounded to `dtype`, as a 16-bit weight would be (errors are
+   some sqrt(2) of those of dx's own rounding); sums are fp32, dx is rounded once.
+   fp16: a power of two common to the call's scales is taken out first and put back into
+   the sums, so that no term overflows and scales down to 2^-21 of the largest
+   finite one keep fp16's digits.
    dy: [B, Cout, P], dx: [B, Cin, P], bf16 or fp16 (DISCO_ERR_UNSUPPORTED
    else).  Workspace, overlaps and order as above. */
 DISCO_API size_t disco_matmul_i8_bwd_input_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P,
@@ -557,8 +561,8 @@ DISCO_API int disco_matmul_i8_bwd_input(const void* dy, const void* W, const flo
 /* Gradient of the product with respect to the weight that W and wscale stand
    for, from the kept 8-bit activation:
      dW[o,c] = sum_{b,p} dy[b,o,p] (scale[b,p] q[b,c,p])
-   scale[b,p] q[b,c,p] is rounded to `dtype`; sums are fp32 in a fixed order
-   (deterministic), dW is rounded once.  dy: [B, Cout, P], dW: [Cout, Cin], bf16
+   scale[b,p] q[b,c,p] is rounded to `dtype` as above, fp16 with a power of two
+   taken out; sums are fp32 in a fixed order (deterministic), dW is rounded once.  dy: [B, Cout, P], dW: [Cout, Cin], bf16
    or fp16.  Workspace, overlaps and order as above. */
 DISCO_API size_t disco_matmul_i8_bwd_weight_workspace_bytes(int32_t B, int32_t Cin, int32_t Cout, int64_t P,
                                                             disco_dtype dtype);

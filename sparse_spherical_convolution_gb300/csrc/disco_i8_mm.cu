@@ -39,6 +39,18 @@ __global__ void __launch_bounds__(kAnyThreads) mm_join_kernel(const MmArgs a, co
   }
 }
 
+// The largest finite scale of each block's share (Range).
+__global__ void __launch_bounds__(kAnyThreads) mm_range_kernel(const float* scale, long long n, float* part) {
+  __shared__ uint32_t most;
+  norm::let_next_begin();
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
+  const uint32_t m = largest(scale, n, (long long)blockIdx.x * kAnyThreads + threadIdx.x, (long long)gridDim.x * kAnyThreads);
+  if ((threadIdx.x & 31) == 0) atomicMax(&most, m);
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = __uint_as_float(most);
+}
+
 // ---- operands laid out once a call --------------------------------------------
 // Bound by HBM, or by a launch: a thread writes one 16-byte word of a row, from two aligned
 // words shifted together where the source's rows start anywhere.  With its
@@ -66,20 +78,22 @@ struct Layout {
 struct Layouts {
   Layout t[3];
   int n;
+  Range range;  // of the scales of kind 2
 };
 
 __global__ void __launch_bounds__(kAnyThreads) mm_layout_kernel(const Layouts a) {
+  __shared__ uint32_t most;
   norm::let_next_begin();
   int k = 0;
   if (a.n > 1 && blockIdx.x >= a.t[1].block0) k = 1;
   if (a.n > 2 && blockIdx.x >= a.t[2].block0) k = 2;
   const Layout& t = a.t[k];
   const long long i = (long long)(blockIdx.x - t.block0) * kAnyThreads + threadIdx.x;
-  if (i >= t.total) return;
+  const bool live = i < t.total;
   const long long row = t.total <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)t.words) : i / t.words;
   const int step = t.kind ? 8 : 16;  // source bytes of a word
   const long long at = (i - row * t.words) * step;
-  const int nb = (int)max(0LL, min((long long)step, t.len * t.es - at));
+  const int nb = live ? (int)max(0LL, min((long long)step, t.len * t.es - at)) : 0;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (nb > 0) {
     const uint8_t* p = t.src + row * t.len * t.es + at;
@@ -89,9 +103,21 @@ __global__ void __launch_bounds__(kAnyThreads) mm_layout_kernel(const Layouts a)
       v = shifted(lo, sh + nb > 16 ? load16(p - sh + 16, t.end) : v, sh, nb);
     }
   }
+  // every block waits for the range, so that this kernel's end tells the next one that it is there
+  norm::wait_for_previous();
+  float down = 1.0f;
+  if (t.kind == 2) {
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    const uint32_t m = largest(a.range.v, a.range.n, threadIdx.x, kAnyThreads);
+    if ((threadIdx.x & 31) == 0) atomicMax(&most, m);
+    __syncthreads();
+    down = fit_down(most);
+  }
+  if (!live) return;
   if (t.kind) {
     const uint32_t w[2] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u};
-    const float f = t.kind > 1 ? t.scale[row] : 1.0f;
+    const float f = t.kind > 1 ? t.scale[row] * down : 1.0f;
     auto two = [&](int e) { return pack2_16(from_byte(w[e / 4], e & 3) * f, from_byte(w[e / 4], (e & 3) + 1) * f, t.kind < 3); };
     v = make_uint4(two(0), two(2), two(4), two(6));
   }
@@ -197,6 +223,11 @@ bool takes_few(int32_t B, int32_t Cin, int64_t P) {
   return P == 1 && B <= kFewRows && (size_t)NB * ((Cin + 15) / 16) * 16 <= kFewSmem;
 }
 
+// As many scales each block of the kernels that need the largest one reads for itself; of more, mm_range_kernel's
+// parts.  dx of 512 rows 1024 -> 4096 takes 19.9 us with the parts, 21.4 without; 4 x 64 -> 48 on 33x65 6.4
+// without, 7.6 with them.  (5.7 and 17.8 if the scales stayed as they are.)
+constexpr long long kRangeDirect = 1024;
+
 // The cut of a product by its sizes alone (the workspace's bytes follow from it).
 // Tiles of 256 n; where they do not fill the SMs, the reduction is split into parts of 8 steps
 // at least (2 where the sums are few), and where that leaves half of the SMs idle, tiles get narrower.
@@ -230,6 +261,8 @@ struct Product {
   char* ws;
   size_t bytes = 0;
   uint32_t blocks = 0;
+  const float* scales = nullptr;
+  long long nscales = 0;
 
   Product(void* workspace, long long M, long long N, long long K, int Z, int R, bool transposed) : cut(M, N, K, Z, R), ws((char*)workspace) {
     m.M = M, m.N = N, m.K = K, m.Z = Z, m.R = R, m.transposed = transposed;
@@ -262,20 +295,34 @@ struct Product {
     const long long words = (C + 7) / 8;
     return {add(q, scale, rows, C, words, 1, !scaled ? 1 : f16 ? 2 : 3), nullptr, 0, 0, words * 8, 0, 16, k_major};
   }
+  // fp16 gradients: the range of n scales (its words are taken for every type: one size for all)
+  void ranged(const float* scale, long long n) {
+    float* p = (float*)take(kSMs * 4);
+    if (!m.f16) return;
+    if (n <= kRangeDirect) {
+      m.range = {scale, (int)n};
+      return;
+    }
+    scales = scale, nscales = n;
+    m.range = {p, kSMs};
+  }
   float* parts() { return cut.nsplit > 1 ? (float*)take((size_t)cut.nsplit * m.Z * m.M * m.N * 4) : nullptr; }
 
   int run(float* part, disco_dtype dtype, int (*tc)(const TcArgs&, cudaStream_t), cudaStream_t st) const {
     if (cut.mt * cut.nt * m.Z * cut.nsplit >= 1LL << 31) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 by %d", cut.NB);
+    if (scales) {
+      mm_range_kernel<<<kSMs, kAnyThreads, 0, st>>>(scales, nscales, const_cast<float*>(m.range.v));
+      if (int rc = check_launch("mm_range_kernel")) return rc;
+    }
     if (lay.n) {
-      mm_layout_kernel<<<blocks, kAnyThreads, 0, st>>>(lay);
-      if (int rc = check_launch("mm_layout_kernel")) return rc;
+      if (int rc = norm::launch(mm_layout_kernel, (int)blocks, kAnyThreads, 1, scales != nullptr, 0, 0, st, "mm_layout_kernel", lay)) return rc;
     }
     TcArgs a = {};
     a.m = m;
     a.NB = cut.NB, a.nsplit = (int)cut.nsplit, a.mt = (uint32_t)cut.mt, a.nt = (uint32_t)cut.nt, a.nkp = cut.nkp, a.steps = cut.steps;
     a.part = cut.nsplit > 1 ? part : nullptr;
     a.out_type = dtype;
-    a.after = lay.n > 0;
+    a.after = lay.n > 0 || scales;
     a.vec = (m.transposed ? m.M : m.N) * (a.part ? 4 : elem_bytes(dtype)) % 16 == 0;
     a.tiles = (uint32_t)(cut.mt * cut.nt * m.Z * cut.nsplit);
     int rc = tc(a, st);
@@ -316,6 +363,8 @@ Product product_dx(const void* dy, const void* W, const float* wscale, void* dx,
   Product p = P == 1 ? Product(ws, B, Cin, Cout, 1, 1, false) : Product(ws, P, Cin, Cout, B, 1, true);
   p.m.out = dx;
   p.m.f16 = f16;
+  p.ranged(wscale, Cout);
+  p.lay.range = p.m.range;
   p.m.B = p.halves(W, true, wscale, Cout, Cin, f16, false);
   if (P == 1) p.m.A = p.rows({dy, nullptr, 0, 0, Cout, 0, 16, true}, B);  // m = row
   else p.m.A = p.rows({dy, nullptr, Cout * P, 0, P, 0, 16, false}, (long long)B * Cout);  // m = pixel
@@ -327,6 +376,7 @@ Product product_dw(const void* dy, const void* q, const float* scale, void* dW, 
   Product p = P == 1 ? Product(ws, Cin, Cout, B, 1, 1, true) : Product(ws, Cin, Cout, P, 1, B, true);  // m = input channel
   p.m.out = dW;
   p.m.f16 = f16;
+  p.ranged(scale, (long long)B * P);
   if (P == 1) {  // k = row
     p.m.A = p.rows({q, scale, 0, 0, Cin, 0, 8, false}, B);
     p.m.B = p.rows({dy, nullptr, 0, 0, Cout, 0, 16, false}, B);

@@ -17,6 +17,35 @@ struct Operand {
   bool k_major;
 };
 
+// The power of two that is taken out of the scales of an fp16 gradient before scale * integer is rounded
+// to fp16: with it the largest finite scale lies in [128, 256), so no term overflows, and small scales keep
+// their digits down to 2^-21 of the largest.  (Without it weights below 1e-5 lost digits to fp16's
+// subnormals, and scales above 516 became infinite.)
+struct Range {
+  const float* v;  // n values with the largest magnitude of the scales: the scales, or the largest of parts of them; null: scales as they are
+  int n;
+};
+// The bits of a block's share of the largest finite |v|; all lanes of a warp call it, the i-th of `step` threads.
+__device__ __forceinline__ uint32_t largest(const float* v, long long n, long long i, long long step) {
+  uint32_t m = 0;
+  auto add = [&](float f) {
+    const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
+    if (b < 0x7f800000u) m = max(m, b);
+  };
+  const long long words = n / 4;
+  if (i < n - 4 * words) add(__ldcg(v + 4 * words + i));
+  for (; i < words; i += step) {
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(v) + i);
+    add(f.x), add(f.y), add(f.z), add(f.w);
+  }
+  return __reduce_max_sync(0xffffffffu, m);
+}
+// What a scale is multiplied by, and what a sum of terms is, from the bits of the largest
+// scale; both are normal numbers.
+__device__ __forceinline__ int fit(uint32_t most) { return max((int)(most >> 23), 14); }
+__device__ __forceinline__ float fit_down(uint32_t most) { return __uint_as_float((uint32_t)(261 - fit(most)) << 23); }
+__device__ __forceinline__ float fit_up(uint32_t most) { return __uint_as_float((uint32_t)(fit(most) - 7) << 23); }
+
 // out[z][m][n] = rs[z rs_z + m] cs[n] sum_{r < R, k < K} A(m, k) B(n, k), or with
 // `transposed` out[z][n][m]; rs and cs may both be null.
 struct MmArgs {
@@ -26,6 +55,7 @@ struct MmArgs {
   long long rs_z, M, N, K;
   int Z, R, f16;
   bool transposed;
+  Range range;  // of A's ks, or of the scales that B's integers were multiplied by
 };
 
 // The steps (of 64 k) of one sum in an accumulator, at most.  The tensor cores cut off what a sum's

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
   using C = Plan<FA>;
   constexpr int kMmaWarp = C::kMmaWarp, kTmaBWarp = kMmaWarp + 1, kTmaAWarp = kMmaWarp + 2, kStages = C::kStages, kAs = C::kAs, kRaws = C::kRaws;
   constexpr int kEpiWarps = C::kEpi, kGroups = C::kGroups, kGroupWarps = C::kGroupWarps, kConverters = 32 * kGroupWarps;
-  constexpr bool kRaw = C::kRaw;
+  constexpr bool kRaw = C::kRaw, kFit = HALF && (FA::SC || !kRaw);  // kFit: fp16 gradients
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *bring = smem + kAs * kABytes, *raws = bring + kStages * kBBytes;
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
   uint64_t *empty = full + 4, *accf = empty + 4, *acce = accf + 8, *rawf = acce + 8, *rawe = rawf + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(rawe + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  uint32_t* most = tslot + 2;  // of the scales (Range)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int accs = a.NB <= 64 ? 8 : a.NB <= 128 ? 4 : 2, acc_cols = 512 / accs;  // accumulators, their columns
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       mbar_init(&rawe[r], kGroupWarps);
     }
     *abort_flag = 0;
+    *most = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -268,6 +270,11 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tslot;
   norm::wait_for_previous();  // the operand that was converted into the workspace
+  if constexpr (kFit) {
+    const uint32_t m = largest(a.m.range.v, a.m.range.n, tid, C::kThreads);
+    if (lane == 0) atomicMax(most, m);
+    __syncthreads();
+  }
 
   // reduction steps of a tile's part
   auto first_step = [&](int sp) { return a.nsplit > 1 ? a.steps * sp / a.nsplit : 0; };
@@ -279,6 +286,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       const int group = (warp - kEpiWarps) / kGroupWarps, t0 = tid - 32 * kEpiWarps - group * kConverters;
       using U = Units<FA, kConverters>;
       const U units(t0);
+      [[maybe_unused]] const float down = kFit ? fit_down(*most) : 1.0f;
       auto start = [&](Pos& p) {
         p.q = first_step(p.w.sp), p.q1 = last_step(p.w.sp);
         p.r = p.q == 0 || a.m.R == 1 ? 0 : p.q / a.nkp;
@@ -300,6 +308,17 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       if (group == 1) advance(cur);
       float sc[U::NS], scn[U::NS];
       if (cur.w.in(a)) scales(cur, sc);
+      auto fitted = [&](float (&s)[U::NS]) {
+        if constexpr (kFit) {
+          norm::F<U::NS> f;
+#pragma unroll
+          for (int k = 0; k < U::NS; ++k) f.v[k] = s[k];
+          f = norm::mul(f, norm::fill<U::NS>(down));
+#pragma unroll
+          for (int k = 0; k < U::NS; ++k) s[k] = f.v[k];
+        }
+      };
+      fitted(sc);
       bool ok = true;
       for (int i = group; cur.w.in(a); i += kGroups) {
         Pos nxt = cur;
@@ -327,6 +346,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
         cur = nxt;
 #pragma unroll
         for (int k = 0; k < U::NS; ++k) sc[k] = scn[k];
+        fitted(sc);
       }
       if (!ok) {
         i8_flag();
@@ -434,6 +454,7 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
     uint8_t* stg = staging + warp * C::kStaging;  // 16-byte piece s of row r at piece s ^ (r / 2 % 4): no bank conflicts
     float* cs = reinterpret_cast<float*>(colscale + warp * C::kCols);
     const bool split = a.part != nullptr, scaled = C::kCols && !split;
+    [[maybe_unused]] const float up = kFit ? fit_up(*most) : 1.0f;
     const int type = split ? DISCO_F32 : a.out_type, eb = type == DISCO_F32 ? 4 : 2;
     const bool h16 = type == DISCO_F16;
     // chunks of 32 columns; where two warps share the lanes, every second chunk, or all of every second tile
@@ -477,6 +498,9 @@ __global__ void __launch_bounds__(Plan<FA>::kThreads, 1)
       for (int c0 = c00; c0 < cols && rows > 0; c0 += step) {
         uint32_t v[32];
         tmem_ld32(tmem + ab * acc_cols + ((uint32_t)(q4 * 32) << 16) + c0, v);
+        if constexpr (kFit)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * up);
         if (scaled) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
