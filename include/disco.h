@@ -572,7 +572,7 @@ DISCO_API int disco_matmul_i8_bwd_weight(const void* dy, const void* q, const fl
 
 /* SiLU: g / (1 + exp(-g)).  GELU: g Phi(g), Phi the normal distribution.  With
    bf16 and fp16 tensors the SiLU takes the approximate exponential and
-   reciprocal (2^-21 and 2^-23 |g| relative), and gates below -87 give 0. */
+   reciprocal (within 2^-20 + 2^-23 |g| relative), and gates below -87 give 0. */
 typedef enum { DISCO_SILU = 0, DISCO_GELU = 1 } disco_activation;
 
 /* Gated activation of x [B, 2 C, P], its gates in the first C channels:

@@ -84,9 +84,10 @@ __device__ __forceinline__ uint32_t quantize_y(float y, const Quantizer& z) {
 
 // act(g) and act'(g).  SiLU: g s, s (1 + g (1 - s)) with s = 1 / (1 + e^-g).
 // GELU: g Phi, Phi + g phi with the normal distribution Phi and its density phi.
-// T: the tensors' type.  16-bit ones take the approximate exponential and
-// reciprocal (2^-22 relative and 2^-23 |g| of the exponent, below their rounding of
-// 2^-9 or 2^-12) of t = e^-|g|, s = (1 or t) / (1 + t): gates below -87 give 0.
+// T: the tensors' type.  16-bit ones take the approximate exponential and reciprocal of
+// t = e^-|g|, s = (1 or t) / (1 + t): 2^-22 of the exponential, 2^-23 |g| of its argument's
+// rounding, 2^-23 of the reciprocal and 2^-24 of each sum and product, within 2^-20 + 2^-23 |g| together,
+// below the types' rounding of 2^-8 or 2^-11; gates below -87 give 0.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(T) == 4) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-g)));

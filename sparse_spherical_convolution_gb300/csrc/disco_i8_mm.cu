@@ -1,6 +1,7 @@
 // disco_i8_mm.cu -- products over the channels of each token with activations and
 // weights in 8-bit integers, and their gradients from the 8-bit activation:
-// checks, the choice of a kernel, and the general one.
+// checks, the cut into tiles and parts, operands laid out once a call, the kernel of a few
+// rows, and the joining of parts.  All else goes to the tensor cores (disco_i8_tc.cuh).
 //
 //   y[b,o,p]  = scale[b,p] wscale[o] sum_c W[o,c] q[b,c,p]      (disco_matmul_i8)
 //   dx[b,c,p] = sum_o wscale[o] W[o,c] dy[b,o,p]                (disco_matmul_i8_bwd_input)

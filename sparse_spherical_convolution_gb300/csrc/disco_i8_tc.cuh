@@ -4,18 +4,22 @@
 //   out[z][m][n] = rs[m] cs[n] sum_{r, k} A(m, k) B(n, k)
 //
 // sm_103a's tensor cores have no 8-bit integer form worth the name, so integers
-// become fp16 (or the tensors' 16-bit type, where a scale belongs to k): fp16 holds -128 .. 127,
-// their products are exact, and sums are fp32.  A is the activation (8-bit integers,
+// become fp16: it holds -128 .. 127, their products are exact, and sums are fp32.  Where a scale belongs
+// to k (both gradients) the integer times its scale is rounded to the tensors' 16-bit type, as a 16-bit operand
+// would be (errors sqrt(2) of the output's rounding; a high and a low part would double the matrix work).  A is the activation (8-bit integers,
 // converted on the way into shared memory, or 16-bit); B is 16-bit: a weight converted
 // once a call into the workspace, or dy.  A tile is 128 m x NB n (NB <= 256), 64 k to a
 // stage, so a step converts 128 lines and multiplies 128 by 256: with both operands
 // converted in the main loop the product of 16384 rows of 2048 by 2048 took 261 us.
 // Measured (GB300, bf16): that product 106 us, 1.30 PFLOP/s, dx 91, dW 132; 512 -> 512
 // channels on 360x720 128 us, dx 124, dW 126; 2 x 128 -> 256 on 361x720 85, 68 and 74.
-// Large products are bound by shared memory (a step of 128 x 256 x 64 writes 56 KB of it and
-// reads as much, 900 cycles; dx's 48 and 48 KB 770), grids of few channels by what a tile costs at least (1.3 us of an SM),
-// between them by HBM.  Dropped: pairs of CTAs (256 x 256 tiles, half of B each; rows 134 us and
-// dx 118), and prefetches to L2 four steps ahead (rows 119, dx 184, dW 246).
+// What the counters say of the large ones, while their CTAs run: 512 channels, the threads' accesses to shared
+// memory (converters and epilogue) 80 % of their pipe, the matrix unit 46 %; that product of rows, no unit above
+// 60 % (matrix unit 59, accesses 53); its dx, the matrix unit 73 %, 18 TB/s from L2; its dW, 128 tiles on as many of
+// the 152 SMs, there the matrix unit 52 %, issue slots 48 %.  Shared memory's banks are read and written a quarter of the
+// time each.  Grids of few channels are bound by what a tile costs at least (1.3 us of an SM), those between by HBM.
+// Dropped: pairs of CTAs (256 x 256 tiles, half of B each; rows 134 us and dx 118, before the issuing threads were
+// elected), and prefetches to L2 four steps ahead (rows 119, dx 184, dW 246).
 // Persistent kernel:
 //   epilogue     (8 warps; 4 for the weight's gradient, whose tiles are few): tcgen05.ld,
 //                scales, rounding, stores along the output's rows

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) glu_bwd_odd_kernel(const GluBwdArgs a, co
 template <typename T, int V>
 int glu_bwd(const GluBwdArgs& a, cudaStream_t st) {
   const long long grid = (a.n / V + 255) / 256;
-  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^39 elements");
+  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 - 1 blocks of %d elements", 256 * V);
   if (a.P == 1) glu_bwd_kernel<T, V, true><<<(unsigned)grid, 256, 0, st>>>(a);
   else glu_bwd_kernel<T, V, false><<<(unsigned)grid, 256, 0, st>>>(a);
   return check_launch("glu_bwd_kernel");
@@ -232,7 +232,7 @@ template <typename T>
 int glu_bwd_odd(const GluBwdArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
   const long long per_row = (a.P + 32 * V - 1) / (32 * V), units = a.n / a.P * per_row, grid = (units + 7) / 8;
-  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^39 elements");
+  if (grid > 0x7fffffffLL) return fail(DISCO_ERR_UNSUPPORTED, "more than 2^31 - 1 blocks of 8 times %d pixels", 32 * V);
   glu_bwd_odd_kernel<T><<<(unsigned)grid, 256, 0, st>>>(a, per_row, units);
   return check_launch("glu_bwd_odd_kernel");
 }

@@ -65,6 +65,50 @@ def test_zeros_and_the_ends_of_fp32(lib, shape):
         assert bool((dx == 0).all()) and bool((dW == 0).all())
 
 
+@pytest.mark.parametrize("shape", [(40, 96, 160, 1), (2, 48, 1030, 72), (2, 48, 72, 1165)], ids=t.ids)
+def test_streams_graphs_and_spoilt_workspaces(lib, shape):
+    """Up to 1024 scales and more: captured and replayed with the workspace spoilt between, and two calls at once."""
+    B, Cin, Cout, P = shape
+    code = lib.dtype_code(HF)
+    runs = []
+    for seed in (0, 1):
+        q, scale, W, wscale, dy = [v.cuda() for v in t._operands(shape, HF, seed)]
+        scale, wscale = scale * 2.0 ** (-20 + 30 * seed), wscale * 2.0 ** (-20 + 30 * seed)
+        dx, dW = torch.empty((B, Cin, P), dtype=HF, device="cuda"), torch.empty((Cout, Cin), dtype=HF, device="cuda")
+        ws = t._ws(max(f(*shape, code) for f in (lib.disco_matmul_i8_bwd_input_workspace_bytes, lib.disco_matmul_i8_bwd_weight_workspace_bytes)))
+
+        def both(dy=dy, q=q, scale=scale, W=W, wscale=wscale, dx=dx, dW=dW, ws=ws):
+            lib.disco_matmul_i8_bwd_input(dy, W, wscale, dx, *shape, ws)
+            lib.disco_matmul_i8_bwd_weight(dy, q, scale, dW, *shape, ws)
+        both()
+        torch.cuda.synchronize()
+        runs.append((both, (dx, dW), (dx.clone(), dW.clone()), ws))
+
+    def check():
+        torch.cuda.synchronize()
+        for _, got, want, ws in runs:
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+                a.zero_()
+            ws.fill_(255)
+        torch.cuda.synchronize()
+    check()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(4):
+        for s, (both, *_) in zip(streams, runs):
+            with torch.cuda.stream(s):
+                both()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for both, *_ in runs:
+            both()
+    for _ in range(3):
+        graph.replay()
+        check()
+    assert lib.disco_device_status() == 0
+
+
 def test_scales_of_one_call_far_apart(lib):
     """Tokens, and output channels, 2^-24 of the others keep what fp16 holds at the largest one's size."""
     shape = (64, 48, 40, 1)
