@@ -638,7 +638,9 @@ int tokens_tiles(const TokenArgs& a, cudaStream_t st) {
   g.nj = (a.C + g.NT / g.LX - 1) / (g.NT / g.LX);
   const size_t smem = (size_t)G * g.nj * g.NT * 16 + (size_t)g.LX * V * (4 * kOwn + g.NT / 32 * kSum);
   if (smem > norm::kMaxSmem) return DISCO_ERR_UNSUPPORTED;
-  g.roomy = (long long)G * a.C * a.P >= 2 * V ? a.B : 0;  // samples of one channel by two pixels are shorter: decided here, as in the kernel it cost registers (221 us became 257)
+  // Samples of one channel by two pixels are shorter.  Decided here: in the kernel it cost
+  // registers (2 x 128 channels on 361x719 with the checkpoint 221 us, 257 then).
+  g.roomy = (long long)G * a.C * a.P >= 2 * V ? a.B : 0;
   g.per_sample = (a.P + g.LX * V - 1) / (g.LX * V);
   g.tiles = g.per_sample * a.B;
   auto kern = tokens_tile_kernel<T, GLU, XQ, YQ, ODD>;
